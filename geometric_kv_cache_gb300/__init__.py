@@ -33,10 +33,21 @@ MKV_DEV_BAD_SEQ_LEN = 0x1
 MKV_DEV_BAD_N_KEEP = 0x2
 MKV_DEV_INTERNAL = 0x4
 MKV_DEV_TIMEOUT = 0x8
+MKV_DEV_BAD_PAGE = 0x10
+MKV_DEV_NO_PAGES = 0x20
+MKV_DEV_BAD_PARENT = 0x40
+MKV_DEV_BAD_TOKENS = 0x80
+MKV_DEV_BAD_INDEX = 0x100
 
 MKV_MODE_L2 = 0
 MKV_MODE_COSINE = 1
 _MODES = {"l2": MKV_MODE_L2, "cosine": MKV_MODE_COSINE, MKV_MODE_L2: MKV_MODE_L2, MKV_MODE_COSINE: MKV_MODE_COSINE}
+
+MKV_ROPE_HALF = 0
+MKV_ROPE_INTERLEAVED = 1
+_ROPE_LAYOUTS = {"half": MKV_ROPE_HALF, "interleaved": MKV_ROPE_INTERLEAVED, MKV_ROPE_HALF: MKV_ROPE_HALF,
+                 MKV_ROPE_INTERLEAVED: MKV_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "by_parts": 2, 0: 0, 1: 1, 2: 2}
 
 HEAD_DIM = 128
 
@@ -50,12 +61,28 @@ EXPORTED = (
     "mkv_compress_quota", "mkv_oja_workspace_size", "mkv_oja_score", "mkv_compress_oja", "mkv_oja_score_profiled",
     "mkv_compress_inplace", "mkv_set_head_groups", "mkv_set_fused", "mkv_centroid_score",
     "mkv_inject_stalled_fused", "mkv_set_head_group_ring", "mkv_head_group_plan", "mkv_set_oja_pair",
+    "mkv_page_workspace_size", "mkv_page_update", "mkv_page_compact", "mkv_rope_append", "mkv_rope_frequencies",
+    "mkv_attention_workspace_size", "mkv_paged_attention",
 )
 
 
 class MkvShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("t_max", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("seq_lens", ctypes.c_void_p)]
+
+
+class MkvPagePool(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p)]
+
+
+class MkvPageLists(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+class MkvNewTokens(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("q_start", ctypes.c_void_p)]
 
 
 # mkv_dtype of each supported cache element type
@@ -89,6 +116,7 @@ def load(build_if_missing: bool = True):
             _build.build_library()
         lib = ctypes.CDLL(path)
         i32, u32, f64, vp, sz = ctypes.c_int32, ctypes.c_uint32, ctypes.c_double, ctypes.c_void_p, ctypes.c_size_t
+        i64, f32 = ctypes.c_int64, ctypes.c_float
         sig = {
             "mkv_num_keep": (i32, [i32, f64]),
             "mkv_num_windows": (i32, [i32, i32]),
@@ -127,6 +155,16 @@ def load(build_if_missing: bool = True):
             "mkv_num_keep_quota": (i32, [i32, f64, i32]),
             "mkv_select_quota": (i32, [vp, MkvShape, f64, i32, i32, vp, vp, vp, sz, vp]),
             "mkv_compress_quota": (i32, [vp, vp, MkvShape, f64, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+            "mkv_page_workspace_size": (sz, [MkvPagePool, MkvPageLists]),
+            "mkv_page_update": (i32, [MkvPagePool, MkvPageLists, vp, vp, vp, MkvPageLists, vp, vp, sz, vp]),
+            "mkv_page_compact": (i32, [MkvPagePool, MkvPageLists, vp, vp, i32, vp, vp, vp, i32, vp, MkvPageLists, vp,
+                                       vp, sz, vp]),
+            "mkv_rope_append": (i32, [vp, i64, vp, i64, vp, i64, MkvNewTokens, vp, vp, i32, i32, f32, vp, MkvPagePool,
+                                      MkvPageLists, f32, f32, vp, sz, vp]),
+            "mkv_rope_frequencies": (i32, [i32, f64, i32, f64, i32, f64, f64, vp]),
+            "mkv_attention_workspace_size": (sz, [MkvPagePool, MkvPageLists, MkvNewTokens, i32, i32]),
+            "mkv_paged_attention": (i32, [vp, i64, MkvNewTokens, i32, MkvPagePool, MkvPageLists, i32, f32, f32, f32,
+                                          i32, i32, vp, i64, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -461,6 +499,179 @@ def mkv_inject_stalled_fused(K, V, ratio, mode, keep_stride, K_out, V_out, idx, 
                                            int(keep_stride), _ptr(K_out), _ptr(V_out), _ptr(idx), _ptr(kept),
                                            int(stage), _ptr(workspace), workspace.numel(), _stream(stream)),
            "mkv_inject_stalled_fused")
+
+
+# --------------------------------------------------------------- paged caches --
+
+def _on_device(*ts):
+    """The one CUDA device of a call's tensors, which must be the current one
+    (the launches go to a stream of the current device)."""
+    devs = {t.device for t in ts if t is not None}
+    if any(d.type != "cuda" for d in devs):
+        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
+    if len(devs) != 1 or next(iter(devs)).index != torch.cuda.current_device():
+        raise ValueError("tensors of one call must live on one CUDA device, the current one")
+
+
+def _int32(t, shape, what):
+    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous int32 tensor {list(shape)}")
+
+
+def _workspace(ws):
+    if ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous uint8 tensor")
+
+
+def pool_of(k_pages: torch.Tensor, v_pages: torch.Tensor) -> MkvPagePool:
+    """mkv_page_pool of two [n_pages, page_size, head_dim] bf16 or float8_e4m3fn tensors."""
+    if k_pages.dim() != 3 or k_pages.dtype not in DTYPES:
+        raise ValueError("k_pages must be a bf16 or float8_e4m3fn tensor [n_pages, page_size, head_dim]")
+    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages and v_pages must have one shape and dtype")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        raise ValueError("k_pages and v_pages must be contiguous")
+    n, p, d = k_pages.shape
+    return MkvPagePool(n, p, d, DTYPES[k_pages.dtype], k_pages.data_ptr(), v_pages.data_ptr())
+
+
+def lists_of(table: torch.Tensor, lens: Optional[torch.Tensor] = None) -> MkvPageLists:
+    """mkv_page_lists of table int32 [batch, heads, max_pages] and lens int32 [batch, heads]."""
+    if table.dim() != 3:
+        raise ValueError("table must be an int32 tensor [batch, heads, max_pages]")
+    _int32(table, table.shape, "table")
+    _int32(lens, table.shape[:2], "lens")
+    b, h, m = table.shape
+    return MkvPageLists(b, h, m, table.data_ptr(), None if lens is None else lens.data_ptr())
+
+
+def _token_rows(t, heads, d, n_tokens, what):
+    """Stride (elements) between the tokens of a bf16 [n_tokens, heads, d] tensor, whose tokens may lie apart."""
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != (n_tokens, heads, d):
+        raise ValueError(f"{what} must be a bf16 tensor [{n_tokens}, {heads}, {d}]")
+    if n_tokens and ((heads > 1 and t.stride(1) != d) or t.stride(2) != 1):
+        raise ValueError(f"the heads of one token of {what} must be contiguous")
+    return heads * d if n_tokens <= 1 else t.stride(0)
+
+
+def page_workspace_for(k_pages: torch.Tensor, table: torch.Tensor) -> torch.Tensor:
+    """A zeroed workspace for mkv_page_update, mkv_page_compact and mkv_rope_append."""
+    n = int(load().mkv_page_workspace_size(pool_of(k_pages, k_pages), lists_of(table)))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=k_pages.device)
+
+
+def mkv_page_update(k_pages, v_pages, table, lens, refs, table_out, lens_out, refs_out, workspace, parent=None,
+                    n_new=None, stream=None):
+    """Page lists after a step: row b continues row parent[b] (-1: it ends; None: itself) and grows by n_new[b]
+    tokens. table int32 [batch, heads, max_pages], lens int32 [batch, heads], refs int32 [n_pages]; parent and n_new
+    int32 [batch]. Full pages are shared, partly filled last pages copied for all but one child. With parent None,
+    table_out and lens_out may be table and lens; refs_out may always be refs."""
+    _on_device(k_pages, v_pages, table, lens, refs, table_out, lens_out, refs_out, workspace, parent, n_new)
+    pool, src, dst = pool_of(k_pages, v_pages), lists_of(table, lens), lists_of(table_out, lens_out)
+    _int32(refs, (pool.n_pages,), "refs")
+    _int32(refs_out, (pool.n_pages,), "refs_out")
+    _int32(parent, (src.batch,), "parent")
+    _int32(n_new, (src.batch,), "n_new")
+    _workspace(workspace)
+    _check(load().mkv_page_update(pool, src, _ptr(refs), _ptr(parent), _ptr(n_new), dst, _ptr(refs_out),
+                                  _ptr(workspace), workspace.numel(), _stream(stream)), "mkv_page_update")
+
+
+def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K=None,
+                     V=None, seq_lens=None, stream=None):
+    """Compaction in pages: list h keeps its tokens idx[h][:kept[h]] in new pages, its old pages lose a holder. idx
+    int32 [batch, heads, n] (None: the first kept tokens), kept int32 [batch, heads], as mkv_compress writes them.
+    With K and V [batch, heads, t_max, head_dim] (and seq_lens) the tokens come from that contiguous cache instead."""
+    _on_device(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K, V, seq_lens)
+    pool, src, dst = pool_of(k_pages, v_pages), lists_of(table, lens), lists_of(table_out, lens_out)
+    _int32(refs, (pool.n_pages,), "refs")
+    _int32(refs_out, (pool.n_pages,), "refs_out")
+    _int32(kept, (src.batch, src.heads), "kept")
+    if idx is not None:
+        _int32(idx, (src.batch, src.heads, idx.shape[-1]), "idx")
+    _workspace(workspace)
+    t_max = 0
+    if (K is None) != (V is None) or (K is None and seq_lens is not None):
+        raise ValueError("K and V come together (and seq_lens only with them)")
+    if K is not None:
+        _cache_types(K, V, k_pages)
+        t_max = K.shape[2] if K.dim() == 4 else 0
+        if tuple(K.shape) != (src.batch, src.heads, t_max, pool.head_dim) or K.shape != V.shape:
+            raise ValueError("K and V must be [batch, heads, t_max, head_dim] of the lists' sizes")
+        if not (K.is_contiguous() and V.is_contiguous()):
+            raise ValueError("tensors passed to the CUDA library must be contiguous")
+        _int32(seq_lens, (src.batch,), "seq_lens")
+    _check(load().mkv_page_compact(pool, src, _ptr(refs), _ptr(idx), 0 if idx is None else idx.shape[-1], _ptr(kept),
+                                   _ptr(K), _ptr(V), t_max, _ptr(seq_lens), dst, _ptr(refs_out), _ptr(workspace),
+                                   workspace.numel(), _stream(stream)), "mkv_page_compact")
+
+
+def mkv_rope_frequencies(rot_dim: int, theta: float, scaling="plain", scale: float = 1.0, original_len: int = 0,
+                         low_turns: float = 0.0, high_turns: float = 0.0) -> torch.Tensor:
+    """Rotary frequencies (host helper): fp32 [rot_dim / 2] on the CPU. scaling "plain", "linear" (all divided by
+    scale) or "by_parts" (pairs of fewer than low_turns turns over original_len positions divided by scale, pairs of
+    more than high_turns kept, a ramp between)."""
+    out = torch.empty(max(int(rot_dim) // 2, 0), dtype=torch.float32)
+    st = load().mkv_rope_frequencies(int(rot_dim), float(theta), _ROPE_SCALINGS[scaling], float(scale),
+                                     int(original_len), float(low_turns), float(high_turns), _ptr(out))
+    if st != 0:
+        raise MKVError(MKV_ERR_INVALID_ARG, "mkv_rope_frequencies")
+    return out
+
+
+def mkv_rope_append(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace,
+                    layout="half", factor: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """Rotary positions of a step's new tokens: Q [n_tokens, q_heads, d] turned into Q_out, K [n_tokens, heads, d]
+    turned into the pages, V into the pages (all bf16; tokens may lie apart, as in a fused projection). Row b's tokens
+    are [q_start[b], q_start[b + 1]) and the last ones of its lists. inv_freq fp32 [rot_dim / 2] on the device."""
+    _on_device(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace)
+    pool, lists = pool_of(k_pages, v_pages), lists_of(table, lens)
+    if Q.dim() != 3:
+        raise ValueError("Q must be a bf16 tensor [n_tokens, q_heads, head_dim]")
+    n, hq, d = Q.shape[0], Q.shape[1], pool.head_dim
+    qs, ks, vs = (_token_rows(t, h, d, n, w) for t, h, w in ((Q, hq, "Q"), (K, lists.heads, "K"), (V, lists.heads, "V")))
+    _token_rows(Q_out, hq, d, n, "Q_out")
+    if not Q_out.is_contiguous():
+        raise ValueError("Q_out must be contiguous")
+    _int32(positions, (n,), "positions")
+    _int32(q_start, (lists.batch + 1,), "q_start")
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous fp32 tensor [rot_dim / 2]")
+    _workspace(workspace)
+    _check(load().mkv_rope_append(_ptr(Q), qs, _ptr(K), ks, _ptr(V), vs, MkvNewTokens(n, hq, q_start.data_ptr()),
+                                  _ptr(positions), _ptr(inv_freq), 2 * inv_freq.numel(), _ROPE_LAYOUTS[layout],
+                                  float(factor), _ptr(Q_out), pool, lists, float(k_scale), float(v_scale),
+                                  _ptr(workspace), workspace.numel(), _stream(stream)), "mkv_rope_append")
+
+
+def attention_workspace_for(Q, k_pages, table, max_q: int, max_len: int) -> torch.Tensor:
+    """A zeroed workspace for mkv_paged_attention on these shapes."""
+    n = int(load().mkv_attention_workspace_size(pool_of(k_pages, k_pages), lists_of(table),
+                                                MkvNewTokens(Q.shape[0], Q.shape[1], None), int(max_q), int(max_len)))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=Q.device)
+
+
+def mkv_paged_attention(Q, k_pages, v_pages, table, lens, q_start, max_q: int, max_len: int, O, workspace,
+                        scale: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0, window: int = 0,
+                        sinks: int = 0, lse=None, stream=None):
+    """Attention of new tokens Q bf16 [n_tokens, q_heads, d] over the paged cache, into O (like Q) and, if given, lse
+    fp32 [n_tokens, q_heads]. Row b's tokens are [q_start[b], q_start[b + 1]) and the last ones of its lists; each sees
+    the tokens up to its own, with window > 0 the last `window` of them and the first `sinks`. max_q and max_len bound
+    the rows' new tokens and the lists' lengths. scale defaults to 1 / sqrt(d)."""
+    _on_device(Q, k_pages, v_pages, table, lens, q_start, O, workspace, lse)
+    pool, lists = pool_of(k_pages, v_pages), lists_of(table, lens)
+    if Q.dim() != 3:
+        raise ValueError("Q must be a bf16 tensor [n_tokens, q_heads, head_dim]")
+    n, hq, d = Q.shape[0], Q.shape[1], pool.head_dim
+    qs, os_ = _token_rows(Q, hq, d, n, "Q"), _token_rows(O, hq, d, n, "O")
+    _int32(q_start, (lists.batch + 1,), "q_start")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, hq) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 tensor [n_tokens, q_heads]")
+    _workspace(workspace)
+    _check(load().mkv_paged_attention(_ptr(Q), qs, MkvNewTokens(n, hq, q_start.data_ptr()), int(max_q), pool, lists,
+                                      int(max_len), float(d ** -0.5 if scale is None else scale), float(k_scale),
+                                      float(v_scale), int(window), int(sinks), _ptr(O), os_, _ptr(lse),
+                                      _ptr(workspace), workspace.numel(), _stream(stream)), "mkv_paged_attention")
 
 
 def mkv_device_status(workspace, stream=None) -> int:

@@ -1,0 +1,582 @@
+// sm_103a attention of a step's new tokens over a paged cache
+// (mkv_paged_attention): the consumer of the compacted cache ("ManifoldKV:
+// Training-Free KV Cache Compression via Euclidean Outlier Detection", ICML
+// 2026 poster 62526, abstract: the tokens the cache retains are what later
+// queries see).
+//
+// For the rows (new token i, query head g of the KV head's group) of one list,
+// packed 16 to a tile, with scores x_s = scale q.k_s over the visible tokens:
+//     m = max x, l = sum 2^(x - m), O = sum 2^(x - m) v / l
+// kept as running values over blocks of keys (m, l and O in fp32; a new maximum
+// multiplies l and O by 2^(m_old - m_new)).
+//
+// Item = (list, tile of 16 rows, part of the key axis), one CTA each. Every
+// warp of the CTA walks its own blocks of KT keys with its own ring of
+// cp.async stages (16 bytes per lane, the block's page entries read one block
+// ahead), so the loop has no CTA barrier; scores and values run on mma.sync
+// m16n8k16 with the 16 rows as M. The warps' (m, l, O) meet in shared memory at
+// the end, the parts of the key axis in k_attend_combine, in part order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "mkv_device.cuh"
+#include "mkv_pages.h"
+
+namespace mkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kRows = 16;  // rows per tile (the MMA's M)
+
+// Shape of one instantiation.
+template <int D, int ES>
+struct Attend {
+    static constexpr int KT = D == 256 ? 16 : 32;      // keys per block
+    static constexpr int WARPS = ES == 1 ? 8 : 4;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int RB = D * ES;                  // bytes per cached row
+    static constexpr int CPR = RB / 16;                // 16-byte chunks per row
+    static constexpr int HALF = KT * RB;               // bytes of a block's keys
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int STAGES = 4 * WARPS * STAGE <= 200 * 1024 ? 4 : 3;  // what shared memory holds
+    static constexpr int RING = STAGES * STAGE;        // per warp
+    static constexpr int MERGE = WARPS * kRows * D * 4;
+    static constexpr int SMEM = WARPS * RING > MERGE ? WARPS * RING : MERGE;
+};
+
+__device__ __forceinline__ uint32_t saddr(const void *p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// 16 bytes to shared memory; zeros when !real.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Bytes s.x and s.y of v (a __byte_perm selector that puts them in the upper
+// byte of each half) as two bf16: an E4M3 code's sign to the sign, its
+// exponent and mantissa fields to the lowest exponent bits and highest
+// mantissa bits, which is the value times 2^-120 (subnormal codes too), then
+// times 2^120: exact.
+__device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t v, uint32_t sel)
+{
+    const uint32_t w = __byte_perm(v, 0u, sel);
+    const uint32_t r = (w & 0x80008000u) | ((w >> 4) & 0x07F007F0u);
+    const uint32_t up = 0x7B807B80u;  // 2^120, twice
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&r),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&up));
+    return *reinterpret_cast<const uint32_t *>(&y);
+}
+
+// Where 16-byte chunk c of row r of a block lies: rows of CPR chunks, chunks
+// exchanged so that the eight rows (ldmatrix) or the two rows (16-byte loads
+// of E4M3 keys) that one access reads fall into distinct banks.
+template <int CPR>
+__device__ __forceinline__ uint32_t at_rows8(int r, int c)
+{
+    return (uint32_t)(r * CPR + (c ^ (CPR >= 8 ? r & 7 : (r >> 1) & 3))) * 16u;
+}
+template <int CPR>
+__device__ __forceinline__ uint32_t at_rows2(int r, int c)
+{
+    return (uint32_t)(r * CPR + (c ^ (CPR >= 8 ? (r & 1) << 2 : 0))) * 16u;
+}
+
+// What one tile of rows of one list is.
+struct Tile {
+    int b, j, n, L, row0, rows;  // batch row, head, new tokens, list length, first packed row, rows
+    int p_lo, p_hi;              // places of the first and last row's token
+    int end;                     // keys from here on are visible to no row
+    int sink_blocks, win_block;  // blocks of keys: [0, sink_blocks) and [win_block, ...)
+    int blocks;                  // in all
+};
+
+template <int KT>
+__device__ __forceinline__ bool make_tile(const AttnArgs &a, int64_t list, int tile, Tile &t, bool report)
+{
+    t.b = (int)(list / a.heads);
+    t.j = (int)(list - (int64_t)t.b * a.heads);
+    const int lo = a.q_start[t.b], hi = a.q_start[t.b + 1];
+    t.n = hi - lo;
+    t.L = a.lens[list];
+    if (lo < 0 || hi < lo || hi > a.n_tokens || t.n > a.max_q) {
+        if (report) atomicOr(a.status, MKV_DEV_BAD_TOKENS);
+        return false;
+    }
+    if (t.L < 0 || t.L > a.max_len) {
+        if (report) atomicOr(a.status, MKV_DEV_BAD_SEQ_LEN);
+        return false;
+    }
+    t.row0 = tile * kRows;
+    t.rows = min(kRows, t.n * a.group - t.row0);
+    if (t.rows <= 0) return false;
+    t.p_lo = t.L - t.n + t.row0 / a.group;
+    t.p_hi = t.L - t.n + (t.row0 + t.rows - 1) / a.group;
+    t.end = max(0, t.p_hi + 1);
+    const int all = (t.end + KT - 1) / KT;
+    t.win_block = t.sink_blocks = 0;
+    if (a.window > 0) {
+        const int start = max(0, t.p_lo - a.window + 1);  // the first key inside any row's window
+        const int sinks = (min(a.sinks, t.end) + KT - 1) / KT;
+        t.win_block = min(start / KT, all);
+        t.sink_blocks = min(sinks, t.win_block);
+    }
+    t.blocks = t.sink_blocks + all - t.win_block;
+    return true;
+}
+
+template <int D, int ES>
+__global__ void __launch_bounds__(Attend<D, ES>::THREADS, 1)
+k_attend(const AttnArgs a)
+{
+    using A = Attend<D, ES>;
+    constexpr int KT = A::KT, NT = KT / 8, KS = D / 16;  // key tiles of 8, dim steps of 16
+    constexpr bool Q_REGS = D <= 128;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) uint8_t s_q[Q_REGS ? 16 : kRows * D * 2];
+    __shared__ float2 s_ml[A::WARPS][kRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
+    // the parts of a tile lie next to each other, tiles of a list too
+    const int64_t item = blockIdx.x;
+    const int split = (int)(item % a.splits);
+    const int64_t lt = item / a.splits;
+    const int64_t list = lt / a.tiles;
+    const int tile = (int)(lt - list * a.tiles);
+    Tile t;
+    pdl_trigger();
+    if (!make_tile<KT>(a, list, tile, t, split == 0 && tile == 0 && threadIdx.x == 0)) return;
+    const int first = (int)((int64_t)t.blocks * split / a.splits), last = (int)((int64_t)t.blocks * (split + 1) / a.splits);
+    const int32_t *table = a.table + list * a.max_pages;
+    const int page_mask = a.page_size - 1;
+
+    // the two rows of this lane: packed row -> (new token, query head)
+    const int qrow0 = a.q_start[t.b];
+    auto q_row = [&](int r) -> const uint8_t * {
+        const int R = t.row0 + min(r, t.rows - 1);
+        const int i = R / a.group, g = R - i * a.group;
+        return a.Q + 2 * ((int64_t)(qrow0 + i) * a.q_stride + (int64_t)(t.j * a.group + g) * D);
+    };
+    // dims of an A fragment: pairs (2t, 2t + 1) and (2t + 8, 2t + 9) of a step,
+    // for E4M3 keys the dims that the lane's 16-byte load holds
+    auto q_dim = [&](int k, int hi) -> int {
+        return ES == 2 ? k * 16 + 2 * tq + 8 * hi : (k / 4) * 64 + 16 * tq + (k % 4) * 4 + 2 * hi;
+    };
+    uint32_t q[Q_REGS ? KS : 1][4];
+    if constexpr (Q_REGS) {
+        const uint8_t *q0 = q_row(gr), *q1 = q_row(gr + 8);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                q[k][2 * hi] = *reinterpret_cast<const uint32_t *>(q0 + 2 * q_dim(k, hi));
+                q[k][2 * hi + 1] = *reinterpret_cast<const uint32_t *>(q1 + 2 * q_dim(k, hi));
+            }
+    } else {
+        for (int o = threadIdx.x; o < kRows * D / 8; o += A::THREADS)
+            reinterpret_cast<uint4 *>(s_q)[o] = *reinterpret_cast<const uint4 *>(q_row(o / (D / 8)) + 16 * (o % (D / 8)));
+        __syncthreads();
+    }
+    const int p0 = t.L - t.n + (t.row0 + min(gr, t.rows - 1)) / a.group;
+    const int p1 = t.L - t.n + (t.row0 + min(gr + 8, t.rows - 1)) / a.group;
+
+    const uint32_t ring = saddr(smem) + warp * A::RING;
+    auto key0 = [&](int blk) -> int { return (blk < t.sink_blocks ? blk : blk - t.sink_blocks + t.win_block) * KT; };
+    // the pool row of this lane's key of a block, -1 where there is none
+    auto lookup = [&](int blk) -> int {
+        if (blk >= last || lane >= KT) return -1;
+        const int s = key0(blk) + lane;
+        if (s >= t.end) return -1;
+        const int id = table[s >> a.page_shift];
+        if ((uint32_t)id >= (uint32_t)a.n_pages) {
+            atomicOr(a.status, MKV_DEV_BAD_PAGE);
+            return -1;
+        }
+        return (id << a.page_shift) + (s & page_mask);
+    };
+    auto issue = [&](int stage, int blk, int row) {
+        if (blk < last) {
+            const uint32_t dst = ring + stage * A::STAGE;
+#pragma unroll
+            for (int i = 0; i < KT * A::CPR / 32; ++i) {
+                const int o = lane + 32 * i, r = o / A::CPR, c = o % A::CPR;
+                const int src = __shfl_sync(kFull, row, r);
+                const size_t off = (size_t)max(src, 0) * A::RB + c * 16;
+                cp16(dst + (ES == 2 ? at_rows8<A::CPR>(r, c) : at_rows2<A::CPR>(r, c)), a.k + off, src >= 0);
+                cp16(dst + A::HALF + at_rows8<A::CPR>(r, c), a.v + off, src >= 0);
+            }
+        }
+        cp_commit();
+    };
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+
+    int blk = first + warp;
+    int row = lookup(blk);
+#pragma unroll
+    for (int s = 0; s < A::STAGES - 1; ++s) {
+        const int next = lookup(blk + (s + 1) * A::WARPS);
+        issue(s, blk + s * A::WARPS, row);
+        row = next;
+    }
+    for (int it = 0; blk < last; blk += A::WARPS, ++it) {
+        {
+            const int ahead = blk + (A::STAGES - 1) * A::WARPS;
+            const int next = lookup(ahead + A::WARPS);
+            issue((it + A::STAGES - 1) % A::STAGES, ahead, row);
+            row = next;
+        }
+        cp_wait<A::STAGES - 1>();
+        __syncwarp();
+        const uint32_t kb = ring + (it % A::STAGES) * A::STAGE, vb = kb + A::HALF;
+
+        // scores
+        float s[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        auto q_frag = [&](int k, uint32_t (&f)[4]) {
+            if constexpr (Q_REGS) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = q[k][e];
+            } else {
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                    f[2 * hi] = *reinterpret_cast<const uint32_t *>(s_q + 2 * (gr * D + q_dim(k, hi)));
+                    f[2 * hi + 1] = *reinterpret_cast<const uint32_t *>(s_q + 2 * ((gr + 8) * D + q_dim(k, hi)));
+                }
+            }
+        };
+        if constexpr (ES == 2) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t f[4];
+                q_frag(k, f);
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i) {
+                    uint32_t b[4];
+                    ldsm4(kb + at_rows8<A::CPR>(i * 16 + (lane >> 4) * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)), b);
+                    mma_bf16(s[2 * i], f, b[0], b[1]);
+                    mma_bf16(s[2 * i + 1], f, b[2], b[3]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k4 = 0; k4 < KS / 4; ++k4) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const uint4 w = lds16(kb + at_rows2<A::CPR>(i * 8 + gr, 4 * k4 + tq));
+                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t f[4];
+                        q_frag(4 * k4 + e, f);
+                        mma_bf16(s[i], f, e4m3_to_bf16x2(ws[e], 0x1404), e4m3_to_bf16x2(ws[e], 0x3424));
+                    }
+                }
+            }
+        }
+
+        // mask, running maximum, weights
+        const int k0 = key0(blk), k1 = k0 + KT - 1;
+        const bool whole = k1 <= t.p_lo && (a.window <= 0 || k0 > t.p_hi - a.window || k1 < a.sinks);
+        float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = s[i][e] * a.scale_log2;
+                if (!whole) {
+                    const int key = k0 + i * 8 + 2 * tq + (e & 1), p = e < 2 ? p0 : p1;
+                    const bool seen = key <= p && (a.window <= 0 || key > p - a.window || key < a.sinks);
+                    x = seen ? x : -CUDART_INF_F;
+                }
+                s[i][e] = x;
+                if (e < 2) x0 = fmaxf(x0, x);
+                else x1 = fmaxf(x1, x);
+            }
+        x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 2));
+        if (__any_sync(kFull, x0 > m0 || x1 > m1)) {
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            // (a row that has seen nothing yet has l = 0 and O = 0: any finite factor)
+            const float f0 = m0 == -CUDART_INF_F ? 0.f : exp2_approx(m0 - n0);
+            const float f1 = m1 == -CUDART_INF_F ? 0.f : exp2_approx(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                o[i][0] *= f0;
+                o[i][1] *= f0;
+                o[i][2] *= f1;
+                o[i][3] *= f1;
+            }
+        }
+        const float b0 = m0 == -CUDART_INF_F ? 0.f : m0, b1 = m1 == -CUDART_INF_F ? 0.f : m1;
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const float e0 = exp2_approx(s[i][0] - b0), e1 = exp2_approx(s[i][1] - b0);
+            const float e2 = exp2_approx(s[i][2] - b1), e3 = exp2_approx(s[i][3] - b1);
+            l0 += e0 + e1;
+            l1 += e2 + e3;
+            // the weights rounded for the product with V: to bf16, the MMA's
+            // type next to bf16 values; to fp16 (11 bits) next to E4M3 ones,
+            // which fp16 holds exactly
+            p[i][0] = ES == 2 ? pack_bf16(e0, e1) : pack_f16(e0, e1);
+            p[i][1] = ES == 2 ? pack_bf16(e2, e3) : pack_f16(e2, e3);
+        }
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk) {
+            const uint32_t f[4] = {p[2 * kk][0], p[2 * kk][1], p[2 * kk + 1][0], p[2 * kk + 1][1]};
+            if constexpr (ES == 2) {
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t b[4];
+                    ldsm4_t(vb + at_rows8<A::CPR>(kk * 16 + (lane & 15), 2 * c + (lane >> 4)), b);
+                    mma_bf16(o[2 * c], f, b[0], b[1]);
+                    mma_bf16(o[2 * c + 1], f, b[2], b[3]);
+                }
+            } else {
+                // a 16-byte chunk holds 16 dims: even dims to one column tile, odd to the next
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t b[4];
+                    ldsm4_t(vb + at_rows8<A::CPR>(kk * 16 + (lane & 15), 2 * c + (lane >> 4)), b);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t v0 = b[2 * hf], v1 = b[2 * hf + 1];
+                        mma_f16(o[4 * c + 2 * hf], f, e4m3x2_to_f16x2(__byte_perm(v0, 0, 0x0020)),
+                                e4m3x2_to_f16x2(__byte_perm(v1, 0, 0x0020)));
+                        mma_f16(o[4 * c + 2 * hf + 1], f, e4m3x2_to_f16x2(__byte_perm(v0, 0, 0x0031)),
+                                e4m3x2_to_f16x2(__byte_perm(v1, 0, 0x0031)));
+                    }
+                }
+            }
+        }
+        __syncwarp();  // the stage is free for the next copies
+    }
+    cp_wait<0>();
+    l0 += __shfl_xor_sync(kFull, l0, 1);
+    l1 += __shfl_xor_sync(kFull, l1, 1);
+    l0 += __shfl_xor_sync(kFull, l0, 2);
+    l1 += __shfl_xor_sync(kFull, l1, 2);
+    __syncthreads();  // every ring is done with: the warps' results take its place
+    float *mine = reinterpret_cast<float *>(smem) + warp * kRows * D;
+    if (tq == 0) {
+        s_ml[warp][gr] = make_float2(m0, l0);
+        s_ml[warp][gr + 8] = make_float2(m1, l1);
+    }
+    if constexpr (ES == 2) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            *reinterpret_cast<float2 *>(mine + gr * D + i * 8 + 2 * tq) = make_float2(o[i][0], o[i][1]);
+            *reinterpret_cast<float2 *>(mine + (gr + 8) * D + i * 8 + 2 * tq) = make_float2(o[i][2], o[i][3]);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            *reinterpret_cast<float4 *>(mine + gr * D + c * 16 + 4 * tq) =
+                make_float4(o[2 * c][0], o[2 * c + 1][0], o[2 * c][1], o[2 * c + 1][1]);
+            *reinterpret_cast<float4 *>(mine + (gr + 8) * D + c * 16 + 4 * tq) =
+                make_float4(o[2 * c][2], o[2 * c + 1][2], o[2 * c][3], o[2 * c + 1][3]);
+        }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < t.rows * (D / 4); x += A::THREADS) {
+        const int r = x / (D / 4), c = x % (D / 4);
+        float M = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < A::WARPS; ++w) M = fmaxf(M, s_ml[w][r].x);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < A::WARPS; ++w) {
+            const float2 ml = s_ml[w][r];
+            const float f = ml.x == -CUDART_INF_F ? 0.f : exp2_approx(ml.x - M);
+            const float4 v = reinterpret_cast<const float4 *>(smem)[(w * kRows + r) * (D / 4) + c];
+            sum.x += f * v.x;
+            sum.y += f * v.y;
+            sum.z += f * v.z;
+            sum.w += f * v.w;
+            l += f * ml.y;
+        }
+        if (a.splits > 1) {
+            reinterpret_cast<float4 *>(a.part_o)[(item * kRows + r) * (D / 4) + c] = sum;
+            if (c == 0) a.part_ml[item * kRows + r] = make_float2(M, l);
+            continue;
+        }
+        const float inv = l > 0.f ? a.v_scale / l : 0.f;
+        const int R = t.row0 + r, i = R / a.group, head = t.j * a.group + R - i * a.group;
+        *reinterpret_cast<uint2 *>(a.O + 2 * ((int64_t)(qrow0 + i) * a.o_stride + (int64_t)head * D + 4 * c)) =
+            make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+        if (c == 0 && a.lse)
+            a.lse[(int64_t)(qrow0 + i) * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+    }
+}
+
+// One warp per row: the parts of the key axis, in order.
+template <int D, int KT>
+__global__ void __launch_bounds__(256)
+k_attend_combine(const AttnArgs a)
+{
+    constexpr int E = D / 32;
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t w = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+    const int64_t lt = w / kRows;
+    const int r = (int)(w - lt * kRows);
+    const int64_t list = lt / a.tiles;
+    Tile t;
+    if (list >= (int64_t)a.batch * a.heads || !make_tile<KT>(a, list, (int)(lt - list * a.tiles), t, false) || r >= t.rows)
+        return;
+    float M = -CUDART_INF_F;
+    for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, a.part_ml[(lt * a.splits + s) * kRows + r].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
+    float sum[E], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+        const int64_t at = (lt * a.splits + s) * kRows + r;
+        const float2 ml = a.part_ml[at];
+        if (ml.x == -CUDART_INF_F) continue;
+        const float f = exp2_approx(ml.x - M);
+        l += f * ml.y;
+        const float *v = a.part_o + at * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] += f * v[e];
+    }
+    const float inv = l > 0.f ? a.v_scale / l : 0.f;
+    const int R = t.row0 + r, i = R / a.group, head = t.j * a.group + R - i * a.group;
+    const int64_t token = a.q_start[t.b] + i;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[2 * e] * inv, sum[2 * e + 1] * inv);
+    if (lane == 0 && a.lse)
+        a.lse[token * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+}
+
+template <int D, int ES>
+cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
+{
+    using A = Attend<D, ES>;
+    cudaError_t e = cudaFuncSetAttribute(k_attend<D, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)a.batch * a.heads * a.tiles;
+    k_attend<D, ES><<<(unsigned)(tiles * a.splits), A::THREADS, A::SMEM, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((tiles * kRows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attend_combine<D, A::KT>, a);
+}
+
+}  // namespace
+
+AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int sms)
+{
+    AttnPlan p;
+    p.tiles = (int32_t)(((int64_t)max_q * group + kRows - 1) / kRows);
+    const int64_t base = std::max<int64_t>(1, lists * p.tiles);
+    const int64_t want = (8 * sms + base - 1) / base, most = ((int64_t)max_len + 127) / 128;
+    p.splits = (int32_t)std::max<int64_t>(1, std::min(want, most));
+    if (p.splits > 1) p.bytes = (size_t)base * p.splits * kRows * (head_dim * sizeof(float) + sizeof(float2));
+    return p;
+}
+
+cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t st)
+{
+    if (a.es == 2) {
+        switch (a.head_dim) {
+        case 64: return launch_one<64, 2>(a, st);
+        case 128: return launch_one<128, 2>(a, st);
+        case 256: return launch_one<256, 2>(a, st);
+        }
+    } else {
+        switch (a.head_dim) {
+        case 64: return launch_one<64, 1>(a, st);
+        case 128: return launch_one<128, 1>(a, st);
+        case 256: return launch_one<256, 1>(a, st);
+        }
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace mkv

@@ -1,0 +1,470 @@
+// sm_103a page lists of a paged cache: fork, copy, free and extend
+// (mkv_page_update), and compaction into new pages (mkv_page_compact).
+//
+// The ManifoldKV path ends with a compacted cache whose heads differ in
+// length ("ManifoldKV: Training-Free KV Cache Compression via Euclidean
+// Outlier Detection", ICML 2026 poster 62526, abstract: which past tokens the
+// cache retains). A serving engine keeps it in pages, one list per head.
+//
+// A call is three launches, each a programmatic dependent of the one before:
+//  1. k_page_count: per chunk of rows the pages its lists need, per chunk of
+//     the pool the free pages (refs 0);
+//  2. k_page_assign: every CTA sums the chunk totals before its own (a few KB
+//     from L2), so that lists get their first rank among the new pages and
+//     the lowest free pages land in free_ids[rank]; every CTA also comes to the
+//     same verdict (enough pages, every device argument valid), which CTA 0
+//     writes down;
+//  3. k_page_update / k_page_compact: tables, counts and rows. On a bad
+//     verdict they write the input's lists.
+// Integers only decide, and every rank is a prefix sum: nothing depends on
+// the order of the atomics (counts are sums).
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "mkv_device.cuh"
+#include "mkv_pages.h"
+
+namespace mkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kPageThreads = 256;
+constexpr int kCopyRows = 64;  // output tokens per item of the compaction
+
+__device__ __forceinline__ int pages_of(int len, const PageArgs &a)
+{
+    return (len + a.page_size - 1) >> a.page_shift;
+}
+
+__device__ __forceinline__ bool len_ok(int len, const PageArgs &a)
+{
+    return len >= 0 && len <= (a.max_pages << a.page_shift);
+}
+
+// What one list of `out` becomes (update): its length, how many of the
+// parent's pages it shares, and its pages in all.
+struct ListPlan {
+    int old_len, len, shared, total;
+};
+
+__device__ __forceinline__ ListPlan plan_list(const PageArgs &a, int b, int j, int src, bool keeps)
+{
+    ListPlan p = {0, 0, 0, 0};
+    if (a.kept) {
+        p.len = a.kept[(int64_t)b * a.heads + j];
+        p.total = pages_of(p.len, a);
+        return p;
+    }
+    if (src < 0) return p;
+    p.old_len = a.lens[(int64_t)src * a.heads + j];
+    p.len = p.old_len + (a.n_new ? a.n_new[b] : 0);
+    p.shared = keeps ? pages_of(p.old_len, a) : p.old_len >> a.page_shift;
+    p.total = pages_of(p.len, a);
+    return p;
+}
+
+__device__ __forceinline__ long long warp_sum(long long v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+k_page_count(const PageArgs a)
+{
+    __shared__ long long s_need[kPlanRows];
+    __shared__ uint32_t s_bits[kPlanRows];
+    __shared__ int s_free[kPageThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_trigger();
+    if ((int)blockIdx.x < a.row_chunks) {
+        const int64_t b = (int64_t)blockIdx.x * kPlanRows + warp;
+        long long need = 0;
+        uint32_t bits = 0;
+        if (b < a.batch) {
+            int src = (int)b;
+            bool keeps = true;
+            if (a.parent) {
+                src = a.parent[b];
+                if (src < -1 || src >= a.batch) {
+                    bits |= MKV_DEV_BAD_PARENT;
+                    src = -1;
+                }
+                // the row that keeps the parent's partly filled last pages:
+                // the parent itself if it goes on, else its lowest child
+                if (src >= 0 && src != b) {
+                    keeps = a.parent[src] != src;
+                    for (int64_t i = 0; keeps && i < b; i += 32)
+                        keeps = !__any_sync(kFull, i + lane < b && a.parent[i + lane] == src);
+                }
+            }
+            if (lane == 0) a.row_src[b] = make_int2(src, keeps ? 1 : 0);
+            const int add = a.n_new && src >= 0 && !a.kept ? a.n_new[b] : 0;
+            if (add < 0) bits |= MKV_DEV_BAD_PARENT;
+            for (int j = lane; j < a.heads; j += 32) {
+                const int64_t h = b * a.heads + j;
+                if (!len_ok(a.lens[h], a)) bits |= MKV_DEV_BAD_SEQ_LEN;
+                if (a.kept) {
+                    const int n = a.kept[h];
+                    bool ok = len_ok(n, a) && (!a.idx || n <= a.idx_stride);
+                    if (ok && !a.idx) {  // tokens 0 .. n-1 must be there
+                        const int T = !a.K ? a.lens[h] : a.seq_lens ? a.seq_lens[b] : a.t_max;
+                        ok = n <= T;
+                    }
+                    if (!ok) {
+                        bits |= MKV_DEV_BAD_N_KEEP;
+                        continue;
+                    }
+                } else if (src >= 0) {
+                    const int L = a.lens[(int64_t)src * a.heads + j];
+                    if (!len_ok(L, a)) continue;  // reported by its own row
+                    if (add < 0 || (long long)L + add > ((long long)a.max_pages << a.page_shift)) {
+                        bits |= MKV_DEV_BAD_PARENT;
+                        continue;
+                    }
+                }
+                const ListPlan p = plan_list(a, (int)b, j, src, keeps);
+                need += p.total - p.shared;
+            }
+            if (a.kept && a.K && a.seq_lens && (a.seq_lens[b] < 0 || a.seq_lens[b] > a.t_max))
+                bits |= MKV_DEV_BAD_SEQ_LEN;
+            need = warp_sum(need);
+            bits = __reduce_or_sync(kFull, bits);
+        }
+        if (lane == 0) {
+            s_need[warp] = need;
+            s_bits[warp] = bits;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            long long n = 0;
+            uint32_t x = 0;
+            for (int i = 0; i < kPlanRows; ++i) {
+                n += s_need[i];
+                x |= s_bits[i];
+            }
+            a.row_need[blockIdx.x] = n;
+            a.row_bits[blockIdx.x] = x;
+        }
+    } else {
+        const int chunk = (int)blockIdx.x - a.row_chunks;
+        int n = 0;
+        for (int i = 0; i < kPlanPages / kPageThreads; ++i) {
+            const int64_t p = (int64_t)chunk * kPlanPages + i * kPageThreads + threadIdx.x;
+            if (p < a.n_pages) n += a.refs[p] == 0;
+        }
+        n = __reduce_add_sync(kFull, n);
+        if (lane == 0) s_free[warp] = n;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int t = 0;
+            for (int i = 0; i < kPageThreads / 32; ++i) t += s_free[i];
+            a.page_free[chunk] = t;
+        }
+    }
+}
+
+// Sums over the CTA of three values at once.
+__device__ __forceinline__ void block_sums(long long &x, long long &y, long long &z, uint32_t &bits)
+{
+    __shared__ long long s[3][kPageThreads / 32];
+    __shared__ uint32_t sb[kPageThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    x = warp_sum(x);
+    y = warp_sum(y);
+    z = warp_sum(z);
+    bits = __reduce_or_sync(kFull, bits);
+    if (lane == 0) {
+        s[0][warp] = x;
+        s[1][warp] = y;
+        s[2][warp] = z;
+        sb[warp] = bits;
+    }
+    __syncthreads();
+    x = y = z = 0;
+    bits = 0;
+    for (int i = 0; i < kPageThreads / 32; ++i) {
+        x += s[0][i];
+        y += s[1][i];
+        z += s[2][i];
+        bits |= sb[i];
+    }
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+k_page_assign(const PageArgs a)
+{
+    __shared__ uint32_t scratch[kPageThreads / 32];
+    __shared__ long long s_row[kPlanRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_trigger();
+    pdl_wait();
+    const bool rows = (int)blockIdx.x < a.row_chunks;
+    const int chunk = rows ? (int)blockIdx.x : (int)blockIdx.x - a.row_chunks;
+    // pages needed and free in all, and (rows: needed, pages: free) in the chunks before this one
+    long long need = 0, free_pages = 0, before = 0;
+    uint32_t bits = 0;
+    for (int i = threadIdx.x; i < a.row_chunks; i += kPageThreads) {
+        const long long n = a.row_need[i];
+        need += n;
+        bits |= a.row_bits[i];
+        if (rows && i < chunk) before += n;
+    }
+    for (int i = threadIdx.x; i < a.page_chunks; i += kPageThreads) {
+        const int n = a.page_free[i];
+        free_pages += n;
+        if (!rows && i < chunk) before += n;
+    }
+    block_sums(need, free_pages, before, bits);
+    if (need > free_pages) bits |= MKV_DEV_NO_PAGES;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.verdict = bits;
+        if (bits) atomicOr(a.status, bits);
+    }
+    if (rows) {
+        if (bits) return;  // no list gets a page
+        const int64_t b = (int64_t)chunk * kPlanRows + warp;
+        const int2 src = b < a.batch ? a.row_src[b] : make_int2(-1, 0);
+        long long row = 0;
+        if (b < a.batch)
+            for (int j = lane; j < a.heads; j += 32) {
+                const ListPlan p = plan_list(a, (int)b, j, src.x, src.y != 0);
+                row += p.total - p.shared;
+            }
+        row = warp_sum(row);
+        if (lane == 0) s_row[warp] = row;
+        __syncthreads();
+        int off = (int)before;  // at most n_pages: the verdict was good
+        for (int i = 0; i < warp; ++i) off += (int)s_row[i];
+        if (b >= a.batch) return;
+        for (int j0 = 0; j0 < a.heads; j0 += 32) {
+            const int j = j0 + lane;
+            int n = 0;
+            if (j < a.heads) {
+                const ListPlan p = plan_list(a, (int)b, j, src.x, src.y != 0);
+                n = p.total - p.shared;
+            }
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o) x += y;
+            }
+            if (j < a.heads) a.list_off[b * a.heads + j] = off + x - n;
+            off += __shfl_sync(kFull, x, 31);
+        }
+    } else {
+        long long rank = before;
+        for (int i = 0; i < kPlanPages / kPageThreads; ++i) {
+            const int64_t p = (int64_t)chunk * kPlanPages + i * kPageThreads + threadIdx.x;
+            const int r = p < a.n_pages ? a.refs[p] : -1;
+            if (a.refs_out != a.refs && p < a.n_pages) a.refs_out[p] = r;
+            uint32_t total;
+            const uint32_t x = block_exclusive_scan<kPageThreads>(r == 0 ? 1u : 0u, scratch, &total);
+            if (r == 0 && !bits && rank + x < need) a.free_ids[rank + x] = (int32_t)p;
+            rank += total;
+        }
+    }
+}
+
+__device__ __forceinline__ void add_ref(const PageArgs &a, int page, int by)
+{
+    if ((uint32_t)page < (uint32_t)a.n_pages)
+        atomicAdd(a.refs_out + page, by);
+    else
+        atomicOr(a.status, MKV_DEV_BAD_PAGE);
+}
+
+// One warp per list.
+__global__ void __launch_bounds__(kPageThreads)
+k_page_update(const PageArgs a)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t h = ((int64_t)blockIdx.x * kPageThreads + threadIdx.x) >> 5;
+    if (h >= (int64_t)a.batch * a.heads) return;
+    const int b = (int)(h / a.heads), j = (int)(h - (int64_t)b * a.heads);
+    const bool in_place = a.table_out == a.table;
+    const int32_t *mine = a.table + h * a.max_pages;
+    int32_t *out = a.table_out + h * a.max_pages;
+    const int own_len = a.lens[h];
+    if (*a.verdict) {  // the lists stay as they were
+        if (in_place) return;
+        if (lane == 0) a.lens_out[h] = own_len;
+        if (len_ok(own_len, a))
+            for (int p = lane; p < pages_of(own_len, a); p += 32) out[p] = mine[p];
+        return;
+    }
+    const int2 src = a.row_src[b];
+    const bool keeps = src.y != 0, moved = src.x != b;
+    const ListPlan lp = plan_list(a, b, j, src.x, keeps);
+    const int32_t *from = a.table + ((int64_t)(src.x < 0 ? b : src.x) * a.heads + j) * a.max_pages;
+    const int first = a.list_off[h];
+    __syncwarp();
+    if (!in_place)
+        for (int p = lane; p < lp.shared; p += 32) {
+            const int id = from[p];
+            out[p] = id;
+            if (moved) add_ref(a, id, 1);
+        }
+    for (int p = lp.shared + lane; p < lp.total; p += 32) {
+        const int id = a.free_ids[first + p - lp.shared];
+        out[p] = id;
+        atomicAdd(a.refs_out + id, 1);
+    }
+    if (moved)  // nobody continues this list under its own row: its holder goes
+        for (int p = lane; p < pages_of(own_len, a); p += 32) add_ref(a, mine[p], -1);
+    if (lane == 0) a.lens_out[h] = lp.len;
+    const int rest = lp.old_len & (a.page_size - 1);
+    if (!keeps && rest > 0) {  // a copy of the partly filled last page
+        const int s = from[lp.shared], d = a.free_ids[first];
+        if ((uint32_t)s >= (uint32_t)a.n_pages) {
+            if (lane == 0) atomicOr(a.status, MKV_DEV_BAD_PAGE);
+            return;
+        }
+        const int64_t page_bytes = a.row_bytes << a.page_shift, n = rest * a.row_bytes;
+        const uint8_t *ks = a.k + s * page_bytes, *vs = a.v + s * page_bytes;
+        uint8_t *kd = a.k + d * page_bytes, *vd = a.v + d * page_bytes;
+        for (int64_t o = lane * 16; o < n; o += 512) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(ks + o), y = *reinterpret_cast<const uint4 *>(vs + o);
+            st_v4(kd + o, x);
+            st_v4(vd + o, y);
+        }
+    }
+}
+
+// Item = (list, block of 64 output tokens); groups of LPR lanes (16 bytes
+// each) copy rows. The list's first item also writes its table and counts.
+template <int LPR>
+__global__ void __launch_bounds__(kPageThreads)
+k_page_compact(const PageArgs a, int blocks, int64_t n_items)
+{
+    constexpr int RB = LPR * 16, SLOTS = kPageThreads / LPR, R = kCopyRows / SLOTS;
+    pdl_wait();
+    const bool bad = *a.verdict != 0;
+    const int g = threadIdx.x / LPR, lr = threadIdx.x % LPR;
+    for (int64_t item = blockIdx.x; item < n_items; item += gridDim.x) {
+        const int64_t h = item / blocks;
+        const int i0 = (int)(item - h * blocks) * kCopyRows;
+        const int own_len = a.lens[h];
+        const int32_t *mine = a.table + h * a.max_pages;
+        int32_t *out = a.table_out + h * a.max_pages;
+        if (bad) {
+            if (i0 == 0) {
+                if (threadIdx.x == 0) a.lens_out[h] = own_len;
+                if (len_ok(own_len, a))
+                    for (int p = threadIdx.x; p < pages_of(own_len, a); p += kPageThreads) out[p] = mine[p];
+            }
+            continue;
+        }
+        const int n = a.kept[h], first = a.list_off[h];
+        if (i0 == 0) {
+            if (threadIdx.x == 0) a.lens_out[h] = n;
+            for (int p = threadIdx.x; p < pages_of(n, a); p += kPageThreads) {
+                const int id = a.free_ids[first + p];
+                out[p] = id;
+                atomicAdd(a.refs_out + id, 1);
+            }
+            for (int p = threadIdx.x; p < pages_of(own_len, a); p += kPageThreads) add_ref(a, mine[p], -1);
+        }
+        const int m = min(kCopyRows, n - i0);
+        if (m <= 0) continue;
+        const int T = !a.K ? own_len : a.seq_lens ? a.seq_lens[h / a.heads] : a.t_max;
+        const uint8_t *ks = a.K ? a.K + (size_t)h * a.t_max * RB : a.k;
+        const uint8_t *vs = a.K ? a.V + (size_t)h * a.t_max * RB : a.v;
+        uint4 kr[R], vr[R];
+        int64_t dst[R];
+        int64_t from[R];
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const int i = i0 + u * SLOTS + g;
+            dst[u] = from[u] = -1;
+            if (u * SLOTS + g < m) {
+                const int s = a.idx ? a.idx[h * a.idx_stride + i] : i;
+                if (s < 0 || s >= T) {
+                    atomicOr(a.status, MKV_DEV_BAD_INDEX);
+                    continue;
+                }
+                from[u] = s;
+                if (!a.K) {
+                    const int id = mine[s >> a.page_shift];
+                    if ((uint32_t)id >= (uint32_t)a.n_pages) {
+                        atomicOr(a.status, MKV_DEV_BAD_PAGE);
+                        from[u] = -1;
+                        continue;
+                    }
+                    from[u] = ((int64_t)id << a.page_shift) + (s & (a.page_size - 1));
+                }
+                dst[u] = ((int64_t)a.free_ids[first + (i >> a.page_shift)] << a.page_shift) + (i & (a.page_size - 1));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+            if (from[u] >= 0) {
+                kr[u] = ld_stream(ks + from[u] * RB + lr * 16);
+                vr[u] = ld_stream(vs + from[u] * RB + lr * 16);
+            }
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+            if (from[u] >= 0) {
+                st_v4(a.k + dst[u] * RB + lr * 16, kr[u]);
+                st_v4(a.v + dst[u] * RB + lr * 16, vr[u]);
+            }
+    }
+}
+
+const void *compact_fn(int64_t row_bytes)
+{
+    switch (row_bytes) {
+    case 64: return (const void *)k_page_compact<4>;
+    case 128: return (const void *)k_page_compact<8>;
+    case 256: return (const void *)k_page_compact<16>;
+    case 512: return (const void *)k_page_compact<32>;
+    default: return nullptr;
+    }
+}
+
+cudaError_t launch_dependent(const void *fn, int64_t grid, void **args, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kPageThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace
+
+cudaError_t launch_page_call(const PageArgs &pa, cudaStream_t st)
+{
+    PageArgs a = pa;
+    const int64_t lists = (int64_t)a.batch * a.heads;
+    const unsigned plan = (unsigned)(a.row_chunks + a.page_chunks);
+    k_page_count<<<plan, kPageThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    void *args[] = {&a};
+    if ((e = launch_dependent((const void *)k_page_assign, plan, args, st)) != cudaSuccess) return e;
+    if (!a.kept)
+        return launch_dependent((const void *)k_page_update, (lists * 32 + kPageThreads - 1) / kPageThreads, args, st);
+    const void *fn = compact_fn(a.row_bytes);
+    if (!fn) return cudaErrorInvalidValue;
+    const int64_t most = a.idx ? std::min((int64_t)a.idx_stride, (int64_t)a.max_pages << a.page_shift)
+                               : std::min((int64_t)(a.K ? a.t_max : INT32_MAX), (int64_t)a.max_pages << a.page_shift);
+    int blocks = (int)std::max<int64_t>(1, (most + kCopyRows - 1) / kCopyRows);
+    int64_t items = lists * blocks;
+    void *cargs[] = {&a, &blocks, &items};
+    return launch_dependent(fn, grid_for_items(fn, kPageThreads, 0, items), cargs, st);
+}
+
+}  // namespace mkv

@@ -1,0 +1,85 @@
+// Internal declarations of the paged-cache kernels (mkv_pages.cu,
+// mkv_rope.cu, mkv_attention.cu) and their C ABI (mkv_pages_api.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "mkv_internal.h"
+
+namespace mkv {
+
+constexpr int kPlanPages = 4096;  // pages of refs per CTA of the plan kernels (256 threads x 16)
+constexpr int kPlanRows = 8;      // batch rows per CTA of the plan kernels (one warp each)
+
+// Byte offsets of the page workspace (each 256-byte aligned).
+struct PageLayout {
+    size_t status = 0, verdict = 0, row_src = 0, row_need = 0, row_bits = 0, page_free = 0, list_off = 0, free_ids = 0,
+           total = 0;
+};
+
+// What the page calls share. Pointers of `in` and `out` lists; in place when
+// table_out == table.
+struct PageArgs {
+    int32_t n_pages, page_size, page_shift, batch, heads, max_pages;
+    int64_t row_bytes;
+    uint8_t *k, *v;
+    const int32_t *table, *lens, *refs;
+    int32_t *table_out, *lens_out, *refs_out;
+    // update
+    const int32_t *parent, *n_new;
+    // compact (kept != NULL)
+    const int32_t *idx, *kept, *seq_lens;
+    const uint8_t *K, *V;
+    int32_t idx_stride, t_max;
+    // workspace
+    uint32_t *status, *verdict;
+    int2 *row_src;
+    long long *row_need;
+    uint32_t *row_bits;
+    int32_t *page_free, *list_off, *free_ids;
+    int32_t row_chunks, page_chunks;
+};
+
+cudaError_t launch_page_call(const PageArgs &a, cudaStream_t st);
+
+struct RopeArgs {
+    const uint8_t *Q, *K, *V;
+    int64_t q_stride, k_stride, v_stride;  // elements
+    uint8_t *Q_out;
+    const int32_t *positions, *q_start, *table, *lens;
+    const float *inv_freq;
+    uint8_t *k, *v;
+    int32_t n_tokens, q_heads, batch, heads, max_pages, n_pages, page_size, page_shift, head_dim, es, rot_dim, layout;
+    float factor, k_scale, v_scale;
+    uint32_t *status;
+};
+cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t st);
+
+struct AttnArgs {
+    const uint8_t *Q;
+    uint8_t *O;
+    float *lse;
+    int64_t q_stride, o_stride;  // elements
+    const int32_t *q_start, *table, *lens;
+    const uint8_t *k, *v;
+    int32_t n_tokens, q_heads, group, batch, heads, max_pages, n_pages, page_size, page_shift, head_dim, es;
+    int32_t max_q, max_len, window, sinks;
+    float scale_log2;  // scale * k_scale * log2(e)
+    float v_scale;
+    int32_t tiles;     // 16-row tiles per list (of max_q * group rows)
+    int32_t splits;    // parts of the key axis
+    float *part_o;     // [items, 16, head_dim] of the splits (items = (list, tile, split))
+    float2 *part_ml;   // [items, 16]: running maximum (log2 units) and sum
+    uint32_t *status;
+};
+// The launch of a shape: splits and the workspace bytes behind the status word.
+struct AttnPlan {
+    int32_t tiles = 0, splits = 0;
+    size_t bytes = 0;
+};
+AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int sms);
+cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t st);
+
+}  // namespace mkv

@@ -90,6 +90,11 @@ typedef enum {
 #define MKV_DEV_BAD_N_KEEP 0x2u   /* an n_keep entry outside [0, min(T_b, keep_stride)] */
 #define MKV_DEV_INTERNAL 0x4u     /* a kept count disagreed with n_keep (a library bug) */
 #define MKV_DEV_TIMEOUT 0x8u      /* a bounded wait between CTAs ran out; the scores it guarded are missing */
+#define MKV_DEV_BAD_PAGE 0x10u    /* a page list names a page outside the pool */
+#define MKV_DEV_NO_PAGES 0x20u    /* fewer free pages than a page call needs: its lists stay as they were */
+#define MKV_DEV_BAD_PARENT 0x40u  /* a parent outside [-1, batch), or an n_new below 0 or beyond the list's capacity */
+#define MKV_DEV_BAD_TOKENS 0x80u  /* q_start decreases, leaves [0, n_tokens], or gives a row more than max_q tokens */
+#define MKV_DEV_BAD_INDEX 0x100u  /* a kept index outside its list (or contiguous head) */
 
 typedef enum {
     MKV_MODE_L2 = 0,     /* s_t = |k_t - c| (ManifoldKV, abstract) */
@@ -495,6 +500,178 @@ mkv_status mkv_compress_noalloc(const void *K, const void *V, mkv_shape shape, d
 mkv_status mkv_inject_stalled_windows(const void *K, const void *V, mkv_shape shape, double ratio, mkv_mode mode,
                                       int32_t window, int32_t keep_stride, void *K_out, void *V_out, int32_t *idx,
                                       int32_t *kept, void *workspace, size_t workspace_bytes, mkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged caches
+ * ---------------------------------------------------------------------------
+ * Compression leaves every (row, KV head) with its own number of tokens, so a
+ * paged cache here has one page list per (row, head). A pool holds n_pages
+ * pages of page_size tokens, keys and values apart ([n_pages, page_size,
+ * head_dim] each, bf16 or E4M3); token s of a list is row s % page_size of
+ * page table[list][s / page_size], and a list of `len` tokens uses its first
+ * ceil(len / page_size) table entries (the others are never read). refs
+ * counts, for every page, the lists that hold it; 0 means free. A caller whose
+ * pool is [n_pages, heads, page_size, head_dim] with one table per row passes
+ * n_pages * heads pages and table entries page * heads + head.
+ *
+ * Sharing. A full page may be held by several lists (a forked sequence); a
+ * partly filled last page is held by one, which mkv_page_update keeps so: what
+ * appends to a list then never writes into another. refs is read for 0 alone
+ * and changed by whole holders, so a caller may hold a page back (its own
+ * count on it).
+ *
+ * Order. New pages are the free pages (refs 0 before the call) in ascending
+ * order, given to the lists in (row, head, position) order: results do not
+ * depend on the GPU. Pages that a call releases can be taken from the next
+ * call on. If the free pages do not suffice (MKV_DEV_NO_PAGES), or an argument
+ * on the device is invalid, the call changes nothing: the output lists and
+ * counts are those of the input.
+ *
+ * Input and output lists are distinct buffers (a program keeps two and swaps
+ * them), of the same sizes; refs_out may be refs itself. mkv_page_update with
+ * parent NULL may also run in place (table and lens both those of the input).
+ * Table entries past a list's pages are not written.
+ *
+ * Contents. Tokens in [0, len) of a list are finite; anything may stand in
+ * the rows behind them. The workspace of all calls on a paged cache is
+ * mkv_page_workspace_size() bytes (attention: mkv_attention_workspace_size()),
+ * with the status word in front as elsewhere. Limits: page_size 16, 32, 64 or
+ * 128; n_pages * page_size and max_pages * page_size at most 2^30; batch at
+ * most 65536, batch * heads at most 2^24; q_heads at most 1024; else
+ * MKV_ERR_UNSUPPORTED. */
+typedef struct {
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t head_dim; /* 64, 128 or 256 */
+    int32_t dtype;    /* an mkv_dtype */
+    void *k_pages;    /* [n_pages, page_size, head_dim], 16-byte aligned */
+    void *v_pages;
+} mkv_page_pool;
+
+typedef struct {
+    int32_t batch, heads, max_pages;
+    int32_t *table; /* device int32 [batch, heads, max_pages] */
+    int32_t *lens;  /* device int32 [batch, heads] */
+} mkv_page_lists;
+
+/* New tokens of a step, packed row after row: row b's are tokens
+ * [q_start[b], q_start[b + 1]) (q_start: device int32 [batch + 1], not
+ * decreasing, within [0, n_tokens]); a row may have none. Tokens outside
+ * every row (padding) are neither read nor written. The lists already count
+ * them: the n new tokens of row b are the last n of each of its lists. */
+typedef struct {
+    int32_t n_tokens;
+    int32_t q_heads; /* query heads: a multiple of the lists' heads; query head h reads KV head h / (q_heads / heads) */
+    const int32_t *q_start;
+} mkv_new_tokens;
+
+/* Bytes of workspace for mkv_page_update, mkv_page_compact and
+ * mkv_rope_append (0 on a bad shape; pointers are not looked at). */
+size_t mkv_page_workspace_size(mkv_page_pool pool, mkv_page_lists lists);
+
+/* Page lists after a step (no counterpart on the pages this library follows;
+ * the compacted cache lives on in a serving engine, where sequences fork, end
+ * and grow). Row b of `out` continues row parent[b] of `in` (parent: device
+ * int32 [batch], -1: the row becomes empty; NULL: every row continues itself)
+ * and grows by n_new[b] tokens in every head (device int32 [batch]; NULL: 0;
+ * ignored where the parent is -1): new tokens have pages but no contents yet.
+ * Full pages are shared. A partly filled last page stays with the row itself
+ * if it continues itself, else with the lowest row that continues it; the
+ * other rows get a copy of its tokens in a new page. refs_out = refs, plus 1
+ * for every list of `out` that holds the page, minus 1 for every list of `in`
+ * that held it. */
+mkv_status mkv_page_update(mkv_page_pool pool, mkv_page_lists in, const int32_t *refs, const int32_t *parent,
+                           const int32_t *n_new, mkv_page_lists out, int32_t *refs_out, void *workspace,
+                           size_t workspace_bytes, mkv_stream_t stream);
+
+/* Compaction in pages (abstract: the retained tokens form the compressed
+ * cache): list h of `out` has kept[h] tokens in new pages, token i a bit copy
+ * of token idx[h * idx_stride + i] of list h of `in` -- or, with K and V
+ * given, of the contiguous cache [batch, heads, t_max, head_dim] of the
+ * pool's type (seq_lens: device int32 [batch] or NULL for t_max). idx NULL
+ * copies tokens 0 .. kept[h]-1 (idx_stride is then not looked at). idx and
+ * kept are as mkv_compact and mkv_compress write them; any order of indices
+ * is allowed, also the same one twice. Every page that the lists of `in` held
+ * loses that holder. kept[h] must be in [0, max_pages * page_size] and at most
+ * idx_stride (MKV_DEV_BAD_N_KEEP; nothing changes); a token whose index is out
+ * of range is left uncopied (MKV_DEV_BAD_INDEX). */
+mkv_status mkv_page_compact(mkv_page_pool pool, mkv_page_lists in, const int32_t *refs, const int32_t *idx,
+                            int32_t idx_stride, const int32_t *kept, const void *K, const void *V, int32_t t_max,
+                            const int32_t *seq_lens, mkv_page_lists out, int32_t *refs_out, void *workspace,
+                            size_t workspace_bytes, mkv_stream_t stream);
+
+typedef enum {
+    MKV_ROPE_HALF = 0,       /* pairs (i, i + rot_dim / 2) */
+    MKV_ROPE_INTERLEAVED = 1 /* pairs (2i, 2i + 1) */
+} mkv_rope_layout;
+
+/* Rotary positions of a step's new queries and keys, the keys and values
+ * written into their pages. Pair i < rot_dim / 2 of a row turns by the angle
+ * positions[t] * inv_freq[i]: (x, y) -> factor * (x cos - y sin, x sin + y
+ * cos); dims from rot_dim on are copied. Angles are reduced in 64 bits, the
+ * rotation runs in fp32, and the result is rounded once. Q, K, V: bf16
+ * [n_tokens, q_heads | heads | heads, head_dim], token t at element
+ * t * stride (a multiple of 8, at least heads * head_dim), 16-byte aligned;
+ * they may be slices of one fused projection. positions: device int32
+ * [n_tokens], 0 and up. inv_freq: device fp32 [rot_dim / 2] (mkv_rope_frequencies).
+ * rot_dim: a multiple of 16 in [16, head_dim]. Q_out: bf16 [n_tokens, q_heads,
+ * head_dim], contiguous; may be Q itself when Q is contiguous. E4M3 pools
+ * store round(value / k_scale) (keys) and round(value / v_scale) (values),
+ * saturated at 448; for bf16 pools the scales must be 1. A token whose list
+ * or page is invalid is not written (MKV_DEV_BAD_SEQ_LEN when the list is
+ * shorter than the row's new tokens or longer than its capacity,
+ * MKV_DEV_BAD_PAGE, MKV_DEV_BAD_TOKENS); its query is written all the same. */
+mkv_status mkv_rope_append(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V,
+                           int64_t v_stride, mkv_new_tokens tokens, const int32_t *positions, const float *inv_freq,
+                           int32_t rot_dim, mkv_rope_layout layout, float factor, void *Q_out, mkv_page_pool pool,
+                           mkv_page_lists lists, float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
+                           mkv_stream_t stream);
+
+typedef enum {
+    MKV_ROPE_PLAIN = 0,   /* f_i = theta^(-2i / rot_dim) */
+    MKV_ROPE_LINEAR = 1,  /* f_i / scale (position interpolation) */
+    MKV_ROPE_BY_PARTS = 2 /* fast pairs keep f_i, slow ones get f_i / scale, a ramp between */
+} mkv_rope_scaling;
+
+/* Frequencies for mkv_rope_append (host helper): inv_freq[i], i < rot_dim / 2,
+ * rounded to fp32 from 64 bits. BY_PARTS ("YaRN: Efficient Context Window
+ * Extension of Large Language Models", section 3.2, the by-parts
+ * interpolation): with r_i = original_len f_i / (2 pi) the turns of pair i
+ * over the original context and g = clamp((r_i - low_turns) / (high_turns -
+ * low_turns), 0, 1), f_i (g + (1 - g) / scale); YaRN takes turns 1 and 32 and
+ * the factor 0.1 ln(scale) + 1, Llama-3.1 turns 1 and 4 and the factor 1.
+ * original_len and the turns are looked at for BY_PARTS alone. Returns 0, or
+ * -1 on a bad argument (rot_dim not a positive multiple of 16, theta not
+ * above 1, scale below 1, original_len < 1, not 0 < low_turns < high_turns,
+ * an unknown scaling, NULL). */
+int32_t mkv_rope_frequencies(int32_t rot_dim, double theta, mkv_rope_scaling scaling, double scale,
+                             int32_t original_len, double low_turns, double high_turns, float *inv_freq);
+
+/* Bytes of workspace for mkv_paged_attention (0 on a bad shape). */
+size_t mkv_attention_workspace_size(mkv_page_pool pool, mkv_page_lists lists, mkv_new_tokens tokens, int32_t max_q,
+                                    int32_t max_len);
+
+/* Attention of a step's new tokens over the paged cache. For the n new tokens
+ * of row b and a list of L tokens, new token i stands at p = L - n + i and
+ * sees the tokens s <= p of the list, with window > 0 only those with
+ * s > p - window or s < sinks (positions are places in the list, also after
+ * compression). O = sum_s softmax_s(scale * q.k_s) v_s, with keys and values
+ * times k_scale and v_scale; lse = log sum_s exp(scale * q.k_s) (natural log;
+ * may be NULL), fp32 [n_tokens, q_heads]. A token that sees nothing gives O =
+ * 0 and lse = -inf. One new token per row is a decode step; max_q bounds the
+ * rows' new tokens and max_len their lists (both host values that size the
+ * launch; larger ones cost time only; max_len at most max_pages * page_size).
+ * A row with more than max_q tokens sets MKV_DEV_BAD_TOKENS, a list longer
+ * than max_len or shorter than 0 MKV_DEV_BAD_SEQ_LEN, and nothing is written
+ * for it; a page outside the pool sets MKV_DEV_BAD_PAGE (its tokens count as
+ * zeros). Q, O: bf16 [n_tokens, q_heads, head_dim], token t at element
+ * t * stride (a multiple of 8, at least q_heads * head_dim), 16-byte aligned, distinct.
+ * Scores, sums and accumulators are fp32; the softmax weights are rounded to
+ * 16 bits for the product with the values. */
+mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens tokens, int32_t max_q,
+                               mkv_page_pool pool, mkv_page_lists lists, int32_t max_len, float scale, float k_scale,
+                               float v_scale, int32_t window, int32_t sinks, void *O, int64_t o_stride, float *lse,
+                               void *workspace, size_t workspace_bytes, mkv_stream_t stream);
 
 /* Synchronise `stream`, read the status word of `workspace` into *bits (may
  * be NULL) and reset it to zero. MKV_OK if it was zero, MKV_ERR_DEVICE if
