@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 OUT_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(OUT_DIR, "libmkv.so")
 SOURCES = ["mkv_kernels.cu", "mkv_gather.cu", "mkv_inplace.cu", "mkv_summaries.cu", "mkv_oja.cu", "mkv_piece.cu", "mkv_api.cu", "mkv_noalloc.cu",
-           "mkv_pages.cu", "mkv_rope.cu", "mkv_attention.cu", "mkv_pages_api.cu"]
+           "mkv_pages.cu", "mkv_rope.cu", "mkv_attention.cu", "mkv_attention_chunk.cu",
+           "mkv_pages_api.cu"]
 HEADERS = [os.path.join(CSRC, "mkv_internal.h"), os.path.join(CSRC, "mkv_device.cuh"),
            os.path.join(CSRC, "mkv_select.cuh"), os.path.join(CSRC, "mkv_gather.cuh"),
            os.path.join(CSRC, "mkv_pages.h"),

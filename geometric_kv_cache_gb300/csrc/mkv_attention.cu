@@ -33,6 +33,7 @@ namespace {
 using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
+constexpr int kFewRows = 64;  // most query rows of a list that this form takes (bf16)
 
 // Shape of one instantiation.
 template <int D, int ES>
@@ -550,19 +551,33 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 
 }  // namespace
 
-AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int sms)
+AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int32_t es,
+                        int sms)
 {
     AttnPlan p;
-    p.tiles = (int32_t)(((int64_t)max_q * group + kRows - 1) / kRows);
+    const int64_t rows = (int64_t)max_q * group;
+    if (es == 2 && rows > kFewRows) {
+        p.chunked = 1;
+        p.tiles = (int32_t)((rows + chunk_tile_rows(head_dim) - 1) / chunk_tile_rows(head_dim));
+        p.splits = sms;
+        p.part_rows = (int64_t)sms * 2 * chunk_tile_rows(head_dim);
+        p.bytes = chunk_workspace_bytes(sms, head_dim);
+        return p;
+    }
+    p.tiles = (int32_t)((rows + kRows - 1) / kRows);
     const int64_t base = std::max<int64_t>(1, lists * p.tiles);
     const int64_t want = (8 * sms + base - 1) / base, most = ((int64_t)max_len + 127) / 128;
     p.splits = (int32_t)std::max<int64_t>(1, std::min(want, most));
-    if (p.splits > 1) p.bytes = (size_t)base * p.splits * kRows * (head_dim * sizeof(float) + sizeof(float2));
+    if (p.splits > 1) {
+        p.part_rows = base * p.splits * kRows;
+        p.bytes = (size_t)p.part_rows * (head_dim * sizeof(float) + sizeof(float2));
+    }
     return p;
 }
 
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t st)
 {
+    if (a.chunked) return launch_attend_chunk(a, st);
     if (a.es == 2) {
         switch (a.head_dim) {
         case 64: return launch_one<64, 2>(a, st);

@@ -1,0 +1,842 @@
+// sm_103a attention of chunks of new tokens over a paged cache, on the
+// 5th-generation tensor cores (the form of mkv_paged_attention for lists with
+// many query rows; see mkv_attention.cu for the definition and the form for
+// few).
+//
+// A tile is NSUB x 128 packed rows (new token, query head of the KV head's
+// group) of one list; a block is 128 keys. Per block and sub-tile
+//     S = Q K^T          tcgen05.mma, M = 128, N = 128, fp32 in TMEM
+//     P = 2^(S c - m)    one thread per row, P rounded to bf16 over S in TMEM
+//     O += P V           tcgen05.mma with P as the A operand from TMEM
+// with the row's maximum m allowed to lag: O is multiplied by 2^(m_old - m_new)
+// only when the maximum has grown by more than 2^8, so weights stay below 256
+// and the rescaling, which has to wait for the tensor core, is rare.
+//
+// Roles (12 warps, one CTA per SM): warp 0 brings the pages of K and V blocks
+// into a ring of shared-memory slots (TMA, 128-byte swizzle, one box of 64 dims
+// per page, page entries read a block ahead); warp 1 issues the MMAs, for the
+// two sub-tiles in turn, so that the tensor core works on one while the other's
+// softmax runs; warps 4-7 and 8-11 are the softmax of sub-tile 0 and 1 (they
+// also load its queries and write its output).
+//
+// The blocks of all tiles form one line, cut into equal parts, one per CTA: no
+// CTA idles behind a long list or an uneven number of tiles. A tile that is
+// cut leaves its parts (unnormalised O, m, l) in the workspace and
+// k_chunk_combine joins them in order.
+//
+// Every wait is bounded (1 s); when one runs out the CTA reports
+// MKV_DEV_TIMEOUT, its roles leave their loops, the copies and MMAs in flight
+// are waited for (bounded) and the TMEM is freed.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "mkv_device.cuh"
+#include "mkv_pages.h"
+
+namespace mkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 384;
+constexpr int kKeys = 128;                   // keys per block
+constexpr int kSubRows = 128;                // rows per sub-tile: the MMA's M, the TMEM lanes
+constexpr int kBoxBytes = kKeys * 128;       // 64 dims of a block: 128 rows of 128 bytes
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr float kLag = 8.f;                  // log2 of how far a row's maximum may lag
+constexpr int kMinBlocks = 4;                // blocks that make a CTA worth its start
+
+template <int D>
+struct Chunk {
+    static constexpr int NSUB = D == 256 ? 1 : 2;  // O of two sub-tiles fits the 512 TMEM columns up to D = 128
+    static constexpr int ROWS = NSUB * kSubRows;
+    static constexpr int BOXES = D / 64;
+    static constexpr int SLOT = BOXES * kBoxBytes;  // one block of K or of V
+    static constexpr int SLOTS = D == 64 ? 8 : D == 128 ? 4 : 2;
+    static constexpr int QBYTES = SLOT;             // one sub-tile of queries has a block's shape
+    static constexpr int SMEM = NSUB * QBYTES + SLOTS * SLOT + 1024;
+    static constexpr int TMEM = 512;
+    static constexpr int O_COL = NSUB * kKeys;      // S of the sub-tiles, then O
+};
+
+__device__ __forceinline__ uint32_t saddr(const void *p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void bar_init(uint64_t *b, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t *b, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
+}
+
+// Bounded wait for a phase; false on a timeout (reported, the CTA's abort flag
+// raised) or, when abortable, as soon as another role raised the flag.
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, uint32_t *status, volatile uint32_t *abort_flag,
+                                         bool abortable = true)
+{
+    const uint32_t a = saddr(b);
+    uint64_t t0 = 0;
+    for (uint32_t spin = 0;; ++spin) {
+        uint32_t done;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(done)
+                     : "r"(a), "r"(parity)
+                     : "memory");
+        if (done) return true;
+        if ((spin & 63u) == 63u) {
+            if (abortable && *abort_flag) return false;
+            if (t0 == 0) t0 = global_ns();
+            else if (global_ns() - t0 > kWaitNs) {
+                atomicOr(status, MKV_DEV_TIMEOUT);
+                *abort_flag = 1u;
+                return false;
+            }
+        }
+    }
+}
+
+// The same for a whole warp: all lanes get one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, uint32_t *status, volatile uint32_t *abort_flag)
+{
+    return __all_sync(kFull, bar_wait(b, parity, status, abort_flag));
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint64_t *b)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(saddr(b))
+        : "memory");
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle (layout type 2, version
+// 1), 8-row groups 1024 bytes apart. Keys and queries are K-major (the
+// contraction runs along the 128-byte rows; leading offset unused). Values
+// are MN-major (the contraction runs over the rows): the leading offset is
+// the distance of the 64-dim boxes.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kBoxBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// kind::f16, fp32 accumulator, bf16 operands, M = 128, N = n; bit 16: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kSubRows >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+            d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *b)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(b))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v)
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+        "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+        "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two fp32 operations in one instruction: (a.x b.x + c.x, a.y b.y + c.y).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; fma.rn.f32x2 d, a, b, c; "
+        "mov.b64 {%0, %1}, d; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// What one tile of packed rows of one list is.
+struct Tile {
+    int b, j, n, L, row0, rows;  // batch row, head, new tokens, list length, first packed row, rows
+    int end;                     // keys from here on are visible to no row
+    int sink_blocks, win_block, blocks;  // blocks of keys: [0, sink_blocks) and from win_block on; in all
+};
+
+// The tile's rows and blocks; rows 0 where there is nothing to do.
+__device__ __forceinline__ Tile make_tile(const AttnArgs &a, int64_t at, int tile_rows, bool report)
+{
+    Tile t;
+    const int64_t list = at / a.tiles;
+    const int tile = (int)(at - list * a.tiles);
+    t.b = (int)(list / a.heads);
+    t.j = (int)(list - (int64_t)t.b * a.heads);
+    t.row0 = tile * tile_rows;
+    t.rows = t.blocks = t.sink_blocks = t.win_block = t.end = 0;
+    const int lo = a.q_start[t.b], hi = a.q_start[t.b + 1];
+    t.n = hi - lo;
+    t.L = a.lens[list];
+    if (lo < 0 || hi < lo || hi > a.n_tokens || t.n > a.max_q) {
+        if (report) atomicOr(a.status, MKV_DEV_BAD_TOKENS);
+        return t;
+    }
+    if (t.L < 0 || t.L > a.max_len) {
+        if (report) atomicOr(a.status, MKV_DEV_BAD_SEQ_LEN);
+        return t;
+    }
+    t.rows = max(0, min(tile_rows, t.n * a.group - t.row0));
+    if (t.rows == 0) return t;
+    const int p_lo = t.L - t.n + t.row0 / a.group, p_hi = t.L - t.n + (t.row0 + t.rows - 1) / a.group;
+    t.end = max(0, p_hi + 1);
+    const int all = (t.end + kKeys - 1) / kKeys;
+    if (a.window > 0) {
+        const int start = max(0, p_lo - a.window + 1);
+        t.win_block = min(start / kKeys, all);
+        t.sink_blocks = min((min(a.sinks, t.end) + kKeys - 1) / kKeys, t.win_block);
+    }
+    t.blocks = t.sink_blocks + all - t.win_block;
+    return t;
+}
+
+__device__ __forceinline__ int block_key(const Tile &t, int blk)
+{
+    return (blk < t.sink_blocks ? blk : blk - t.sink_blocks + t.win_block) * kKeys;
+}
+
+// Units of a tile on the line: its blocks; one for a tile whose rows see nothing.
+__device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max(t.blocks, 1) : 0; }
+
+// A CTA's walk over its part of the line, the same in every role.
+struct Walk {
+    int64_t tile, left;  // the next tile, units left
+    int skip;            // units of that tile that belong to the CTA before
+    Tile t;
+    int first, last, units;  // blocks [first, last) of the tile's units
+    __device__ __forceinline__ bool next(const AttnArgs &a, int tile_rows)
+    {
+        if (left <= 0) return false;
+        const int64_t n_tiles = (int64_t)a.batch * a.heads * a.tiles;
+        for (;; ++tile) {
+            if (tile >= n_tiles) return false;
+            t = make_tile(a, tile, tile_rows, false);
+            units = units_of(t);
+            if (units > skip) break;
+            skip -= units;  // (0 units: nothing to do)
+        }
+        first = skip;
+        last = (int)min((int64_t)units, first + left);
+        left -= last - first;
+        skip = 0;
+        ++tile;
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return first == 0 && last == units; }
+    __device__ __forceinline__ int blocks() const { return min(last, t.blocks) - min(first, t.blocks); }
+};
+
+struct ChunkInfo {
+    int32_t open_tile;  // the tile whose first part is this CTA's last segment, -1: none
+    int32_t carries;    // this CTA's first segment continues a tile
+    int32_t ends;       // ... and ends it
+    int32_t pad;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
+               ChunkInfo *info)
+{
+    using C = Chunk<D>;
+    constexpr int NSUB = C::NSUB, SLOTS = C::SLOTS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *q_smem = smem;                      // NSUB x [D / 64 boxes][128 rows x 128 B]
+    uint8_t *ring = smem + NSUB * C::QBYTES;     // SLOTS blocks: K, V, K, V, ...
+    __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_ready[2], o_done[2], o_free[2], q_full[2],
+        drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile uint32_t abort_flag;
+    __shared__ long long s_sum[kThreads / 32];
+    __shared__ long long s_first_tile, s_left;
+    __shared__ int s_skip;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t n_tiles = (int64_t)a.batch * a.heads * a.tiles;
+    pdl_trigger();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SLOTS; ++s) {
+            bar_init(&full[s], 1);
+            bar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            bar_init(&s_full[s], 1);
+            bar_init(&p_ready[s], 4);
+            bar_init(&o_done[s], 1);
+            bar_init(&o_free[s], 4);
+            bar_init(&q_full[s], 4);
+        }
+        bar_init(&drain, 1);
+        abort_flag = 0u;
+        s_first_tile = 0;
+        s_left = 0;
+        s_skip = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_base)),
+                     "n"(C::TMEM)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // the line's length, then this CTA's part of it
+    auto block_sum = [&](long long v) -> long long {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+        if (lane == 0) s_sum[warp] = v;
+        __syncthreads();
+        long long t = 0;
+        for (int i = 0; i < kThreads / 32; ++i) t += s_sum[i];
+        __syncthreads();
+        return t;
+    };
+    long long units = 0;
+    for (int64_t x = threadIdx.x; x < n_tiles; x += kThreads)
+        units += units_of(make_tile(a, x, C::ROWS, blockIdx.x == 0 && x % a.tiles == 0));
+    units = block_sum(units);
+    const long long parts = max(1LL, min((long long)gridDim.x, units / kMinBlocks));
+    const long long u0 = units * min((long long)blockIdx.x, parts) / parts;
+    const long long u1 = units * min((long long)blockIdx.x + 1, parts) / parts;
+    if (u1 > u0) {
+        long long before = 0;
+        for (int64_t x0 = 0; x0 < n_tiles && before <= u0; x0 += kThreads) {
+            const int64_t x = x0 + threadIdx.x;
+            const long long mine = x < n_tiles ? units_of(make_tile(a, x, C::ROWS, false)) : 0;
+            long long pre = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(kFull, pre, o);
+                if (lane >= o) pre += y;
+            }
+            if (lane == 31) s_sum[warp] = pre;
+            __syncthreads();
+            long long off = before, all = 0;
+            for (int i = 0; i < kThreads / 32; ++i) {
+                if (i < warp) off += s_sum[i];
+                all += s_sum[i];
+            }
+            off += pre - mine;
+            if (mine > 0 && off <= u0 && u0 < off + mine) {
+                s_first_tile = x;
+                s_skip = (int)(u0 - off);
+                s_left = u1 - u0;
+            }
+            before += all;
+            __syncthreads();
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_base;
+    Walk w;
+    w.tile = s_first_tile;
+    w.left = s_left;
+    w.skip = s_skip;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == 0) {
+            // ---------------------------------------------------- pages of K and V --
+            const int per_block = kKeys >> a.page_shift;  // pages of a block: one lane each
+            uint32_t seq = 0;
+            bool ok = true;
+            while (ok && w.next(a, C::ROWS)) {
+                const int32_t *table = a.table + ((int64_t)w.t.b * a.heads + w.t.j) * a.max_pages;
+                const int last = min(w.last, w.t.blocks);
+                // the pool row of this lane's page of a block; past every row (zero fill) for a bad page, -1: none
+                auto lookup = [&](int blk) -> int {
+                    const int key = block_key(w.t, blk) + (lane << a.page_shift);
+                    if (blk >= last || lane >= per_block || key >= w.t.end) return -1;
+                    const int id = table[key >> a.page_shift];
+                    if ((uint32_t)id >= (uint32_t)a.n_pages) {
+                        atomicOr(a.status, MKV_DEV_BAD_PAGE);
+                        return a.n_pages << a.page_shift;
+                    }
+                    return id << a.page_shift;
+                };
+                int row = lookup(w.first);
+                for (int blk = w.first; ok && blk < last; ++blk) {
+                    const int next = lookup(blk + 1);
+                    const uint32_t bytes = __popc(__ballot_sync(kFull, row >= 0)) * (uint32_t)(C::BOXES * 128) << a.page_shift;
+                    for (int kv = 0; kv < 2; ++kv, ++seq) {
+                        const int s = (int)(seq % SLOTS);
+                        ok = seq < SLOTS || warp_wait(&empty[s], ((seq / SLOTS) - 1) & 1u, a.status, &abort_flag);
+                        if (!ok) break;
+                        if (lane == 0) bar_expect(&full[s], bytes);
+                        __syncwarp();
+                        if (row >= 0) {
+                            const uint32_t dst = saddr(ring + s * C::SLOT) + ((uint32_t)lane * 128u << a.page_shift);
+#pragma unroll
+                            for (int x = 0; x < C::BOXES; ++x)
+                                tma_load_2d(dst + x * kBoxBytes, kv ? &map_v : &map_k, x * 64, row, &full[s]);
+                        }
+                    }
+                    row = next;
+                }
+            }
+            // every copy issued lands before the CTA may exit
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s)
+                if (seq > (uint32_t)s) bar_wait(&full[s], ((seq - 1 - s) / SLOTS) & 1u, a.status, &abort_flag, false);
+        } else if (warp == 1) {
+            // ------------------------------------------------------------- MMAs --
+            constexpr uint32_t id_qk = idesc_bf16(kKeys, false), id_pv = idesc_bf16(D, true);
+            uint32_t seq = 0;  // slots used before this block
+            uint32_t n_p[2] = {0, 0}, n_seg[2] = {0, 0};  // blocks and segments of each sub-tile so far
+            bool ok = true, issued = false;
+            auto qk = [&](int t, int slot) {
+                if (lane != 0) return;
+                const uint64_t qd = desc_k(saddr(q_smem + t * C::QBYTES)), kd = desc_k(saddr(ring + slot * C::SLOT));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t step = (uint64_t)(((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4);
+                    mma_ss(tmem + t * kKeys, qd + step, kd + step, id_qk, k > 0);
+                }
+                mma_commit(&s_full[t]);
+            };
+            while (ok && w.next(a, C::ROWS)) {
+                const int nb = w.blocks(), sub = NSUB == 1 || w.t.rows <= kSubRows ? 1 : 2;
+                if (nb == 0) continue;
+                issued = true;
+                const int first = min(w.first, w.t.blocks);
+                for (int blk = 0; ok && blk < nb; ++blk, seq += 2) {
+                    const int ks = (int)(seq % SLOTS), vs = (int)((seq + 1) % SLOTS), kn = (int)((seq + 2) % SLOTS);
+                    if (blk == 0) {
+                        ok = warp_wait(&full[ks], (seq / SLOTS) & 1u, a.status, &abort_flag);
+                        for (int t = 0; ok && t < sub; ++t) {
+                            ok = warp_wait(&q_full[t], n_seg[t] & 1u, a.status, &abort_flag);
+                            fence_after();
+                            if (ok) qk(t, ks);
+                        }
+                        if (ok && lane == 0) mma_commit(&empty[ks]);
+                    }
+                    ok = ok && warp_wait(&full[vs], ((seq + 1) / SLOTS) & 1u, a.status, &abort_flag);
+                    if (!ok) break;
+                    // values behind the list's end may be anything, also NaN: zero them, their weights are zero too
+                    const int live = w.t.end - block_key(w.t, first + blk);
+                    if (live < kKeys) {
+                        const uint32_t base = saddr(ring + vs * C::SLOT);
+                        for (int o = max(live, 0) * 8 + lane; o < kKeys * 8; o += 32)
+#pragma unroll
+                            for (int x = 0; x < C::BOXES; ++x)
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + x * kBoxBytes + o * 16),
+                                             "r"(0u)
+                                             : "memory");
+                        fence_async();
+                        __syncwarp();
+                    }
+                    const bool more = blk + 1 < nb;
+                    for (int t = 0; ok && t < sub; ++t) {
+                        if (blk == 0) ok = n_seg[t] == 0 || warp_wait(&o_free[t], (n_seg[t] - 1) & 1u, a.status, &abort_flag);
+                        ok = ok && warp_wait(&p_ready[t], n_p[t] & 1u, a.status, &abort_flag);
+                        if (!ok) break;
+                        fence_after();
+                        if (lane == 0) {
+                            const uint64_t vd = desc_mn(saddr(ring + vs * C::SLOT));
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                mma_ts(tmem + C::O_COL + t * D, tmem + t * kKeys + k * 8, vd + (uint64_t)(k * 2048 >> 4),
+                                       id_pv, blk > 0 || k > 0);
+                            mma_commit(&o_done[t]);
+                        }
+                        ++n_p[t];
+                        if (more) {
+                            if (t == 0) ok = warp_wait(&full[kn], ((seq + 2) / SLOTS) & 1u, a.status, &abort_flag);
+                            if (ok) qk(t, kn);
+                        }
+                    }
+                    if (ok && lane == 0) {
+                        mma_commit(&empty[vs]);
+                        if (more) mma_commit(&empty[kn]);
+                    }
+                }
+                for (int t = 0; t < sub; ++t) ++n_seg[t];
+            }
+            // the tensor core is done with shared memory and TMEM
+            if (issued) {
+                if (lane == 0) mma_commit(&drain);
+                bar_wait(&drain, 0, a.status, &abort_flag, false);
+            }
+        } else if (warp == 2 && lane == 0) {
+            // -------------------------------------------- what the combine reads --
+            ChunkInfo ci = {-1, 0, 0, 0};
+            for (bool start = true; w.next(a, C::ROWS); start = false) {
+                if (start && w.first > 0) {
+                    ci.carries = 1;
+                    ci.ends = w.last == w.units;
+                }
+                if (w.first == 0 && w.last < w.units) ci.open_tile = (int32_t)(w.tile - 1);
+            }
+            info[blockIdx.x] = ci;
+        }
+    } else {
+        // ------------------------------------------ softmax, queries, output --
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;  // sub-tile, row of it
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lanes + t * kKeys, o_addr = tmem + lanes + C::O_COL + t * D;
+        // scores c x_s with c > 0: the queries take the sign, and all zeros for c = 0
+        const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
+        uint32_t n_s = 0;  // blocks so far
+        bool ok = t < NSUB;
+        while (ok && w.next(a, C::ROWS)) {
+            if (t * kSubRows >= w.t.rows) continue;
+            const int R = w.t.row0 + t * kSubRows + row;
+            const bool real = t * kSubRows + row < w.t.rows;
+            const int i = R / a.group, head = w.t.j * a.group + R - i * a.group;
+            const int64_t token = (int64_t)a.q_start[w.t.b] + i;
+            const int nb = w.blocks(), first = min(w.first, w.t.blocks);
+            const int p = real ? w.t.L - w.t.n + i : -1;  // the row's own key; rows that are not there see nothing
+            // (every wait for this sub-tile's last block of the segment before has ended: Q is free)
+            if (nb > 0) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.Q + 2 * (token * a.q_stride + (int64_t)head * D));
+                const uint32_t dst = saddr(q_smem + t * C::QBYTES) + row * 128;
+#pragma unroll 8
+                for (int x = 0; x < D / 8; ++x) {
+                    uint4 v = real ? src[x] : make_uint4(0u, 0u, 0u, 0u);
+                    v.x = (v.x ^ flip) & keep;
+                    v.y = (v.y ^ flip) & keep;
+                    v.z = (v.z ^ flip) & keep;
+                    v.w = (v.w ^ flip) & keep;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (x >> 3) * kBoxBytes +
+                                                                                   (((x & 7) ^ (row & 7)) << 4)),
+                                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&q_full[t]);
+            }
+            // places of the sub-tile's first and last row
+            const int r_last = min(w.t.rows, (t + 1) * kSubRows) - 1;
+            const int p_lo = w.t.L - w.t.n + (w.t.row0 + t * kSubRows) / a.group;
+            const int p_hi = w.t.L - w.t.n + (w.t.row0 + r_last) / a.group;
+            float m = -CUDART_INF_F, l = 0.f;
+            for (int blk = 0; blk < nb; ++blk, ++n_s) {
+                ok = warp_wait(&s_full[t], n_s & 1u, a.status, &abort_flag);
+                if (!ok) break;
+                fence_after();
+                float s[kKeys];
+#pragma unroll
+                for (int x = 0; x < kKeys; x += 32) tmem_ld32(s_addr + x, s + x);
+                wait_ld();
+                const int k0 = block_key(w.t, first + blk), k1 = k0 + kKeys - 1;
+                if (!(k1 <= p_lo && (a.window <= 0 || k0 > p_hi - a.window || k1 < a.sinks))) {
+                    const int seen = p - k0, from = a.window > 0 ? seen - a.window : -1, sinks = a.sinks - k0;
+#pragma unroll
+                    for (int x = 0; x < kKeys; ++x)
+                        if (!(x <= seen && (x > from || x < sinks))) s[x] = -CUDART_INF_F;
+                }
+                float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int x = 4; x < kKeys; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+                const float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const bool grow = best > m + kLag || (m == -CUDART_INF_F && best > m);
+                if (blk == 0) {
+                    m = best;
+                } else if (__any_sync(kFull, grow)) {
+                    const float f = !grow || m == -CUDART_INF_F ? (grow ? 0.f : 1.f) : exp2_approx(m - best);
+                    if (grow) m = best;
+                    l *= f;
+                    // O is complete up to the block before: its MMAs are done
+                    ok = warp_wait(&o_done[t], (n_s - 1) & 1u, a.status, &abort_flag);
+                    if (!ok) break;
+                    fence_after();
+#pragma unroll
+                    for (int x = 0; x < D; x += 32) {
+                        float o[32];
+                        tmem_ld32(o_addr + x, o);
+                        wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                        tmem_st32(o_addr + x, o);
+                    }
+                }
+                const float base = m == -CUDART_INF_F ? 0.f : m;
+                const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int x = 0; x < kKeys; x += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 v = fma2(make_float2(s[x + e], s[x + e + 1]), c2, b2);
+                        v.x = exp2_approx(v.x);
+                        v.y = exp2_approx(v.y);
+                        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
+                        // rounded to bf16, the type of the values in the product
+                        pk[e >> 1] = pack_bf16(v.x, v.y);
+                    }
+                    tmem_st16(s_addr + (x >> 1), pk);
+                }
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&p_ready[t]);
+            }
+            if (!ok) break;
+            if (nb > 0) {
+                ok = warp_wait(&o_done[t], (n_s - 1) & 1u, a.status, &abort_flag);
+                if (!ok) break;
+                fence_after();
+            }
+            const bool whole = w.whole();
+            const int64_t part = ((int64_t)blockIdx.x * 2 + (w.first > 0 ? 0 : 1)) * C::ROWS + t * kSubRows + row;
+            const float inv = l > 0.f ? a.v_scale / l : 0.f;
+            uint4 *dst = reinterpret_cast<uint4 *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D));
+            float4 *dst_part = reinterpret_cast<float4 *>(a.part_o + part * D);
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+                float o[32];
+                if (nb > 0) {
+                    tmem_ld32(o_addr + x, o);
+                    wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+                if (real && whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        dst[(x + e) >> 3] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                                       pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+                } else if (real) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) dst_part[(x + e) >> 2] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+                __syncwarp();
+            }
+            if (real && whole && a.lse)
+                a.lse[token * a.q_heads + head] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+            if (real && !whole) a.part_ml[part] = make_float2(m, l);
+            if (nb > 0) {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&o_free[t]);
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::TMEM) : "memory");
+    }
+}
+
+// Joins the parts of the tiles that were cut: blockIdx.y is the CTA whose last
+// segment begins a tile; the tile's other parts are the first segments of the
+// CTAs after it, up to the one that ends the tile. One warp per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+k_chunk_combine(const AttnArgs a, const ChunkInfo *__restrict__ info)
+{
+    using C = Chunk<D>;
+    constexpr int E = D / 32;
+    pdl_wait();
+    const int c0 = (int)blockIdx.y, lane = threadIdx.x & 31;
+    const int tile = info[c0].open_tile;
+    if (tile < 0) return;
+    const Tile t = make_tile(a, tile, C::ROWS, false);
+    const int row = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= t.rows) return;
+    int c1 = c0 + 1;  // the last CTA of the tile
+    while (c1 + 1 < (int)gridDim.y && !info[c1].ends) ++c1;
+    auto at = [&](int c) -> int64_t { return ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * C::ROWS + row; };
+    float M = -CUDART_INF_F;
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.part_ml[at(c)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    float sum[E], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        const float2 ml = a.part_ml[at(c)];
+        if (ml.x == -CUDART_INF_F) continue;
+        const float f = exp2_approx(ml.x - M);
+        l += f * ml.y;
+        const float *v = a.part_o + at(c) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] += f * v[e];
+    }
+    const float inv = l > 0.f ? a.v_scale / l : 0.f;
+    const int R = t.row0 + row, i = R / a.group, head = t.j * a.group + R - i * a.group;
+    const int64_t token = (int64_t)a.q_start[t.b] + i;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[2 * e] * inv, sum[2 * e + 1] * inv);
+    if (lane == 0 && a.lse)
+        a.lse[token * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+}
+
+// --------------------------------------------------------------- host side --
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// The pool as rows of head_dim bf16; boxes of 64 dims x one page.
+bool make_map(CUtensorMap *map, const void *base, const AttnArgs &a)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_pages * a.page_size};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.head_dim * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)a.page_size};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_one(const AttnArgs &a, int ctas, cudaStream_t st)
+{
+    using C = Chunk<D>;
+    CUtensorMap mk, mv;
+    if (!make_map(&mk, a.k, a) || !make_map(&mv, a.v, a)) return cudaErrorUnknown;
+    cudaError_t e = cudaFuncSetAttribute(k_attend_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    ChunkInfo *info = reinterpret_cast<ChunkInfo *>(a.part_ml + (int64_t)ctas * 2 * C::ROWS);
+    k_attend_chunk<D><<<ctas, kThreads, C::SMEM, st>>>(mk, mv, a, info);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(C::ROWS / 8), (unsigned)ctas);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_chunk_combine<D>, a, (const ChunkInfo *)info);
+}
+
+}  // namespace
+
+int chunk_tile_rows(int head_dim) { return head_dim == 256 ? kSubRows : 2 * kSubRows; }
+
+size_t chunk_workspace_bytes(int ctas, int head_dim)
+{
+    const size_t rows = (size_t)ctas * 2 * chunk_tile_rows(head_dim);
+    return rows * (head_dim * sizeof(float) + sizeof(float2)) + ctas * sizeof(ChunkInfo);
+}
+
+cudaError_t launch_attend_chunk(const AttnArgs &a, cudaStream_t st)
+{
+    switch (a.head_dim) {
+    case 64: return launch_one<64>(a, a.splits, st);
+    case 128: return launch_one<128>(a, a.splits, st);
+    case 256: return launch_one<256>(a, a.splits, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace mkv

@@ -307,9 +307,10 @@ static mkv_status attention_sizes(const mkv_page_pool &pool, const mkv_page_list
     *plan = AttnPlan();
     if (no_lists(lists) || max_q == 0) return MKV_OK;
     const int64_t n = (int64_t)lists.batch * lists.heads;
-    *plan = attention_plan(n, tokens.q_heads / lists.heads, max_q, max_len, pool.head_dim, kPlanSms);
+    *plan = attention_plan(n, tokens.q_heads / lists.heads, max_q, max_len, pool.head_dim,
+                           elem_bytes(pool.dtype), kPlanSms);
     // CTAs of the two launches, 32-bit grids
-    if (n * plan->tiles * plan->splits > (int64_t)INT32_MAX || n * plan->tiles * 2 > (int64_t)INT32_MAX)
+    if ((!plan->chunked && n * plan->tiles * plan->splits > (int64_t)INT32_MAX) || n * plan->tiles * 2 > (int64_t)INT32_MAX)
         return MKV_ERR_UNSUPPORTED;
     return MKV_OK;
 }
@@ -337,6 +338,7 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     const int d = pool.head_dim;
     const bool none = tokens.n_tokens == 0 || no_lists(lists) || max_q == 0;
     if (!none) {
+        if (pool.n_pages == 0) return MKV_ERR_INVALID_ARG;
         if (!rows_ok(Q, q_stride, tokens.q_heads, d) || !rows_ok(O, o_stride, tokens.q_heads, d) || O == Q)
             return MKV_ERR_INVALID_ARG;
         if (!tokens.q_start || !aligned(tokens.q_start, 4) || !aligned(lse, 4)) return MKV_ERR_INVALID_ARG;
@@ -373,9 +375,9 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     a.v_scale = v_scale;
     a.tiles = plan.tiles;
     a.splits = plan.splits;
-    const int64_t items = (int64_t)lists.batch * lists.heads * plan.tiles * plan.splits;
+    a.chunked = plan.chunked;
     a.part_o = region<float>(workspace, kAlign);
-    a.part_ml = reinterpret_cast<float2 *>(a.part_o + items * 16 * d);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + plan.part_rows * d);
     a.status = region<uint32_t>(workspace, 0);
     return cuda_status(launch_paged_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }

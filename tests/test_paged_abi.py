@@ -110,6 +110,7 @@ def _attend(Q=A, qs=4096, tokens=_tokens(), max_q=8, pool=_pool(k=7 * A, v=8 * A
 
 @pytest.mark.parametrize("kwargs,status", [(dict(max_len=0) | k if "lists" in k else k, s) for k, s in SIZES] + POINTERS + [
     (dict(Q=0), ARG), (dict(O=0), ARG), (dict(O=A), ARG), (dict(Q=A + 2), ARG), (dict(qs=4092), ARG), (dict(os_=4088), ARG),
+    (dict(pool=_pool(n_pages=0)), ARG),
     (dict(lse=3 * A + 2), ARG), (dict(max_q=-1), ARG), (dict(max_q=(1 << 20) + 1), UNS), (dict(max_len=161), ARG),
     (dict(max_len=-1), ARG), (dict(window=-1), ARG), (dict(sinks=-1), ARG), (dict(scale=float("inf")), ARG),
     (dict(k_scale=2.0), ARG), (dict(pool=_pool(dtype=1), k_scale=0.0), ARG), (dict(tokens=_tokens(q_heads=20)), ARG),
