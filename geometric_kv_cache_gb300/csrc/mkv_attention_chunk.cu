@@ -168,6 +168,15 @@ __device__ __forceinline__ void mma_commit(uint64_t *b)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(b))
                  : "memory");
 }
+// One lane of the converged warp. (Issued under this the MMAs go out back to
+// back; under a test of the lane number they took 90 cycles each, more than
+// the 64 that the tensor core needs for one.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -340,6 +349,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         drain;
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t abort_flag;
+    __shared__ Walk s_walk[kThreads / 32];
     __shared__ long long s_sum[kThreads / 32];
     __shared__ long long s_first_tile, s_left;
     __shared__ int s_skip;
@@ -428,7 +438,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     w.skip = s_skip;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             // ---------------------------------------------------- pages of K and V --
             const int per_block = kKeys >> a.page_shift;  // pages of a block: one lane each
@@ -479,7 +489,6 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             uint32_t n_p[2] = {0, 0}, n_seg[2] = {0, 0};  // blocks and segments of each sub-tile so far
             bool ok = true, issued = false;
             auto qk = [&](int t, int slot) {
-                if (lane != 0) return;
                 const uint64_t qd = desc_k(saddr(q_smem + t * C::QBYTES)), kd = desc_k(saddr(ring + slot * C::SLOT));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
@@ -493,18 +502,23 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 if (nb == 0) continue;
                 issued = true;
                 const int first = min(w.first, w.t.blocks);
-                for (int blk = 0; ok && blk < nb; ++blk, seq += 2) {
-                    const int ks = (int)(seq % SLOTS), vs = (int)((seq + 1) % SLOTS), kn = (int)((seq + 2) % SLOTS);
-                    if (blk == 0) {
-                        ok = warp_wait(&full[ks], (seq / SLOTS) & 1u, a.status, &abort_flag);
-                        for (int t = 0; ok && t < sub; ++t) {
-                            ok = warp_wait(&q_full[t], n_seg[t] & 1u, a.status, &abort_flag);
-                            fence_after();
-                            if (ok) qk(t, ks);
-                        }
-                        if (ok && lane == 0) mma_commit(&empty[ks]);
+                const int ks = (int)(seq % SLOTS);
+                ok = warp_wait(&full[ks], (seq / SLOTS) & 1u, a.status, &abort_flag);
+                for (int t = 0; ok && t < sub; ++t) {
+                    ok = warp_wait(&q_full[t], n_seg[t] & 1u, a.status, &abort_flag);
+                    fence_after();
+                    if (ok && elect_one()) {
+                        qk(t, ks);
+                        if (t == sub - 1) mma_commit(&empty[ks]);
                     }
-                    ok = ok && warp_wait(&full[vs], ((seq + 1) / SLOTS) & 1u, a.status, &abort_flag);
+                    __syncwarp();
+                }
+                for (int blk = 0; ok && blk < nb; ++blk, seq += 2) {
+                    // values of this block, keys of the next
+                    const int vs = (int)((seq + 1) % SLOTS), kn = (int)((seq + 2) % SLOTS);
+                    const bool more = blk + 1 < nb;
+                    ok = warp_wait(&full[vs], ((seq + 1) / SLOTS) & 1u, a.status, &abort_flag);
+                    if (more) ok = ok && warp_wait(&full[kn], ((seq + 2) / SLOTS) & 1u, a.status, &abort_flag);
                     if (!ok) break;
                     // values behind the list's end may be anything, also NaN: zero them, their weights are zero too
                     const int live = w.t.end - block_key(w.t, first + blk);
@@ -519,36 +533,34 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         fence_async();
                         __syncwarp();
                     }
-                    const bool more = blk + 1 < nb;
                     for (int t = 0; ok && t < sub; ++t) {
                         if (blk == 0) ok = n_seg[t] == 0 || warp_wait(&o_free[t], (n_seg[t] - 1) & 1u, a.status, &abort_flag);
                         ok = ok && warp_wait(&p_ready[t], n_p[t] & 1u, a.status, &abort_flag);
                         if (!ok) break;
                         fence_after();
-                        if (lane == 0) {
+                        if (elect_one()) {
                             const uint64_t vd = desc_mn(saddr(ring + vs * C::SLOT));
 #pragma unroll
                             for (int k = 0; k < kKeys / 16; ++k)
                                 mma_ts(tmem + C::O_COL + t * D, tmem + t * kKeys + k * 8, vd + (uint64_t)(k * 2048 >> 4),
                                        id_pv, blk > 0 || k > 0);
-                            mma_commit(&o_done[t]);
+                            // MMAs run in order: the next scores are complete only after this block's O
+                            if (more) qk(t, kn);
+                            else mma_commit(&o_done[t]);
+                            if (t == sub - 1) {
+                                mma_commit(&empty[vs]);
+                                if (more) mma_commit(&empty[kn]);
+                            }
                         }
+                        __syncwarp();
                         ++n_p[t];
-                        if (more) {
-                            if (t == 0) ok = warp_wait(&full[kn], ((seq + 2) / SLOTS) & 1u, a.status, &abort_flag);
-                            if (ok) qk(t, kn);
-                        }
-                    }
-                    if (ok && lane == 0) {
-                        mma_commit(&empty[vs]);
-                        if (more) mma_commit(&empty[kn]);
                     }
                 }
                 for (int t = 0; t < sub; ++t) ++n_seg[t];
             }
             // the tensor core is done with shared memory and TMEM
             if (issued) {
-                if (lane == 0) mma_commit(&drain);
+                if (elect_one()) mma_commit(&drain);
                 bar_wait(&drain, 0, a.status, &abort_flag, false);
             }
         } else if (warp == 2 && lane == 0) {
@@ -572,19 +584,20 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         // scores c x_s with c > 0: the queries take the sign, and all zeros for c = 0
         const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
-        uint32_t n_s = 0;  // blocks so far
+        uint32_t n_s = 0, n_o = 0;  // blocks, segments with blocks so far
         bool ok = t < NSUB;
         while (ok && w.next(a, C::ROWS)) {
             if (t * kSubRows >= w.t.rows) continue;
-            const int R = w.t.row0 + t * kSubRows + row;
             const bool real = t * kSubRows + row < w.t.rows;
-            const int i = R / a.group, head = w.t.j * a.group + R - i * a.group;
-            const int64_t token = (int64_t)a.q_start[w.t.b] + i;
             const int nb = w.blocks(), first = min(w.first, w.t.blocks);
-            const int p = real ? w.t.L - w.t.n + i : -1;  // the row's own key; rows that are not there see nothing
+            const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
+            // the row's own key; rows that are not there see nothing
+            const int p = real ? w.t.L - w.t.n + (w.t.row0 + t * kSubRows + row) / a.group : -1;
             // (every wait for this sub-tile's last block of the segment before has ended: Q is free)
             if (nb > 0) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.Q + 2 * (token * a.q_stride + (int64_t)head * D));
+                const int R = w.t.row0 + t * kSubRows + row, i = R / a.group, head = w.t.j * a.group + R - i * a.group;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.Q + 2 * (((int64_t)a.q_start[w.t.b] + i) * a.q_stride + (int64_t)head * D));
                 const uint32_t dst = saddr(q_smem + t * C::QBYTES) + row * 128;
 #pragma unroll 8
                 for (int x = 0; x < D / 8; ++x) {
@@ -602,10 +615,13 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) bar_arrive(&q_full[t]);
             }
-            // places of the sub-tile's first and last row
+            // the first and last place that is visible to every row: blocks inside need no mask
             const int r_last = min(w.t.rows, (t + 1) * kSubRows) - 1;
-            const int p_lo = w.t.L - w.t.n + (w.t.row0 + t * kSubRows) / a.group;
-            const int p_hi = w.t.L - w.t.n + (w.t.row0 + r_last) / a.group;
+            const int whole_to = w.t.L - w.t.n + (w.t.row0 + t * kSubRows) / a.group;
+            const int whole_from = a.window > 0 ? w.t.L - w.t.n + (w.t.row0 + r_last) / a.group - a.window : -1;
+            // what the loop does not need waits in shared memory: it has 128 scores to hold
+            if (lane == 0) s_walk[warp] = w;
+            __syncwarp();
             float m = -CUDART_INF_F, l = 0.f;
             for (int blk = 0; blk < nb; ++blk, ++n_s) {
                 ok = warp_wait(&s_full[t], n_s & 1u, a.status, &abort_flag);
@@ -615,8 +631,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 #pragma unroll
                 for (int x = 0; x < kKeys; x += 32) tmem_ld32(s_addr + x, s + x);
                 wait_ld();
-                const int k0 = block_key(w.t, first + blk), k1 = k0 + kKeys - 1;
-                if (!(k1 <= p_lo && (a.window <= 0 || k0 > p_hi - a.window || k1 < a.sinks))) {
+                const int k0 = (first + blk + (first + blk < sink_blocks ? 0 : past_sinks)) * kKeys, k1 = k0 + kKeys - 1;
+                if (!(k1 <= whole_to && (k0 > whole_from || k1 < a.sinks))) {
                     const int seen = p - k0, from = a.window > 0 ? seen - a.window : -1, sinks = a.sinks - k0;
 #pragma unroll
                     for (int x = 0; x < kKeys; ++x)
@@ -633,10 +649,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     const float f = !grow || m == -CUDART_INF_F ? (grow ? 0.f : 1.f) : exp2_approx(m - best);
                     if (grow) m = best;
                     l *= f;
-                    // O is complete up to the block before: its MMAs are done
-                    ok = warp_wait(&o_done[t], (n_s - 1) & 1u, a.status, &abort_flag);
-                    if (!ok) break;
-                    fence_after();
+                    // (O is complete up to the block before: its MMAs came before the ones of these scores)
 #pragma unroll
                     for (int x = 0; x < D; x += 32) {
                         float o[32];
@@ -673,10 +686,13 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             }
             if (!ok) break;
             if (nb > 0) {
-                ok = warp_wait(&o_done[t], (n_s - 1) & 1u, a.status, &abort_flag);
+                ok = warp_wait(&o_done[t], n_o++ & 1u, a.status, &abort_flag);
                 if (!ok) break;
                 fence_after();
             }
+            w = s_walk[warp];
+            const int R = w.t.row0 + t * kSubRows + row, i = R / a.group, head = w.t.j * a.group + R - i * a.group;
+            const int64_t token = (int64_t)a.q_start[w.t.b] + i;
             const bool whole = w.whole();
             const int64_t part = ((int64_t)blockIdx.x * 2 + (w.first > 0 ? 0 : 1)) * C::ROWS + t * kSubRows + row;
             const float inv = l > 0.f ? a.v_scale / l : 0.f;
