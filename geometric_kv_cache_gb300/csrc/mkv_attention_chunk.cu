@@ -14,10 +14,10 @@
 //
 // Roles (12 warps, one CTA per SM): warp 0 brings the pages of K and V blocks
 // into a ring of shared-memory slots (TMA, 128-byte swizzle, one box of 64 dims
-// per page, page entries read a block ahead); warp 1 issues the MMAs, for the
-// two sub-tiles in turn, so that the tensor core works on one while the other's
-// softmax runs; warps 4-7 and 8-11 are the softmax of sub-tile 0 and 1 (they
-// also load its queries and write its output).
+// per page, page entries read a block ahead); warps 1 and 2 issue the MMAs of
+// sub-tile 0 and 1, so that the tensor core works on one while the other waits
+// for its softmax or its operands; warps 4-7 and 8-11 are the softmax of
+// sub-tile 0 and 1 (they also load its queries and write its output).
 //
 // The blocks of all tiles form one line, cut into equal parts, one per CTA: no
 // CTA idles behind a long list or an uneven number of tiles. A tile that is
@@ -346,7 +346,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     uint8_t *q_smem = smem;                      // NSUB x [D / 64 boxes][128 rows x 128 B]
     uint8_t *ring = smem + NSUB * C::QBYTES;     // SLOTS blocks: K, V, K, V, ...
     __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_ready[2], o_done[2], o_free[2], q_full[2],
-        drain;
+        drain[2];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t abort_flag;
     __shared__ Walk s_walk[kThreads / 32];
@@ -360,7 +360,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int s = 0; s < SLOTS; ++s) {
             bar_init(&full[s], 1);
-            bar_init(&empty[s], 1);
+            bar_init(&empty[s], NSUB);
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(&s_full[s], 1);
@@ -369,7 +369,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             bar_init(&o_free[s], 4);
             bar_init(&q_full[s], 4);
         }
-        bar_init(&drain, 1);
+        bar_init(&drain[0], 1);
+        bar_init(&drain[1], 1);
         abort_flag = 0u;
         s_first_tile = 0;
         s_left = 0;
@@ -482,37 +483,43 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 #pragma unroll
             for (int s = 0; s < SLOTS; ++s)
                 if (seq > (uint32_t)s) bar_wait(&full[s], ((seq - 1 - s) / SLOTS) & 1u, a.status, &abort_flag, false);
-        } else if (warp == 1) {
-            // ------------------------------------------------------------- MMAs --
+        } else if (warp <= NSUB) {
+            // ----------------------------- MMAs of sub-tile 0 (warp 1), 1 (warp 2) --
             constexpr uint32_t id_qk = idesc_bf16(kKeys, false), id_pv = idesc_bf16(D, true);
-            uint32_t seq = 0;  // slots used before this block
-            uint32_t n_p[2] = {0, 0}, n_seg[2] = {0, 0};  // blocks and segments of each sub-tile so far
-            bool ok = true, issued = false;
-            auto qk = [&](int t, int slot) {
+            const int t = warp - 1;
+            const uint32_t s_col = tmem + t * kKeys, o_col = tmem + C::O_COL + t * D;
+            uint32_t seq = 0, n_p = 0, n_seg = 0;  // slots, blocks and segments so far
+            bool ok = true;
+            auto qk = [&](int slot) {
                 const uint64_t qd = desc_k(saddr(q_smem + t * C::QBYTES)), kd = desc_k(saddr(ring + slot * C::SLOT));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t step = (uint64_t)(((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4);
-                    mma_ss(tmem + t * kKeys, qd + step, kd + step, id_qk, k > 0);
+                    mma_ss(s_col, qd + step, kd + step, id_qk, k > 0);
                 }
                 mma_commit(&s_full[t]);
             };
             while (ok && w.next(a, C::ROWS)) {
-                const int nb = w.blocks(), sub = NSUB == 1 || w.t.rows <= kSubRows ? 1 : 2;
+                const int nb = w.blocks();
                 if (nb == 0) continue;
-                issued = true;
+                if (t * kSubRows >= w.t.rows) {
+                    // no rows for this warp: it keeps step (a slot is free when both warps have let it go)
+                    for (int x = 0; ok && x < 2 * nb; ++x, ++seq) {
+                        ok = warp_wait(&full[seq % SLOTS], (seq / SLOTS) & 1u, a.status, &abort_flag);
+                        if (ok && lane == 0) bar_arrive(&empty[seq % SLOTS]);
+                    }
+                    continue;
+                }
                 const int first = min(w.first, w.t.blocks);
                 const int ks = (int)(seq % SLOTS);
-                ok = warp_wait(&full[ks], (seq / SLOTS) & 1u, a.status, &abort_flag);
-                for (int t = 0; ok && t < sub; ++t) {
-                    ok = warp_wait(&q_full[t], n_seg[t] & 1u, a.status, &abort_flag);
-                    fence_after();
-                    if (ok && elect_one()) {
-                        qk(t, ks);
-                        if (t == sub - 1) mma_commit(&empty[ks]);
-                    }
-                    __syncwarp();
+                ok = warp_wait(&full[ks], (seq / SLOTS) & 1u, a.status, &abort_flag) &&
+                     warp_wait(&q_full[t], n_seg & 1u, a.status, &abort_flag);
+                fence_after();
+                if (ok && elect_one()) {
+                    qk(ks);
+                    mma_commit(&empty[ks]);
                 }
+                __syncwarp();
                 for (int blk = 0; ok && blk < nb; ++blk, seq += 2) {
                     // values of this block, keys of the next
                     const int vs = (int)((seq + 1) % SLOTS), kn = (int)((seq + 2) % SLOTS);
@@ -521,6 +528,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     if (more) ok = ok && warp_wait(&full[kn], ((seq + 2) / SLOTS) & 1u, a.status, &abort_flag);
                     if (!ok) break;
                     // values behind the list's end may be anything, also NaN: zero them, their weights are zero too
+                    // (both warps write the same zeros, each before its own MMAs)
                     const int live = w.t.end - block_key(w.t, first + blk);
                     if (live < kKeys) {
                         const uint32_t base = saddr(ring + vs * C::SLOT);
@@ -533,37 +541,32 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         fence_async();
                         __syncwarp();
                     }
-                    for (int t = 0; ok && t < sub; ++t) {
-                        if (blk == 0) ok = n_seg[t] == 0 || warp_wait(&o_free[t], (n_seg[t] - 1) & 1u, a.status, &abort_flag);
-                        ok = ok && warp_wait(&p_ready[t], n_p[t] & 1u, a.status, &abort_flag);
-                        if (!ok) break;
-                        fence_after();
-                        if (elect_one()) {
-                            const uint64_t vd = desc_mn(saddr(ring + vs * C::SLOT));
+                    if (blk == 0) ok = n_seg == 0 || warp_wait(&o_free[t], (n_seg - 1) & 1u, a.status, &abort_flag);
+                    ok = ok && warp_wait(&p_ready[t], n_p & 1u, a.status, &abort_flag);
+                    if (!ok) break;
+                    fence_after();
+                    if (elect_one()) {
+                        const uint64_t vd = desc_mn(saddr(ring + vs * C::SLOT));
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                mma_ts(tmem + C::O_COL + t * D, tmem + t * kKeys + k * 8, vd + (uint64_t)(k * 2048 >> 4),
-                                       id_pv, blk > 0 || k > 0);
-                            // MMAs run in order: the next scores are complete only after this block's O
-                            if (more) qk(t, kn);
-                            else mma_commit(&o_done[t]);
-                            if (t == sub - 1) {
-                                mma_commit(&empty[vs]);
-                                if (more) mma_commit(&empty[kn]);
-                            }
-                        }
-                        __syncwarp();
-                        ++n_p[t];
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            mma_ts(o_col, s_col + k * 8, vd + (uint64_t)(k * 2048 >> 4), id_pv, blk > 0 || k > 0);
+                        // one thread's MMAs run in order: the next scores are complete only after this block's O
+                        if (more) qk(kn);
+                        else mma_commit(&o_done[t]);
+                        mma_commit(&empty[vs]);
+                        if (more) mma_commit(&empty[kn]);
                     }
+                    __syncwarp();
+                    ++n_p;
                 }
-                for (int t = 0; t < sub; ++t) ++n_seg[t];
+                ++n_seg;
             }
             // the tensor core is done with shared memory and TMEM
-            if (issued) {
-                if (elect_one()) mma_commit(&drain);
-                bar_wait(&drain, 0, a.status, &abort_flag, false);
+            if (n_seg > 0 || !ok) {
+                if (elect_one()) mma_commit(&drain[t]);
+                bar_wait(&drain[t], 0, a.status, &abort_flag, false);
             }
-        } else if (warp == 2 && lane == 0) {
+        } else if (warp == 3 && lane == 0) {
             // -------------------------------------------- what the combine reads --
             ChunkInfo ci = {-1, 0, 0, 0};
             for (bool start = true; w.next(a, C::ROWS); start = false) {

@@ -206,6 +206,15 @@ def test_captured_call_replays_on_longer_lists():
     assert mkv.mkv_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("d,dtype,page", [(64, BF, 16), (128, BF, 64), (256, BF, 16), (128, F8, 32)])
+def test_long_lists_of_full_and_nearly_empty_tiles(d, dtype, page):
+    # tiles of many blocks of keys, of which some have all their rows and some a few, cut in several parts
+    p = Problem(12, [70, 1, 130, 3, 1], [[5000, 900], [4000, 2500], [300, 6000], [5200, 33], [1, 3000]], 2, d, page, dtype)
+    O, lse = p.run()
+    assert p.status == 0
+    p.check(O, lse)
+
+
 @pytest.mark.parametrize("counts", [[1, 1], [90, 1]])
 def test_same_bits_on_every_call(counts):
     p = Problem(11, counts, [[2000, 200], [50, 1500]], 4, 128, 16, BF)
