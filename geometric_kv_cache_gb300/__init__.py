@@ -503,55 +503,76 @@ def mkv_inject_stalled_fused(K, V, ratio, mode, keep_stride, K_out, V_out, idx, 
 
 # --------------------------------------------------------------- paged caches --
 
-def _on_device(*ts):
+# (The checks below run on every step of a serving loop: plain comparisons, no
+# temporary objects.)
+
+def _on_device(ts) -> int:
     """The one CUDA device of a call's tensors, which must be the current one
     (the launches go to a stream of the current device)."""
-    devs = {t.device for t in ts if t is not None}
-    if any(d.type != "cuda" for d in devs):
-        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
-    if len(devs) != 1 or next(iter(devs)).index != torch.cuda.current_device():
-        raise ValueError("tensors of one call must live on one CUDA device, the current one")
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
+            if dev == -2 and t.get_device() == torch.cuda.current_device():
+                dev = t.get_device()
+                continue
+            raise ValueError("tensors of one call must live on one CUDA device, the current one")
+    return dev
+
+
+def _raw_stream(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _int32(t, shape, what):
-    if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+    if t is not None and (t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous int32 tensor {list(shape)}")
 
 
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _workspace(ws):
-    if ws.dtype != torch.uint8 or not ws.is_contiguous():
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError("the workspace must be a contiguous uint8 tensor")
 
 
 def pool_of(k_pages: torch.Tensor, v_pages: torch.Tensor) -> MkvPagePool:
     """mkv_page_pool of two [n_pages, page_size, head_dim] bf16 or float8_e4m3fn tensors."""
-    if k_pages.dim() != 3 or k_pages.dtype not in DTYPES:
+    dtype, shape = DTYPES.get(k_pages.dtype), k_pages.shape
+    if len(shape) != 3 or dtype is None:
         raise ValueError("k_pages must be a bf16 or float8_e4m3fn tensor [n_pages, page_size, head_dim]")
-    if v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+    if v_pages.shape != shape or v_pages.dtype is not k_pages.dtype:
         raise ValueError("k_pages and v_pages must have one shape and dtype")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
-    n, p, d = k_pages.shape
-    return MkvPagePool(n, p, d, DTYPES[k_pages.dtype], k_pages.data_ptr(), v_pages.data_ptr())
+    n, p, d = shape
+    return MkvPagePool(n, p, d, dtype, k_pages.data_ptr(), v_pages.data_ptr())
 
 
 def lists_of(table: torch.Tensor, lens: Optional[torch.Tensor] = None) -> MkvPageLists:
     """mkv_page_lists of table int32 [batch, heads, max_pages] and lens int32 [batch, heads]."""
-    if table.dim() != 3:
+    shape = table.shape
+    if len(shape) != 3:
         raise ValueError("table must be an int32 tensor [batch, heads, max_pages]")
-    _int32(table, table.shape, "table")
-    _int32(lens, table.shape[:2], "lens")
-    b, h, m = table.shape
+    b, h, m = shape
+    _int32(table, shape, "table")
+    _int32(lens, (b, h), "lens")
     return MkvPageLists(b, h, m, table.data_ptr(), None if lens is None else lens.data_ptr())
 
 
 def _token_rows(t, heads, d, n_tokens, what):
     """Stride (elements) between the tokens of a bf16 [n_tokens, heads, d] tensor, whose tokens may lie apart."""
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != (n_tokens, heads, d):
+    if t.dtype is not torch.bfloat16 or t.shape != (n_tokens, heads, d):
         raise ValueError(f"{what} must be a bf16 tensor [{n_tokens}, {heads}, {d}]")
-    if n_tokens and ((heads > 1 and t.stride(1) != d) or t.stride(2) != 1):
+    if n_tokens == 0:
+        return heads * d
+    s0, s1, s2 = t.stride()
+    if (heads > 1 and s1 != d) or s2 != 1:
         raise ValueError(f"the heads of one token of {what} must be contiguous")
-    return heads * d if n_tokens <= 1 else t.stride(0)
+    return heads * d if n_tokens == 1 else s0
 
 
 def page_workspace_for(k_pages: torch.Tensor, table: torch.Tensor) -> torch.Tensor:
@@ -566,15 +587,16 @@ def mkv_page_update(k_pages, v_pages, table, lens, refs, table_out, lens_out, re
     tokens. table int32 [batch, heads, max_pages], lens int32 [batch, heads], refs int32 [n_pages]; parent and n_new
     int32 [batch]. Full pages are shared, partly filled last pages copied for all but one child. With parent None,
     table_out and lens_out may be table and lens; refs_out may always be refs."""
-    _on_device(k_pages, v_pages, table, lens, refs, table_out, lens_out, refs_out, workspace, parent, n_new)
+    dev = _on_device((k_pages, v_pages, table, lens, refs, table_out, lens_out, refs_out, workspace, parent, n_new))
     pool, src, dst = pool_of(k_pages, v_pages), lists_of(table, lens), lists_of(table_out, lens_out)
     _int32(refs, (pool.n_pages,), "refs")
     _int32(refs_out, (pool.n_pages,), "refs_out")
     _int32(parent, (src.batch,), "parent")
     _int32(n_new, (src.batch,), "n_new")
     _workspace(workspace)
-    _check(load().mkv_page_update(pool, src, _ptr(refs), _ptr(parent), _ptr(n_new), dst, _ptr(refs_out),
-                                  _ptr(workspace), workspace.numel(), _stream(stream)), "mkv_page_update")
+    _check((_lib or load()).mkv_page_update(pool, src, refs.data_ptr(), _at(parent), _at(n_new), dst, refs_out.data_ptr(),
+                                            workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)),
+           "mkv_page_update")
 
 
 def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K=None,
@@ -582,7 +604,8 @@ def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, 
     """Compaction in pages: list h keeps its tokens idx[h][:kept[h]] in new pages, its old pages lose a holder. idx
     int32 [batch, heads, n] (None: the first kept tokens), kept int32 [batch, heads], as mkv_compress writes them.
     With K and V [batch, heads, t_max, head_dim] (and seq_lens) the tokens come from that contiguous cache instead."""
-    _on_device(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K, V, seq_lens)
+    dev = _on_device((k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K, V,
+                      seq_lens))
     pool, src, dst = pool_of(k_pages, v_pages), lists_of(table, lens), lists_of(table_out, lens_out)
     _int32(refs, (pool.n_pages,), "refs")
     _int32(refs_out, (pool.n_pages,), "refs_out")
@@ -601,9 +624,10 @@ def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, 
         if not (K.is_contiguous() and V.is_contiguous()):
             raise ValueError("tensors passed to the CUDA library must be contiguous")
         _int32(seq_lens, (src.batch,), "seq_lens")
-    _check(load().mkv_page_compact(pool, src, _ptr(refs), _ptr(idx), 0 if idx is None else idx.shape[-1], _ptr(kept),
-                                   _ptr(K), _ptr(V), t_max, _ptr(seq_lens), dst, _ptr(refs_out), _ptr(workspace),
-                                   workspace.numel(), _stream(stream)), "mkv_page_compact")
+    _check((_lib or load()).mkv_page_compact(pool, src, refs.data_ptr(), _at(idx), 0 if idx is None else idx.shape[-1],
+                                             kept.data_ptr(), _at(K), _at(V), t_max, _at(seq_lens), dst,
+                                             refs_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                             _raw_stream(stream, dev)), "mkv_page_compact")
 
 
 def mkv_rope_frequencies(rot_dim: int, theta: float, scaling="plain", scale: float = 1.0, original_len: int = 0,
@@ -624,12 +648,12 @@ def mkv_rope_append(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens,
     """Rotary positions of a step's new tokens: Q [n_tokens, q_heads, d] turned into Q_out, K [n_tokens, heads, d]
     turned into the pages, V into the pages (all bf16; tokens may lie apart, as in a fused projection). Row b's tokens
     are [q_start[b], q_start[b + 1]) and the last ones of its lists. inv_freq fp32 [rot_dim / 2] on the device."""
-    _on_device(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace)
+    dev = _on_device((Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace))
     pool, lists = pool_of(k_pages, v_pages), lists_of(table, lens)
     if Q.dim() != 3:
         raise ValueError("Q must be a bf16 tensor [n_tokens, q_heads, head_dim]")
     n, hq, d = Q.shape[0], Q.shape[1], pool.head_dim
-    qs, ks, vs = (_token_rows(t, h, d, n, w) for t, h, w in ((Q, hq, "Q"), (K, lists.heads, "K"), (V, lists.heads, "V")))
+    qs, ks, vs = _token_rows(Q, hq, d, n, "Q"), _token_rows(K, lists.heads, d, n, "K"), _token_rows(V, lists.heads, d, n, "V")
     _token_rows(Q_out, hq, d, n, "Q_out")
     if not Q_out.is_contiguous():
         raise ValueError("Q_out must be contiguous")
@@ -638,10 +662,10 @@ def mkv_rope_append(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens,
     if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous fp32 tensor [rot_dim / 2]")
     _workspace(workspace)
-    _check(load().mkv_rope_append(_ptr(Q), qs, _ptr(K), ks, _ptr(V), vs, MkvNewTokens(n, hq, q_start.data_ptr()),
-                                  _ptr(positions), _ptr(inv_freq), 2 * inv_freq.numel(), _ROPE_LAYOUTS[layout],
-                                  float(factor), _ptr(Q_out), pool, lists, float(k_scale), float(v_scale),
-                                  _ptr(workspace), workspace.numel(), _stream(stream)), "mkv_rope_append")
+    _check((_lib or load()).mkv_rope_append(
+        Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, MkvNewTokens(n, hq, q_start.data_ptr()), positions.data_ptr(),
+        inv_freq.data_ptr(), 2 * inv_freq.shape[0], _ROPE_LAYOUTS[layout], factor, Q_out.data_ptr(), pool, lists, k_scale,
+        v_scale, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)), "mkv_rope_append")
 
 
 def attention_workspace_for(Q, k_pages, table, max_q: int, max_len: int) -> torch.Tensor:
@@ -658,20 +682,20 @@ def mkv_paged_attention(Q, k_pages, v_pages, table, lens, q_start, max_q: int, m
     fp32 [n_tokens, q_heads]. Row b's tokens are [q_start[b], q_start[b + 1]) and the last ones of its lists; each sees
     the tokens up to its own, with window > 0 the last `window` of them and the first `sinks`. max_q and max_len bound
     the rows' new tokens and the lists' lengths. scale defaults to 1 / sqrt(d)."""
-    _on_device(Q, k_pages, v_pages, table, lens, q_start, O, workspace, lse)
+    dev = _on_device((Q, k_pages, v_pages, table, lens, q_start, O, workspace, lse))
     pool, lists = pool_of(k_pages, v_pages), lists_of(table, lens)
     if Q.dim() != 3:
         raise ValueError("Q must be a bf16 tensor [n_tokens, q_heads, head_dim]")
     n, hq, d = Q.shape[0], Q.shape[1], pool.head_dim
     qs, os_ = _token_rows(Q, hq, d, n, "Q"), _token_rows(O, hq, d, n, "O")
     _int32(q_start, (lists.batch + 1,), "q_start")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, hq) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 tensor [n_tokens, q_heads]")
     _workspace(workspace)
-    _check(load().mkv_paged_attention(_ptr(Q), qs, MkvNewTokens(n, hq, q_start.data_ptr()), int(max_q), pool, lists,
-                                      int(max_len), float(d ** -0.5 if scale is None else scale), float(k_scale),
-                                      float(v_scale), int(window), int(sinks), _ptr(O), os_, _ptr(lse),
-                                      _ptr(workspace), workspace.numel(), _stream(stream)), "mkv_paged_attention")
+    _check((_lib or load()).mkv_paged_attention(
+        Q.data_ptr(), qs, MkvNewTokens(n, hq, q_start.data_ptr()), max_q, pool, lists, max_len,
+        d ** -0.5 if scale is None else scale, k_scale, v_scale, window, sinks, O.data_ptr(), os_, _at(lse),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)), "mkv_paged_attention")
 
 
 def mkv_device_status(workspace, stream=None) -> int:

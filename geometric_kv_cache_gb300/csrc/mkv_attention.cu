@@ -33,6 +33,7 @@ namespace {
 using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
+constexpr int kJoinWarps = 4;
 constexpr int kFewRows = 64;  // most query rows of a list that this form takes (bf16)
 
 // Shape of one instantiation.
@@ -486,45 +487,87 @@ k_attend(const AttnArgs a)
     }
 }
 
-// One warp per row: the parts of the key axis, in order.
+// One CTA per row: its warps take the parts of the key axis in turn, four
+// loads of a part's row in flight per lane, and meet in shared memory. Always
+// the same order.
 template <int D, int KT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 k_attend_combine(const AttnArgs a)
 {
-    constexpr int E = D / 32;
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t w = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
-    const int64_t lt = w / kRows;
-    const int r = (int)(w - lt * kRows);
+    constexpr int E = D / 32, U = 4;
+    __shared__ float s_o[kJoinWarps][D];
+    __shared__ float2 s_ml[kJoinWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t lt = blockIdx.x / kRows;
+    const int r = (int)(blockIdx.x % kRows);
     const int64_t list = lt / a.tiles;
     Tile t;
-    if (list >= (int64_t)a.batch * a.heads || !make_tile<KT>(a, list, (int)(lt - list * a.tiles), t, false) || r >= t.rows)
-        return;
-    float M = -CUDART_INF_F;
-    for (int s = lane; s < a.splits; s += 32) M = fmaxf(M, a.part_ml[(lt * a.splits + s) * kRows + r].x);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, x));
-    float sum[E], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] = 0.f;
-    for (int s = 0; s < a.splits; ++s) {
-        const int64_t at = (lt * a.splits + s) * kRows + r;
-        const float2 ml = a.part_ml[at];
-        if (ml.x == -CUDART_INF_F) continue;
-        const float f = exp2_approx(ml.x - M);
-        l += f * ml.y;
-        const float *v = a.part_o + at * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] += f * v[e];
-    }
-    const float inv = l > 0.f ? a.v_scale / l : 0.f;
+    if (!make_tile<KT>(a, list, (int)(lt - list * a.tiles), t, false) || r >= t.rows) return;
     const int R = t.row0 + r, i = R / a.group, head = t.j * a.group + R - i * a.group;
     const int64_t token = a.q_start[t.b] + i;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
+    pdl_wait();
+    float sum[E], l = 0.f, M = -CUDART_INF_F;
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[2 * e] * inv, sum[2 * e + 1] * inv);
-    if (lane == 0 && a.lse)
+    for (int e = 0; e < E; ++e) sum[e] = 0.f;
+    for (int s0 = warp; s0 < a.splits; s0 += U * kJoinWarps) {
+        float2 ml[U];
+        float v[U][E];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * kJoinWarps;
+            ml[u] = make_float2(-CUDART_INF_F, 0.f);
+            if (s < a.splits) {
+                const int64_t at = (lt * a.splits + s) * kRows + r;
+                ml[u] = a.part_ml[at];
+                const float *src = a.part_o + at * D + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(&v[u][e]) = *reinterpret_cast<const float2 *>(src + e);
+            }
+        }
+        float best = M;
+#pragma unroll
+        for (int u = 0; u < U; ++u) best = fmaxf(best, ml[u].x);
+        if (best == -CUDART_INF_F) continue;
+        const float f0 = M == -CUDART_INF_F ? 0.f : exp2_approx(M - best);
+        M = best;
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] *= f0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (ml[u].x == -CUDART_INF_F) continue;
+            const float f = exp2_approx(ml[u].x - M);
+            l += f * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[e] += f * v[u][e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = sum[e];
+    if (lane == 0) s_ml[warp] = make_float2(M, l);
+    __syncthreads();
+    M = -CUDART_INF_F;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
+    float f[kJoinWarps];
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        f[w] = s_ml[w].x == -CUDART_INF_F ? 0.f : exp2_approx(s_ml[w].x - M);
+        l += f[w] * s_ml[w].y;
+    }
+    const float inv = l > 0.f ? a.v_scale / l : 0.f;
+    if (threadIdx.x < D / 2) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            x += f[w] * s_o[w][2 * threadIdx.x];
+            y += f[w] * s_o[w][2 * threadIdx.x + 1];
+        }
+        reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D))[threadIdx.x] =
+            pack_bf16(x * inv, y * inv);
+    }
+    if (threadIdx.x == 0 && a.lse)
         a.lse[token * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
 }
 
@@ -538,8 +581,8 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
     k_attend<D, ES><<<(unsigned)(tiles * a.splits), A::THREADS, A::SMEM, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((tiles * kRows + 7) / 8));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)(tiles * kRows));
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

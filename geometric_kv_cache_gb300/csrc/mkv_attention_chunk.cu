@@ -766,14 +766,19 @@ k_chunk_combine(const AttnArgs a, const ChunkInfo *__restrict__ info)
     float sum[E], l = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[e] = 0.f;
+#pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
         const float2 ml = a.part_ml[at(c)];
-        if (ml.x == -CUDART_INF_F) continue;
-        const float f = exp2_approx(ml.x - M);
+        // (a part that saw nothing: its O is zero)
+        const float f = ml.x == -CUDART_INF_F ? 0.f : exp2_approx(ml.x - M);
         l += f * ml.y;
-        const float *v = a.part_o + at(c) * D + lane * E;
+        const float2 *v = reinterpret_cast<const float2 *>(a.part_o + at(c) * D + lane * E);
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] += f * v[e];
+        for (int e = 0; e < E; e += 2) {
+            const float2 x = v[e / 2];
+            sum[e] += f * x.x;
+            sum[e + 1] += f * x.y;
+        }
     }
     const float inv = l > 0.f ? a.v_scale / l : 0.f;
     const int R = t.row0 + row, i = R / a.group, head = t.j * a.group + R - i * a.group;

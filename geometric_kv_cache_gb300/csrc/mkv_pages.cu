@@ -73,6 +73,26 @@ __device__ __forceinline__ long long warp_sum(long long v)
     return v;
 }
 
+// The holders of this thread's pages of a chunk, consecutive ones; -1 past the pool.
+__device__ __forceinline__ void load_refs(const PageArgs &a, int chunk, int (&r)[kPlanPages / kPageThreads])
+{
+    constexpr int N = kPlanPages / kPageThreads;
+    const int64_t p0 = (int64_t)chunk * kPlanPages + threadIdx.x * N;
+    if (p0 + N <= a.n_pages && (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const int4 v = *reinterpret_cast<const int4 *>(a.refs + p0 + i);
+            r[i] = v.x;
+            r[i + 1] = v.y;
+            r[i + 2] = v.z;
+            r[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = p0 + i < a.n_pages ? a.refs[p0 + i] : -1;
+    }
+}
+
 __global__ void __launch_bounds__(kPageThreads)
 k_page_count(const PageArgs a)
 {
@@ -152,11 +172,10 @@ k_page_count(const PageArgs a)
         }
     } else {
         const int chunk = (int)blockIdx.x - a.row_chunks;
-        int n = 0;
-        for (int i = 0; i < kPlanPages / kPageThreads; ++i) {
-            const int64_t p = (int64_t)chunk * kPlanPages + i * kPageThreads + threadIdx.x;
-            if (p < a.n_pages) n += a.refs[p] == 0;
-        }
+        int r[kPlanPages / kPageThreads], n = 0;
+        load_refs(a, chunk, r);
+#pragma unroll
+        for (int i = 0; i < kPlanPages / kPageThreads; ++i) n += r[i] == 0;
         n = __reduce_add_sync(kFull, n);
         if (lane == 0) s_free[warp] = n;
         __syncthreads();
@@ -259,16 +278,31 @@ k_page_assign(const PageArgs a)
             off += __shfl_sync(kFull, x, 31);
         }
     } else {
-        long long rank = before;
-        for (int i = 0; i < kPlanPages / kPageThreads; ++i) {
-            const int64_t p = (int64_t)chunk * kPlanPages + i * kPageThreads + threadIdx.x;
-            const int r = p < a.n_pages ? a.refs[p] : -1;
-            if (a.refs_out != a.refs && p < a.n_pages) a.refs_out[p] = r;
-            uint32_t total;
-            const uint32_t x = block_exclusive_scan<kPageThreads>(r == 0 ? 1u : 0u, scratch, &total);
-            if (r == 0 && !bits && rank + x < need) a.free_ids[rank + x] = (int32_t)p;
-            rank += total;
+        constexpr int N = kPlanPages / kPageThreads;
+        const int64_t p0 = (int64_t)chunk * kPlanPages + threadIdx.x * N;
+        int r[N], n = 0;
+        load_refs(a, chunk, r);
+#pragma unroll
+        for (int i = 0; i < N; ++i) n += r[i] == 0;
+        if (a.refs_out != a.refs) {
+            if (p0 + N <= a.n_pages && (reinterpret_cast<uintptr_t>(a.refs_out) & 15) == 0) {
+#pragma unroll
+                for (int i = 0; i < N; i += 4)
+                    *reinterpret_cast<int4 *>(a.refs_out + p0 + i) = make_int4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (p0 + i < a.n_pages) a.refs_out[p0 + i] = r[i];
+            }
         }
+        if (bits || before >= need) return;  // no page of this chunk is taken
+        long long rank = before + block_exclusive_scan<kPageThreads>((uint32_t)n, scratch, nullptr);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (r[i] == 0) {
+                if (rank < need) a.free_ids[rank] = (int32_t)(p0 + i);
+                ++rank;
+            }
     }
 }
 
@@ -330,10 +364,22 @@ k_page_update(const PageArgs a)
         const int64_t page_bytes = a.row_bytes << a.page_shift, n = rest * a.row_bytes;
         const uint8_t *ks = a.k + s * page_bytes, *vs = a.v + s * page_bytes;
         uint8_t *kd = a.k + d * page_bytes, *vd = a.v + d * page_bytes;
-        for (int64_t o = lane * 16; o < n; o += 512) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(ks + o), y = *reinterpret_cast<const uint4 *>(vs + o);
-            st_v4(kd + o, x);
-            st_v4(vd + o, y);
+        // one round trip for 16 rows of 256 bytes
+        constexpr int U = 8;
+        for (int64_t o = lane * 16; o < n; o += 512 * U) {
+            uint4 x[U], y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (o + 512 * u < n) {
+                    x[u] = ld_stream(ks + o + 512 * u);
+                    y[u] = ld_stream(vs + o + 512 * u);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (o + 512 * u < n) {
+                    st_v4(kd + o + 512 * u, x[u]);
+                    st_v4(vd + o + 512 * u, y[u]);
+                }
         }
     }
 }

@@ -310,7 +310,7 @@ static mkv_status attention_sizes(const mkv_page_pool &pool, const mkv_page_list
     *plan = attention_plan(n, tokens.q_heads / lists.heads, max_q, max_len, pool.head_dim,
                            elem_bytes(pool.dtype), kPlanSms);
     // CTAs of the two launches, 32-bit grids
-    if ((!plan->chunked && n * plan->tiles * plan->splits > (int64_t)INT32_MAX) || n * plan->tiles * 2 > (int64_t)INT32_MAX)
+    if ((!plan->chunked && n * plan->tiles * plan->splits > (int64_t)INT32_MAX) || n * plan->tiles * 16 > (int64_t)INT32_MAX)
         return MKV_ERR_UNSUPPORTED;
     return MKV_OK;
 }
