@@ -742,7 +742,10 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 
 // Joins the parts of the tiles that were cut: blockIdx.y is the CTA whose last
 // segment begins a tile; the tile's other parts are the first segments of the
-// CTAs after it, up to the one that ends the tile. One warp per row.
+// CTAs after it, up to the one that ends the tile. A warp takes kJoin rows at
+// a time, their loads in flight together.
+constexpr int kJoin = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256)
 k_chunk_combine(const AttnArgs a, const ChunkInfo *__restrict__ info)
@@ -750,44 +753,72 @@ k_chunk_combine(const AttnArgs a, const ChunkInfo *__restrict__ info)
     using C = Chunk<D>;
     constexpr int E = D / 32;
     pdl_wait();
-    const int c0 = (int)blockIdx.y, lane = threadIdx.x & 31;
+    const int c0 = (int)blockIdx.y, lane = threadIdx.x & 31, ctas = (int)gridDim.y;
+    // this CTA's entry and, in the same round trip, those of the 32 after it
     const int tile = info[c0].open_tile;
+    int ends = c0 + 1 + lane < ctas ? info[c0 + 1 + lane].ends : 1;
     if (tile < 0) return;
     const Tile t = make_tile(a, tile, C::ROWS, false);
-    const int row = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= t.rows) return;
     int c1 = c0 + 1;  // the last CTA of the tile
-    while (c1 + 1 < (int)gridDim.y && !info[c1].ends) ++c1;
-    auto at = [&](int c) -> int64_t { return ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * C::ROWS + row; };
-    float M = -CUDART_INF_F;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.part_ml[at(c)].x);
+    for (;;) {
+        const unsigned hit = __ballot_sync(kFull, ends != 0);
+        if (hit) {
+            c1 += __ffs(hit) - 1;
+            break;
+        }
+        c1 += 32;
+        ends = c1 + lane < ctas ? info[c1 + lane].ends : 1;
+    }
+    c1 = min(c1, ctas - 1);
+    const int row0 = ((int)blockIdx.x * 8 + (threadIdx.x >> 5)) * kJoin;
+    if (row0 >= t.rows) return;
+    float sum[kJoin][E], l[kJoin], M[kJoin];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float sum[E], l = 0.f;
+    for (int u = 0; u < kJoin; ++u) {
+        l[u] = 0.f;
+        M[u] = -CUDART_INF_F;
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] = 0.f;
-#pragma unroll 4
+        for (int e = 0; e < E; ++e) sum[u][e] = 0.f;
+    }
     for (int c = c0; c <= c1; ++c) {
-        const float2 ml = a.part_ml[at(c)];
-        // (a part that saw nothing: its O is zero)
-        const float f = ml.x == -CUDART_INF_F ? 0.f : exp2_approx(ml.x - M);
-        l += f * ml.y;
-        const float2 *v = reinterpret_cast<const float2 *>(a.part_o + at(c) * D + lane * E);
+        const int64_t at = ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * C::ROWS + row0;
+        float2 ml[kJoin], v[kJoin][E / 2];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 x = v[e / 2];
-            sum[e] += f * x.x;
-            sum[e + 1] += f * x.y;
+        for (int u = 0; u < kJoin; ++u) {
+            ml[u] = make_float2(-CUDART_INF_F, 0.f);
+            if (row0 + u < t.rows) {
+                ml[u] = a.part_ml[at + u];
+                const float2 *src = reinterpret_cast<const float2 *>(a.part_o + (at + u) * D + lane * E);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) v[u][e] = src[e];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kJoin; ++u) {
+            if (ml[u].x == -CUDART_INF_F) continue;  // saw nothing
+            const float best = fmaxf(M[u], ml[u].x);
+            const float f0 = M[u] == -CUDART_INF_F ? 0.f : exp2_approx(M[u] - best), f1 = exp2_approx(ml[u].x - best);
+            M[u] = best;
+            l[u] = l[u] * f0 + f1 * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                sum[u][2 * e] = sum[u][2 * e] * f0 + f1 * v[u][e].x;
+                sum[u][2 * e + 1] = sum[u][2 * e + 1] * f0 + f1 * v[u][e].y;
+            }
         }
     }
-    const float inv = l > 0.f ? a.v_scale / l : 0.f;
-    const int R = t.row0 + row, i = R / a.group, head = t.j * a.group + R - i * a.group;
-    const int64_t token = (int64_t)a.q_start[t.b] + i;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[2 * e] * inv, sum[2 * e + 1] * inv);
-    if (lane == 0 && a.lse)
-        a.lse[token * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+    for (int u = 0; u < kJoin; ++u) {
+        if (row0 + u >= t.rows) break;
+        const float inv = l[u] > 0.f ? a.v_scale / l[u] : 0.f;
+        const int R = t.row0 + row0 + u, i = R / a.group, head = t.j * a.group + R - i * a.group;
+        const int64_t token = (int64_t)a.q_start[t.b] + i;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[u][2 * e] * inv, sum[u][2 * e + 1] * inv);
+        if (lane == 0 && a.lse)
+            a.lse[token * a.q_heads + head] = l[u] > 0.f ? (M[u] + log2f(l[u])) * CUDART_LN2_F : -CUDART_INF_F;
+    }
 }
 
 // --------------------------------------------------------------- host side --
@@ -832,7 +863,7 @@ cudaError_t launch_one(const AttnArgs &a, int ctas, cudaStream_t st)
     k_attend_chunk<D><<<ctas, kThreads, C::SMEM, st>>>(mk, mv, a, info);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(C::ROWS / 8), (unsigned)ctas);
+    cfg.gridDim = dim3((unsigned)(C::ROWS / (8 * kJoin)), (unsigned)ctas);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

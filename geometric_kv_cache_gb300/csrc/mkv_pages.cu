@@ -32,7 +32,7 @@ namespace {
 using namespace dev;
 
 constexpr int kPageThreads = 256;
-constexpr int kCopyRows = 64;  // output tokens per item of the compaction
+constexpr int kCopyRows = 32;  // output tokens per item of the compaction: one per lane
 
 __device__ __forceinline__ int pages_of(int len, const PageArgs &a)
 {
@@ -118,8 +118,15 @@ k_page_count(const PageArgs a)
                 // the parent itself if it goes on, else its lowest child
                 if (src >= 0 && src != b) {
                     keeps = a.parent[src] != src;
-                    for (int64_t i = 0; keeps && i < b; i += 32)
-                        keeps = !__any_sync(kFull, i + lane < b && a.parent[i + lane] == src);
+                    for (int64_t i = 0; keeps && i < b; i += 256) {
+                        bool hit = false;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const int64_t x = i + 32 * u + lane;
+                            hit |= x < b && a.parent[x] == src;
+                        }
+                        keeps = !__any_sync(kFull, hit);
+                    }
                 }
             }
             if (lane == 0) a.row_src[b] = make_int2(src, keeps ? 1 : 0);
@@ -326,19 +333,21 @@ k_page_update(const PageArgs a)
     const bool in_place = a.table_out == a.table;
     const int32_t *mine = a.table + h * a.max_pages;
     int32_t *out = a.table_out + h * a.max_pages;
+    // (read together; the last two mean nothing after a bad verdict)
     const int own_len = a.lens[h];
-    if (*a.verdict) {  // the lists stay as they were
+    const uint32_t verdict = *a.verdict;
+    const int2 src = a.row_src[b];
+    const int first = a.list_off[h];
+    if (verdict) {  // the lists stay as they were
         if (in_place) return;
         if (lane == 0) a.lens_out[h] = own_len;
         if (len_ok(own_len, a))
             for (int p = lane; p < pages_of(own_len, a); p += 32) out[p] = mine[p];
         return;
     }
-    const int2 src = a.row_src[b];
     const bool keeps = src.y != 0, moved = src.x != b;
     const ListPlan lp = plan_list(a, b, j, src.x, keeps);
     const int32_t *from = a.table + ((int64_t)(src.x < 0 ? b : src.x) * a.heads + j) * a.max_pages;
-    const int first = a.list_off[h];
     __syncwarp();
     if (!in_place)
         for (int p = lane; p < lp.shared; p += 32) {
@@ -384,83 +393,110 @@ k_page_update(const PageArgs a)
     }
 }
 
-// Item = (list, block of 64 output tokens); groups of LPR lanes (16 bytes
-// each) copy rows. The list's first item also writes its table and counts.
+// The first `list_ctas` CTAs write tables and counts, list by list; the warps
+// of the others copy rows. Item = (list, block of 32 output tokens), one warp,
+// one lane per token for its places: an item's indices are read two items
+// ahead and its page entries one ahead, so that every row copy (groups of LPR
+// lanes, 16 bytes each, 8 rows of K and of V in flight per lane) finds its
+// addresses in registers.
 template <int LPR>
-__global__ void __launch_bounds__(kPageThreads)
-k_page_compact(const PageArgs a, int blocks, int64_t n_items)
+__global__ void __launch_bounds__(kPageThreads, 2)
+k_page_compact(const PageArgs a, int blocks, int64_t n_items, int list_ctas)
 {
-    constexpr int RB = LPR * 16, SLOTS = kPageThreads / LPR, R = kCopyRows / SLOTS;
+    constexpr int RB = LPR * 16, RPS = 32 / LPR, B = LPR < 8 ? LPR : 8;  // rows per step, steps per batch
     pdl_wait();
     const bool bad = *a.verdict != 0;
-    const int g = threadIdx.x / LPR, lr = threadIdx.x % LPR;
-    for (int64_t item = blockIdx.x; item < n_items; item += gridDim.x) {
-        const int64_t h = item / blocks;
-        const int i0 = (int)(item - h * blocks) * kCopyRows;
-        const int own_len = a.lens[h];
-        const int32_t *mine = a.table + h * a.max_pages;
-        int32_t *out = a.table_out + h * a.max_pages;
-        if (bad) {
-            if (i0 == 0) {
-                if (threadIdx.x == 0) a.lens_out[h] = own_len;
-                if (len_ok(own_len, a))
-                    for (int p = threadIdx.x; p < pages_of(own_len, a); p += kPageThreads) out[p] = mine[p];
-            }
-            continue;
-        }
-        const int n = a.kept[h], first = a.list_off[h];
-        if (i0 == 0) {
-            if (threadIdx.x == 0) a.lens_out[h] = n;
+    if ((int)blockIdx.x < list_ctas) {
+        for (int64_t h = blockIdx.x; h < (int64_t)a.batch * a.heads; h += list_ctas) {
+            const int own_len = a.lens[h], n = bad ? 0 : a.kept[h], first = bad ? 0 : a.list_off[h];
+            const int32_t *mine = a.table + h * a.max_pages;
+            int32_t *out = a.table_out + h * a.max_pages;
+            if (threadIdx.x == 0) a.lens_out[h] = bad ? own_len : n;
+            if (bad && !len_ok(own_len, a)) continue;
             for (int p = threadIdx.x; p < pages_of(n, a); p += kPageThreads) {
                 const int id = a.free_ids[first + p];
                 out[p] = id;
                 atomicAdd(a.refs_out + id, 1);
             }
-            for (int p = threadIdx.x; p < pages_of(own_len, a); p += kPageThreads) add_ref(a, mine[p], -1);
+            for (int p = threadIdx.x; p < pages_of(own_len, a); p += kPageThreads) {
+                if (bad) out[p] = mine[p];  // the lists stay as they were
+                else add_ref(a, mine[p], -1);
+            }
         }
-        const int m = min(kCopyRows, n - i0);
-        if (m <= 0) continue;
-        const int T = !a.K ? own_len : a.seq_lens ? a.seq_lens[h / a.heads] : a.t_max;
-        const uint8_t *ks = a.K ? a.K + (size_t)h * a.t_max * RB : a.k;
-        const uint8_t *vs = a.K ? a.V + (size_t)h * a.t_max * RB : a.v;
-        uint4 kr[R], vr[R];
-        int64_t dst[R];
-        int64_t from[R];
+        return;
+    }
+    if (bad) return;
+    const int lane = threadIdx.x & 31, g = lane / LPR, lr = lane % LPR;
+    const int64_t warps = (int64_t)(gridDim.x - list_ctas) * (kPageThreads / 32);
+    const int64_t item0 = (int64_t)(blockIdx.x - list_ctas) * (kPageThreads / 32) + (threadIdx.x >> 5);
+    // this lane's token of an item: its source token (-1: none)
+    auto source = [&](int64_t item) -> int {
+        if (item >= n_items) return -1;
+        const int64_t h = item / blocks;
+        const int i = (int)(item - h * blocks) * 32 + lane;
+        if (i >= a.kept[h]) return -1;
+        const int s = a.idx ? a.idx[h * a.idx_stride + i] : i;
+        const int T = !a.K ? a.lens[h] : a.seq_lens ? a.seq_lens[h / a.heads] : a.t_max;
+        if (s < 0 || s >= T) {
+            atomicOr(a.status, MKV_DEV_BAD_INDEX);
+            return -1;
+        }
+        return s;
+    };
+    // the rows of the pool (or the contiguous cache) it is copied from and to
+    auto places = [&](int64_t item, int s, int64_t &from, int &to) {
+        from = to = -1;
+        if (s < 0) return;
+        const int64_t h = item / blocks;
+        const int i = (int)(item - h * blocks) * 32 + lane;
+        if (a.K) {
+            from = h * a.t_max + s;
+        } else {
+            const int id = a.table[h * a.max_pages + (s >> a.page_shift)];
+            if ((uint32_t)id >= (uint32_t)a.n_pages) {
+                atomicOr(a.status, MKV_DEV_BAD_PAGE);
+                return;
+            }
+            from = (id << a.page_shift) + (s & (a.page_size - 1));
+        }
+        to = (a.free_ids[a.list_off[h] + (i >> a.page_shift)] << a.page_shift) + (i & (a.page_size - 1));
+    };
+    const uint8_t *ks = (a.K ? a.K : a.k) + lr * 16, *vs = (a.K ? a.V : a.v) + lr * 16;
+    uint8_t *kd = a.k + lr * 16, *vd = a.v + lr * 16;
+    int64_t from;
+    int to, ahead = source(item0);
+    places(item0, ahead, from, to);
+    ahead = source(item0 + warps);
+    for (int64_t item = item0; item < n_items; item += warps) {
+        int64_t next_from;
+        int next_to;
+        places(item + warps, ahead, next_from, next_to);
+        ahead = source(item + 2 * warps);
+        if (__any_sync(kFull, to >= 0)) {
 #pragma unroll
-        for (int u = 0; u < R; ++u) {
-            const int i = i0 + u * SLOTS + g;
-            dst[u] = from[u] = -1;
-            if (u * SLOTS + g < m) {
-                const int s = a.idx ? a.idx[h * a.idx_stride + i] : i;
-                if (s < 0 || s >= T) {
-                    atomicOr(a.status, MKV_DEV_BAD_INDEX);
-                    continue;
-                }
-                from[u] = s;
-                if (!a.K) {
-                    const int id = mine[s >> a.page_shift];
-                    if ((uint32_t)id >= (uint32_t)a.n_pages) {
-                        atomicOr(a.status, MKV_DEV_BAD_PAGE);
-                        from[u] = -1;
-                        continue;
+            for (int b0 = 0; b0 < LPR; b0 += B) {
+                uint4 kr[B], vr[B];
+                int dst[B];
+#pragma unroll
+                for (int u = 0; u < B; ++u) {
+                    const int row = (b0 + u) * RPS + g;
+                    const int64_t src = __shfl_sync(kFull, from, row);
+                    dst[u] = __shfl_sync(kFull, to, row);
+                    if (dst[u] >= 0) {
+                        kr[u] = ld_stream(ks + src * RB);
+                        vr[u] = ld_stream(vs + src * RB);
                     }
-                    from[u] = ((int64_t)id << a.page_shift) + (s & (a.page_size - 1));
                 }
-                dst[u] = ((int64_t)a.free_ids[first + (i >> a.page_shift)] << a.page_shift) + (i & (a.page_size - 1));
+#pragma unroll
+                for (int u = 0; u < B; ++u)
+                    if (dst[u] >= 0) {
+                        st_v4(kd + (int64_t)dst[u] * RB, kr[u]);
+                        st_v4(vd + (int64_t)dst[u] * RB, vr[u]);
+                    }
             }
         }
-#pragma unroll
-        for (int u = 0; u < R; ++u)
-            if (from[u] >= 0) {
-                kr[u] = ld_stream(ks + from[u] * RB + lr * 16);
-                vr[u] = ld_stream(vs + from[u] * RB + lr * 16);
-            }
-#pragma unroll
-        for (int u = 0; u < R; ++u)
-            if (from[u] >= 0) {
-                st_v4(a.k + dst[u] * RB + lr * 16, kr[u]);
-                st_v4(a.v + dst[u] * RB + lr * 16, vr[u]);
-            }
+        from = next_from;
+        to = next_to;
     }
 }
 
@@ -509,8 +545,10 @@ cudaError_t launch_page_call(const PageArgs &pa, cudaStream_t st)
                                : std::min((int64_t)(a.K ? a.t_max : INT32_MAX), (int64_t)a.max_pages << a.page_shift);
     int blocks = (int)std::max<int64_t>(1, (most + kCopyRows - 1) / kCopyRows);
     int64_t items = lists * blocks;
-    void *cargs[] = {&a, &blocks, &items};
-    return launch_dependent(fn, grid_for_items(fn, kPageThreads, 0, items), cargs, st);
+    int list_ctas = (int)std::min<int64_t>(lists, 152);
+    const int64_t copy_ctas = grid_for_items(fn, kPageThreads, 0, (items + kPageThreads / 32 - 1) / (kPageThreads / 32));
+    void *cargs[] = {&a, &blocks, &items, &list_ctas};
+    return launch_dependent(fn, list_ctas + copy_ctas, cargs, st);
 }
 
 }  // namespace mkv
