@@ -120,20 +120,19 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Bytes s.x and s.y of v (a __byte_perm selector that puts them in the upper
-// byte of each half) as two bf16: an E4M3 code's sign to the sign, its
-// exponent and mantissa fields to the lowest exponent bits and highest
-// mantissa bits, which is the value times 2^-120 (subnormal codes too), then
-// times 2^120: exact.
-__device__ __forceinline__ uint32_t e4m3_to_bf16x2(uint32_t v, uint32_t sel)
+// Next to E4M3 keys the queries run as fp16, which takes one conversion per two
+// codes where bf16 would take five instructions: a row of queries is scaled by
+// the power of two that brings its largest magnitude into [1, 2). Elements
+// from 2^-14 of that on keep all their bits; smaller ones are off by at most
+// 2^-25 of the largest. E: the biased exponent of the largest magnitude.
+__device__ __forceinline__ int row_exponent(float largest)
 {
-    const uint32_t w = __byte_perm(v, 0u, sel);
-    const uint32_t r = (w & 0x80008000u) | ((w >> 4) & 0x07F007F0u);
-    const uint32_t up = 0x7B807B80u;  // 2^120, twice
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&r),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&up));
-    return *reinterpret_cast<const uint32_t *>(&y);
+    return min(max((int)(__float_as_uint(largest) >> 23), 1), 253);
 }
+__device__ __forceinline__ float down_by(int E) { return __uint_as_float((uint32_t)(254 - E) << 23); }  // 2^(127 - E)
+__device__ __forceinline__ float up_by(int E) { return __uint_as_float((uint32_t)E << 23); }            // 2^(E - 127)
+__device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
 // Where 16-byte chunk c of row r of a block lies: rows of CPR chunks, chunks
 // exchanged so that the eight rows (ldmatrix) or the two rows (16-byte loads
@@ -201,6 +200,7 @@ k_attend(const AttnArgs a)
     constexpr bool Q_REGS = D <= 128;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) uint8_t s_q[Q_REGS ? 16 : kRows * D * 2];
+    __shared__ float s_up[kRows];
     __shared__ float2 s_ml[A::WARPS][kRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
     // the parts of a tile lie next to each other, tiles of a list too
@@ -229,6 +229,7 @@ k_attend(const AttnArgs a)
         return ES == 2 ? k * 16 + 2 * tq + 8 * hi : (k / 4) * 64 + 16 * tq + (k % 4) * 4 + 2 * hi;
     };
     uint32_t q[Q_REGS ? KS : 1][4];
+    float sc0 = a.scale_log2, sc1 = a.scale_log2;  // of this lane's two rows of scores
     if constexpr (Q_REGS) {
         const uint8_t *q0 = q_row(gr), *q1 = q_row(gr + 8);
 #pragma unroll
@@ -238,10 +239,52 @@ k_attend(const AttnArgs a)
                 q[k][2 * hi] = *reinterpret_cast<const uint32_t *>(q0 + 2 * q_dim(k, hi));
                 q[k][2 * hi + 1] = *reinterpret_cast<const uint32_t *>(q1 + 2 * q_dim(k, hi));
             }
+        if constexpr (ES == 1) {
+            float m[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    m[e & 1] = fmaxf(m[e & 1], fmaxf(fabsf(lo_bf16(q[k][e])), fabsf(hi_bf16(q[k][e]))));
+            int E[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                m[r] = fmaxf(m[r], __shfl_xor_sync(kFull, m[r], 1));
+                m[r] = fmaxf(m[r], __shfl_xor_sync(kFull, m[r], 2));
+                E[r] = row_exponent(m[r]);
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    q[k][e] = pack_f16(lo_bf16(q[k][e]) * down_by(E[e & 1]), hi_bf16(q[k][e]) * down_by(E[e & 1]));
+            sc0 *= up_by(E[0]);
+            sc1 *= up_by(E[1]);
+        }
     } else {
-        for (int o = threadIdx.x; o < kRows * D / 8; o += A::THREADS)
-            reinterpret_cast<uint4 *>(s_q)[o] = *reinterpret_cast<const uint4 *>(q_row(o / (D / 8)) + 16 * (o % (D / 8)));
+        static_assert(D == 256 || Q_REGS, "a lane's 8 dims make one row per warp");
+        for (int r = warp; r < kRows; r += A::WARPS) {
+            uint4 v = reinterpret_cast<const uint4 *>(q_row(r))[lane];
+            if constexpr (ES == 1) {
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                float m = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(lo_bf16(w[e])), fabsf(hi_bf16(w[e]))));
+#pragma unroll
+                for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+                const int E = row_exponent(m);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack_f16(lo_bf16(w[e]) * down_by(E), hi_bf16(w[e]) * down_by(E));
+                v = make_uint4(w[0], w[1], w[2], w[3]);
+                if (lane == 0) s_up[r] = up_by(E);
+            }
+            reinterpret_cast<uint4 *>(s_q)[r * (D / 8) + lane] = v;
+        }
         __syncthreads();
+        if constexpr (ES == 1) {
+            sc0 *= s_up[gr];
+            sc1 *= s_up[gr + 8];
+        }
     }
     const int p0 = t.L - t.n + (t.row0 + min(gr, t.rows - 1)) / a.group;
     const int p1 = t.L - t.n + (t.row0 + min(gr + 8, t.rows - 1)) / a.group;
@@ -339,7 +382,7 @@ k_attend(const AttnArgs a)
                     for (int e = 0; e < 4; ++e) {
                         uint32_t f[4];
                         q_frag(4 * k4 + e, f);
-                        mma_bf16(s[i], f, e4m3_to_bf16x2(ws[e], 0x1404), e4m3_to_bf16x2(ws[e], 0x3424));
+                        mma_f16(s[i], f, e4m3x2_to_f16x2(ws[e] & 0xFFFFu), e4m3x2_to_f16x2(ws[e] >> 16));
                     }
                 }
             }
@@ -353,7 +396,7 @@ k_attend(const AttnArgs a)
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float x = s[i][e] * a.scale_log2;
+                float x = s[i][e] * (e < 2 ? sc0 : sc1);
                 if (!whole) {
                     const int key = k0 + i * 8 + 2 * tq + (e & 1), p = e < 2 ? p0 : p1;
                     const bool seen = key <= p && (a.window <= 0 || key > p - a.window || key < a.sinks);
@@ -417,11 +460,10 @@ k_attend(const AttnArgs a)
                     ldsm4_t(vb + at_rows8<A::CPR>(kk * 16 + (lane & 15), 2 * c + (lane >> 4)), b);
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const uint32_t v0 = b[2 * hf], v1 = b[2 * hf + 1];
-                        mma_f16(o[4 * c + 2 * hf], f, e4m3x2_to_f16x2(__byte_perm(v0, 0, 0x0020)),
-                                e4m3x2_to_f16x2(__byte_perm(v1, 0, 0x0020)));
-                        mma_f16(o[4 * c + 2 * hf + 1], f, e4m3x2_to_f16x2(__byte_perm(v0, 0, 0x0031)),
-                                e4m3x2_to_f16x2(__byte_perm(v1, 0, 0x0031)));
+                        // (key, dim) bytes 00 01 10 11 to 00 10 | 01 11: the two dims' key pairs
+                        const uint32_t v0 = __byte_perm(b[2 * hf], 0, 0x3120), v1 = __byte_perm(b[2 * hf + 1], 0, 0x3120);
+                        mma_f16(o[4 * c + 2 * hf], f, e4m3x2_to_f16x2(v0 & 0xFFFFu), e4m3x2_to_f16x2(v1 & 0xFFFFu));
+                        mma_f16(o[4 * c + 2 * hf + 1], f, e4m3x2_to_f16x2(v0 >> 16), e4m3x2_to_f16x2(v1 >> 16));
                     }
                 }
             }

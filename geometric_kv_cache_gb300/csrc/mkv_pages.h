@@ -52,7 +52,7 @@ struct RopeArgs {
     const float *inv_freq;
     uint8_t *k, *v;
     int32_t n_tokens, q_heads, batch, heads, max_pages, n_pages, page_size, page_shift, head_dim, es, rot_dim, layout;
-    float factor, k_scale, v_scale;
+    float factor, k_inv, v_inv;  // (E4M3 pools: the scales' reciprocals)
     uint32_t *status;
 };
 cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t st);

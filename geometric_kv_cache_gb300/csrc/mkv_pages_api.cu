@@ -225,7 +225,8 @@ mkv_status mkv_rope_append(const void *Q, int64_t q_stride, const void *K, int64
     const int d = pool.head_dim, es = elem_bytes(pool.dtype);
     if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return MKV_ERR_INVALID_ARG;
     if (layout != MKV_ROPE_HALF && layout != MKV_ROPE_INTERLEAVED) return MKV_ERR_INVALID_ARG;
-    if (!isfinite(factor) || !isfinite(k_scale) || !isfinite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f))
+    if (!isfinite(factor) || !isfinite(k_scale) || !isfinite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f) ||
+        !isfinite(1.f / k_scale) || !isfinite(1.f / v_scale))
         return MKV_ERR_INVALID_ARG;
     if (es == 2 && (k_scale != 1.f || v_scale != 1.f)) return MKV_ERR_INVALID_ARG;
     const bool none = tokens.n_tokens == 0 || no_lists(lists);
@@ -267,8 +268,8 @@ mkv_status mkv_rope_append(const void *Q, int64_t q_stride, const void *K, int64
     a.rot_dim = rot_dim;
     a.layout = layout;
     a.factor = factor;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
+    a.k_inv = 1.f / k_scale;
+    a.v_inv = 1.f / v_scale;
     a.status = region<uint32_t>(workspace, 0);
     return cuda_status(launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }

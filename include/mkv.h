@@ -616,8 +616,9 @@ typedef enum {
  * [n_tokens], 0 and up. inv_freq: device fp32 [rot_dim / 2] (mkv_rope_frequencies).
  * rot_dim: a multiple of 16 in [16, head_dim]. Q_out: bf16 [n_tokens, q_heads,
  * head_dim], contiguous; may be Q itself when Q is contiguous. E4M3 pools
- * store round(value / k_scale) (keys) and round(value / v_scale) (values),
- * saturated at 448; for bf16 pools the scales must be 1. A token whose list
+ * store round(value * (1 / k_scale)) (keys) and round(value * (1 / v_scale))
+ * (values), saturated at 448, the reciprocals in fp32 (they must be finite);
+ * for bf16 pools the scales must be 1. A token whose list
  * or page is invalid is not written (MKV_DEV_BAD_SEQ_LEN when the list is
  * shorter than the row's new tokens or longer than its capacity,
  * MKV_DEV_BAD_PAGE, MKV_DEV_BAD_TOKENS); its query is written all the same. */

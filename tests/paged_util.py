@@ -97,7 +97,10 @@ def attention_bounds(O, lse, A, W, E, d, dtype):
     truncation of aligned addends; scaling to log2 units and the differences to the maximum round four times more on
     numbers up to 2 E log2(e); 2^x is off by 2^-22 relative and the running factors multiply it a few times over. So a
     weight is off by eps = 2 d 2^-24 E + 16 2^-24 E + 2^-18 relative, and so is the sum l. A weight is then rounded to 16
-    bits: half a step, 2^-8 (bf16) or 2^-11 (fp16, next to E4M3 values; below 2^-14 half a step is 2^-25 absolute). The
+    bits: half a step, 2^-8 (bf16) or 2^-11 (fp16, next to E4M3 values; below 2^-14 half a step is 2^-25 absolute).
+    (Queries next to E4M3 keys run as fp16 scaled to a largest element of 1 to 2: an element is off by at most 2^-25 of the
+    largest, a score by 2^-25 max|q| sum|scale k|, which for the normal queries here, max|q| < 10 mean|q|, is below a
+    twentieth of the 2 d 2^-24 E.) The
     sum's fp32 error adds at most (keys / 8) 2^-24, inside the 2^-18 for the sizes here. The output is rounded to bf16:
     2^-8 relative to what is rounded."""
     eps = (2 * d + 16) * 2.0 ** -24 * E + 2.0 ** -18
