@@ -10,12 +10,14 @@
 // kept as running values over blocks of keys (m, l and O in fp32; a new maximum
 // multiplies l and O by 2^(m_old - m_new)).
 //
-// Item = (list, tile of 16 rows, part of the key axis), one CTA each. Every
-// warp of the CTA walks its own blocks of KT keys with its own ring of
-// cp.async stages (16 bytes per lane, the block's page entries read one block
-// ahead), so the loop has no CTA barrier; scores and values run on mma.sync
-// m16n8k16 with the 16 rows as M. The warps' (m, l, O) meet in shared memory at
-// the end, the parts of the key axis in k_attend_combine, in part order.
+// This file: the form for few rows, whose bound is the bytes of K and V. A
+// tile is 16 rows (the M of mma.sync m16n8k16; a decode step of a group of 4
+// fills 4), a block WARPS x KT keys, KT for each warp of the CTA. Every warp
+// has its own ring of cp.async stages (16 bytes per lane, the block's page
+// entries read one block ahead), so the walk over a tile has no CTA barrier;
+// the warps' (m, l, O) meet in shared memory at its end. The line of blocks is
+// cut over 152 CTAs (mkv_attention.cuh); k_attend_combine joins the parts of
+// cut tiles. mkv_attention_chunk.cu is the form for many rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -24,6 +26,7 @@
 
 #include <algorithm>
 
+#include "mkv_attention.cuh"
 #include "mkv_device.cuh"
 #include "mkv_pages.h"
 
@@ -42,6 +45,7 @@ struct Attend {
     static constexpr int KT = D == 256 ? 16 : 32;      // keys per block
     static constexpr int WARPS = ES == 1 ? 8 : 4;
     static constexpr int THREADS = WARPS * 32;
+    static constexpr int KEYS = WARPS * KT;            // keys per block of the CTA
     static constexpr int RB = D * ES;                  // bytes per cached row
     static constexpr int CPR = RB / 16;                // 16-byte chunks per row
     static constexpr int HALF = KT * RB;               // bytes of a block's keys
@@ -148,52 +152,9 @@ __device__ __forceinline__ uint32_t at_rows2(int r, int c)
     return (uint32_t)(r * CPR + (c ^ (CPR >= 8 ? (r & 1) << 2 : 0))) * 16u;
 }
 
-// What one tile of rows of one list is.
-struct Tile {
-    int b, j, n, L, row0, rows;  // batch row, head, new tokens, list length, first packed row, rows
-    int p_lo, p_hi;              // places of the first and last row's token
-    int end;                     // keys from here on are visible to no row
-    int sink_blocks, win_block;  // blocks of keys: [0, sink_blocks) and [win_block, ...)
-    int blocks;                  // in all
-};
-
-template <int KT>
-__device__ __forceinline__ bool make_tile(const AttnArgs &a, int64_t list, int tile, Tile &t, bool report)
-{
-    t.b = (int)(list / a.heads);
-    t.j = (int)(list - (int64_t)t.b * a.heads);
-    const int lo = a.q_start[t.b], hi = a.q_start[t.b + 1];
-    t.n = hi - lo;
-    t.L = a.lens[list];
-    if (lo < 0 || hi < lo || hi > a.n_tokens || t.n > a.max_q) {
-        if (report) atomicOr(a.status, MKV_DEV_BAD_TOKENS);
-        return false;
-    }
-    if (t.L < 0 || t.L > a.max_len) {
-        if (report) atomicOr(a.status, MKV_DEV_BAD_SEQ_LEN);
-        return false;
-    }
-    t.row0 = tile * kRows;
-    t.rows = min(kRows, t.n * a.group - t.row0);
-    if (t.rows <= 0) return false;
-    t.p_lo = t.L - t.n + t.row0 / a.group;
-    t.p_hi = t.L - t.n + (t.row0 + t.rows - 1) / a.group;
-    t.end = max(0, t.p_hi + 1);
-    const int all = (t.end + KT - 1) / KT;
-    t.win_block = t.sink_blocks = 0;
-    if (a.window > 0) {
-        const int start = max(0, t.p_lo - a.window + 1);  // the first key inside any row's window
-        const int sinks = (min(a.sinks, t.end) + KT - 1) / KT;
-        t.win_block = min(start / KT, all);
-        t.sink_blocks = min(sinks, t.win_block);
-    }
-    t.blocks = t.sink_blocks + all - t.win_block;
-    return true;
-}
-
 template <int D, int ES>
 __global__ void __launch_bounds__(Attend<D, ES>::THREADS, 1)
-k_attend(const AttnArgs a)
+k_attend(const AttnArgs a, LineInfo *info)
 {
     using A = Attend<D, ES>;
     constexpr int KT = A::KT, NT = KT / 8, KS = D / 16;  // key tiles of 8, dim steps of 16
@@ -201,365 +162,368 @@ k_attend(const AttnArgs a)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) uint8_t s_q[Q_REGS ? 16 : kRows * D * 2];
     __shared__ float s_up[kRows];
+    __shared__ LineScratch s_line;
     __shared__ float2 s_ml[A::WARPS][kRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
-    // the parts of a tile lie next to each other, tiles of a list too
-    const int64_t item = blockIdx.x;
-    const int split = (int)(item % a.splits);
-    const int64_t lt = item / a.splits;
-    const int64_t list = lt / a.tiles;
-    const int tile = (int)(lt - list * a.tiles);
-    Tile t;
     pdl_trigger();
-    if (!make_tile<KT>(a, list, tile, t, split == 0 && tile == 0 && threadIdx.x == 0)) return;
-    const int first = (int)((int64_t)t.blocks * split / a.splits), last = (int)((int64_t)t.blocks * (split + 1) / a.splits);
-    const int32_t *table = a.table + list * a.max_pages;
-    const int page_mask = a.page_size - 1;
+    Walk w = cut_line<A::KEYS, A::THREADS>(a, kRows, 1, s_line);
+    LineInfo ci = {-1, 0};
+    while (w.next<A::KEYS>(a, kRows)) {
+        const Tile &t = w.t;
+        const int first = w.from(), last = w.to();
+        const int64_t list = (int64_t)t.b * a.heads + t.j;
+        note_segment(w, ci);
+        const int32_t *table = a.table + list * a.max_pages;
+        const int page_mask = a.page_size - 1;
 
-    // the two rows of this lane: packed row -> (new token, query head)
-    const int qrow0 = a.q_start[t.b];
-    auto q_row = [&](int r) -> const uint8_t * {
-        const int R = t.row0 + min(r, t.rows - 1);
-        const int i = R / a.group, g = R - i * a.group;
-        return a.Q + 2 * ((int64_t)(qrow0 + i) * a.q_stride + (int64_t)(t.j * a.group + g) * D);
-    };
-    // dims of an A fragment: pairs (2t, 2t + 1) and (2t + 8, 2t + 9) of a step,
-    // for E4M3 keys the dims that the lane's 16-byte load holds
-    auto q_dim = [&](int k, int hi) -> int {
-        return ES == 2 ? k * 16 + 2 * tq + 8 * hi : (k / 4) * 64 + 16 * tq + (k % 4) * 4 + 2 * hi;
-    };
-    uint32_t q[Q_REGS ? KS : 1][4];
-    float sc0 = a.scale_log2, sc1 = a.scale_log2;  // of this lane's two rows of scores
-    if constexpr (Q_REGS) {
-        const uint8_t *q0 = q_row(gr), *q1 = q_row(gr + 8);
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int hi = 0; hi < 2; ++hi) {
-                q[k][2 * hi] = *reinterpret_cast<const uint32_t *>(q0 + 2 * q_dim(k, hi));
-                q[k][2 * hi + 1] = *reinterpret_cast<const uint32_t *>(q1 + 2 * q_dim(k, hi));
-            }
-        if constexpr (ES == 1) {
-            float m[2] = {0.f, 0.f};
+        // the two rows of this lane: packed row -> (new token, query head)
+        const int qrow0 = a.q_start[t.b];
+        auto q_row = [&](int r) -> const uint8_t * {
+            const int R = t.row0 + min(r, t.rows - 1);
+            const int i = R / a.group, g = R - i * a.group;
+            return a.Q + 2 * ((int64_t)(qrow0 + i) * a.q_stride + (int64_t)(t.j * a.group + g) * D);
+        };
+        // dims of an A fragment: pairs (2t, 2t + 1) and (2t + 8, 2t + 9) of a step,
+        // for E4M3 keys the dims that the lane's 16-byte load holds
+        auto q_dim = [&](int k, int hi) -> int {
+            return ES == 2 ? k * 16 + 2 * tq + 8 * hi : (k / 4) * 64 + 16 * tq + (k % 4) * 4 + 2 * hi;
+        };
+        uint32_t q[Q_REGS ? KS : 1][4];
+        float sc0 = a.scale_log2, sc1 = a.scale_log2;  // of this lane's two rows of scores
+        if constexpr (Q_REGS) {
+            const uint8_t *q0 = q_row(gr), *q1 = q_row(gr + 8);
 #pragma unroll
             for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    m[e & 1] = fmaxf(m[e & 1], fmaxf(fabsf(lo_bf16(q[k][e])), fabsf(hi_bf16(q[k][e]))));
-            int E[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                m[r] = fmaxf(m[r], __shfl_xor_sync(kFull, m[r], 1));
-                m[r] = fmaxf(m[r], __shfl_xor_sync(kFull, m[r], 2));
-                E[r] = row_exponent(m[r]);
-            }
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    q[k][e] = pack_f16(lo_bf16(q[k][e]) * down_by(E[e & 1]), hi_bf16(q[k][e]) * down_by(E[e & 1]));
-            sc0 *= up_by(E[0]);
-            sc1 *= up_by(E[1]);
-        }
-    } else {
-        static_assert(D == 256 || Q_REGS, "a lane's 8 dims make one row per warp");
-        for (int r = warp; r < kRows; r += A::WARPS) {
-            uint4 v = reinterpret_cast<const uint4 *>(q_row(r))[lane];
-            if constexpr (ES == 1) {
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                float m = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(lo_bf16(w[e])), fabsf(hi_bf16(w[e]))));
-#pragma unroll
-                for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
-                const int E = row_exponent(m);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = pack_f16(lo_bf16(w[e]) * down_by(E), hi_bf16(w[e]) * down_by(E));
-                v = make_uint4(w[0], w[1], w[2], w[3]);
-                if (lane == 0) s_up[r] = up_by(E);
-            }
-            reinterpret_cast<uint4 *>(s_q)[r * (D / 8) + lane] = v;
-        }
-        __syncthreads();
-        if constexpr (ES == 1) {
-            sc0 *= s_up[gr];
-            sc1 *= s_up[gr + 8];
-        }
-    }
-    const int p0 = t.L - t.n + (t.row0 + min(gr, t.rows - 1)) / a.group;
-    const int p1 = t.L - t.n + (t.row0 + min(gr + 8, t.rows - 1)) / a.group;
-
-    const uint32_t ring = saddr(smem) + warp * A::RING;
-    auto key0 = [&](int blk) -> int { return (blk < t.sink_blocks ? blk : blk - t.sink_blocks + t.win_block) * KT; };
-    // the pool row of this lane's key of a block, -1 where there is none
-    auto lookup = [&](int blk) -> int {
-        if (blk >= last || lane >= KT) return -1;
-        const int s = key0(blk) + lane;
-        if (s >= t.end) return -1;
-        const int id = table[s >> a.page_shift];
-        if ((uint32_t)id >= (uint32_t)a.n_pages) {
-            atomicOr(a.status, MKV_DEV_BAD_PAGE);
-            return -1;
-        }
-        return (id << a.page_shift) + (s & page_mask);
-    };
-    auto issue = [&](int stage, int blk, int row) {
-        if (blk < last) {
-            const uint32_t dst = ring + stage * A::STAGE;
-#pragma unroll
-            for (int i = 0; i < KT * A::CPR / 32; ++i) {
-                const int o = lane + 32 * i, r = o / A::CPR, c = o % A::CPR;
-                const int src = __shfl_sync(kFull, row, r);
-                const size_t off = (size_t)max(src, 0) * A::RB + c * 16;
-                cp16(dst + (ES == 2 ? at_rows8<A::CPR>(r, c) : at_rows2<A::CPR>(r, c)), a.k + off, src >= 0);
-                cp16(dst + A::HALF + at_rows8<A::CPR>(r, c), a.v + off, src >= 0);
-            }
-        }
-        cp_commit();
-    };
-
-    float o[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
-
-    int blk = first + warp;
-    int row = lookup(blk);
-#pragma unroll
-    for (int s = 0; s < A::STAGES - 1; ++s) {
-        const int next = lookup(blk + (s + 1) * A::WARPS);
-        issue(s, blk + s * A::WARPS, row);
-        row = next;
-    }
-    for (int it = 0; blk < last; blk += A::WARPS, ++it) {
-        {
-            const int ahead = blk + (A::STAGES - 1) * A::WARPS;
-            const int next = lookup(ahead + A::WARPS);
-            issue((it + A::STAGES - 1) % A::STAGES, ahead, row);
-            row = next;
-        }
-        cp_wait<A::STAGES - 1>();
-        __syncwarp();
-        const uint32_t kb = ring + (it % A::STAGES) * A::STAGE, vb = kb + A::HALF;
-
-        // scores
-        float s[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-        auto q_frag = [&](int k, uint32_t (&f)[4]) {
-            if constexpr (Q_REGS) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = q[k][e];
-            } else {
 #pragma unroll
                 for (int hi = 0; hi < 2; ++hi) {
-                    f[2 * hi] = *reinterpret_cast<const uint32_t *>(s_q + 2 * (gr * D + q_dim(k, hi)));
-                    f[2 * hi + 1] = *reinterpret_cast<const uint32_t *>(s_q + 2 * ((gr + 8) * D + q_dim(k, hi)));
+                    q[k][2 * hi] = *reinterpret_cast<const uint32_t *>(q0 + 2 * q_dim(k, hi));
+                    q[k][2 * hi + 1] = *reinterpret_cast<const uint32_t *>(q1 + 2 * q_dim(k, hi));
+                }
+            if constexpr (ES == 1) {
+                float m[2] = {0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        m[e & 1] = fmaxf(m[e & 1], fmaxf(fabsf(lo_bf16(q[k][e])), fabsf(hi_bf16(q[k][e]))));
+                int E[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    m[r] = fmaxf(m[r], __shfl_xor_sync(kFull, m[r], 1));
+                    m[r] = fmaxf(m[r], __shfl_xor_sync(kFull, m[r], 2));
+                    E[r] = row_exponent(m[r]);
+                }
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        q[k][e] = pack_f16(lo_bf16(q[k][e]) * down_by(E[e & 1]), hi_bf16(q[k][e]) * down_by(E[e & 1]));
+                sc0 *= up_by(E[0]);
+                sc1 *= up_by(E[1]);
+            }
+        } else {
+            static_assert(D == 256 || Q_REGS, "a lane's 8 dims make one row per warp");
+            for (int r = warp; r < kRows; r += A::WARPS) {
+                uint4 v = reinterpret_cast<const uint4 *>(q_row(r))[lane];
+                if constexpr (ES == 1) {
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(lo_bf16(w[e])), fabsf(hi_bf16(w[e]))));
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+                    const int E = row_exponent(m);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = pack_f16(lo_bf16(w[e]) * down_by(E), hi_bf16(w[e]) * down_by(E));
+                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (lane == 0) s_up[r] = up_by(E);
+                }
+                reinterpret_cast<uint4 *>(s_q)[r * (D / 8) + lane] = v;
+            }
+            __syncthreads();
+            if constexpr (ES == 1) {
+                sc0 *= s_up[gr];
+                sc1 *= s_up[gr + 8];
+            }
+        }
+        // places of the tile's first and last row, and of this lane's two
+        const int p_lo = t.L - t.n + t.row0 / a.group, p_hi = t.L - t.n + (t.row0 + t.rows - 1) / a.group;
+        const int p0 = t.L - t.n + (t.row0 + min(gr, t.rows - 1)) / a.group;
+        const int p1 = t.L - t.n + (t.row0 + min(gr + 8, t.rows - 1)) / a.group;
+
+        const uint32_t ring = saddr(smem) + warp * A::RING;
+        auto key0 = [&](int blk) -> int { return block_key<A::KEYS>(t, blk) + warp * KT; };
+        // the pool row of this lane's key of a block, -1 where no row sees it
+        auto lookup = [&](int blk) -> int {
+            if (blk >= last || lane >= KT) return -1;
+            const int s = key0(blk) + lane;
+            if (s >= t.end || (a.window > 0 && s <= p_lo - a.window && s >= a.sinks)) return -1;
+            const int id = table[s >> a.page_shift];
+            if ((uint32_t)id >= (uint32_t)a.n_pages) {
+                atomicOr(a.status, MKV_DEV_BAD_PAGE);
+                return -1;
+            }
+            return (id << a.page_shift) + (s & page_mask);
+        };
+        auto issue = [&](int stage, int blk, int row) {
+            if (blk < last) {
+                const uint32_t dst = ring + stage * A::STAGE;
+#pragma unroll
+                for (int i = 0; i < KT * A::CPR / 32; ++i) {
+                    const int o = lane + 32 * i, r = o / A::CPR, c = o % A::CPR;
+                    const int src = __shfl_sync(kFull, row, r);
+                    const size_t off = (size_t)max(src, 0) * A::RB + c * 16;
+                    cp16(dst + (ES == 2 ? at_rows8<A::CPR>(r, c) : at_rows2<A::CPR>(r, c)), a.k + off, src >= 0);
+                    cp16(dst + A::HALF + at_rows8<A::CPR>(r, c), a.v + off, src >= 0);
                 }
             }
+            cp_commit();
         };
+
+        float o[D / 8][4];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+
+        int row = lookup(first);
+#pragma unroll
+        for (int s = 0; s < A::STAGES - 1; ++s) {
+            const int next = lookup(first + s + 1);
+            issue(s, first + s, row);
+            row = next;
+        }
+        for (int blk = first, it = 0; blk < last; ++blk, ++it) {
+            {
+                const int ahead = blk + A::STAGES - 1, next = lookup(ahead + 1);
+                issue((it + A::STAGES - 1) % A::STAGES, ahead, row);
+                row = next;
+            }
+            cp_wait<A::STAGES - 1>();
+            __syncwarp();
+            const uint32_t kb = ring + (it % A::STAGES) * A::STAGE, vb = kb + A::HALF;
+
+            // scores
+            float s[NT][4];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+            auto q_frag = [&](int k, uint32_t (&f)[4]) {
+                if constexpr (Q_REGS) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = q[k][e];
+                } else {
+#pragma unroll
+                    for (int hi = 0; hi < 2; ++hi) {
+                        f[2 * hi] = *reinterpret_cast<const uint32_t *>(s_q + 2 * (gr * D + q_dim(k, hi)));
+                        f[2 * hi + 1] = *reinterpret_cast<const uint32_t *>(s_q + 2 * ((gr + 8) * D + q_dim(k, hi)));
+                    }
+                }
+            };
+            if constexpr (ES == 2) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t f[4];
+                    q_frag(k, f);
+#pragma unroll
+                    for (int i = 0; i < NT / 2; ++i) {
+                        uint32_t b[4];
+                        ldsm4(kb + at_rows8<A::CPR>(i * 16 + (lane >> 4) * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)), b);
+                        mma_bf16(s[2 * i], f, b[0], b[1]);
+                        mma_bf16(s[2 * i + 1], f, b[2], b[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k4 = 0; k4 < KS / 4; ++k4) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const uint4 w = lds16(kb + at_rows2<A::CPR>(i * 8 + gr, 4 * k4 + tq));
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t f[4];
+                            q_frag(4 * k4 + e, f);
+                            mma_f16(s[i], f, e4m3x2_to_f16x2(ws[e] & 0xFFFFu), e4m3x2_to_f16x2(ws[e] >> 16));
+                        }
+                    }
+                }
+            }
+
+            // mask, running maximum, weights
+            const int k0 = key0(blk), k1 = k0 + KT - 1;
+            const bool whole = k1 <= p_lo && (a.window <= 0 || k0 > p_hi - a.window || k1 < a.sinks);
+            float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = s[i][e] * (e < 2 ? sc0 : sc1);
+                    if (!whole) {
+                        const int key = k0 + i * 8 + 2 * tq + (e & 1), p = e < 2 ? p0 : p1;
+                        const bool seen = key <= p && (a.window <= 0 || key > p - a.window || key < a.sinks);
+                        x = seen ? x : -CUDART_INF_F;
+                    }
+                    s[i][e] = x;
+                    if (e < 2) x0 = fmaxf(x0, x);
+                    else x1 = fmaxf(x1, x);
+                }
+            x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, 1));
+            x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 1));
+            x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, 2));
+            x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 2));
+            if (__any_sync(kFull, x0 > m0 || x1 > m1)) {
+                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+                // (a row that has seen nothing yet has l = 0 and O = 0: any finite factor)
+                const float f0 = m0 == -CUDART_INF_F ? 0.f : exp2_approx(m0 - n0);
+                const float f1 = m1 == -CUDART_INF_F ? 0.f : exp2_approx(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= f0;
+                l1 *= f1;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= f0;
+                    o[i][1] *= f0;
+                    o[i][2] *= f1;
+                    o[i][3] *= f1;
+                }
+            }
+            const float b0 = m0 == -CUDART_INF_F ? 0.f : m0, b1 = m1 == -CUDART_INF_F ? 0.f : m1;
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const float e0 = exp2_approx(s[i][0] - b0), e1 = exp2_approx(s[i][1] - b0);
+                const float e2 = exp2_approx(s[i][2] - b1), e3 = exp2_approx(s[i][3] - b1);
+                l0 += e0 + e1;
+                l1 += e2 + e3;
+                // the weights rounded for the product with V: to bf16, the MMA's
+                // type next to bf16 values; to fp16 (11 bits) next to E4M3 ones,
+                // which fp16 holds exactly
+                p[i][0] = ES == 2 ? pack_bf16(e0, e1) : pack_f16(e0, e1);
+                p[i][1] = ES == 2 ? pack_bf16(e2, e3) : pack_f16(e2, e3);
+            }
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk) {
+                const uint32_t f[4] = {p[2 * kk][0], p[2 * kk][1], p[2 * kk + 1][0], p[2 * kk + 1][1]};
+                if constexpr (ES == 2) {
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t b[4];
+                        ldsm4_t(vb + at_rows8<A::CPR>(kk * 16 + (lane & 15), 2 * c + (lane >> 4)), b);
+                        mma_bf16(o[2 * c], f, b[0], b[1]);
+                        mma_bf16(o[2 * c + 1], f, b[2], b[3]);
+                    }
+                } else {
+                    // a 16-byte chunk holds 16 dims: even dims to one column tile, odd to the next
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t b[4];
+                        ldsm4_t(vb + at_rows8<A::CPR>(kk * 16 + (lane & 15), 2 * c + (lane >> 4)), b);
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            // (key, dim) bytes 00 01 10 11 to 00 10 | 01 11: the two dims' key pairs
+                            const uint32_t v0 = __byte_perm(b[2 * hf], 0, 0x3120), v1 = __byte_perm(b[2 * hf + 1], 0, 0x3120);
+                            mma_f16(o[4 * c + 2 * hf], f, e4m3x2_to_f16x2(v0 & 0xFFFFu), e4m3x2_to_f16x2(v1 & 0xFFFFu));
+                            mma_f16(o[4 * c + 2 * hf + 1], f, e4m3x2_to_f16x2(v0 >> 16), e4m3x2_to_f16x2(v1 >> 16));
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // the stage is free for the next copies
+        }
+        cp_wait<0>();
+        l0 += __shfl_xor_sync(kFull, l0, 1);
+        l1 += __shfl_xor_sync(kFull, l1, 1);
+        l0 += __shfl_xor_sync(kFull, l0, 2);
+        l1 += __shfl_xor_sync(kFull, l1, 2);
+        __syncthreads();  // every ring is done with: the warps' results take its place
+        float *mine = reinterpret_cast<float *>(smem) + warp * kRows * D;
+        if (tq == 0) {
+            s_ml[warp][gr] = make_float2(m0, l0);
+            s_ml[warp][gr + 8] = make_float2(m1, l1);
+        }
         if constexpr (ES == 2) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                uint32_t f[4];
-                q_frag(k, f);
-#pragma unroll
-                for (int i = 0; i < NT / 2; ++i) {
-                    uint32_t b[4];
-                    ldsm4(kb + at_rows8<A::CPR>(i * 16 + (lane >> 4) * 8 + (lane & 7), 2 * k + ((lane >> 3) & 1)), b);
-                    mma_bf16(s[2 * i], f, b[0], b[1]);
-                    mma_bf16(s[2 * i + 1], f, b[2], b[3]);
-                }
+            for (int i = 0; i < D / 8; ++i) {
+                *reinterpret_cast<float2 *>(mine + gr * D + i * 8 + 2 * tq) = make_float2(o[i][0], o[i][1]);
+                *reinterpret_cast<float2 *>(mine + (gr + 8) * D + i * 8 + 2 * tq) = make_float2(o[i][2], o[i][3]);
             }
         } else {
 #pragma unroll
-            for (int k4 = 0; k4 < KS / 4; ++k4) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const uint4 w = lds16(kb + at_rows2<A::CPR>(i * 8 + gr, 4 * k4 + tq));
-                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t f[4];
-                        q_frag(4 * k4 + e, f);
-                        mma_f16(s[i], f, e4m3x2_to_f16x2(ws[e] & 0xFFFFu), e4m3x2_to_f16x2(ws[e] >> 16));
-                    }
-                }
+            for (int c = 0; c < D / 16; ++c) {
+                *reinterpret_cast<float4 *>(mine + gr * D + c * 16 + 4 * tq) =
+                    make_float4(o[2 * c][0], o[2 * c + 1][0], o[2 * c][1], o[2 * c + 1][1]);
+                *reinterpret_cast<float4 *>(mine + (gr + 8) * D + c * 16 + 4 * tq) =
+                    make_float4(o[2 * c][2], o[2 * c + 1][2], o[2 * c][3], o[2 * c + 1][3]);
             }
         }
-
-        // mask, running maximum, weights
-        const int k0 = key0(blk), k1 = k0 + KT - 1;
-        const bool whole = k1 <= t.p_lo && (a.window <= 0 || k0 > t.p_hi - a.window || k1 < a.sinks);
-        float x0 = -CUDART_INF_F, x1 = -CUDART_INF_F;
+        __syncthreads();
+        for (int x = threadIdx.x; x < t.rows * (D / 4); x += A::THREADS) {
+            const int r = x / (D / 4), c = x % (D / 4);
+            float M = -CUDART_INF_F;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+            for (int w = 0; w < A::WARPS; ++w) M = fmaxf(M, s_ml[w][r].x);
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = s[i][e] * (e < 2 ? sc0 : sc1);
-                if (!whole) {
-                    const int key = k0 + i * 8 + 2 * tq + (e & 1), p = e < 2 ? p0 : p1;
-                    const bool seen = key <= p && (a.window <= 0 || key > p - a.window || key < a.sinks);
-                    x = seen ? x : -CUDART_INF_F;
-                }
-                s[i][e] = x;
-                if (e < 2) x0 = fmaxf(x0, x);
-                else x1 = fmaxf(x1, x);
+            for (int w = 0; w < A::WARPS; ++w) {
+                const float2 ml = s_ml[w][r];
+                const float f = ml.x == -CUDART_INF_F ? 0.f : exp2_approx(ml.x - M);
+                const float4 v = reinterpret_cast<const float4 *>(smem)[(w * kRows + r) * (D / 4) + c];
+                sum.x += f * v.x;
+                sum.y += f * v.y;
+                sum.z += f * v.z;
+                sum.w += f * v.w;
+                l += f * ml.y;
             }
-        x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, 1));
-        x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 1));
-        x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, 2));
-        x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 2));
-        if (__any_sync(kFull, x0 > m0 || x1 > m1)) {
-            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-            // (a row that has seen nothing yet has l = 0 and O = 0: any finite factor)
-            const float f0 = m0 == -CUDART_INF_F ? 0.f : exp2_approx(m0 - n0);
-            const float f1 = m1 == -CUDART_INF_F ? 0.f : exp2_approx(m1 - n1);
-            m0 = n0;
-            m1 = n1;
-            l0 *= f0;
-            l1 *= f1;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                o[i][0] *= f0;
-                o[i][1] *= f0;
-                o[i][2] *= f1;
-                o[i][3] *= f1;
+            if (!w.whole()) {
+                const int64_t part = part_row(w, kRows) + r;
+                reinterpret_cast<float4 *>(a.part_o)[part * (D / 4) + c] = sum;
+                if (c == 0) a.part_ml[part] = make_float2(M, l);
+                continue;
             }
+            const float inv = l > 0.f ? a.v_scale / l : 0.f;
+            const int R = t.row0 + r, i = R / a.group, head = t.j * a.group + R - i * a.group;
+            *reinterpret_cast<uint2 *>(a.O + 2 * ((int64_t)(qrow0 + i) * a.o_stride + (int64_t)head * D + 4 * c)) =
+                make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+            if (c == 0 && a.lse)
+                a.lse[(int64_t)(qrow0 + i) * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
         }
-        const float b0 = m0 == -CUDART_INF_F ? 0.f : m0, b1 = m1 == -CUDART_INF_F ? 0.f : m1;
-        uint32_t p[NT][2];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const float e0 = exp2_approx(s[i][0] - b0), e1 = exp2_approx(s[i][1] - b0);
-            const float e2 = exp2_approx(s[i][2] - b1), e3 = exp2_approx(s[i][3] - b1);
-            l0 += e0 + e1;
-            l1 += e2 + e3;
-            // the weights rounded for the product with V: to bf16, the MMA's
-            // type next to bf16 values; to fp16 (11 bits) next to E4M3 ones,
-            // which fp16 holds exactly
-            p[i][0] = ES == 2 ? pack_bf16(e0, e1) : pack_f16(e0, e1);
-            p[i][1] = ES == 2 ? pack_bf16(e2, e3) : pack_f16(e2, e3);
-        }
-#pragma unroll
-        for (int kk = 0; kk < KT / 16; ++kk) {
-            const uint32_t f[4] = {p[2 * kk][0], p[2 * kk][1], p[2 * kk + 1][0], p[2 * kk + 1][1]};
-            if constexpr (ES == 2) {
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t b[4];
-                    ldsm4_t(vb + at_rows8<A::CPR>(kk * 16 + (lane & 15), 2 * c + (lane >> 4)), b);
-                    mma_bf16(o[2 * c], f, b[0], b[1]);
-                    mma_bf16(o[2 * c + 1], f, b[2], b[3]);
-                }
-            } else {
-                // a 16-byte chunk holds 16 dims: even dims to one column tile, odd to the next
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t b[4];
-                    ldsm4_t(vb + at_rows8<A::CPR>(kk * 16 + (lane & 15), 2 * c + (lane >> 4)), b);
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        // (key, dim) bytes 00 01 10 11 to 00 10 | 01 11: the two dims' key pairs
-                        const uint32_t v0 = __byte_perm(b[2 * hf], 0, 0x3120), v1 = __byte_perm(b[2 * hf + 1], 0, 0x3120);
-                        mma_f16(o[4 * c + 2 * hf], f, e4m3x2_to_f16x2(v0 & 0xFFFFu), e4m3x2_to_f16x2(v1 & 0xFFFFu));
-                        mma_f16(o[4 * c + 2 * hf + 1], f, e4m3x2_to_f16x2(v0 >> 16), e4m3x2_to_f16x2(v1 >> 16));
-                    }
-                }
-            }
-        }
-        __syncwarp();  // the stage is free for the next copies
+        __syncthreads();  // the next segment's copies may overwrite the results
     }
-    cp_wait<0>();
-    l0 += __shfl_xor_sync(kFull, l0, 1);
-    l1 += __shfl_xor_sync(kFull, l1, 1);
-    l0 += __shfl_xor_sync(kFull, l0, 2);
-    l1 += __shfl_xor_sync(kFull, l1, 2);
-    __syncthreads();  // every ring is done with: the warps' results take its place
-    float *mine = reinterpret_cast<float *>(smem) + warp * kRows * D;
-    if (tq == 0) {
-        s_ml[warp][gr] = make_float2(m0, l0);
-        s_ml[warp][gr + 8] = make_float2(m1, l1);
-    }
-    if constexpr (ES == 2) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            *reinterpret_cast<float2 *>(mine + gr * D + i * 8 + 2 * tq) = make_float2(o[i][0], o[i][1]);
-            *reinterpret_cast<float2 *>(mine + (gr + 8) * D + i * 8 + 2 * tq) = make_float2(o[i][2], o[i][3]);
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-            *reinterpret_cast<float4 *>(mine + gr * D + c * 16 + 4 * tq) =
-                make_float4(o[2 * c][0], o[2 * c + 1][0], o[2 * c][1], o[2 * c + 1][1]);
-            *reinterpret_cast<float4 *>(mine + (gr + 8) * D + c * 16 + 4 * tq) =
-                make_float4(o[2 * c][2], o[2 * c + 1][2], o[2 * c][3], o[2 * c + 1][3]);
-        }
-    }
-    __syncthreads();
-    for (int x = threadIdx.x; x < t.rows * (D / 4); x += A::THREADS) {
-        const int r = x / (D / 4), c = x % (D / 4);
-        float M = -CUDART_INF_F;
-#pragma unroll
-        for (int w = 0; w < A::WARPS; ++w) M = fmaxf(M, s_ml[w][r].x);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll
-        for (int w = 0; w < A::WARPS; ++w) {
-            const float2 ml = s_ml[w][r];
-            const float f = ml.x == -CUDART_INF_F ? 0.f : exp2_approx(ml.x - M);
-            const float4 v = reinterpret_cast<const float4 *>(smem)[(w * kRows + r) * (D / 4) + c];
-            sum.x += f * v.x;
-            sum.y += f * v.y;
-            sum.z += f * v.z;
-            sum.w += f * v.w;
-            l += f * ml.y;
-        }
-        if (a.splits > 1) {
-            reinterpret_cast<float4 *>(a.part_o)[(item * kRows + r) * (D / 4) + c] = sum;
-            if (c == 0) a.part_ml[item * kRows + r] = make_float2(M, l);
-            continue;
-        }
-        const float inv = l > 0.f ? a.v_scale / l : 0.f;
-        const int R = t.row0 + r, i = R / a.group, head = t.j * a.group + R - i * a.group;
-        *reinterpret_cast<uint2 *>(a.O + 2 * ((int64_t)(qrow0 + i) * a.o_stride + (int64_t)head * D + 4 * c)) =
-            make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-        if (c == 0 && a.lse)
-            a.lse[(int64_t)(qrow0 + i) * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
-    }
+    if (threadIdx.x == 0) info[blockIdx.x] = ci;
 }
 
-// One CTA per row: its warps take the parts of the key axis in turn, four
-// loads of a part's row in flight per lane, and meet in shared memory. Always
-// the same order.
-template <int D, int KT>
+// One CTA per row of the tile that CTA blockIdx.y opened, if it did: its warps
+// take the tile's parts in turn, four loads of a part's row in flight per
+// lane, and meet in shared memory. Always the same order.
+template <int D, int KEYS>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-k_attend_combine(const AttnArgs a)
+k_attend_combine(const AttnArgs a, const LineInfo *__restrict__ info)
 {
     constexpr int E = D / 32, U = 4;
     __shared__ float s_o[kJoinWarps][D];
     __shared__ float2 s_ml[kJoinWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t lt = blockIdx.x / kRows;
-    const int r = (int)(blockIdx.x % kRows);
-    const int64_t list = lt / a.tiles;
-    Tile t;
-    if (!make_tile<KT>(a, list, (int)(lt - list * a.tiles), t, false) || r >= t.rows) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = (int)blockIdx.x, c0 = (int)blockIdx.y;
+    pdl_wait();
+    int c1;
+    const int tile = opened_tile(info, c0, (int)gridDim.y, c1);
+    if (tile < 0) return;
+    const Tile t = make_tile<KEYS>(a, tile, kRows, false);
+    if (r >= t.rows) return;
     const int R = t.row0 + r, i = R / a.group, head = t.j * a.group + R - i * a.group;
     const int64_t token = a.q_start[t.b] + i;
-    pdl_wait();
     float sum[E], l = 0.f, M = -CUDART_INF_F;
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[e] = 0.f;
-    for (int s0 = warp; s0 < a.splits; s0 += U * kJoinWarps) {
+    for (int s0 = c0 + warp; s0 <= c1; s0 += U * kJoinWarps) {
         float2 ml[U];
         float v[U][E];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * kJoinWarps;
             ml[u] = make_float2(-CUDART_INF_F, 0.f);
-            if (s < a.splits) {
-                const int64_t at = (lt * a.splits + s) * kRows + r;
+            if (s <= c1) {
+                const int64_t at = ((int64_t)s * 2 + (s == c0 ? 1 : 0)) * kRows + r;
                 ml[u] = a.part_ml[at];
                 const float *src = a.part_o + at * D + lane * E;
 #pragma unroll
@@ -619,11 +583,11 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
     using A = Attend<D, ES>;
     cudaError_t e = cudaFuncSetAttribute(k_attend<D, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)a.batch * a.heads * a.tiles;
-    k_attend<D, ES><<<(unsigned)(tiles * a.splits), A::THREADS, A::SMEM, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+    LineInfo *info = reinterpret_cast<LineInfo *>(a.part_ml + (int64_t)a.ctas * 2 * kRows);
+    k_attend<D, ES><<<a.ctas, A::THREADS, A::SMEM, st>>>(a, info);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * kRows));
+    cfg.gridDim = dim3(kRows, (unsigned)a.ctas);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -631,32 +595,21 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attend_combine<D, A::KT>, a);
+    return cudaLaunchKernelEx(&cfg, k_attend_combine<D, A::KEYS>, a, (const LineInfo *)info);
 }
 
 }  // namespace
 
-AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int32_t es,
-                        int sms)
+AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t head_dim, int32_t es, int ctas)
 {
     AttnPlan p;
     const int64_t rows = (int64_t)max_q * group;
-    if (es == 2 && rows > kFewRows) {
-        p.chunked = 1;
-        p.tiles = (int32_t)((rows + chunk_tile_rows(head_dim) - 1) / chunk_tile_rows(head_dim));
-        p.splits = sms;
-        p.part_rows = (int64_t)sms * 2 * chunk_tile_rows(head_dim);
-        p.bytes = chunk_workspace_bytes(sms, head_dim);
-        return p;
-    }
-    p.tiles = (int32_t)((rows + kRows - 1) / kRows);
-    const int64_t base = std::max<int64_t>(1, lists * p.tiles);
-    const int64_t want = (8 * sms + base - 1) / base, most = ((int64_t)max_len + 127) / 128;
-    p.splits = (int32_t)std::max<int64_t>(1, std::min(want, most));
-    if (p.splits > 1) {
-        p.part_rows = base * p.splits * kRows;
-        p.bytes = (size_t)p.part_rows * (head_dim * sizeof(float) + sizeof(float2));
-    }
+    p.chunked = es == 2 && rows > kFewRows;
+    const int tile = p.chunked ? chunk_tile_rows(head_dim) : kRows;
+    p.tiles = (int32_t)((rows + tile - 1) / tile);
+    p.ctas = ctas;
+    p.part_rows = (int64_t)ctas * 2 * tile;
+    p.bytes = (size_t)p.part_rows * (head_dim * sizeof(float) + sizeof(float2)) + ctas * sizeof(LineInfo);
     return p;
 }
 

@@ -19,10 +19,8 @@
 // for its softmax or its operands; warps 4-7 and 8-11 are the softmax of
 // sub-tile 0 and 1 (they also load its queries and write its output).
 //
-// The blocks of all tiles form one line, cut into equal parts, one per CTA: no
-// CTA idles behind a long list or an uneven number of tiles. A tile that is
-// cut leaves its parts (unnormalised O, m, l) in the workspace and
-// k_chunk_combine joins them in order.
+// The line of blocks is cut over 152 CTAs (mkv_attention.cuh);
+// k_chunk_combine joins the parts of cut tiles.
 //
 // Every wait is bounded (1 s); when one runs out the CTA reports
 // MKV_DEV_TIMEOUT, its roles leave their loops, the copies and MMAs in flight
@@ -37,6 +35,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "mkv_attention.cuh"
 #include "mkv_device.cuh"
 #include "mkv_pages.h"
 
@@ -249,95 +248,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// What one tile of packed rows of one list is.
-struct Tile {
-    int b, j, n, L, row0, rows;  // batch row, head, new tokens, list length, first packed row, rows
-    int end;                     // keys from here on are visible to no row
-    int sink_blocks, win_block, blocks;  // blocks of keys: [0, sink_blocks) and from win_block on; in all
-};
-
-// The tile's rows and blocks; rows 0 where there is nothing to do.
-__device__ __forceinline__ Tile make_tile(const AttnArgs &a, int64_t at, int tile_rows, bool report)
-{
-    Tile t;
-    const int64_t list = at / a.tiles;
-    const int tile = (int)(at - list * a.tiles);
-    t.b = (int)(list / a.heads);
-    t.j = (int)(list - (int64_t)t.b * a.heads);
-    t.row0 = tile * tile_rows;
-    t.rows = t.blocks = t.sink_blocks = t.win_block = t.end = 0;
-    const int lo = a.q_start[t.b], hi = a.q_start[t.b + 1];
-    t.n = hi - lo;
-    t.L = a.lens[list];
-    if (lo < 0 || hi < lo || hi > a.n_tokens || t.n > a.max_q) {
-        if (report) atomicOr(a.status, MKV_DEV_BAD_TOKENS);
-        return t;
-    }
-    if (t.L < 0 || t.L > a.max_len) {
-        if (report) atomicOr(a.status, MKV_DEV_BAD_SEQ_LEN);
-        return t;
-    }
-    t.rows = max(0, min(tile_rows, t.n * a.group - t.row0));
-    if (t.rows == 0) return t;
-    const int p_lo = t.L - t.n + t.row0 / a.group, p_hi = t.L - t.n + (t.row0 + t.rows - 1) / a.group;
-    t.end = max(0, p_hi + 1);
-    const int all = (t.end + kKeys - 1) / kKeys;
-    if (a.window > 0) {
-        const int start = max(0, p_lo - a.window + 1);
-        t.win_block = min(start / kKeys, all);
-        t.sink_blocks = min((min(a.sinks, t.end) + kKeys - 1) / kKeys, t.win_block);
-    }
-    t.blocks = t.sink_blocks + all - t.win_block;
-    return t;
-}
-
-__device__ __forceinline__ int block_key(const Tile &t, int blk)
-{
-    return (blk < t.sink_blocks ? blk : blk - t.sink_blocks + t.win_block) * kKeys;
-}
-
-// Units of a tile on the line: its blocks; one for a tile whose rows see nothing.
-__device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max(t.blocks, 1) : 0; }
-
-// A CTA's walk over its part of the line, the same in every role.
-struct Walk {
-    int64_t tile, left;  // the next tile, units left
-    int skip;            // units of that tile that belong to the CTA before
-    Tile t;
-    int first, last, units;  // blocks [first, last) of the tile's units
-    __device__ __forceinline__ bool next(const AttnArgs &a, int tile_rows)
-    {
-        if (left <= 0) return false;
-        const int64_t n_tiles = (int64_t)a.batch * a.heads * a.tiles;
-        for (;; ++tile) {
-            if (tile >= n_tiles) return false;
-            t = make_tile(a, tile, tile_rows, false);
-            units = units_of(t);
-            if (units > skip) break;
-            skip -= units;  // (0 units: nothing to do)
-        }
-        first = skip;
-        last = (int)min((int64_t)units, first + left);
-        left -= last - first;
-        skip = 0;
-        ++tile;
-        return true;
-    }
-    __device__ __forceinline__ bool whole() const { return first == 0 && last == units; }
-    __device__ __forceinline__ int blocks() const { return min(last, t.blocks) - min(first, t.blocks); }
-};
-
-struct ChunkInfo {
-    int32_t open_tile;  // the tile whose first part is this CTA's last segment, -1: none
-    int32_t carries;    // this CTA's first segment continues a tile
-    int32_t ends;       // ... and ends it
-    int32_t pad;
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
-               ChunkInfo *info)
+               LineInfo *info)
 {
     using C = Chunk<D>;
     constexpr int NSUB = C::NSUB, SLOTS = C::SLOTS;
@@ -350,11 +264,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t abort_flag;
     __shared__ Walk s_walk[kThreads / 32];
-    __shared__ long long s_sum[kThreads / 32];
-    __shared__ long long s_first_tile, s_left;
-    __shared__ int s_skip;
+    __shared__ LineScratch s_line;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t n_tiles = (int64_t)a.batch * a.heads * a.tiles;
     pdl_trigger();
 
     if (threadIdx.x == 0) {
@@ -372,9 +283,6 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         bar_init(&drain[0], 1);
         bar_init(&drain[1], 1);
         abort_flag = 0u;
-        s_first_tile = 0;
-        s_left = 0;
-        s_skip = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -383,60 +291,11 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // the line's length, then this CTA's part of it
-    auto block_sum = [&](long long v) -> long long {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-        if (lane == 0) s_sum[warp] = v;
-        __syncthreads();
-        long long t = 0;
-        for (int i = 0; i < kThreads / 32; ++i) t += s_sum[i];
-        __syncthreads();
-        return t;
-    };
-    long long units = 0;
-    for (int64_t x = threadIdx.x; x < n_tiles; x += kThreads)
-        units += units_of(make_tile(a, x, C::ROWS, blockIdx.x == 0 && x % a.tiles == 0));
-    units = block_sum(units);
-    const long long parts = max(1LL, min((long long)gridDim.x, units / kMinBlocks));
-    const long long u0 = units * min((long long)blockIdx.x, parts) / parts;
-    const long long u1 = units * min((long long)blockIdx.x + 1, parts) / parts;
-    if (u1 > u0) {
-        long long before = 0;
-        for (int64_t x0 = 0; x0 < n_tiles && before <= u0; x0 += kThreads) {
-            const int64_t x = x0 + threadIdx.x;
-            const long long mine = x < n_tiles ? units_of(make_tile(a, x, C::ROWS, false)) : 0;
-            long long pre = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(kFull, pre, o);
-                if (lane >= o) pre += y;
-            }
-            if (lane == 31) s_sum[warp] = pre;
-            __syncthreads();
-            long long off = before, all = 0;
-            for (int i = 0; i < kThreads / 32; ++i) {
-                if (i < warp) off += s_sum[i];
-                all += s_sum[i];
-            }
-            off += pre - mine;
-            if (mine > 0 && off <= u0 && u0 < off + mine) {
-                s_first_tile = x;
-                s_skip = (int)(u0 - off);
-                s_left = u1 - u0;
-            }
-            before += all;
-            __syncthreads();
-        }
-    }
+    Walk w = cut_line<kKeys, kThreads>(a, C::ROWS, kMinBlocks, s_line);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
-    Walk w;
-    w.tile = s_first_tile;
-    w.left = s_left;
-    w.skip = s_skip;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -445,12 +304,12 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const int per_block = kKeys >> a.page_shift;  // pages of a block: one lane each
             uint32_t seq = 0;
             bool ok = true;
-            while (ok && w.next(a, C::ROWS)) {
+            while (ok && w.next<kKeys>(a, C::ROWS)) {
                 const int32_t *table = a.table + ((int64_t)w.t.b * a.heads + w.t.j) * a.max_pages;
-                const int last = min(w.last, w.t.blocks);
+                const int last = w.to();
                 // the pool row of this lane's page of a block; past every row (zero fill) for a bad page, -1: none
                 auto lookup = [&](int blk) -> int {
-                    const int key = block_key(w.t, blk) + (lane << a.page_shift);
+                    const int key = block_key<kKeys>(w.t, blk) + (lane << a.page_shift);
                     if (blk >= last || lane >= per_block || key >= w.t.end) return -1;
                     const int id = table[key >> a.page_shift];
                     if ((uint32_t)id >= (uint32_t)a.n_pages) {
@@ -499,8 +358,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 }
                 mma_commit(&s_full[t]);
             };
-            while (ok && w.next(a, C::ROWS)) {
-                const int nb = w.blocks();
+            while (ok && w.next<kKeys>(a, C::ROWS)) {
+                const int nb = w.to() - w.from();
                 if (nb == 0) continue;
                 if (t * kSubRows >= w.t.rows) {
                     // no rows for this warp: it keeps step (a slot is free when both warps have let it go)
@@ -510,7 +369,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     }
                     continue;
                 }
-                const int first = min(w.first, w.t.blocks);
+                const int first = w.from();
                 const int ks = (int)(seq % SLOTS);
                 ok = warp_wait(&full[ks], (seq / SLOTS) & 1u, a.status, &abort_flag) &&
                      warp_wait(&q_full[t], n_seg & 1u, a.status, &abort_flag);
@@ -529,7 +388,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     if (!ok) break;
                     // values behind the list's end may be anything, also NaN: zero them, their weights are zero too
                     // (both warps write the same zeros, each before its own MMAs)
-                    const int live = w.t.end - block_key(w.t, first + blk);
+                    const int live = w.t.end - block_key<kKeys>(w.t, first + blk);
                     if (live < kKeys) {
                         const uint32_t base = saddr(ring + vs * C::SLOT);
                         for (int o = max(live, 0) * 8 + lane; o < kKeys * 8; o += 32)
@@ -568,14 +427,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             }
         } else if (warp == 3 && lane == 0) {
             // -------------------------------------------- what the combine reads --
-            ChunkInfo ci = {-1, 0, 0, 0};
-            for (bool start = true; w.next(a, C::ROWS); start = false) {
-                if (start && w.first > 0) {
-                    ci.carries = 1;
-                    ci.ends = w.last == w.units;
-                }
-                if (w.first == 0 && w.last < w.units) ci.open_tile = (int32_t)(w.tile - 1);
-            }
+            LineInfo ci = {-1, 0};
+            while (w.next<kKeys>(a, C::ROWS)) note_segment(w, ci);
             info[blockIdx.x] = ci;
         }
     } else {
@@ -589,10 +442,10 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
         uint32_t n_s = 0, n_o = 0;  // blocks, segments with blocks so far
         bool ok = t < NSUB;
-        while (ok && w.next(a, C::ROWS)) {
+        while (ok && w.next<kKeys>(a, C::ROWS)) {
             if (t * kSubRows >= w.t.rows) continue;
             const bool real = t * kSubRows + row < w.t.rows;
-            const int nb = w.blocks(), first = min(w.first, w.t.blocks);
+            const int first = w.from(), nb = w.to() - first;
             const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
             // the row's own key; rows that are not there see nothing
             const int p = real ? w.t.L - w.t.n + (w.t.row0 + t * kSubRows + row) / a.group : -1;
@@ -697,7 +550,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const int R = w.t.row0 + t * kSubRows + row, i = R / a.group, head = w.t.j * a.group + R - i * a.group;
             const int64_t token = (int64_t)a.q_start[w.t.b] + i;
             const bool whole = w.whole();
-            const int64_t part = ((int64_t)blockIdx.x * 2 + (w.first > 0 ? 0 : 1)) * C::ROWS + t * kSubRows + row;
+            const int64_t part = part_row(w, C::ROWS) + t * kSubRows + row;
             const float inv = l > 0.f ? a.v_scale / l : 0.f;
             uint4 *dst = reinterpret_cast<uint4 *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D));
             float4 *dst_part = reinterpret_cast<float4 *>(a.part_o + part * D);
@@ -740,36 +593,22 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     }
 }
 
-// Joins the parts of the tiles that were cut: blockIdx.y is the CTA whose last
-// segment begins a tile; the tile's other parts are the first segments of the
-// CTAs after it, up to the one that ends the tile. A warp takes kJoin rows at
-// a time, their loads in flight together.
+// Joins the parts of the tile that CTA blockIdx.y opened, if it did. A warp
+// takes kJoin rows at a time, their loads in flight together.
 constexpr int kJoin = 4;
 
 template <int D>
 __global__ void __launch_bounds__(256)
-k_chunk_combine(const AttnArgs a, const ChunkInfo *__restrict__ info)
+k_chunk_combine(const AttnArgs a, const LineInfo *__restrict__ info)
 {
     using C = Chunk<D>;
     constexpr int E = D / 32;
     pdl_wait();
-    const int c0 = (int)blockIdx.y, lane = threadIdx.x & 31, ctas = (int)gridDim.y;
-    // this CTA's entry and, in the same round trip, those of the 32 after it
-    const int tile = info[c0].open_tile;
-    int ends = c0 + 1 + lane < ctas ? info[c0 + 1 + lane].ends : 1;
+    const int c0 = (int)blockIdx.y, lane = threadIdx.x & 31;
+    int c1;
+    const int tile = opened_tile(info, c0, (int)gridDim.y, c1);
     if (tile < 0) return;
-    const Tile t = make_tile(a, tile, C::ROWS, false);
-    int c1 = c0 + 1;  // the last CTA of the tile
-    for (;;) {
-        const unsigned hit = __ballot_sync(kFull, ends != 0);
-        if (hit) {
-            c1 += __ffs(hit) - 1;
-            break;
-        }
-        c1 += 32;
-        ends = c1 + lane < ctas ? info[c1 + lane].ends : 1;
-    }
-    c1 = min(c1, ctas - 1);
+    const Tile t = make_tile<kKeys>(a, tile, C::ROWS, false);
     const int row0 = ((int)blockIdx.x * 8 + (threadIdx.x >> 5)) * kJoin;
     if (row0 >= t.rows) return;
     float sum[kJoin][E], l[kJoin], M[kJoin];
@@ -852,18 +691,18 @@ bool make_map(CUtensorMap *map, const void *base, const AttnArgs &a)
 }
 
 template <int D>
-cudaError_t launch_one(const AttnArgs &a, int ctas, cudaStream_t st)
+cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 {
     using C = Chunk<D>;
     CUtensorMap mk, mv;
     if (!make_map(&mk, a.k, a) || !make_map(&mv, a.v, a)) return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(k_attend_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    ChunkInfo *info = reinterpret_cast<ChunkInfo *>(a.part_ml + (int64_t)ctas * 2 * C::ROWS);
-    k_attend_chunk<D><<<ctas, kThreads, C::SMEM, st>>>(mk, mv, a, info);
+    LineInfo *info = reinterpret_cast<LineInfo *>(a.part_ml + (int64_t)a.ctas * 2 * C::ROWS);
+    k_attend_chunk<D><<<a.ctas, kThreads, C::SMEM, st>>>(mk, mv, a, info);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(C::ROWS / (8 * kJoin)), (unsigned)ctas);
+    cfg.gridDim = dim3((unsigned)(C::ROWS / (8 * kJoin)), (unsigned)a.ctas);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -871,25 +710,19 @@ cudaError_t launch_one(const AttnArgs &a, int ctas, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_chunk_combine<D>, a, (const ChunkInfo *)info);
+    return cudaLaunchKernelEx(&cfg, k_chunk_combine<D>, a, (const LineInfo *)info);
 }
 
 }  // namespace
 
 int chunk_tile_rows(int head_dim) { return head_dim == 256 ? kSubRows : 2 * kSubRows; }
 
-size_t chunk_workspace_bytes(int ctas, int head_dim)
-{
-    const size_t rows = (size_t)ctas * 2 * chunk_tile_rows(head_dim);
-    return rows * (head_dim * sizeof(float) + sizeof(float2)) + ctas * sizeof(ChunkInfo);
-}
-
 cudaError_t launch_attend_chunk(const AttnArgs &a, cudaStream_t st)
 {
     switch (a.head_dim) {
-    case 64: return launch_one<64>(a, a.splits, st);
-    case 128: return launch_one<128>(a, a.splits, st);
-    case 256: return launch_one<256>(a, a.splits, st);
+    case 64: return launch_one<64>(a, st);
+    case 128: return launch_one<128>(a, st);
+    case 256: return launch_one<256>(a, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -68,23 +68,21 @@ struct AttnArgs {
     int32_t max_q, max_len, window, sinks;
     float scale_log2;  // scale * k_scale * log2(e)
     float v_scale;
-    int32_t chunked;   // mkv_attention_chunk.cu's kernel
-    int32_t tiles;     // tiles per list (of max_q * group rows, 16 each; chunked: chunk_tile_rows)
-    int32_t splits;    // parts of the key axis (chunked: CTAs)
-    float *part_o;     // [parts, rows of a tile, head_dim] (parts: (list, tile, split); chunked: two per CTA)
-    float2 *part_ml;   // [parts, rows of a tile]: running maximum (log2 units) and sum
+    int32_t chunked;   // the form for many rows (mkv_attention_chunk.cu)
+    int32_t tiles;     // tiles per list (of max_q * group rows)
+    int32_t ctas;      // CTAs that the line of key blocks is cut over
+    float *part_o;     // [2 ctas, rows of a tile, head_dim]: parts of cut tiles, before the division
+    float2 *part_ml;   // [2 ctas, rows of a tile]: running maximum (log2 units) and sum; the CTAs' LineInfo follows
     uint32_t *status;
 };
-// The launch of a shape: splits and the workspace bytes behind the status word.
+// The launch of a shape, and the workspace bytes behind the status word.
 struct AttnPlan {
-    int32_t chunked = 0, tiles = 0, splits = 0;
+    int32_t chunked = 0, tiles = 0, ctas = 0;
     int64_t part_rows = 0;  // rows of part_o
     size_t bytes = 0;
 };
-AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int32_t es,
-                        int sms);
+AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t head_dim, int32_t es, int ctas);
 int chunk_tile_rows(int head_dim);
-size_t chunk_workspace_bytes(int ctas, int head_dim);
 cudaError_t launch_attend_chunk(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t st);
 

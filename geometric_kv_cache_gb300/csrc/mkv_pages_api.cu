@@ -308,10 +308,8 @@ static mkv_status attention_sizes(const mkv_page_pool &pool, const mkv_page_list
     *plan = AttnPlan();
     if (no_lists(lists) || max_q == 0) return MKV_OK;
     const int64_t n = (int64_t)lists.batch * lists.heads;
-    *plan = attention_plan(n, tokens.q_heads / lists.heads, max_q, max_len, pool.head_dim,
-                           elem_bytes(pool.dtype), kPlanSms);
-    // CTAs of the two launches, 32-bit grids
-    if ((!plan->chunked && n * plan->tiles * plan->splits > (int64_t)INT32_MAX) || n * plan->tiles * 16 > (int64_t)INT32_MAX)
+    *plan = attention_plan(n, tokens.q_heads / lists.heads, max_q, pool.head_dim, elem_bytes(pool.dtype), kPlanSms);
+    if (n * plan->tiles > (int64_t)INT32_MAX)  // tiles count in 32 bits
         return MKV_ERR_UNSUPPORTED;
     return MKV_OK;
 }
@@ -375,7 +373,7 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     a.scale_log2 = (float)((double)scale * (double)k_scale * M_LOG2E);
     a.v_scale = v_scale;
     a.tiles = plan.tiles;
-    a.splits = plan.splits;
+    a.ctas = plan.ctas;
     a.chunked = plan.chunked;
     a.part_o = region<float>(workspace, kAlign);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + plan.part_rows * d);
