@@ -36,7 +36,8 @@ namespace {
 using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 4;  // warps that share the parts of a row in the join
+constexpr float kLag = 8.f;    // log2 of how far a row's maximum may lag
 constexpr int kFewRows = 64;  // most query rows of a list that this form takes (bf16)
 
 // Shape of one instantiation.
@@ -180,7 +181,7 @@ k_attend(const AttnArgs a, LineInfo *info)
         const int qrow0 = a.q_start[t.b];
         auto q_row = [&](int r) -> const uint8_t * {
             const int R = t.row0 + min(r, t.rows - 1);
-            const int i = R / a.group, g = R - i * a.group;
+            const int i = a.by_group(R), g = R - i * a.group;
             return a.Q + 2 * ((int64_t)(qrow0 + i) * a.q_stride + (int64_t)(t.j * a.group + g) * D);
         };
         // dims of an A fragment: pairs (2t, 2t + 1) and (2t + 8, 2t + 9) of a step,
@@ -247,9 +248,9 @@ k_attend(const AttnArgs a, LineInfo *info)
             }
         }
         // places of the tile's first and last row, and of this lane's two
-        const int p_lo = t.L - t.n + t.row0 / a.group, p_hi = t.L - t.n + (t.row0 + t.rows - 1) / a.group;
-        const int p0 = t.L - t.n + (t.row0 + min(gr, t.rows - 1)) / a.group;
-        const int p1 = t.L - t.n + (t.row0 + min(gr + 8, t.rows - 1)) / a.group;
+        const int p_lo = t.L - t.n + a.by_group(t.row0), p_hi = t.L - t.n + a.by_group(t.row0 + t.rows - 1);
+        const int p0 = t.L - t.n + a.by_group(t.row0 + min(gr, t.rows - 1));
+        const int p1 = t.L - t.n + a.by_group(t.row0 + min(gr + 8, t.rows - 1));
 
         const uint32_t ring = saddr(smem) + warp * A::RING;
         auto key0 = [&](int blk) -> int { return block_key<A::KEYS>(t, blk) + warp * KT; };
@@ -334,16 +335,23 @@ k_attend(const AttnArgs a, LineInfo *info)
             } else {
 #pragma unroll
                 for (int k4 = 0; k4 < KS / 4; ++k4) {
+                    uint32_t kw[NT][4];
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        const uint4 w = lds16(kb + at_rows2<A::CPR>(i * 8 + gr, 4 * k4 + tq));
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                        const uint4 v = lds16(kb + at_rows2<A::CPR>(i * 8 + gr, 4 * k4 + tq));
+                        kw[i][0] = v.x;
+                        kw[i][1] = v.y;
+                        kw[i][2] = v.z;
+                        kw[i][3] = v.w;
+                    }
+                    // (consecutive MMAs add to different tiles of scores)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t f[4];
-                            q_frag(4 * k4 + e, f);
-                            mma_f16(s[i], f, e4m3x2_to_f16x2(ws[e] & 0xFFFFu), e4m3x2_to_f16x2(ws[e] >> 16));
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t f[4];
+                        q_frag(4 * k4 + e, f);
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            mma_f16(s[i], f, e4m3x2_to_f16x2(kw[i][e] & 0xFFFFu), e4m3x2_to_f16x2(kw[i][e] >> 16));
                     }
                 }
             }
@@ -370,7 +378,8 @@ k_attend(const AttnArgs a, LineInfo *info)
             x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 1));
             x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, 2));
             x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 2));
-            if (__any_sync(kFull, x0 > m0 || x1 > m1)) {
+            // The maximum may lag by 2^8 (weights stay below 256): rescaling O is rare.
+            if (__any_sync(kFull, x0 > m0 + kLag || x1 > m1 + kLag)) {
                 const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
                 // (a row that has seen nothing yet has l = 0 and O = 0: any finite factor)
                 const float f0 = m0 == -CUDART_INF_F ? 0.f : exp2_approx(m0 - n0);
@@ -461,14 +470,14 @@ k_attend(const AttnArgs a, LineInfo *info)
             const int r = x / (D / 4), c = x % (D / 4);
             float M = -CUDART_INF_F;
 #pragma unroll
-            for (int w = 0; w < A::WARPS; ++w) M = fmaxf(M, s_ml[w][r].x);
+            for (int y = 0; y < A::WARPS; ++y) M = fmaxf(M, s_ml[y][r].x);
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             float l = 0.f;
 #pragma unroll
-            for (int w = 0; w < A::WARPS; ++w) {
-                const float2 ml = s_ml[w][r];
+            for (int y = 0; y < A::WARPS; ++y) {
+                const float2 ml = s_ml[y][r];
                 const float f = ml.x == -CUDART_INF_F ? 0.f : exp2_approx(ml.x - M);
-                const float4 v = reinterpret_cast<const float4 *>(smem)[(w * kRows + r) * (D / 4) + c];
+                const float4 v = reinterpret_cast<const float4 *>(smem)[(y * kRows + r) * (D / 4) + c];
                 sum.x += f * v.x;
                 sum.y += f * v.y;
                 sum.z += f * v.z;
@@ -482,7 +491,7 @@ k_attend(const AttnArgs a, LineInfo *info)
                 continue;
             }
             const float inv = l > 0.f ? a.v_scale / l : 0.f;
-            const int R = t.row0 + r, i = R / a.group, head = t.j * a.group + R - i * a.group;
+            const int R = t.row0 + r, i = a.by_group(R), head = t.j * a.group + R - i * a.group;
             *reinterpret_cast<uint2 *>(a.O + 2 * ((int64_t)(qrow0 + i) * a.o_stride + (int64_t)head * D + 4 * c)) =
                 make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
             if (c == 0 && a.lse)
@@ -510,7 +519,7 @@ k_attend_combine(const AttnArgs a, const LineInfo *__restrict__ info)
     if (tile < 0) return;
     const Tile t = make_tile<KEYS>(a, tile, kRows, false);
     if (r >= t.rows) return;
-    const int R = t.row0 + r, i = R / a.group, head = t.j * a.group + R - i * a.group;
+    const int R = t.row0 + r, i = a.by_group(R), head = t.j * a.group + R - i * a.group;
     const int64_t token = a.q_start[t.b] + i;
     float sum[E], l = 0.f, M = -CUDART_INF_F;
 #pragma unroll

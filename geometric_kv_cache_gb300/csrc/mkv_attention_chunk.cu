@@ -448,10 +448,10 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const int first = w.from(), nb = w.to() - first;
             const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
             // the row's own key; rows that are not there see nothing
-            const int p = real ? w.t.L - w.t.n + (w.t.row0 + t * kSubRows + row) / a.group : -1;
+            const int p = real ? w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows + row) : -1;
             // (every wait for this sub-tile's last block of the segment before has ended: Q is free)
             if (nb > 0) {
-                const int R = w.t.row0 + t * kSubRows + row, i = R / a.group, head = w.t.j * a.group + R - i * a.group;
+                const int R = w.t.row0 + t * kSubRows + row, i = a.by_group(R), head = w.t.j * a.group + R - i * a.group;
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     a.Q + 2 * (((int64_t)a.q_start[w.t.b] + i) * a.q_stride + (int64_t)head * D));
                 const uint32_t dst = saddr(q_smem + t * C::QBYTES) + row * 128;
@@ -473,8 +473,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             }
             // the first and last place that is visible to every row: blocks inside need no mask
             const int r_last = min(w.t.rows, (t + 1) * kSubRows) - 1;
-            const int whole_to = w.t.L - w.t.n + (w.t.row0 + t * kSubRows) / a.group;
-            const int whole_from = a.window > 0 ? w.t.L - w.t.n + (w.t.row0 + r_last) / a.group - a.window : -1;
+            const int whole_to = w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows);
+            const int whole_from = a.window > 0 ? w.t.L - w.t.n + a.by_group(w.t.row0 + r_last) - a.window : -1;
             // what the loop does not need waits in shared memory: it has 128 scores to hold
             if (lane == 0) s_walk[warp] = w;
             __syncwarp();
@@ -547,7 +547,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 fence_after();
             }
             w = s_walk[warp];
-            const int R = w.t.row0 + t * kSubRows + row, i = R / a.group, head = w.t.j * a.group + R - i * a.group;
+            const int R = w.t.row0 + t * kSubRows + row, i = a.by_group(R), head = w.t.j * a.group + R - i * a.group;
             const int64_t token = (int64_t)a.q_start[w.t.b] + i;
             const bool whole = w.whole();
             const int64_t part = part_row(w, C::ROWS) + t * kSubRows + row;
@@ -650,7 +650,7 @@ k_chunk_combine(const AttnArgs a, const LineInfo *__restrict__ info)
     for (int u = 0; u < kJoin; ++u) {
         if (row0 + u >= t.rows) break;
         const float inv = l[u] > 0.f ? a.v_scale / l[u] : 0.f;
-        const int R = t.row0 + row0 + u, i = R / a.group, head = t.j * a.group + R - i * a.group;
+        const int R = t.row0 + row0 + u, i = a.by_group(R), head = t.j * a.group + R - i * a.group;
         const int64_t token = (int64_t)a.q_start[t.b] + i;
         uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
 #pragma unroll

@@ -57,6 +57,22 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t st);
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiplication: with l =
+// ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d is the high word of
+// m n, plus n, shifted right by l.
+struct FastDiv {
+    uint32_t d = 1, m = 1, l = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t div) : d(div)
+    {
+        while ((1ull << l) < d) ++l;
+        m = (uint32_t)((((1ull << l) - d) << 32) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> l); }
+#endif
+};
+
 struct AttnArgs {
     const uint8_t *Q;
     uint8_t *O;
@@ -70,6 +86,7 @@ struct AttnArgs {
     float v_scale;
     int32_t chunked;   // the form for many rows (mkv_attention_chunk.cu)
     int32_t tiles;     // tiles per list (of max_q * group rows)
+    FastDiv by_tiles, by_heads, by_group;
     int32_t ctas;      // CTAs that the line of key blocks is cut over
     float *part_o;     // [2 ctas, rows of a tile, head_dim]: parts of cut tiles, before the division
     float2 *part_ml;   // [2 ctas, rows of a tile]: running maximum (log2 units) and sum; the CTAs' LineInfo follows

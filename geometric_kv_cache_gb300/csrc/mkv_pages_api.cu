@@ -309,7 +309,8 @@ static mkv_status attention_sizes(const mkv_page_pool &pool, const mkv_page_list
     if (no_lists(lists) || max_q == 0) return MKV_OK;
     const int64_t n = (int64_t)lists.batch * lists.heads;
     *plan = attention_plan(n, tokens.q_heads / lists.heads, max_q, pool.head_dim, elem_bytes(pool.dtype), kPlanSms);
-    if (n * plan->tiles > (int64_t)INT32_MAX)  // tiles count in 32 bits
+    // blocks of at least 64 keys of all tiles are counted in 32 bits
+    if (n * plan->tiles > (int64_t)INT32_MAX / ((int64_t)max_len / 64 + 2))
         return MKV_ERR_UNSUPPORTED;
     return MKV_OK;
 }
@@ -374,6 +375,9 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     a.v_scale = v_scale;
     a.tiles = plan.tiles;
     a.ctas = plan.ctas;
+    a.by_tiles = FastDiv(plan.tiles);
+    a.by_heads = FastDiv(lists.heads);
+    a.by_group = FastDiv(a.group);
     a.chunked = plan.chunked;
     a.part_o = region<float>(workspace, kAlign);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + plan.part_rows * d);

@@ -667,7 +667,9 @@ size_t mkv_attention_workspace_size(mkv_page_pool pool, mkv_page_lists lists, mk
  * for it; a page outside the pool sets MKV_DEV_BAD_PAGE (its tokens count as
  * zeros). Q, O: bf16 [n_tokens, q_heads, head_dim], token t at element
  * t * stride (a multiple of 8, at least q_heads * head_dim), 16-byte aligned,
- * distinct. With tokens to attend, the pool has at least one page.
+ * distinct. With tokens to attend, the pool has at least one page; the launch
+ * counts blocks of keys in 32 bits: batch * q_heads * max_q * max_len / 1024
+ * beyond 2^31 is MKV_ERR_UNSUPPORTED.
  * Scores, sums and accumulators are fp32; the softmax weights are rounded to
  * 16 bits for the product with the values. */
 mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens tokens, int32_t max_q,
