@@ -36,9 +36,9 @@ namespace {
 using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
+constexpr int64_t kAgainBytes = 28000000;  // see takes_chunks
 constexpr int kJoinWarps = 4;  // warps that share the parts of a row in the join
 constexpr float kLag = 8.f;    // log2 of how far a row's maximum may lag
-constexpr int kFewRows = 64;  // most query rows of a list that this form takes (bf16)
 
 // Shape of one instantiation.
 template <int D, int ES>
@@ -125,17 +125,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Next to E4M3 keys the queries run as fp16, which takes one conversion per two
-// codes where bf16 would take five instructions: a row of queries is scaled by
-// the power of two that brings its largest magnitude into [1, 2). Elements
-// from 2^-14 of that on keep all their bits; smaller ones are off by at most
-// 2^-25 of the largest. E: the biased exponent of the largest magnitude.
-__device__ __forceinline__ int row_exponent(float largest)
-{
-    return min(max((int)(__float_as_uint(largest) >> 23), 1), 253);
-}
-__device__ __forceinline__ float down_by(int E) { return __uint_as_float((uint32_t)(254 - E) << 23); }  // 2^(127 - E)
-__device__ __forceinline__ float up_by(int E) { return __uint_as_float((uint32_t)E << 23); }            // 2^(E - 127)
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
@@ -367,7 +356,7 @@ k_attend(const AttnArgs a, LineInfo *info)
                     float x = s[i][e] * (e < 2 ? sc0 : sc1);
                     if (!whole) {
                         const int key = k0 + i * 8 + 2 * tq + (e & 1), p = e < 2 ? p0 : p1;
-                        const bool seen = key <= p && (a.window <= 0 || key > p - a.window || key < a.sinks);
+                        const bool seen = (key <= p) & ((a.window <= 0) | (key > p - a.window) | (key < a.sinks));
                         x = seen ? x : -CUDART_INF_F;
                     }
                     s[i][e] = x;
@@ -609,11 +598,25 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 
 }  // namespace
 
-AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t head_dim, int32_t es, int ctas)
+// Which form: this file's reads K and V once per 16 rows, the other once per
+// 128 or 256, but takes 10 to 17 us more from launch to end. Up to 16 rows (E4M3:
+// 32, the other form expands its codes) this one always; beyond, while the
+// bytes that its further tiles read again, 12 to 18 ns per MB, cost less.
+// Measured (us, this form / the other, 128 dims): 8 lists of 4096 keys, bf16, 32
+// rows 15 / 22, 96 rows 25 / 25, 128 rows 28 / 27; 128 lists of 16384 keys, 16 rows 171 /
+// 186, 32 rows 327 / 188; E4M3 16 rows 114 / 265, 32 rows 216 / 265, 48 rows 301 / 268.
+bool takes_chunks(int64_t lists, int64_t rows, int64_t max_len, int32_t head_dim, int32_t es)
+{
+    const int64_t again = (rows + kRows - 1) / kRows - (es == 1 ? 2 : 1);
+    return again > 0 && lists * max_len * again > kAgainBytes / (head_dim * es);
+}
+
+AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int32_t es,
+                        int ctas)
 {
     AttnPlan p;
     const int64_t rows = (int64_t)max_q * group;
-    p.chunked = es == 2 && rows > kFewRows;
+    p.chunked = takes_chunks(lists, rows, max_len, head_dim, es);
     const int tile = p.chunked ? chunk_tile_rows(head_dim) : kRows;
     p.tiles = (int32_t)((rows + tile - 1) / tile);
     p.ctas = ctas;

@@ -1,0 +1,251 @@
+// What the two forms of mkv_paged_attention share (internal): tiles of packed
+// rows, the line of key blocks and its cut into one part per CTA, and the
+// bookkeeping that lets the parts of a cut tile be joined.
+//
+// The rows (new token, query head of the KV head's group) of a list are packed
+// token by token into tiles; a tile walks the blocks of KEYS keys that any of
+// its rows sees. The blocks of all tiles of all lists form one line, cut into
+// equal parts, one per CTA: no CTA idles behind a long list or an uneven
+// number of tiles. A tile that is cut leaves its parts (O before the division,
+// m, l) in the workspace, at most two per CTA, and a second kernel joins them
+// in order.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mkv_device.cuh"
+#include "mkv_pages.h"
+
+namespace mkv {
+namespace {
+
+using namespace dev;
+
+// Next to E4M3 keys the queries run as fp16, which takes one conversion per two
+// codes where bf16 would take five instructions: a row of queries is scaled by
+// the power of two that brings its largest magnitude into [1, 2). Elements
+// from 2^-14 of that on keep all their bits; smaller ones are off by at most
+// 2^-25 of the largest. E: the biased exponent of the largest magnitude.
+__device__ __forceinline__ int row_exponent(float largest)
+{
+    return min(max((int)(__float_as_uint(largest) >> 23), 1), 253);
+}
+__device__ __forceinline__ float down_by(int E) { return __uint_as_float((uint32_t)(254 - E) << 23); }  // 2^(127 - E)
+__device__ __forceinline__ float up_by(int E) { return __uint_as_float((uint32_t)E << 23); }            // 2^(E - 127)
+
+struct Tile {
+    int b, j, n, L, row0, rows;  // batch row, head, new tokens, list length, first packed row, rows
+    int end;                     // keys from here on are visible to no row
+    int sink_blocks, win_block, blocks;  // blocks of keys: [0, sink_blocks) and from win_block on; in all
+};
+
+// Tile `at` (list-major); rows 0 where there is nothing to do.
+template <int KEYS>
+__device__ __forceinline__ Tile make_tile(const AttnArgs &a, int at, int tile_rows, bool report)
+{
+    Tile t;
+    const int list = a.by_tiles(at), tile = at - list * a.tiles;
+    t.b = a.by_heads(list);
+    t.j = list - t.b * a.heads;
+    t.row0 = tile * tile_rows;
+    t.rows = t.blocks = t.sink_blocks = t.win_block = t.end = 0;
+    const int lo = a.q_start[t.b], hi = a.q_start[t.b + 1];
+    t.n = hi - lo;
+    t.L = a.lens[list];
+    if (lo < 0 || hi < lo || hi > a.n_tokens || t.n > a.max_q) {
+        if (report) atomicOr(a.status, MKV_DEV_BAD_TOKENS);
+        return t;
+    }
+    if (t.L < 0 || t.L > a.max_len) {
+        if (report) atomicOr(a.status, MKV_DEV_BAD_SEQ_LEN);
+        return t;
+    }
+    t.rows = max(0, min(tile_rows, t.n * a.group - t.row0));
+    if (t.rows == 0) return t;
+    const int p_lo = t.L - t.n + a.by_group(t.row0), p_hi = t.L - t.n + a.by_group(t.row0 + t.rows - 1);
+    t.end = max(0, p_hi + 1);
+    const int all = (t.end + KEYS - 1) / KEYS;
+    if (a.window > 0) {
+        const int start = max(0, p_lo - a.window + 1);  // the first key inside any row's window
+        t.win_block = min(start / KEYS, all);
+        t.sink_blocks = min((min(a.sinks, t.end) + KEYS - 1) / KEYS, t.win_block);
+    }
+    t.blocks = t.sink_blocks + all - t.win_block;
+    return t;
+}
+
+template <int KEYS>
+__device__ __forceinline__ int block_key(const Tile &t, int blk)
+{
+    return (blk < t.sink_blocks ? blk : blk - t.sink_blocks + t.win_block) * KEYS;
+}
+
+// Units of a tile on the line: its blocks; one for a tile whose rows see nothing.
+__device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max(t.blocks, 1) : 0; }
+
+// A CTA's walk over its part of the line.
+struct Walk {
+    int tile, left;  // the next tile, units left
+    int skip;        // units of that tile that belong to the CTA before
+    bool have;       // t is that tile already
+    Tile t;
+    int first, last, units;  // units [first, last) of the tile's
+    template <int KEYS>
+    __device__ __forceinline__ bool next(const AttnArgs &a, int tile_rows)
+    {
+        if (left <= 0) return false;
+        const int n_tiles = a.batch * a.heads * a.tiles;
+        for (;; ++tile) {
+            if (tile >= n_tiles) return false;
+            if (!have) t = make_tile<KEYS>(a, tile, tile_rows, false);
+            have = false;
+            units = units_of(t);
+            if (units > skip) break;
+            skip -= units;  // (0 units: nothing to do)
+        }
+        first = skip;
+        last = min(units, first + left);
+        left -= last - first;
+        skip = 0;
+        ++tile;
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return first == 0 && last == units; }
+    // blocks [from(), to()) of the segment
+    __device__ __forceinline__ int from() const { return min(first, t.blocks); }
+    __device__ __forceinline__ int to() const { return min(last, t.blocks); }
+};
+
+// This CTA's part of the line; every thread of the CTA must call it. (The
+// host has checked that the line's length fits 32 bits.)
+struct LineScratch {
+    int sum[32], rest[32];
+    Walk walk;
+};
+template <int KEYS, int THREADS>
+__device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int min_units, LineScratch &s)
+{
+    constexpr int WARPS = THREADS / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_tiles = a.batch * a.heads * a.tiles;
+    // the first THREADS tiles, one per thread, and the sum of the others
+    Tile t;
+    int mine = 0, rest = 0;
+    if ((int)threadIdx.x < n_tiles) {
+        t = make_tile<KEYS>(a, threadIdx.x, tile_rows, blockIdx.x == 0);
+        mine = units_of(t);
+    }
+    for (int x = threadIdx.x + THREADS; x < n_tiles; x += THREADS)
+        rest += units_of(make_tile<KEYS>(a, x, tile_rows, blockIdx.x == 0));
+    auto scan = [&](int v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, v, o);
+            if (lane >= o) v += y;
+        }
+        return v;
+    };
+    int upto = scan(mine);
+    if (n_tiles > THREADS) rest = __reduce_add_sync(kFull, rest);
+    if (lane == 31) {
+        s.sum[warp] = upto;
+        s.rest[warp] = rest;
+    }
+    if (threadIdx.x == 0) s.walk.left = 0;
+    __syncthreads();
+    int before = 0, units = 0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        before += i < warp ? s.sum[i] : 0;
+        units += s.sum[i];
+    }
+    int seen = units;  // in the tiles looked at so far
+    if (n_tiles > THREADS)
+        for (int i = 0; i < WARPS; ++i) units += s.rest[i];
+    const int parts = max(1, min((int)gridDim.x, units / min_units));
+    // part c begins at c units / parts, rounded down (in 32 bits where they do)
+    auto begin = [&](int c) -> int {
+        c = min(c, parts);
+        if (units < (1 << 23)) return (int)((uint32_t)units * (uint32_t)c / (uint32_t)parts);  // (at most 512 CTAs)
+        return (int)((long long)units * c / parts);
+    };
+    const int u0 = begin((int)blockIdx.x), u1 = begin((int)blockIdx.x + 1);
+    auto claim = [&](int x, int off) {  // the thread whose tile holds u0 begins the walk
+        if (mine > 0 && off <= u0 && u0 < off + mine) {
+            s.walk.tile = x;
+            s.walk.skip = u0 - off;
+            s.walk.have = true;
+            s.walk.t = t;
+            s.walk.left = u1 - u0;
+        }
+    };
+    if (u1 > u0) {
+        claim(threadIdx.x, before + upto - mine);
+        for (int x0 = THREADS; x0 < n_tiles && seen <= u0; x0 += THREADS) {
+            const int x = x0 + threadIdx.x;
+            mine = 0;
+            if (x < n_tiles) {
+                t = make_tile<KEYS>(a, x, tile_rows, false);
+                mine = units_of(t);
+            }
+            upto = scan(mine);
+            __syncthreads();
+            if (lane == 31) s.sum[warp] = upto;
+            __syncthreads();
+            before = seen;
+            for (int i = 0; i < WARPS; ++i) {
+                before += i < warp ? s.sum[i] : 0;
+                seen += s.sum[i];
+            }
+            claim(x, before + upto - mine);
+        }
+    }
+    __syncthreads();
+    return s.walk;
+}
+
+// What the joining kernel needs of each CTA.
+struct LineInfo {
+    int32_t open_tile;  // the tile whose first part is this CTA's last segment, -1: none
+    int32_t ends;       // this CTA's first segment continues a tile and ends it
+};
+
+// The workspace's part of a segment that is not a whole tile, of `rows` rows.
+__device__ __forceinline__ int64_t part_row(const Walk &w, int rows)
+{
+    return ((int64_t)blockIdx.x * 2 + (w.first > 0 ? 0 : 1)) * rows;
+}
+
+// Notes a segment in the CTA's entry (one thread).
+__device__ __forceinline__ void note_segment(const Walk &w, LineInfo &info)
+{
+    if (w.first > 0 && w.last == w.units) info.ends = 1;
+    if (w.first == 0 && w.last < w.units) info.open_tile = w.tile - 1;
+}
+
+// The tile that CTA c0 opened, -1 when none; c1 is the last CTA with a part of
+// it. For a whole warp. The parts: c0's second, then the first of c0 + 1 .. c1.
+__device__ __forceinline__ int opened_tile(const LineInfo *__restrict__ info, int c0, int ctas, int &c1)
+{
+    const int lane = threadIdx.x & 31;
+    // this CTA's entry and, in the same round trip, those of the 32 after it
+    const int tile = info[c0].open_tile;
+    int ends = c0 + 1 + lane < ctas ? info[c0 + 1 + lane].ends : 1;
+    if (tile < 0) return -1;
+    c1 = c0 + 1;
+    for (;;) {
+        const unsigned hit = __ballot_sync(kFull, ends != 0);
+        if (hit) {
+            c1 += __ffs(hit) - 1;
+            break;
+        }
+        c1 += 32;
+        ends = c1 + lane < ctas ? info[c1 + lane].ends : 1;
+    }
+    c1 = min(c1, ctas - 1);
+    return tile;
+}
+
+}  // namespace
+}  // namespace mkv

@@ -17,7 +17,10 @@
 // per page, page entries read a block ahead); warps 1 and 2 issue the MMAs of
 // sub-tile 0 and 1, so that the tensor core works on one while the other waits
 // for its softmax or its operands; warps 4-7 and 8-11 are the softmax of
-// sub-tile 0 and 1 (they also load its queries and write its output).
+// sub-tile 0 and 1 (they also load its queries and write its output). E4M3
+// pages land as codes in a ring of their own; warps 12-15 expand them into the
+// slots as fp16, which holds every code exactly, and the queries are fp16 too,
+// each row scaled by a power of two (mkv_attention.cuh).
 //
 // The line of blocks is cut over 152 CTAs (mkv_attention.cuh);
 // k_chunk_combine joins the parts of cut tiles.
@@ -28,6 +31,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -44,7 +48,6 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreads = 384;
 constexpr int kKeys = 128;                   // keys per block
 constexpr int kSubRows = 128;                // rows per sub-tile: the MMA's M, the TMEM lanes
 constexpr int kBoxBytes = kKeys * 128;       // 64 dims of a block: 128 rows of 128 bytes
@@ -52,15 +55,22 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLag = 8.f;                  // log2 of how far a row's maximum may lag
 constexpr int kMinBlocks = 4;                // blocks that make a CTA worth its start
 
-template <int D>
+template <int D, int ES>
 struct Chunk {
     static constexpr int NSUB = D == 256 ? 1 : 2;  // O of two sub-tiles fits the 512 TMEM columns up to D = 128
     static constexpr int ROWS = NSUB * kSubRows;
     static constexpr int BOXES = D / 64;
-    static constexpr int SLOT = BOXES * kBoxBytes;  // one block of K or of V
-    static constexpr int SLOTS = D == 64 ? 8 : D == 128 ? 4 : 2;
+    static constexpr int SLOT = BOXES * kBoxBytes;  // one block of K or of V as the MMA reads it
+    static constexpr int RAW = kKeys * D;           // ... as E4M3 codes
+    static constexpr int RAWS = ES == 2 ? 0 : D == 256 ? 1 : 3;
+    static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 2) : (D == 64 ? 6 : D == 128 ? 3 : 2);
     static constexpr int QBYTES = SLOT;             // one sub-tile of queries has a block's shape
-    static constexpr int SMEM = NSUB * QBYTES + SLOTS * SLOT + 1024;
+    static constexpr int SMEM = NSUB * QBYTES + SLOTS * SLOT + RAWS * RAW + 1024;
+    // 12 warps; 4 more expand E4M3 codes. Registers per thread of warps 0-3, of
+    // the softmax warps and of the expanding ones: in all what the launch has
+    // (384 x 168 or 512 x 128).
+    static constexpr int THREADS = ES == 2 ? 384 : 512;
+    static constexpr int REGS_FEED = ES == 2 ? 88 : 80, REGS_SOFT = ES == 2 ? 208 : 176, REGS_CODES = 80;
     static constexpr int TMEM = 512;
     static constexpr int O_COL = NSUB * kKeys;      // S of the sub-tiles, then O
 };
@@ -139,10 +149,11 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// kind::f16, fp32 accumulator, bf16 operands, M = 128, N = n; bit 16: B is MN-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn)
+// kind::f16, fp32 accumulator, both operands bf16 or both fp16, M = 128, N = n;
+// bit 16: B is MN-major.
+__host__ __device__ constexpr uint32_t idesc_16bit(bool bf16, int n, bool b_mn)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kSubRows >> 4) << 24);
 }
 
@@ -218,6 +229,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v)
         : "memory");
 }
 
+// The lowest n bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n)
+{
+    return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
@@ -247,31 +264,51 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int ES>
+__global__ void __launch_bounds__(Chunk<D, ES>::THREADS, 1)
 k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
                LineInfo *info)
 {
-    using C = Chunk<D>;
-    constexpr int NSUB = C::NSUB, SLOTS = C::SLOTS;
+    using C = Chunk<D, ES>;
+    constexpr int NSUB = C::NSUB, SLOTS = C::SLOTS, RAWS = C::RAWS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *q_smem = smem;                      // NSUB x [D / 64 boxes][128 rows x 128 B]
     uint8_t *ring = smem + NSUB * C::QBYTES;     // SLOTS blocks: K, V, K, V, ...
-    __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], s_full[2], p_ready[2], o_done[2], o_free[2], q_full[2],
+    uint8_t *raws = ring + SLOTS * C::SLOT;      // RAWS blocks of E4M3 codes, in the same order
+    __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], raw_full[RAWS + 1], raw_empty[RAWS + 1], s_full[2], p_ready[2], o_done[2], o_free[2], q_full[2],
         drain[2];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t abort_flag;
-    __shared__ Walk s_walk[kThreads / 32];
+    __shared__ Walk s_walk[C::THREADS / 32];
     __shared__ LineScratch s_line;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SLOTS; ++s) {
-            bar_init(&full[s], 1);
+            bar_init(&full[s], ES == 2 ? 1 : 4);
             bar_init(&empty[s], NSUB);
+        }
+        for (int s = 0; s < RAWS; ++s) {
+            bar_init(&raw_full[s], 1);
+            bar_init(&raw_empty[s], 4);
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(&s_full[s], 1);
@@ -291,17 +328,20 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    Walk w = cut_line<kKeys, kThreads>(a, C::ROWS, kMinBlocks, s_line);
+    Walk w = cut_line<kKeys, C::THREADS>(a, C::ROWS, kMinBlocks, s_line);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_base;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_FEED));
         if (warp == 0) {
             // ---------------------------------------------------- pages of K and V --
             const int per_block = kKeys >> a.page_shift;  // pages of a block: one lane each
+            // the ring that the copies land in: the MMAs' slots, or the codes
+            constexpr int N = ES == 2 ? SLOTS : RAWS;
+            uint64_t *landed = ES == 2 ? full : raw_full, *taken = ES == 2 ? empty : raw_empty;
             uint32_t seq = 0;
             bool ok = true;
             while (ok && w.next<kKeys>(a, C::ROWS)) {
@@ -321,18 +361,24 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 int row = lookup(w.first);
                 for (int blk = w.first; ok && blk < last; ++blk) {
                     const int next = lookup(blk + 1);
-                    const uint32_t bytes = __popc(__ballot_sync(kFull, row >= 0)) * (uint32_t)(C::BOXES * 128) << a.page_shift;
+                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, row >= 0)) * D * ES) << a.page_shift;
                     for (int kv = 0; kv < 2; ++kv, ++seq) {
-                        const int s = (int)(seq % SLOTS);
-                        ok = seq < SLOTS || warp_wait(&empty[s], ((seq / SLOTS) - 1) & 1u, a.status, &abort_flag);
+                        const int s = (int)(seq % N);
+                        ok = seq < N || warp_wait(&taken[s], ((seq / N) - 1) & 1u, a.status, &abort_flag);
                         if (!ok) break;
-                        if (lane == 0) bar_expect(&full[s], bytes);
+                        if (lane == 0) bar_expect(&landed[s], bytes);
                         __syncwarp();
                         if (row >= 0) {
-                            const uint32_t dst = saddr(ring + s * C::SLOT) + ((uint32_t)lane * 128u << a.page_shift);
+                            const CUtensorMap *map = kv ? &map_v : &map_k;
+                            if constexpr (ES == 2) {
+                                const uint32_t dst = saddr(ring + s * C::SLOT) + ((uint32_t)lane * 128u << a.page_shift);
 #pragma unroll
-                            for (int x = 0; x < C::BOXES; ++x)
-                                tma_load_2d(dst + x * kBoxBytes, kv ? &map_v : &map_k, x * 64, row, &full[s]);
+                                for (int x = 0; x < C::BOXES; ++x)
+                                    tma_load_2d(dst + x * kBoxBytes, map, x * 64, row, &landed[s]);
+                            } else {
+                                tma_load_2d(saddr(raws + s * C::RAW) + ((uint32_t)lane * D << a.page_shift), map, 0, row,
+                                            &landed[s]);
+                            }
                         }
                     }
                     row = next;
@@ -340,11 +386,11 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             }
             // every copy issued lands before the CTA may exit
 #pragma unroll
-            for (int s = 0; s < SLOTS; ++s)
-                if (seq > (uint32_t)s) bar_wait(&full[s], ((seq - 1 - s) / SLOTS) & 1u, a.status, &abort_flag, false);
+            for (int s = 0; s < N; ++s)
+                if (seq > (uint32_t)s) bar_wait(&landed[s], ((seq - 1 - s) / N) & 1u, a.status, &abort_flag, false);
         } else if (warp <= NSUB) {
             // ----------------------------- MMAs of sub-tile 0 (warp 1), 1 (warp 2) --
-            constexpr uint32_t id_qk = idesc_bf16(kKeys, false), id_pv = idesc_bf16(D, true);
+            constexpr uint32_t id_qk = idesc_16bit(ES == 2, kKeys, false), id_pv = idesc_16bit(ES == 2, D, true);
             const int t = warp - 1;
             const uint32_t s_col = tmem + t * kKeys, o_col = tmem + C::O_COL + t * D;
             uint32_t seq = 0, n_p = 0, n_seg = 0;  // slots, blocks and segments so far
@@ -387,9 +433,9 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     if (more) ok = ok && warp_wait(&full[kn], ((seq + 2) / SLOTS) & 1u, a.status, &abort_flag);
                     if (!ok) break;
                     // values behind the list's end may be anything, also NaN: zero them, their weights are zero too
-                    // (both warps write the same zeros, each before its own MMAs)
+                    // (both warps write the same zeros, each before its own MMAs; codes are zeroed when converted)
                     const int live = w.t.end - block_key<kKeys>(w.t, first + blk);
-                    if (live < kKeys) {
+                    if (ES == 2 && live < kKeys) {
                         const uint32_t base = saddr(ring + vs * C::SLOT);
                         for (int o = max(live, 0) * 8 + lane; o < kKeys * 8; o += 32)
 #pragma unroll
@@ -431,14 +477,55 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             while (w.next<kKeys>(a, C::ROWS)) note_segment(w, ci);
             info[blockIdx.x] = ci;
         }
+    } else if (warp >= 12) {
+        // -------------------------------------------- E4M3 codes to fp16 (exact) --
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CODES));
+        if constexpr (ES == 1) {
+            const int quarter = warp - 12;
+            uint32_t seq = 0;
+            bool ok = true;
+            while (ok && w.next<kKeys>(a, C::ROWS)) {
+                for (int blk = w.from(); ok && blk < w.to(); ++blk) {
+                    // codes behind the list's end may be anything: zeros (see the MMAs)
+                    const int live = w.t.end - block_key<kKeys>(w.t, blk);
+                    for (int kv = 0; ok && kv < 2; ++kv, ++seq) {
+                        const int s = (int)(seq % SLOTS), q = (int)(seq % RAWS);
+                        ok = warp_wait(&raw_full[q], (seq / RAWS) & 1u, a.status, &abort_flag) &&
+                             (seq < SLOTS || warp_wait(&empty[s], ((seq / SLOTS) - 1) & 1u, a.status, &abort_flag));
+                        if (!ok) break;
+                        const uint32_t from = saddr(raws + q * C::RAW), to = saddr(ring + s * C::SLOT);
+                        constexpr int CPR = D / 16;  // 16-byte chunks of codes per row
+#pragma unroll 4
+                        for (int o = quarter * 32 + lane; o < kKeys * CPR; o += 128) {
+                            const int key = o / CPR, c = o % CPR;
+                            uint4 v = lds16(from + o * 16);
+                            if (key >= live) v = make_uint4(0u, 0u, 0u, 0u);
+                            const uint32_t row = to + (c >> 2) * kBoxBytes + key * 128, x = (uint32_t)(c & 3) * 2;
+                            sts16(row + ((x ^ (key & 7)) << 4),
+                                  make_uint4(e4m3x2_to_f16x2(v.x & 0xFFFFu), e4m3x2_to_f16x2(v.x >> 16),
+                                             e4m3x2_to_f16x2(v.y & 0xFFFFu), e4m3x2_to_f16x2(v.y >> 16)));
+                            sts16(row + (((x + 1) ^ (key & 7)) << 4),
+                                  make_uint4(e4m3x2_to_f16x2(v.z & 0xFFFFu), e4m3x2_to_f16x2(v.z >> 16),
+                                             e4m3x2_to_f16x2(v.w & 0xFFFFu), e4m3x2_to_f16x2(v.w >> 16)));
+                        }
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            bar_arrive(&raw_empty[q]);
+                            bar_arrive(&full[s]);
+                        }
+                    }
+                }
+            }
+        }
     } else {
         // ------------------------------------------ softmax, queries, output --
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
         const int t = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;  // sub-tile, row of it
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + t * kKeys, o_addr = tmem + lanes + C::O_COL + t * D;
         // scores c x_s with c > 0: the queries take the sign, and all zeros for c = 0
-        const float c = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+        const float c_all = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
         uint32_t n_s = 0, n_o = 0;  // blocks, segments with blocks so far
         bool ok = t < NSUB;
@@ -449,23 +536,42 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
             // the row's own key; rows that are not there see nothing
             const int p = real ? w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows + row) : -1;
+            float c = c_all;
             // (every wait for this sub-tile's last block of the segment before has ended: Q is free)
             if (nb > 0) {
                 const int R = w.t.row0 + t * kSubRows + row, i = a.by_group(R), head = w.t.j * a.group + R - i * a.group;
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     a.Q + 2 * (((int64_t)a.q_start[w.t.b] + i) * a.q_stride + (int64_t)head * D));
                 const uint32_t dst = saddr(q_smem + t * C::QBYTES) + row * 128;
+                float down = 1.f;
+                if constexpr (ES == 1) {  // fp16 next to E4M3 keys, the row scaled by a power of two
+                    float largest = 0.f;
+                    if (real)
+#pragma unroll 8
+                        for (int x = 0; x < D / 8; ++x) {
+                            float f[8];
+                            bf16x8_to_f32(src[x], f);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) largest = fmaxf(largest, fabsf(f[e]));
+                        }
+                    const int E = row_exponent(largest);
+                    down = down_by(E);
+                    c = c_all * up_by(E);
+                }
 #pragma unroll 8
                 for (int x = 0; x < D / 8; ++x) {
                     uint4 v = real ? src[x] : make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (ES == 1) {
+                        float f[8];
+                        bf16x8_to_f32(v, f);
+                        v = make_uint4(pack_f16(f[0] * down, f[1] * down), pack_f16(f[2] * down, f[3] * down),
+                                       pack_f16(f[4] * down, f[5] * down), pack_f16(f[6] * down, f[7] * down));
+                    }
                     v.x = (v.x ^ flip) & keep;
                     v.y = (v.y ^ flip) & keep;
                     v.z = (v.z ^ flip) & keep;
                     v.w = (v.w ^ flip) & keep;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (x >> 3) * kBoxBytes +
-                                                                                   (((x & 7) ^ (row & 7)) << 4)),
-                                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                                 : "memory");
+                    sts16(dst + (x >> 3) * kBoxBytes + (((x & 7) ^ (row & 7)) << 4), v);
                 }
                 fence_async();
                 __syncwarp();
@@ -489,10 +595,14 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 wait_ld();
                 const int k0 = (first + blk + (first + blk < sink_blocks ? 0 : past_sinks)) * kKeys, k1 = k0 + kKeys - 1;
                 if (!(k1 <= whole_to && (k0 > whole_from || k1 < a.sinks))) {
+                    // bit x: key k0 + x is visible -- up to the row's own, and in its window or the first tokens
                     const int seen = p - k0, from = a.window > 0 ? seen - a.window : -1, sinks = a.sinks - k0;
 #pragma unroll
-                    for (int x = 0; x < kKeys; ++x)
-                        if (!(x <= seen && (x > from || x < sinks))) s[x] = -CUDART_INF_F;
+                    for (int x = 0; x < kKeys; x += 32) {
+                        const uint32_t ok = low_bits(seen + 1 - x) & (~low_bits(from + 1 - x) | low_bits(sinks - x));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[x + e] = ok >> e & 1u ? s[x + e] : -CUDART_INF_F;
+                    }
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -528,8 +638,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         v.x = exp2_approx(v.x);
                         v.y = exp2_approx(v.y);
                         sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
-                        // rounded to bf16, the type of the values in the product
-                        pk[e >> 1] = pack_bf16(v.x, v.y);
+                        // rounded to the type of the values in the product: bf16, or fp16 (11 bits)
+                        pk[e >> 1] = ES == 2 ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y);
                     }
                     tmem_st16(s_addr + (x >> 1), pk);
                 }
@@ -597,11 +707,11 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 // takes kJoin rows at a time, their loads in flight together.
 constexpr int kJoin = 4;
 
-template <int D>
+template <int D, int ES>
 __global__ void __launch_bounds__(256)
 k_chunk_combine(const AttnArgs a, const LineInfo *__restrict__ info)
 {
-    using C = Chunk<D>;
+    using C = Chunk<D, ES>;
     constexpr int E = D / 32;
     pdl_wait();
     const int c0 = (int)blockIdx.y, lane = threadIdx.x & 31;
@@ -676,30 +786,33 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// The pool as rows of head_dim bf16; boxes of 64 dims x one page.
+// The pool as rows of head_dim elements; boxes of one page x 64 bf16 dims
+// (swizzled) or all the codes of a row.
 bool make_map(CUtensorMap *map, const void *base, const AttnArgs &a)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) return false;
+    const bool bf16 = a.es == 2;
     const cuuint64_t dims[2] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_pages * a.page_size};
-    const cuuint64_t strides[1] = {(cuuint64_t)a.head_dim * 2};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)a.page_size};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.head_dim * a.es};
+    const cuuint32_t box[2] = {bf16 ? 64u : (cuuint32_t)a.head_dim, (cuuint32_t)a.page_size};
     const cuuint32_t estr[2] = {1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int ES>
 cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 {
-    using C = Chunk<D>;
+    using C = Chunk<D, ES>;
     CUtensorMap mk, mv;
     if (!make_map(&mk, a.k, a) || !make_map(&mv, a.v, a)) return cudaErrorUnknown;
-    cudaError_t e = cudaFuncSetAttribute(k_attend_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(k_attend_chunk<D, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     LineInfo *info = reinterpret_cast<LineInfo *>(a.part_ml + (int64_t)a.ctas * 2 * C::ROWS);
-    k_attend_chunk<D><<<a.ctas, kThreads, C::SMEM, st>>>(mk, mv, a, info);
+    k_attend_chunk<D, ES><<<a.ctas, C::THREADS, C::SMEM, st>>>(mk, mv, a, info);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(C::ROWS / (8 * kJoin)), (unsigned)a.ctas);
@@ -710,7 +823,7 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_chunk_combine<D>, a, (const LineInfo *)info);
+    return cudaLaunchKernelEx(&cfg, k_chunk_combine<D, ES>, a, (const LineInfo *)info);
 }
 
 }  // namespace
@@ -719,10 +832,11 @@ int chunk_tile_rows(int head_dim) { return head_dim == 256 ? kSubRows : 2 * kSub
 
 cudaError_t launch_attend_chunk(const AttnArgs &a, cudaStream_t st)
 {
+    const bool bf16 = a.es == 2;
     switch (a.head_dim) {
-    case 64: return launch_one<64>(a, st);
-    case 128: return launch_one<128>(a, st);
-    case 256: return launch_one<256>(a, st);
+    case 64: return bf16 ? launch_one<64, 2>(a, st) : launch_one<64, 1>(a, st);
+    case 128: return bf16 ? launch_one<128, 2>(a, st) : launch_one<128, 1>(a, st);
+    case 256: return bf16 ? launch_one<256, 2>(a, st) : launch_one<256, 1>(a, st);
     }
     return cudaErrorInvalidValue;
 }
