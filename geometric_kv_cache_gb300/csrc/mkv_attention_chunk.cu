@@ -6,7 +6,7 @@
 // A tile is NSUB x 128 packed rows (new token, query head of the KV head's
 // group) of one list; a block is 128 keys. Per block and sub-tile
 //     S = Q K^T          tcgen05.mma, M = 128, N = 128, fp32 in TMEM
-//     P = 2^(S c - m)    one thread per row, P rounded to bf16 over S in TMEM
+//     P = 2^(S c - m)    one or two threads per row, P rounded to 16 bits over S in TMEM
 //     O += P V           tcgen05.mma with P as the A operand from TMEM
 // with the row's maximum m allowed to lag: O is multiplied by 2^(m_old - m_new)
 // only when the maximum has grown by more than 2^8, so weights stay below 256
@@ -66,11 +66,19 @@ struct Chunk {
     static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 2) : (D == 64 ? 6 : D == 128 ? 3 : 2);
     static constexpr int QBYTES = SLOT;             // one sub-tile of queries has a block's shape
     static constexpr int SMEM = NSUB * QBYTES + SLOTS * SLOT + RAWS * RAW + 1024;
-    // 12 warps; 4 more expand E4M3 codes. Registers per thread of warps 0-3, of
-    // the softmax warps and of the expanding ones: in all what the launch has
-    // (384 x 168 or 512 x 128).
-    static constexpr int THREADS = ES == 2 ? 384 : 512;
-    static constexpr int REGS_FEED = ES == 2 ? 88 : 80, REGS_SOFT = ES == 2 ? 208 : 176, REGS_CODES = 80;
+    // Softmax threads per row, each with its share of the block's keys: two
+    // where registers and shared memory allow it.
+    static constexpr int HALVES = ES == 2 && D == 256 ? 2 : 1;
+    static constexpr int SOFT = NSUB * HALVES * 4;            // softmax warps, from warp 4 on
+    static constexpr int CODES = ES == 2 ? 0 : 4;             // warps that expand E4M3 codes, after them
+    static constexpr int THREADS = (4 + SOFT + CODES) * 32;   // 384, 512 or 640
+    // Registers per thread of warps 0-3, the softmax warps and the expanding
+    // ones: at most what the launch has (384 x 168, 512 x 128 or 640 x 96).
+    static constexpr int REGS_FEED = THREADS == 384 ? 88 : THREADS == 512 ? 80 : 64;
+    static constexpr int REGS_SOFT = THREADS == 384 ? 208 : THREADS == 512 ? 176 : 104;
+    static constexpr int REGS_CODES = 80;
+    static constexpr int REGS_LAUNCH = THREADS == 384 ? 168 : THREADS == 512 ? 128 : 96;
+    static_assert(4 * REGS_FEED + SOFT * REGS_SOFT + CODES * REGS_CODES <= THREADS / 32 * REGS_LAUNCH, "register split");
     static constexpr int TMEM = 512;
     static constexpr int O_COL = NSUB * kKeys;      // S of the sub-tiles, then O
 };
@@ -208,16 +216,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v)
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float *v)
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
-        "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
-        "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v)
 {
@@ -293,9 +299,12 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     uint8_t *ring = smem + NSUB * C::QBYTES;     // SLOTS blocks: K, V, K, V, ...
     uint8_t *raws = ring + SLOTS * C::SLOT;      // RAWS blocks of E4M3 codes, in the same order
     __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], raw_full[RAWS + 1], raw_empty[RAWS + 1], s_full[2], p_ready[2], o_done[2], o_free[2], q_full[2],
-        drain[2];
+        pair[2][4], drain[2];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t abort_flag;
+    // what the two threads of a row tell each other: the row's maximum over
+    // their keys (two buffers in turn), at the end their sums
+    __shared__ float s_pair[2][NSUB][C::HALVES][C::HALVES == 2 ? kSubRows : 1];
     __shared__ Walk s_walk[C::THREADS / 32];
     __shared__ LineScratch s_line;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -312,10 +321,11 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(&s_full[s], 1);
-            bar_init(&p_ready[s], 4);
+            bar_init(&p_ready[s], 4 * C::HALVES);
             bar_init(&o_done[s], 1);
-            bar_init(&o_free[s], 4);
-            bar_init(&q_full[s], 4);
+            bar_init(&o_free[s], 4 * C::HALVES);
+            bar_init(&q_full[s], 4 * C::HALVES);
+            for (int x = 0; x < 4; ++x) bar_init(&pair[s][x], 2);
         }
         bar_init(&drain[0], 1);
         bar_init(&drain[1], 1);
@@ -328,7 +338,21 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    Walk w = cut_line<kKeys, C::THREADS>(a, C::ROWS, kMinBlocks, s_line);
+    {
+        const Walk start = cut_line<kKeys, C::THREADS>(a, C::ROWS, kMinBlocks, s_line);
+        if (lane == 0) s_walk[warp] = start;
+    }
+    // A warp's walk lies in shared memory: registers are for the loops.
+    const Walk &w = s_walk[warp];
+    auto next_segment = [&]() -> bool {
+        __syncwarp();
+        Walk x = w;
+        __syncwarp();
+        const bool more = x.next<kKeys>(a, C::ROWS);
+        if (lane == 0) s_walk[warp] = x;
+        __syncwarp();
+        return more;
+    };
     fence_before();
     __syncthreads();
     fence_after();
@@ -344,7 +368,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             uint64_t *landed = ES == 2 ? full : raw_full, *taken = ES == 2 ? empty : raw_empty;
             uint32_t seq = 0;
             bool ok = true;
-            while (ok && w.next<kKeys>(a, C::ROWS)) {
+            while (ok && next_segment()) {
                 const int32_t *table = a.table + ((int64_t)w.t.b * a.heads + w.t.j) * a.max_pages;
                 const int last = w.to();
                 // the pool row of this lane's page of a block; past every row (zero fill) for a bad page, -1: none
@@ -404,7 +428,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 }
                 mma_commit(&s_full[t]);
             };
-            while (ok && w.next<kKeys>(a, C::ROWS)) {
+            while (ok && next_segment()) {
                 const int nb = w.to() - w.from();
                 if (nb == 0) continue;
                 if (t * kSubRows >= w.t.rows) {
@@ -471,20 +495,20 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 if (elect_one()) mma_commit(&drain[t]);
                 bar_wait(&drain[t], 0, a.status, &abort_flag, false);
             }
-        } else if (warp == 3 && lane == 0) {
+        } else if (warp == 3) {
             // -------------------------------------------- what the combine reads --
             LineInfo ci = {-1, 0};
-            while (w.next<kKeys>(a, C::ROWS)) note_segment(w, ci);
-            info[blockIdx.x] = ci;
+            while (next_segment()) note_segment(w, ci);
+            if (lane == 0) info[blockIdx.x] = ci;
         }
-    } else if (warp >= 12) {
+    } else if (warp >= 4 + C::SOFT) {
         // -------------------------------------------- E4M3 codes to fp16 (exact) --
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CODES));
         if constexpr (ES == 1) {
-            const int quarter = warp - 12;
+            const int quarter = warp - 4 - C::SOFT;
             uint32_t seq = 0;
             bool ok = true;
-            while (ok && w.next<kKeys>(a, C::ROWS)) {
+            while (ok && next_segment()) {
                 for (int blk = w.from(); ok && blk < w.to(); ++blk) {
                     // codes behind the list's end may be anything: zeros (see the MMAs)
                     const int live = w.t.end - block_key<kKeys>(w.t, blk);
@@ -521,15 +545,20 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     } else {
         // ------------------------------------------ softmax, queries, output --
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
-        const int t = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;  // sub-tile, row of it
+        constexpr int HALVES = C::HALVES, KH = kKeys / HALVES, DH = D / HALVES;  // this thread's keys of a block, dims of O
+        const int t = ((warp >> 2) - 1) / HALVES, half = ((warp >> 2) - 1) % HALVES;  // sub-tile, share of its rows
+        const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem + lanes + t * kKeys, o_addr = tmem + lanes + C::O_COL + t * D;
+        // the weights (16 bits) take the place of the scores of the first half of the keys
+        const uint32_t s_addr = tmem + lanes + t * kKeys + half * KH, p_addr = tmem + lanes + t * kKeys + half * (KH / 2);
+        const uint32_t o_addr = tmem + lanes + C::O_COL + t * D + half * DH;
+        uint64_t *mate = &pair[t][warp & 3];
         // scores c x_s with c > 0: the queries take the sign, and all zeros for c = 0
         const float c_all = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
-        uint32_t n_s = 0, n_o = 0;  // blocks, segments with blocks so far
-        bool ok = t < NSUB;
-        while (ok && w.next<kKeys>(a, C::ROWS)) {
+        uint32_t n_s = 0, n_o = 0, n_x = 0;  // blocks, segments with blocks, exchanges so far
+        bool ok = true;
+        while (ok && next_segment()) {
             if (t * kSubRows >= w.t.rows) continue;
             const bool real = t * kSubRows + row < w.t.rows;
             const int first = w.from(), nb = w.to() - first;
@@ -559,7 +588,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     c = c_all * up_by(E);
                 }
 #pragma unroll 8
-                for (int x = 0; x < D / 8; ++x) {
+                for (int x = half * (DH / 8); x < (half + 1) * (DH / 8); ++x) {
                     uint4 v = real ? src[x] : make_uint4(0u, 0u, 0u, 0u);
                     if constexpr (ES == 1) {
                         float f[8];
@@ -581,67 +610,89 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const int r_last = min(w.t.rows, (t + 1) * kSubRows) - 1;
             const int whole_to = w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows);
             const int whole_from = a.window > 0 ? w.t.L - w.t.n + a.by_group(w.t.row0 + r_last) - a.window : -1;
-            // what the loop does not need waits in shared memory: it has 128 scores to hold
-            if (lane == 0) s_walk[warp] = w;
-            __syncwarp();
             float m = -CUDART_INF_F, l = 0.f;
             for (int blk = 0; blk < nb; ++blk, ++n_s) {
                 ok = warp_wait(&s_full[t], n_s & 1u, a.status, &abort_flag);
                 if (!ok) break;
                 fence_after();
-                float s[kKeys];
+                float s[KH];
 #pragma unroll
-                for (int x = 0; x < kKeys; x += 32) tmem_ld32(s_addr + x, s + x);
+                for (int x = 0; x < KH; x += 32) tmem_ld32(s_addr + x, s + x);
                 wait_ld();
                 const int k0 = (first + blk + (first + blk < sink_blocks ? 0 : past_sinks)) * kKeys, k1 = k0 + kKeys - 1;
                 if (!(k1 <= whole_to && (k0 > whole_from || k1 < a.sinks))) {
-                    // bit x: key k0 + x is visible -- up to the row's own, and in its window or the first tokens
-                    const int seen = p - k0, from = a.window > 0 ? seen - a.window : -1, sinks = a.sinks - k0;
+                    // bit x: this thread's key x is visible -- up to the row's own, and in its window or the first tokens
+                    const int mine = k0 + half * KH;
+                    const int seen = p - mine, from = a.window > 0 ? seen - a.window : -1, sinks = a.sinks - mine;
 #pragma unroll
-                    for (int x = 0; x < kKeys; x += 32) {
-                        const uint32_t ok = low_bits(seen + 1 - x) & (~low_bits(from + 1 - x) | low_bits(sinks - x));
+                    for (int x = 0; x < KH; x += 32) {
+                        const uint32_t vis = low_bits(seen + 1 - x) & (~low_bits(from + 1 - x) | low_bits(sinks - x));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[x + e] = ok >> e & 1u ? s[x + e] : -CUDART_INF_F;
+                        for (int e = 0; e < 32; ++e) s[x + e] = vis >> e & 1u ? s[x + e] : -CUDART_INF_F;
                     }
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int x = 4; x < kKeys; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
-                const float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                const bool grow = best > m + kLag || (m == -CUDART_INF_F && best > m);
-                if (blk == 0) {
-                    m = best;
-                } else if (__any_sync(kFull, grow)) {
-                    const float f = !grow || m == -CUDART_INF_F ? (grow ? 0.f : 1.f) : exp2_approx(m - best);
-                    if (grow) m = best;
-                    l *= f;
-                    // (O is complete up to the block before: its MMAs came before the ones of these scores)
-#pragma unroll
-                    for (int x = 0; x < D; x += 32) {
-                        float o[32];
-                        tmem_ld32(o_addr + x, o);
-                        wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f;
-                        tmem_st32(o_addr + x, o);
-                    }
-                }
-                const float base = m == -CUDART_INF_F ? 0.f : m;
-                const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int x = 0; x < kKeys; x += 32) {
-                    uint32_t pk[16];
+                for (int x = 4; x < KH; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+                float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                float2 sum[2];
+                uint32_t pk[16];
+                // the weights of 32 keys under the maximum m, rounded to the type of the
+                // values in the product: bf16, or fp16 (11 bits)
+                auto weights = [&](int x) {
+                    const float base = m == -CUDART_INF_F ? 0.f : m;
+                    const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float2 v = fma2(make_float2(s[x + e], s[x + e + 1]), c2, b2);
                         v.x = exp2_approx(v.x);
                         v.y = exp2_approx(v.y);
                         sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
-                        // rounded to the type of the values in the product: bf16, or fp16 (11 bits)
                         pk[e >> 1] = ES == 2 ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y);
                     }
-                    tmem_st16(s_addr + (x >> 1), pk);
+                };
+                sum[0] = sum[1] = make_float2(0.f, 0.f);
+                if constexpr (HALVES == 2) {
+                    // The other thread's maximum; that both have read their scores also frees the place of the
+                    // weights. While the answer is on the way, 32 weights under the maximum so far: it rarely changes.
+                    float *told = &s_pair[n_x & 1][t][0][row];
+                    told[half * kSubRows] = best;
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(mate);
+                    if (blk > 0) weights(0);
+                    ok = warp_wait(mate, n_x++ & 1u, a.status, &abort_flag);
+                    if (!ok) break;
+                    fence_after();
+                    best = fmaxf(best, told[(1 - half) * kSubRows]);
+                }
+                const bool grow = best > m + kLag;
+                if (blk == 0) {
+                    m = best;
+                    weights(0);
+                } else if (__any_sync(kFull, grow)) {
+                    const float f = !grow ? 1.f : m == -CUDART_INF_F ? 0.f : exp2_approx(m - best);
+                    if (grow) m = best;
+                    l *= f;
+                    // (O is complete up to the block before: its MMAs came before the ones of these scores)
+#pragma unroll
+                    for (int x = 0; x < DH; x += 16) {
+                        tmem_ld16(o_addr + x, pk);
+                        wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = __float_as_uint(__uint_as_float(pk[e]) * f);
+                        tmem_st16(o_addr + x, pk);
+                    }
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
+                    weights(0);
+                } else if (HALVES == 1) {
+                    weights(0);
+                }
+                tmem_st16(p_addr, pk);
+#pragma unroll
+                for (int x = 32; x < KH; x += 32) {
+                    weights(x);
+                    tmem_st16(p_addr + (x >> 1), pk);
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
@@ -652,20 +703,28 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             }
             if (!ok) break;
             if (nb > 0) {
+                if constexpr (HALVES == 2) {  // the row's sum
+                    float *told = &s_pair[n_x & 1][t][0][row];
+                    told[half * kSubRows] = l;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(mate);
+                    ok = warp_wait(mate, n_x++ & 1u, a.status, &abort_flag);
+                    if (!ok) break;
+                    l += told[(1 - half) * kSubRows];
+                }
                 ok = warp_wait(&o_done[t], n_o++ & 1u, a.status, &abort_flag);
                 if (!ok) break;
                 fence_after();
             }
-            w = s_walk[warp];
             const int R = w.t.row0 + t * kSubRows + row, i = a.by_group(R), head = w.t.j * a.group + R - i * a.group;
             const int64_t token = (int64_t)a.q_start[w.t.b] + i;
             const bool whole = w.whole();
             const int64_t part = part_row(w, C::ROWS) + t * kSubRows + row;
             const float inv = l > 0.f ? a.v_scale / l : 0.f;
-            uint4 *dst = reinterpret_cast<uint4 *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D));
-            float4 *dst_part = reinterpret_cast<float4 *>(a.part_o + part * D);
+            uint4 *dst = reinterpret_cast<uint4 *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + half * DH));
+            float4 *dst_part = reinterpret_cast<float4 *>(a.part_o + part * D + half * DH);
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
+            for (int x = 0; x < DH; x += 32) {
                 float o[32];
                 if (nb > 0) {
                     tmem_ld32(o_addr + x, o);
@@ -685,9 +744,9 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 }
                 __syncwarp();
             }
-            if (real && whole && a.lse)
+            if (real && whole && half == 0 && a.lse)
                 a.lse[token * a.q_heads + head] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
-            if (real && !whole) a.part_ml[part] = make_float2(m, l);
+            if (real && !whole && half == 0) a.part_ml[part] = make_float2(m, l);
             if (nb > 0) {
                 fence_before();
                 __syncwarp();
