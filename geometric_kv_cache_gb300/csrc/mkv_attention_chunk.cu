@@ -6,13 +6,13 @@
 // A tile is NSUB x 128 packed rows (new token, query head of the KV head's
 // group) of one list; a block is 128 keys. Per block and sub-tile
 //     S = Q K^T          tcgen05.mma, M = 128, N = 128, fp32 in TMEM
-//     P = 2^(S c - m)    one or two threads per row, P rounded to 16 bits over S in TMEM
+//     P = 2^(S c - m)    one thread per row, P rounded to 16 bits over S in TMEM
 //     O += P V           tcgen05.mma with P as the A operand from TMEM
 // with the row's maximum m allowed to lag: O is multiplied by 2^(m_old - m_new)
 // only when the maximum has grown by more than 2^8, so weights stay below 256
 // and the rescaling, which has to wait for the tensor core, is rare.
 //
-// Roles (12 warps, one CTA per SM): warp 0 brings the pages of K and V blocks
+// Roles (one CTA per SM): warps 0 and 3 bring the pages of K and of V blocks
 // into a ring of shared-memory slots (TMA, 128-byte swizzle, one box of 64 dims
 // per page, page entries read a block ahead); warps 1 and 2 issue the MMAs of
 // sub-tile 0 and 1, so that the tensor core works on one while the other waits
@@ -48,9 +48,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kKeys = 128;                   // keys per block
 constexpr int kSubRows = 128;                // rows per sub-tile: the MMA's M, the TMEM lanes
-constexpr int kBoxBytes = kKeys * 128;       // 64 dims of a block: 128 rows of 128 bytes
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLag = 8.f;                  // log2 of how far a row's maximum may lag
 constexpr int kMinBlocks = 4;                // blocks that make a CTA worth its start
@@ -59,28 +57,30 @@ template <int D, int ES>
 struct Chunk {
     static constexpr int NSUB = D == 256 ? 1 : 2;  // O of two sub-tiles fits the 512 TMEM columns up to D = 128
     static constexpr int ROWS = NSUB * kSubRows;
+    // Keys per block: 128; 64 at 256 dims, where shared memory then holds five
+    // blocks instead of two and the copies run ahead.
+    static constexpr int KEYS = D == 256 ? 64 : 128;
     static constexpr int BOXES = D / 64;
-    static constexpr int SLOT = BOXES * kBoxBytes;  // one block of K or of V as the MMA reads it
-    static constexpr int RAW = kKeys * D;           // ... as E4M3 codes
-    static constexpr int RAWS = ES == 2 ? 0 : D == 256 ? 1 : 3;
-    static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 2) : (D == 64 ? 6 : D == 128 ? 3 : 2);
-    static constexpr int QBYTES = SLOT;             // one sub-tile of queries has a block's shape
+    static constexpr int BOX = KEYS * 128;          // 64 dims of a block: rows of 128 bytes
+    static constexpr int SLOT = BOXES * BOX;        // one block of K or of V as the MMA reads it
+    static constexpr int RAW = KEYS * D;            // ... as E4M3 codes
+    static constexpr int RAWS = ES == 2 ? 0 : D == 256 ? 2 : 3;
+    static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 5) : (D == 64 ? 9 : D == 128 ? 3 : 4);
+    static constexpr int QBOX = kSubRows * 128;
+    static constexpr int QBYTES = BOXES * QBOX;     // one sub-tile of queries
     static constexpr int SMEM = NSUB * QBYTES + SLOTS * SLOT + RAWS * RAW + 1024;
-    // Softmax threads per row, each with its share of the block's keys: two
-    // where registers and shared memory allow it.
-    static constexpr int HALVES = ES == 2 && D == 256 ? 2 : 1;
-    static constexpr int SOFT = NSUB * HALVES * 4;            // softmax warps, from warp 4 on
+    static constexpr int SOFT = NSUB * 4;                     // softmax warps, from warp 4 on
     static constexpr int CODES = ES == 2 ? 0 : 4;             // warps that expand E4M3 codes, after them
-    static constexpr int THREADS = (4 + SOFT + CODES) * 32;   // 384, 512 or 640
+    static constexpr int THREADS = (4 + SOFT + CODES) * 32;   // 256, 384 or 512
     // Registers per thread of warps 0-3, the softmax warps and the expanding
-    // ones: at most what the launch has (384 x 168, 512 x 128 or 640 x 96).
-    static constexpr int REGS_FEED = THREADS == 384 ? 88 : THREADS == 512 ? 80 : 64;
-    static constexpr int REGS_SOFT = THREADS == 384 ? 208 : THREADS == 512 ? 176 : 104;
+    // ones: at most what the launch has (256 x 224, 384 x 168 or 512 x 128).
+    static constexpr int REGS_FEED = THREADS == 256 ? 168 : THREADS == 384 ? 88 : 80;
+    static constexpr int REGS_SOFT = THREADS == 256 ? 240 : THREADS == 384 ? 208 : 176;
     static constexpr int REGS_CODES = 80;
-    static constexpr int REGS_LAUNCH = THREADS == 384 ? 168 : THREADS == 512 ? 128 : 96;
+    static constexpr int REGS_LAUNCH = THREADS == 256 ? 224 : THREADS == 384 ? 168 : 128;
     static_assert(4 * REGS_FEED + SOFT * REGS_SOFT + CODES * REGS_CODES <= THREADS / 32 * REGS_LAUNCH, "register split");
     static constexpr int TMEM = 512;
-    static constexpr int O_COL = NSUB * kKeys;      // S of the sub-tiles, then O
+    static constexpr int O_COL = NSUB * KEYS;      // S of the sub-tiles, then O
 };
 
 __device__ __forceinline__ uint32_t saddr(const void *p)
@@ -151,9 +151,10 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t addr)
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+template <int BOX>
 __device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
 {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kBoxBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(BOX >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
@@ -292,19 +293,16 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                LineInfo *info)
 {
     using C = Chunk<D, ES>;
-    constexpr int NSUB = C::NSUB, SLOTS = C::SLOTS, RAWS = C::RAWS;
+    constexpr int NSUB = C::NSUB, SLOTS = C::SLOTS, RAWS = C::RAWS, kKeys = C::KEYS, kBoxBytes = C::BOX;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *q_smem = smem;                      // NSUB x [D / 64 boxes][128 rows x 128 B]
     uint8_t *ring = smem + NSUB * C::QBYTES;     // SLOTS blocks: K, V, K, V, ...
     uint8_t *raws = ring + SLOTS * C::SLOT;      // RAWS blocks of E4M3 codes, in the same order
     __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], raw_full[RAWS + 1], raw_empty[RAWS + 1], s_full[2], p_ready[2], o_done[2], o_free[2], q_full[2],
-        pair[2][4], drain[2];
+        drain[2];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t abort_flag;
-    // what the two threads of a row tell each other: the row's maximum over
-    // their keys (two buffers in turn), at the end their sums
-    __shared__ float s_pair[2][NSUB][C::HALVES][C::HALVES == 2 ? kSubRows : 1];
     __shared__ Walk s_walk[C::THREADS / 32];
     __shared__ LineScratch s_line;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -321,11 +319,10 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         }
         for (int s = 0; s < 2; ++s) {
             bar_init(&s_full[s], 1);
-            bar_init(&p_ready[s], 4 * C::HALVES);
+            bar_init(&p_ready[s], 4);
             bar_init(&o_done[s], 1);
-            bar_init(&o_free[s], 4 * C::HALVES);
-            bar_init(&q_full[s], 4 * C::HALVES);
-            for (int x = 0; x < 4; ++x) bar_init(&pair[s][x], 2);
+            bar_init(&o_free[s], 4);
+            bar_init(&q_full[s], 4);
         }
         bar_init(&drain[0], 1);
         bar_init(&drain[1], 1);
@@ -360,58 +357,60 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_FEED));
-        if (warp == 0) {
-            // ---------------------------------------------------- pages of K and V --
-            const int per_block = kKeys >> a.page_shift;  // pages of a block: one lane each
+        if (warp == 0 || warp == 3) {
+            // -------------------------- pages of K (warp 0) and of V (warp 3) --
+            const int kv = warp == 0 ? 0 : 1;
+            const CUtensorMap *map = kv ? &map_v : &map_k;
+            // boxes of a page's rows, or of a block's if that is less: one lane each
+            const int box_shift = min(a.page_shift, kKeys == 64 ? 6 : 7), per_block = kKeys >> box_shift;
             // the ring that the copies land in: the MMAs' slots, or the codes
             constexpr int N = ES == 2 ? SLOTS : RAWS;
             uint64_t *landed = ES == 2 ? full : raw_full, *taken = ES == 2 ? empty : raw_empty;
-            uint32_t seq = 0;
+            LineInfo ci = {-1, 0};
+            uint32_t seq = kv;  // K blocks take the even places of the ring's order, V blocks the odd ones
             bool ok = true;
-            while (ok && next_segment()) {
+            while (next_segment()) {
+                note_segment(w, ci);
                 const int32_t *table = a.table + ((int64_t)w.t.b * a.heads + w.t.j) * a.max_pages;
-                const int last = w.to();
-                // the pool row of this lane's page of a block; past every row (zero fill) for a bad page, -1: none
+                const int from = w.from(), to = w.to(), end = w.t.end;
+                const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
+                // the pool row of this lane's box of a block; past every row (zero fill) for a bad page, -1: none
                 auto lookup = [&](int blk) -> int {
-                    const int key = block_key<kKeys>(w.t, blk) + (lane << a.page_shift);
-                    if (blk >= last || lane >= per_block || key >= w.t.end) return -1;
+                    const int key = (blk + (blk < sink_blocks ? 0 : past_sinks)) * kKeys + (lane << box_shift);
+                    if (blk >= to || lane >= per_block || key >= end) return -1;
                     const int id = table[key >> a.page_shift];
                     if ((uint32_t)id >= (uint32_t)a.n_pages) {
                         atomicOr(a.status, MKV_DEV_BAD_PAGE);
                         return a.n_pages << a.page_shift;
                     }
-                    return id << a.page_shift;
+                    return (id << a.page_shift) + (key & (a.page_size - 1));
                 };
-                int row = lookup(w.first);
-                for (int blk = w.first; ok && blk < last; ++blk) {
-                    const int next = lookup(blk + 1);
-                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, row >= 0)) * D * ES) << a.page_shift;
-                    for (int kv = 0; kv < 2; ++kv, ++seq) {
-                        const int s = (int)(seq % N);
-                        ok = seq < N || warp_wait(&taken[s], ((seq / N) - 1) & 1u, a.status, &abort_flag);
-                        if (!ok) break;
-                        if (lane == 0) bar_expect(&landed[s], bytes);
-                        __syncwarp();
-                        if (row >= 0) {
-                            const CUtensorMap *map = kv ? &map_v : &map_k;
-                            if constexpr (ES == 2) {
-                                const uint32_t dst = saddr(ring + s * C::SLOT) + ((uint32_t)lane * 128u << a.page_shift);
+                int row = lookup(from);
+                for (int blk = from; ok && blk < to; ++blk, seq += 2) {
+                    const int next = lookup(blk + 1), s = (int)(seq % N);
+                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, row >= 0)) * D * ES) << box_shift;
+                    ok = seq < N || warp_wait(&taken[s], ((seq / N) - 1) & 1u, a.status, &abort_flag);
+                    if (!ok) break;
+                    if (lane == 0) bar_expect(&landed[s], bytes);
+                    __syncwarp();
+                    if (row >= 0) {
+                        if constexpr (ES == 2) {
+                            const uint32_t dst = saddr(ring + s * C::SLOT) + ((uint32_t)lane * 128u << box_shift);
 #pragma unroll
-                                for (int x = 0; x < C::BOXES; ++x)
-                                    tma_load_2d(dst + x * kBoxBytes, map, x * 64, row, &landed[s]);
-                            } else {
-                                tma_load_2d(saddr(raws + s * C::RAW) + ((uint32_t)lane * D << a.page_shift), map, 0, row,
-                                            &landed[s]);
-                            }
+                            for (int x = 0; x < C::BOXES; ++x)
+                                tma_load_2d(dst + x * kBoxBytes, map, x * 64, row, &landed[s]);
+                        } else {
+                            tma_load_2d(saddr(raws + s * C::RAW) + ((uint32_t)lane * D << box_shift), map, 0, row, &landed[s]);
                         }
                     }
                     row = next;
                 }
+                if (!ok) break;
             }
-            // every copy issued lands before the CTA may exit
-#pragma unroll
-            for (int s = 0; s < N; ++s)
-                if (seq > (uint32_t)s) bar_wait(&landed[s], ((seq - 1 - s) / N) & 1u, a.status, &abort_flag, false);
+            if (warp == 0 && lane == 0) info[blockIdx.x] = ci;
+            // every copy issued lands before the CTA may exit (the last uses of the ring's places)
+            for (int x = (int)seq - 2; x >= 0 && x >= (int)seq - kv - N; x -= 2)
+                bar_wait(&landed[x % N], (uint32_t)(x / N) & 1u, a.status, &abort_flag, false);
         } else if (warp <= NSUB) {
             // ----------------------------- MMAs of sub-tile 0 (warp 1), 1 (warp 2) --
             constexpr uint32_t id_qk = idesc_16bit(ES == 2, kKeys, false), id_pv = idesc_16bit(ES == 2, D, true);
@@ -423,8 +422,9 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 const uint64_t qd = desc_k(saddr(q_smem + t * C::QBYTES)), kd = desc_k(saddr(ring + slot * C::SLOT));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t step = (uint64_t)(((k >> 2) * kBoxBytes + (k & 3) * 32) >> 4);
-                    mma_ss(s_col, qd + step, kd + step, id_qk, k > 0);
+                    const uint32_t in_row = (k & 3) * 32;
+                    mma_ss(s_col, qd + (uint64_t)(((k >> 2) * C::QBOX + in_row) >> 4),
+                           kd + (uint64_t)(((k >> 2) * kBoxBytes + in_row) >> 4), id_qk, k > 0);
                 }
                 mma_commit(&s_full[t]);
             };
@@ -475,7 +475,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     if (!ok) break;
                     fence_after();
                     if (elect_one()) {
-                        const uint64_t vd = desc_mn(saddr(ring + vs * C::SLOT));
+                        const uint64_t vd = desc_mn<kBoxBytes>(saddr(ring + vs * C::SLOT));
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)
                             mma_ts(o_col, s_col + k * 8, vd + (uint64_t)(k * 2048 >> 4), id_pv, blk > 0 || k > 0);
@@ -495,11 +495,6 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 if (elect_one()) mma_commit(&drain[t]);
                 bar_wait(&drain[t], 0, a.status, &abort_flag, false);
             }
-        } else if (warp == 3) {
-            // -------------------------------------------- what the combine reads --
-            LineInfo ci = {-1, 0};
-            while (next_segment()) note_segment(w, ci);
-            if (lane == 0) info[blockIdx.x] = ci;
         }
     } else if (warp >= 4 + C::SOFT) {
         // -------------------------------------------- E4M3 codes to fp16 (exact) --
@@ -545,18 +540,13 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     } else {
         // ------------------------------------------ softmax, queries, output --
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
-        constexpr int HALVES = C::HALVES, KH = kKeys / HALVES, DH = D / HALVES;  // this thread's keys of a block, dims of O
-        const int t = ((warp >> 2) - 1) / HALVES, half = ((warp >> 2) - 1) % HALVES;  // sub-tile, share of its rows
-        const int row = (warp & 3) * 32 + lane;
+        const int t = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;  // sub-tile, row of it
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        // the weights (16 bits) take the place of the scores of the first half of the keys
-        const uint32_t s_addr = tmem + lanes + t * kKeys + half * KH, p_addr = tmem + lanes + t * kKeys + half * (KH / 2);
-        const uint32_t o_addr = tmem + lanes + C::O_COL + t * D + half * DH;
-        uint64_t *mate = &pair[t][warp & 3];
+        const uint32_t s_addr = tmem + lanes + t * kKeys, o_addr = tmem + lanes + C::O_COL + t * D;
         // scores c x_s with c > 0: the queries take the sign, and all zeros for c = 0
         const float c_all = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
-        uint32_t n_s = 0, n_o = 0, n_x = 0;  // blocks, segments with blocks, exchanges so far
+        uint32_t n_s = 0, n_o = 0;  // blocks, segments with blocks so far
         bool ok = true;
         while (ok && next_segment()) {
             if (t * kSubRows >= w.t.rows) continue;
@@ -588,7 +578,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     c = c_all * up_by(E);
                 }
 #pragma unroll 8
-                for (int x = half * (DH / 8); x < (half + 1) * (DH / 8); ++x) {
+                for (int x = 0; x < D / 8; ++x) {
                     uint4 v = real ? src[x] : make_uint4(0u, 0u, 0u, 0u);
                     if constexpr (ES == 1) {
                         float f[8];
@@ -600,7 +590,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     v.y = (v.y ^ flip) & keep;
                     v.z = (v.z ^ flip) & keep;
                     v.w = (v.w ^ flip) & keep;
-                    sts16(dst + (x >> 3) * kBoxBytes + (((x & 7) ^ (row & 7)) << 4), v);
+                    sts16(dst + (x >> 3) * C::QBOX + (((x & 7) ^ (row & 7)) << 4), v);
                 }
                 fence_async();
                 __syncwarp();
@@ -615,17 +605,16 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 ok = warp_wait(&s_full[t], n_s & 1u, a.status, &abort_flag);
                 if (!ok) break;
                 fence_after();
-                float s[KH];
+                float s[kKeys];
 #pragma unroll
-                for (int x = 0; x < KH; x += 32) tmem_ld32(s_addr + x, s + x);
+                for (int x = 0; x < kKeys; x += 32) tmem_ld32(s_addr + x, s + x);
                 wait_ld();
                 const int k0 = (first + blk + (first + blk < sink_blocks ? 0 : past_sinks)) * kKeys, k1 = k0 + kKeys - 1;
                 if (!(k1 <= whole_to && (k0 > whole_from || k1 < a.sinks))) {
-                    // bit x: this thread's key x is visible -- up to the row's own, and in its window or the first tokens
-                    const int mine = k0 + half * KH;
-                    const int seen = p - mine, from = a.window > 0 ? seen - a.window : -1, sinks = a.sinks - mine;
+                    // bit x: key k0 + x is visible -- up to the row's own, and in its window or the first tokens
+                    const int seen = p - k0, from = a.window > 0 ? seen - a.window : -1, sinks = a.sinks - k0;
 #pragma unroll
-                    for (int x = 0; x < KH; x += 32) {
+                    for (int x = 0; x < kKeys; x += 32) {
                         const uint32_t vis = low_bits(seen + 1 - x) & (~low_bits(from + 1 - x) | low_bits(sinks - x));
 #pragma unroll
                         for (int e = 0; e < 32; ++e) s[x + e] = vis >> e & 1u ? s[x + e] : -CUDART_INF_F;
@@ -633,15 +622,33 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int x = 4; x < KH; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
-                float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                float2 sum[2];
+                for (int x = 4; x < kKeys; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
+                const float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 uint32_t pk[16];
-                // the weights of 32 keys under the maximum m, rounded to the type of the
-                // values in the product: bf16, or fp16 (11 bits)
-                auto weights = [&](int x) {
-                    const float base = m == -CUDART_INF_F ? 0.f : m;
-                    const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                const bool grow = best > m + kLag;
+                if (blk == 0) {
+                    m = best;
+                } else if (__any_sync(kFull, grow)) {
+                    const float f = !grow ? 1.f : m == -CUDART_INF_F ? 0.f : exp2_approx(m - best);
+                    if (grow) m = best;
+                    l *= f;
+                    // (O is complete up to the block before: its MMAs came before the ones of these scores)
+#pragma unroll
+                    for (int x = 0; x < D; x += 16) {
+                        tmem_ld16(o_addr + x, pk);
+                        wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = __float_as_uint(__uint_as_float(pk[e]) * f);
+                        tmem_st16(o_addr + x, pk);
+                    }
+                }
+                // the weights under the maximum m, rounded to the type of the values in the
+                // product: bf16, or fp16 (11 bits)
+                const float base = m == -CUDART_INF_F ? 0.f : m;
+                const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int x = 0; x < kKeys; x += 32) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         float2 v = fma2(make_float2(s[x + e], s[x + e + 1]), c2, b2);
@@ -650,49 +657,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
                         pk[e >> 1] = ES == 2 ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y);
                     }
-                };
-                sum[0] = sum[1] = make_float2(0.f, 0.f);
-                if constexpr (HALVES == 2) {
-                    // The other thread's maximum; that both have read their scores also frees the place of the
-                    // weights. While the answer is on the way, 32 weights under the maximum so far: it rarely changes.
-                    float *told = &s_pair[n_x & 1][t][0][row];
-                    told[half * kSubRows] = best;
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(mate);
-                    if (blk > 0) weights(0);
-                    ok = warp_wait(mate, n_x++ & 1u, a.status, &abort_flag);
-                    if (!ok) break;
-                    fence_after();
-                    best = fmaxf(best, told[(1 - half) * kSubRows]);
-                }
-                const bool grow = best > m + kLag;
-                if (blk == 0) {
-                    m = best;
-                    weights(0);
-                } else if (__any_sync(kFull, grow)) {
-                    const float f = !grow ? 1.f : m == -CUDART_INF_F ? 0.f : exp2_approx(m - best);
-                    if (grow) m = best;
-                    l *= f;
-                    // (O is complete up to the block before: its MMAs came before the ones of these scores)
-#pragma unroll
-                    for (int x = 0; x < DH; x += 16) {
-                        tmem_ld16(o_addr + x, pk);
-                        wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = __float_as_uint(__uint_as_float(pk[e]) * f);
-                        tmem_st16(o_addr + x, pk);
-                    }
-                    sum[0] = sum[1] = make_float2(0.f, 0.f);
-                    weights(0);
-                } else if (HALVES == 1) {
-                    weights(0);
-                }
-                tmem_st16(p_addr, pk);
-#pragma unroll
-                for (int x = 32; x < KH; x += 32) {
-                    weights(x);
-                    tmem_st16(p_addr + (x >> 1), pk);
+                    tmem_st16(s_addr + (x >> 1), pk);
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
@@ -703,15 +668,6 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             }
             if (!ok) break;
             if (nb > 0) {
-                if constexpr (HALVES == 2) {  // the row's sum
-                    float *told = &s_pair[n_x & 1][t][0][row];
-                    told[half * kSubRows] = l;
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(mate);
-                    ok = warp_wait(mate, n_x++ & 1u, a.status, &abort_flag);
-                    if (!ok) break;
-                    l += told[(1 - half) * kSubRows];
-                }
                 ok = warp_wait(&o_done[t], n_o++ & 1u, a.status, &abort_flag);
                 if (!ok) break;
                 fence_after();
@@ -721,10 +677,10 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const bool whole = w.whole();
             const int64_t part = part_row(w, C::ROWS) + t * kSubRows + row;
             const float inv = l > 0.f ? a.v_scale / l : 0.f;
-            uint4 *dst = reinterpret_cast<uint4 *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + half * DH));
-            float4 *dst_part = reinterpret_cast<float4 *>(a.part_o + part * D + half * DH);
+            uint4 *dst = reinterpret_cast<uint4 *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D));
+            float4 *dst_part = reinterpret_cast<float4 *>(a.part_o + part * D);
 #pragma unroll 1
-            for (int x = 0; x < DH; x += 32) {
+            for (int x = 0; x < D; x += 32) {
                 float o[32];
                 if (nb > 0) {
                     tmem_ld32(o_addr + x, o);
@@ -744,9 +700,9 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 }
                 __syncwarp();
             }
-            if (real && whole && half == 0 && a.lse)
+            if (real && whole && a.lse)
                 a.lse[token * a.q_heads + head] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
-            if (real && !whole && half == 0) a.part_ml[part] = make_float2(m, l);
+            if (real && !whole) a.part_ml[part] = make_float2(m, l);
             if (nb > 0) {
                 fence_before();
                 __syncwarp();
@@ -777,7 +733,7 @@ k_chunk_combine(const AttnArgs a, const LineInfo *__restrict__ info)
     int c1;
     const int tile = opened_tile(info, c0, (int)gridDim.y, c1);
     if (tile < 0) return;
-    const Tile t = make_tile<kKeys>(a, tile, C::ROWS, false);
+    const Tile t = make_tile<C::KEYS>(a, tile, C::ROWS, false);
     const int row0 = ((int)blockIdx.x * 8 + (threadIdx.x >> 5)) * kJoin;
     if (row0 >= t.rows) return;
     float sum[kJoin][E], l[kJoin], M[kJoin];
@@ -845,16 +801,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// The pool as rows of head_dim elements; boxes of one page x 64 bf16 dims
-// (swizzled) or all the codes of a row.
-bool make_map(CUtensorMap *map, const void *base, const AttnArgs &a)
+// The pool as rows of head_dim elements; boxes of one page (of a block's keys
+// if that is less) x 64 bf16 dims (swizzled) or all the codes of a row.
+bool make_map(CUtensorMap *map, const void *base, const AttnArgs &a, int32_t keys)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
     if (!enc) return false;
     const bool bf16 = a.es == 2;
     const cuuint64_t dims[2] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_pages * a.page_size};
     const cuuint64_t strides[1] = {(cuuint64_t)a.head_dim * a.es};
-    const cuuint32_t box[2] = {bf16 ? 64u : (cuuint32_t)a.head_dim, (cuuint32_t)a.page_size};
+    const cuuint32_t box[2] = {bf16 ? 64u : (cuuint32_t)a.head_dim, (cuuint32_t)std::min(a.page_size, keys)};
     const cuuint32_t estr[2] = {1u, 1u};
     return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -867,7 +823,7 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 {
     using C = Chunk<D, ES>;
     CUtensorMap mk, mv;
-    if (!make_map(&mk, a.k, a) || !make_map(&mv, a.v, a)) return cudaErrorUnknown;
+    if (!make_map(&mk, a.k, a, C::KEYS) || !make_map(&mv, a.v, a, C::KEYS)) return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(k_attend_chunk<D, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     LineInfo *info = reinterpret_cast<LineInfo *>(a.part_ml + (int64_t)a.ctas * 2 * C::ROWS);
