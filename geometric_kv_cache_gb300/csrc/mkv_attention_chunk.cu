@@ -553,8 +553,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const bool real = t * kSubRows + row < w.t.rows;
             const int first = w.from(), nb = w.to() - first;
             const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
-            // the row's own key; rows that are not there see nothing
-            const int p = real ? w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows + row) : -1;
+            // the row's own key (of rows that are not there: the first row's)
+            const int p = w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows + (real ? row : 0));
             float c = c_all;
             // (every wait for this sub-tile's last block of the segment before has ended: Q is free)
             if (nb > 0) {

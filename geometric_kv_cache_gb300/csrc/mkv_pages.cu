@@ -32,7 +32,6 @@ namespace {
 using namespace dev;
 
 constexpr int kPageThreads = 256;
-constexpr int kCopyRows = 32;  // output tokens per item of the compaction: one per lane
 
 __device__ __forceinline__ int pages_of(int len, const PageArgs &a)
 {
@@ -249,7 +248,8 @@ k_page_assign(const PageArgs a)
     block_sums(need, free_pages, before, bits);
     if (need > free_pages) bits |= MKV_DEV_NO_PAGES;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        *a.verdict = bits;
+        a.verdict[0] = bits;
+        a.verdict[1] = bits ? 0u : (uint32_t)need;  // pages taken
         if (bits) atomicOr(a.status, bits);
     }
     if (rows) {
@@ -335,7 +335,7 @@ k_page_update(const PageArgs a)
     int32_t *out = a.table_out + h * a.max_pages;
     // (read together; the last two mean nothing after a bad verdict)
     const int own_len = a.lens[h];
-    const uint32_t verdict = *a.verdict;
+    const uint32_t verdict = a.verdict[0];
     const int2 src = a.row_src[b];
     const int first = a.list_off[h];
     if (verdict) {  // the lists stay as they were
@@ -394,20 +394,22 @@ k_page_update(const PageArgs a)
 }
 
 // The first `list_ctas` CTAs write tables and counts, list by list; the warps
-// of the others copy rows. Item = (list, block of 32 output tokens), one warp,
-// one lane per token for its places: an item's indices are read two items
-// ahead and its page entries one ahead, so that every row copy (groups of LPR
-// lanes, 16 bytes each, 8 rows of K and of V in flight per lane) finds its
-// addresses in registers.
+// of the others copy rows. The new pages stand in one line (rank: the place in
+// free_ids), cut into equal runs, one per warp, whatever the lists' lengths.
+// Item = a page's tokens, 32 at most, one lane per token for its places: an
+// item's indices are read two items ahead and its page entries one ahead, so
+// that every row copy (groups of LPR lanes, 16 bytes each, 8 rows of K and of V
+// in flight per lane) finds its addresses in registers.
 template <int LPR>
 __global__ void __launch_bounds__(kPageThreads, 2)
-k_page_compact(const PageArgs a, int blocks, int64_t n_items, int list_ctas)
+k_page_compact(const PageArgs a, int list_ctas)
 {
     constexpr int RB = LPR * 16, RPS = 32 / LPR, B = LPR < 8 ? LPR : 8;  // rows per step, steps per batch
     pdl_wait();
-    const bool bad = *a.verdict != 0;
+    const bool bad = a.verdict[0] != 0;
+    const int64_t lists = (int64_t)a.batch * a.heads;
     if ((int)blockIdx.x < list_ctas) {
-        for (int64_t h = blockIdx.x; h < (int64_t)a.batch * a.heads; h += list_ctas) {
+        for (int64_t h = blockIdx.x; h < lists; h += list_ctas) {
             const int own_len = a.lens[h], n = bad ? 0 : a.kept[h], first = bad ? 0 : a.list_off[h];
             const int32_t *mine = a.table + h * a.max_pages;
             int32_t *out = a.table_out + h * a.max_pages;
@@ -427,73 +429,104 @@ k_page_compact(const PageArgs a, int blocks, int64_t n_items, int list_ctas)
     }
     if (bad) return;
     const int lane = threadIdx.x & 31, g = lane / LPR, lr = lane % LPR;
+    const int per_shift = max(a.page_shift - 5, 0), tokens = min(a.page_size, 32);  // items of a page, tokens of an item
     const int64_t warps = (int64_t)(gridDim.x - list_ctas) * (kPageThreads / 32);
-    const int64_t item0 = (int64_t)(blockIdx.x - list_ctas) * (kPageThreads / 32) + (threadIdx.x >> 5);
-    // this lane's token of an item: its source token (-1: none)
-    auto source = [&](int64_t item) -> int {
-        if (item >= n_items) return -1;
-        const int64_t h = item / blocks;
-        const int i = (int)(item - h * blocks) * 32 + lane;
-        if (i >= a.kept[h]) return -1;
+    const int64_t warp = (int64_t)(blockIdx.x - list_ctas) * (kPageThreads / 32) + (threadIdx.x >> 5);
+    const int64_t items = (int64_t)a.verdict[1] << per_shift;  // pages taken
+    const int64_t item0 = items * warp / warps, last = items * (warp + 1) / warps;
+    if (item0 >= last) return;
+    // the list that holds the first item's page: the last one that begins at or before it, of which the empty ones have none
+    int64_t h = 0;
+    {
+        const int rank = (int)(item0 >> per_shift);
+        int64_t n = lists;  // list_off[h] <= rank, and for those at h + n and beyond it is above
+        while (n > 1) {
+            const int64_t step = (n + 31) / 32, x = lane * step;
+            const int part = __popc(__ballot_sync(kFull, x < n && a.list_off[h + x] <= rank)) - 1;
+            h += part * step;
+            n = min(step, n - part * step);
+        }
+    }
+    int kept = a.kept[h], off = a.list_off[h];
+    // the next item: its list and this lane's token of it, -1 for none
+    struct Item {
+        int64_t h;
+        int i, s, rank;
+    };
+    auto source = [&](int64_t item) -> Item {
+        Item it = {0, -1, -1, (int)(item >> per_shift)};
+        if (item >= last) return it;
+        while (it.rank >= off + pages_of(kept, a)) {  // the next list with tokens
+            off += pages_of(kept, a);
+            do {
+                const int k = h + 1 + lane < lists ? a.kept[h + 1 + lane] : 1;
+                const unsigned hit = __ballot_sync(kFull, k > 0);
+                const int skip = hit ? __ffs(hit) - 1 : 32;
+                kept = __shfl_sync(kFull, k, skip & 31);
+                h += hit ? skip + 1 : 32;
+                if (hit) break;
+            } while (h < lists);
+        }
+        if (h >= lists) return it;  // (not reached: a rank below the pages taken has a list)
+        it.h = h;
+        const int i = ((it.rank - off) << a.page_shift) + (int)(item & ((1 << per_shift) - 1)) * 32 + lane;
+        if (lane >= tokens || i >= kept) return it;
+        it.i = i;
         const int s = a.idx ? a.idx[h * a.idx_stride + i] : i;
         const int T = !a.K ? a.lens[h] : a.seq_lens ? a.seq_lens[h / a.heads] : a.t_max;
-        if (s < 0 || s >= T) {
-            atomicOr(a.status, MKV_DEV_BAD_INDEX);
-            return -1;
-        }
-        return s;
+        if (s < 0 || s >= T) atomicOr(a.status, MKV_DEV_BAD_INDEX);
+        else it.s = s;
+        return it;
     };
     // the rows of the pool (or the contiguous cache) it is copied from and to
-    auto places = [&](int64_t item, int s, int64_t &from, int &to) {
+    auto places = [&](const Item &it, int64_t &from, int &to) {
         from = to = -1;
-        if (s < 0) return;
-        const int64_t h = item / blocks;
-        const int i = (int)(item - h * blocks) * 32 + lane;
+        if (it.s < 0) return;
         if (a.K) {
-            from = h * a.t_max + s;
+            from = it.h * a.t_max + it.s;
         } else {
-            const int id = a.table[h * a.max_pages + (s >> a.page_shift)];
+            const int id = a.table[it.h * a.max_pages + (it.s >> a.page_shift)];
             if ((uint32_t)id >= (uint32_t)a.n_pages) {
                 atomicOr(a.status, MKV_DEV_BAD_PAGE);
                 return;
             }
-            from = (id << a.page_shift) + (s & (a.page_size - 1));
+            from = (id << a.page_shift) + (it.s & (a.page_size - 1));
         }
-        to = (a.free_ids[a.list_off[h] + (i >> a.page_shift)] << a.page_shift) + (i & (a.page_size - 1));
+        to = (a.free_ids[it.rank] << a.page_shift) + (it.i & (a.page_size - 1));
     };
     const uint8_t *ks = (a.K ? a.K : a.k) + lr * 16, *vs = (a.K ? a.V : a.v) + lr * 16;
     uint8_t *kd = a.k + lr * 16, *vd = a.v + lr * 16;
     int64_t from;
-    int to, ahead = source(item0);
-    places(item0, ahead, from, to);
-    ahead = source(item0 + warps);
-    for (int64_t item = item0; item < n_items; item += warps) {
+    int to;
+    Item ahead = source(item0);
+    places(ahead, from, to);
+    ahead = source(item0 + 1);
+    for (int64_t item = item0; item < last; ++item) {
         int64_t next_from;
         int next_to;
-        places(item + warps, ahead, next_from, next_to);
-        ahead = source(item + 2 * warps);
-        if (__any_sync(kFull, to >= 0)) {
+        places(ahead, next_from, next_to);
+        ahead = source(item + 2);
 #pragma unroll
-            for (int b0 = 0; b0 < LPR; b0 += B) {
-                uint4 kr[B], vr[B];
-                int dst[B];
+        for (int b0 = 0; b0 < LPR; b0 += B) {
+            if (b0 * RPS >= tokens) break;
+            uint4 kr[B], vr[B];
+            int dst[B];
 #pragma unroll
-                for (int u = 0; u < B; ++u) {
-                    const int row = (b0 + u) * RPS + g;
-                    const int64_t src = __shfl_sync(kFull, from, row);
-                    dst[u] = __shfl_sync(kFull, to, row);
-                    if (dst[u] >= 0) {
-                        kr[u] = ld_stream(ks + src * RB);
-                        vr[u] = ld_stream(vs + src * RB);
-                    }
+            for (int u = 0; u < B; ++u) {
+                const int row = (b0 + u) * RPS + g;
+                const int64_t src = __shfl_sync(kFull, from, row);
+                dst[u] = __shfl_sync(kFull, to, row);
+                if (dst[u] >= 0) {
+                    kr[u] = ld_stream(ks + src * RB);
+                    vr[u] = ld_stream(vs + src * RB);
                 }
-#pragma unroll
-                for (int u = 0; u < B; ++u)
-                    if (dst[u] >= 0) {
-                        st_v4(kd + (int64_t)dst[u] * RB, kr[u]);
-                        st_v4(vd + (int64_t)dst[u] * RB, vr[u]);
-                    }
             }
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+                if (dst[u] >= 0) {
+                    st_v4(kd + (int64_t)dst[u] * RB, kr[u]);
+                    st_v4(vd + (int64_t)dst[u] * RB, vr[u]);
+                }
         }
         from = next_from;
         to = next_to;
@@ -541,13 +574,14 @@ cudaError_t launch_page_call(const PageArgs &pa, cudaStream_t st)
         return launch_dependent((const void *)k_page_update, (lists * 32 + kPageThreads - 1) / kPageThreads, args, st);
     const void *fn = compact_fn(a.row_bytes);
     if (!fn) return cudaErrorInvalidValue;
+    // no more items than the pages that can be taken have
     const int64_t most = a.idx ? std::min((int64_t)a.idx_stride, (int64_t)a.max_pages << a.page_shift)
                                : std::min((int64_t)(a.K ? a.t_max : INT32_MAX), (int64_t)a.max_pages << a.page_shift);
-    int blocks = (int)std::max<int64_t>(1, (most + kCopyRows - 1) / kCopyRows);
-    int64_t items = lists * blocks;
+    const int64_t pages = std::min((int64_t)a.n_pages, lists * ((most + a.page_size - 1) >> a.page_shift));
+    const int64_t items = pages << std::max(a.page_shift - 5, 0);
     int list_ctas = (int)std::min<int64_t>(lists, 152);
     const int64_t copy_ctas = grid_for_items(fn, kPageThreads, 0, (items + kPageThreads / 32 - 1) / (kPageThreads / 32));
-    void *cargs[] = {&a, &blocks, &items, &list_ctas};
+    void *cargs[] = {&a, &list_ctas};
     return launch_dependent(fn, list_ctas + copy_ctas, cargs, st);
 }
 

@@ -34,7 +34,7 @@ struct PageArgs {
     const uint8_t *K, *V;
     int32_t idx_stride, t_max;
     // workspace
-    uint32_t *status, *verdict;
+    uint32_t *status, *verdict;  // verdict: status bits (0: the call goes through), pages taken
     int2 *row_src;
     long long *row_need;
     uint32_t *row_bits;

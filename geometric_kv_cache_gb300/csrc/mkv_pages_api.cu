@@ -89,7 +89,7 @@ PageLayout make_page_layout(const mkv_page_pool &p, const mkv_page_lists &l)
         at += round_up(bytes, kAlign);
         return here;
     };
-    L.verdict = take(sizeof(uint32_t));
+    L.verdict = take(2 * sizeof(uint32_t));
     L.row_src = take((size_t)l.batch * sizeof(int2));
     L.row_need = take(row_chunks * sizeof(long long));
     L.row_bits = take(row_chunks * sizeof(uint32_t));
@@ -370,7 +370,7 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     a.es = elem_bytes(pool.dtype);
     a.max_q = max_q;
     a.max_len = max_len;
-    a.window = window;
+    a.window = std::min(window, std::max(max_len, 1));  // no list is longer
     a.sinks = sinks;
     a.scale_log2 = (float)((double)scale * (double)k_scale * M_LOG2E);
     a.v_scale = v_scale;

@@ -164,10 +164,10 @@ k_rope_append(const RopeArgs a, int parts)
                 slot[c] = -1;
                 if (head < 0 || kind == 0) continue;
                 const int len = a.lens[(int64_t)b * a.heads + head];
-                slot[c] = len - left;
-                if (slot[c] < 0 || len > (a.max_pages << a.page_shift)) {
+                if (len < left || len > (a.max_pages << a.page_shift)) {
                     if (u == 0) atomicOr(a.status, MKV_DEV_BAD_SEQ_LEN);
-                    slot[c] = -1;
+                } else {
+                    slot[c] = len - left;
                 }
             }
 #pragma unroll

@@ -116,6 +116,16 @@ def test_window_and_first_tokens(d, dtype, page, window, sinks):
         p.check(O, lse, window, sinks)
 
 
+@pytest.mark.parametrize("counts", [[1, 1], [70, 3]])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (3, 2 ** 31 - 1), (400, 0)])
+def test_largest_window_and_first_tokens(counts, window, sinks):
+    # row 1's second list is shorter than its new tokens: places below zero
+    p = Problem(14, counts, [[counts[0] + 300, counts[0]], [40, counts[1] - 1]], 4, 128, 16, BF)
+    O, lse = p.run(window, sinks)
+    assert p.status == 0
+    p.check(O, lse, window, sinks)
+
+
 @pytest.mark.parametrize("dtype", [BF, F8])
 @pytest.mark.parametrize("q_scale", [0.0, 30.0])
 def test_flat_and_sharp_softmax(dtype, q_scale):

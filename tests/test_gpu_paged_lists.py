@@ -244,6 +244,20 @@ def test_compaction_without_indices_any_order_and_repeats():
     s.same(s.compact(idx, kept), want)
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_compaction_of_many_lists_mostly_empty(page):
+    # runs of empty lists longer than a warp, single tokens, one long list: the copying warps' runs begin and end anywhere
+    for seed in range(3):
+        rng = random.Random(seed)
+        lens = [[0 if rng.random() < 0.8 else rng.choice([1, page, 2 * page + 1]) for _ in range(7)] for _ in range(90)]
+        lens[rng.randrange(90)][3] = 40 * page + 5
+        s = State(seed, 90, 7, page, 64, F8, 41 * page, sum(pu.pages_of(x, page) for r in lens for x in r) + 2, lens=lens)
+        kept = torch.where(torch.rand((90, 7), generator=torch.Generator().manual_seed(seed)) < 0.3, 0, s.lens)
+        want = pu.page_compact(s.k, s.v, s.table, s.lens, s.refs, None, kept, page)
+        s.gpu()
+        s.same(s.compact(None, kept), want)
+
+
 def test_compaction_reports_indices_outside_and_copies_the_others():
     s = State(47, 1, 2, 16, 64, BF, 50, 30, lens=[[50, 17]])
     idx = torch.tensor([[[1, 50, 3], [-1, 16, 2 ** 30]]], dtype=torch.int32)

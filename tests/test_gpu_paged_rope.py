@@ -137,13 +137,16 @@ def test_invalid_lists_are_reported_and_left():
     p = _problem(7, [4, 2, 3], 2, 2, 64, 16, BF)
     p["lens"][0, 1] = 3                       # fewer tokens than the row brings
     p["lens"][2, 0] = 16 * p["table"].shape[2] + 1
+    p["lens"][2, 1] = -2 ** 31
+    p["lens"][1, 0] = 2 ** 31 - 1
+    p["lens"][1, 1] = -1
     res = _run(p, 2, 2, 64, "half")
     assert res[3] == mkv.MKV_DEV_BAD_SEQ_LEN
     # the tokens that do have a place in the short list are written: compare the other lists alone
     t = p["table"][0, 1, 0]
     for pool, old in ((res[1], p["k"]), (res[2], p["v"])):
         pu.raw(pool)[t] = pu.raw(old)[t]
-    _check(p, res, 2, 2, 64, "half", 1.0, (1.0, 1.0), skip_rows={(0, 1), (2, 0)})
+    _check(p, res, 2, 2, 64, "half", 1.0, (1.0, 1.0), skip_rows={(0, 1), (2, 0), (2, 1), (1, 0), (1, 1)})
     p = _problem(8, [4, 2], 2, 2, 64, 16, BF)
     last = pu.pages_of(int(p["lens"][1, 1]), 16) - 1
     p["lens"][1, 1] = last * 16 + 10  # both new tokens inside the last page
