@@ -43,8 +43,11 @@ constexpr float kLag = 8.f;    // log2 of how far a row's maximum may lag
 // Shape of one instantiation.
 template <int D, int ES>
 struct Attend {
-    static constexpr int KT = D == 256 ? 16 : 32;      // keys per block
-    static constexpr int WARPS = ES == 1 ? 8 : 4;
+    // keys per block and warp, and warps: E4M3 blocks have half the bytes for the
+    // same arithmetic, which takes more warps to hide (two rows of 60K-65K tokens, 128
+    // dims: 12 x 16 keys 63.5 us, 8 x 32 65.1, 16 x 16 64.3; the copies alone take 55)
+    static constexpr int KT = ES == 1 || D == 256 ? 16 : 32;
+    static constexpr int WARPS = ES == 2 ? 4 : D == 256 ? 8 : 12;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int KEYS = WARPS * KT;            // keys per block of the CTA
     static constexpr int RB = D * ES;                  // bytes per cached row
@@ -148,9 +151,10 @@ k_attend(const AttnArgs a, LineInfo *info)
 {
     using A = Attend<D, ES>;
     constexpr int KT = A::KT, NT = KT / 8, KS = D / 16;  // key tiles of 8, dim steps of 16
-    constexpr bool Q_REGS = D <= 128;
+    constexpr bool Q_REGS = ES == 2 && D <= 128;  // the queries' fragments: in registers, or read from shared memory
+    constexpr int QS = D * 2 + 16;                // bytes between rows there: rows fall into distinct banks
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(16) uint8_t s_q[Q_REGS ? 16 : kRows * D * 2];
+    __shared__ __align__(16) uint8_t s_q[Q_REGS ? 16 : kRows * QS];
     __shared__ float s_up[kRows];
     __shared__ LineScratch s_line;
     __shared__ float2 s_ml[A::WARPS][kRows];
@@ -189,46 +193,25 @@ k_attend(const AttnArgs a, LineInfo *info)
                     q[k][2 * hi] = *reinterpret_cast<const uint32_t *>(q0 + 2 * q_dim(k, hi));
                     q[k][2 * hi + 1] = *reinterpret_cast<const uint32_t *>(q1 + 2 * q_dim(k, hi));
                 }
-            if constexpr (ES == 1) {
-                float m[2] = {0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        m[e & 1] = fmaxf(m[e & 1], fmaxf(fabsf(lo_bf16(q[k][e])), fabsf(hi_bf16(q[k][e]))));
-                int E[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    m[r] = fmaxf(m[r], __shfl_xor_sync(kFull, m[r], 1));
-                    m[r] = fmaxf(m[r], __shfl_xor_sync(kFull, m[r], 2));
-                    E[r] = row_exponent(m[r]);
-                }
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        q[k][e] = pack_f16(lo_bf16(q[k][e]) * down_by(E[e & 1]), hi_bf16(q[k][e]) * down_by(E[e & 1]));
-                sc0 *= up_by(E[0]);
-                sc1 *= up_by(E[1]);
-            }
         } else {
-            static_assert(D == 256 || Q_REGS, "a lane's 8 dims make one row per warp");
-            for (int r = warp; r < kRows; r += A::WARPS) {
-                uint4 v = reinterpret_cast<const uint4 *>(q_row(r))[lane];
+            constexpr int LANES = D / 8, PASS = 32 / LANES;  // lanes of a row, rows of a warp's pass
+            for (int r0 = warp * PASS; r0 < kRows; r0 += A::WARPS * PASS) {
+                const int r = r0 + lane / LANES, x = lane % LANES;
+                uint4 v = reinterpret_cast<const uint4 *>(q_row(r))[x];
                 if constexpr (ES == 1) {
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t w8[4] = {v.x, v.y, v.z, v.w};
                     float m = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(lo_bf16(w[e])), fabsf(hi_bf16(w[e]))));
+                    for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(lo_bf16(w8[e])), fabsf(hi_bf16(w8[e]))));
 #pragma unroll
-                    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+                    for (int y = LANES / 2; y; y >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, y));
                     const int E = row_exponent(m);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = pack_f16(lo_bf16(w[e]) * down_by(E), hi_bf16(w[e]) * down_by(E));
-                    v = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (lane == 0) s_up[r] = up_by(E);
+                    for (int e = 0; e < 4; ++e) w8[e] = pack_f16(lo_bf16(w8[e]) * down_by(E), hi_bf16(w8[e]) * down_by(E));
+                    v = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+                    if (x == 0) s_up[r] = up_by(E);
                 }
-                reinterpret_cast<uint4 *>(s_q)[r * (D / 8) + lane] = v;
+                *reinterpret_cast<uint4 *>(s_q + r * QS + 16 * x) = v;
             }
             __syncthreads();
             if constexpr (ES == 1) {
@@ -303,8 +286,8 @@ k_attend(const AttnArgs a, LineInfo *info)
                 } else {
 #pragma unroll
                     for (int hi = 0; hi < 2; ++hi) {
-                        f[2 * hi] = *reinterpret_cast<const uint32_t *>(s_q + 2 * (gr * D + q_dim(k, hi)));
-                        f[2 * hi + 1] = *reinterpret_cast<const uint32_t *>(s_q + 2 * ((gr + 8) * D + q_dim(k, hi)));
+                        f[2 * hi] = *reinterpret_cast<const uint32_t *>(s_q + gr * QS + 2 * q_dim(k, hi));
+                        f[2 * hi + 1] = *reinterpret_cast<const uint32_t *>(s_q + (gr + 8) * QS + 2 * q_dim(k, hi));
                     }
                 }
             };
@@ -333,11 +316,22 @@ k_attend(const AttnArgs a, LineInfo *info)
                         kw[i][2] = v.z;
                         kw[i][3] = v.w;
                     }
+                    // four steps' fragments are 32 bytes of each of the lane's rows
+                    uint32_t f4[4][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint4 v = lds16(saddr(s_q) + (gr + 8 * h) * QS + 2 * q_dim(4 * k4, 0) + 16 * x);
+                            f4[2 * x][h] = v.x;
+                            f4[2 * x][2 + h] = v.y;
+                            f4[2 * x + 1][h] = v.z;
+                            f4[2 * x + 1][2 + h] = v.w;
+                        }
                     // (consecutive MMAs add to different tiles of scores)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        uint32_t f[4];
-                        q_frag(4 * k4 + e, f);
+                        const uint32_t(&f)[4] = f4[e];
 #pragma unroll
                         for (int i = 0; i < NT; ++i)
                             mma_f16(s[i], f, e4m3x2_to_f16x2(kw[i][e] & 0xFFFFu), e4m3x2_to_f16x2(kw[i][e] >> 16));

@@ -32,6 +32,12 @@ namespace {
 using namespace dev;
 
 constexpr int kPageThreads = 256;
+// Tokens per item of the compaction: a page holds a whole number of them, and
+// small items even out the warps' shares. With 4 rows of K and of V in flight
+// per lane and 3 CTAs per SM, 8 rows of 8K-32K tokens halved take 123 us (107 us
+// of it the copy, 0.93 of the copy peak); 8 in flight and 2 CTAs 127 us, with
+// items of 32 tokens 128 us.
+constexpr int kItem = 16;
 
 __device__ __forceinline__ int pages_of(int len, const PageArgs &a)
 {
@@ -282,6 +288,11 @@ k_page_assign(const PageArgs a)
                 if (lane >= o) x += y;
             }
             if (j < a.heads) a.list_off[b * a.heads + j] = off + x - n;
+            if (a.kept)  // whose each new page is
+                for (int k = 0; k < min(32, a.heads - j0); ++k) {
+                    const int m = __shfl_sync(kFull, n, k), at = off + __shfl_sync(kFull, x, k) - m;
+                    for (int q = lane; q < m; q += 32) a.owners[at + q] = make_int2((int)(b * a.heads) + j0 + k, q);
+                }
             off += __shfl_sync(kFull, x, 31);
         }
     } else {
@@ -394,17 +405,17 @@ k_page_update(const PageArgs a)
 }
 
 // The first `list_ctas` CTAs write tables and counts, list by list; the warps
-// of the others copy rows. The new pages stand in one line (rank: the place in
-// free_ids), cut into equal runs, one per warp, whatever the lists' lengths.
-// Item = a page's tokens, 32 at most, one lane per token for its places: an
-// item's indices are read two items ahead and its page entries one ahead, so
-// that every row copy (groups of LPR lanes, 16 bytes each, 8 rows of K and of V
-// in flight per lane) finds its addresses in registers.
+// of the others copy rows. Item = 16 tokens of a new page, one lane per token
+// for its places; owners[rank] names a new page's list and place in it,
+// so the items are the pages taken, whatever the lists' lengths and capacities.
+// An item's owner is read three items ahead, its indices two and its page
+// entries one, so that every row copy (groups of LPR lanes, 16 bytes each, 4
+// rows of K and of V in flight per lane) finds its addresses in registers.
 template <int LPR>
-__global__ void __launch_bounds__(kPageThreads, 2)
+__global__ void __launch_bounds__(kPageThreads, 3)
 k_page_compact(const PageArgs a, int list_ctas)
 {
-    constexpr int RB = LPR * 16, RPS = 32 / LPR, B = LPR < 8 ? LPR : 8;  // rows per step, steps per batch
+    constexpr int RB = LPR * 16, RPS = 32 / LPR, STEPS = kItem / RPS, B = STEPS < 4 ? STEPS : 4;  // rows per step, steps per batch
     pdl_wait();
     const bool bad = a.verdict[0] != 0;
     const int64_t lists = (int64_t)a.batch * a.heads;
@@ -429,51 +440,27 @@ k_page_compact(const PageArgs a, int list_ctas)
     }
     if (bad) return;
     const int lane = threadIdx.x & 31, g = lane / LPR, lr = lane % LPR;
-    const int per_shift = max(a.page_shift - 5, 0), tokens = min(a.page_size, 32);  // items of a page, tokens of an item
+    const int per_shift = a.page_shift - 4;  // items of a page
     const int64_t warps = (int64_t)(gridDim.x - list_ctas) * (kPageThreads / 32);
     const int64_t warp = (int64_t)(blockIdx.x - list_ctas) * (kPageThreads / 32) + (threadIdx.x >> 5);
     const int64_t items = (int64_t)a.verdict[1] << per_shift;  // pages taken
-    const int64_t item0 = items * warp / warps, last = items * (warp + 1) / warps;
-    if (item0 >= last) return;
-    // the list that holds the first item's page: the last one that begins at or before it, of which the empty ones have none
-    int64_t h = 0;
-    {
-        const int rank = (int)(item0 >> per_shift);
-        int64_t n = lists;  // list_off[h] <= rank, and for those at h + n and beyond it is above
-        while (n > 1) {
-            const int64_t step = (n + 31) / 32, x = lane * step;
-            const int part = __popc(__ballot_sync(kFull, x < n && a.list_off[h + x] <= rank)) - 1;
-            h += part * step;
-            n = min(step, n - part * step);
-        }
-    }
-    int kept = a.kept[h], off = a.list_off[h];
-    // the next item: its list and this lane's token of it, -1 for none
-    struct Item {
-        int64_t h;
-        int i, s, rank;
+    auto owner = [&](int64_t item) -> int2 {
+        return item < items ? a.owners[item >> per_shift] : make_int2(-1, 0);
     };
-    auto source = [&](int64_t item) -> Item {
-        Item it = {0, -1, -1, (int)(item >> per_shift)};
-        if (item >= last) return it;
-        while (it.rank >= off + pages_of(kept, a)) {  // the next list with tokens
-            off += pages_of(kept, a);
-            do {
-                const int k = h + 1 + lane < lists ? a.kept[h + 1 + lane] : 1;
-                const unsigned hit = __ballot_sync(kFull, k > 0);
-                const int skip = hit ? __ffs(hit) - 1 : 32;
-                kept = __shfl_sync(kFull, k, skip & 31);
-                h += hit ? skip + 1 : 32;
-                if (hit) break;
-            } while (h < lists);
-        }
-        if (h >= lists) return it;  // (not reached: a rank below the pages taken has a list)
-        it.h = h;
-        const int i = ((it.rank - off) << a.page_shift) + (int)(item & ((1 << per_shift) - 1)) * 32 + lane;
-        if (lane >= tokens || i >= kept) return it;
+    // an item: its list, its new page's rank, and this lane's token of it with its source (-1: none)
+    struct Item {
+        int h, rank, i, s;
+    };
+    auto source = [&](int64_t item, int2 own) -> Item {
+        Item it = {own.x, (int)(item >> per_shift), -1, -1};
+        if (own.x < 0 || lane >= kItem) return it;
+        const int64_t h = own.x;
+        const int i = (own.y << a.page_shift) + (int)(item & ((1 << per_shift) - 1)) * kItem + lane;
+        // (read together: an index behind the kept ones is not looked at)
+        const int kept = a.kept[h], s = !a.idx ? i : i < a.idx_stride ? a.idx[h * a.idx_stride + i] : -1;
+        if (i >= kept) return it;
+        const int T = !a.K ? a.lens[h] : a.seq_lens ? a.seq_lens[own.x / a.heads] : a.t_max;
         it.i = i;
-        const int s = a.idx ? a.idx[h * a.idx_stride + i] : i;
-        const int T = !a.K ? a.lens[h] : a.seq_lens ? a.seq_lens[h / a.heads] : a.t_max;
         if (s < 0 || s >= T) atomicOr(a.status, MKV_DEV_BAD_INDEX);
         else it.s = s;
         return it;
@@ -483,9 +470,9 @@ k_page_compact(const PageArgs a, int list_ctas)
         from = to = -1;
         if (it.s < 0) return;
         if (a.K) {
-            from = it.h * a.t_max + it.s;
+            from = (int64_t)it.h * a.t_max + it.s;
         } else {
-            const int id = a.table[it.h * a.max_pages + (it.s >> a.page_shift)];
+            const int id = a.table[(int64_t)it.h * a.max_pages + (it.s >> a.page_shift)];
             if ((uint32_t)id >= (uint32_t)a.n_pages) {
                 atomicOr(a.status, MKV_DEV_BAD_PAGE);
                 return;
@@ -498,17 +485,19 @@ k_page_compact(const PageArgs a, int list_ctas)
     uint8_t *kd = a.k + lr * 16, *vd = a.v + lr * 16;
     int64_t from;
     int to;
-    Item ahead = source(item0);
+    Item ahead = source(warp, owner(warp));
+    int2 own = owner(warp + warps);
     places(ahead, from, to);
-    ahead = source(item0 + 1);
-    for (int64_t item = item0; item < last; ++item) {
+    ahead = source(warp + warps, own);
+    own = owner(warp + 2 * warps);
+    for (int64_t item = warp; item < items; item += warps) {
         int64_t next_from;
         int next_to;
         places(ahead, next_from, next_to);
-        ahead = source(item + 2);
+        ahead = source(item + 2 * warps, own);
+        own = owner(item + 3 * warps);
 #pragma unroll
-        for (int b0 = 0; b0 < LPR; b0 += B) {
-            if (b0 * RPS >= tokens) break;
+        for (int b0 = 0; b0 < STEPS; b0 += B) {
             uint4 kr[B], vr[B];
             int dst[B];
 #pragma unroll
@@ -578,7 +567,7 @@ cudaError_t launch_page_call(const PageArgs &pa, cudaStream_t st)
     const int64_t most = a.idx ? std::min((int64_t)a.idx_stride, (int64_t)a.max_pages << a.page_shift)
                                : std::min((int64_t)(a.K ? a.t_max : INT32_MAX), (int64_t)a.max_pages << a.page_shift);
     const int64_t pages = std::min((int64_t)a.n_pages, lists * ((most + a.page_size - 1) >> a.page_shift));
-    const int64_t items = pages << std::max(a.page_shift - 5, 0);
+    const int64_t items = pages << (a.page_shift - 4);
     int list_ctas = (int)std::min<int64_t>(lists, 152);
     const int64_t copy_ctas = grid_for_items(fn, kPageThreads, 0, (items + kPageThreads / 32 - 1) / (kPageThreads / 32));
     void *cargs[] = {&a, &list_ctas};

@@ -16,7 +16,7 @@ constexpr int kPlanRows = 8;      // batch rows per CTA of the plan kernels (one
 // Byte offsets of the page workspace (each 256-byte aligned).
 struct PageLayout {
     size_t status = 0, verdict = 0, row_src = 0, row_need = 0, row_bits = 0, page_free = 0, list_off = 0, free_ids = 0,
-           total = 0;
+           owners = 0, total = 0;
 };
 
 // What the page calls share. Pointers of `in` and `out` lists; in place when
@@ -39,6 +39,7 @@ struct PageArgs {
     long long *row_need;
     uint32_t *row_bits;
     int32_t *page_free, *list_off, *free_ids;
+    int2 *owners;  // compact: list and place in it of each page taken
     int32_t row_chunks, page_chunks;
 };
 

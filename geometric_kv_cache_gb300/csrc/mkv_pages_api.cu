@@ -96,6 +96,7 @@ PageLayout make_page_layout(const mkv_page_pool &p, const mkv_page_lists &l)
     L.page_free = take(page_chunks * sizeof(int32_t));
     L.list_off = take(lists * sizeof(int32_t));
     L.free_ids = take(taken * sizeof(int32_t));
+    L.owners = take(taken * sizeof(int2));
     L.total = at;
     return L;
 }
@@ -146,6 +147,7 @@ mkv_status page_call(const mkv_page_pool &p, const mkv_page_lists &in, const int
     a->page_free = region<int32_t>(ws, L.page_free);
     a->list_off = region<int32_t>(ws, L.list_off);
     a->free_ids = region<int32_t>(ws, L.free_ids);
+    a->owners = region<int2>(ws, L.owners);
     a->row_chunks = (in.batch + kPlanRows - 1) / kPlanRows;
     a->page_chunks = (p.n_pages + kPlanPages - 1) / kPlanPages;
     return MKV_OK;
