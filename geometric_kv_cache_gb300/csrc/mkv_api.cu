@@ -941,10 +941,14 @@ mkv_status mkv_device_status(void *workspace, mkv_stream_t stream, uint32_t *bit
 {
     if (!workspace || !aligned(workspace, kAlign)) return MKV_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    uint32_t word = 0;
+    // the workspace's head: the status word and, zero between calls, the counts of mkv_paged_attention
+    uint32_t head[kAlign / sizeof(uint32_t)];
     if (cudaStreamSynchronize(st) != cudaSuccess) return MKV_ERR_CUDA;
-    if (cudaMemcpy(&word, workspace, sizeof word, cudaMemcpyDeviceToHost) != cudaSuccess) return MKV_ERR_CUDA;
-    if (word && cudaMemset(workspace, 0, sizeof word) != cudaSuccess) return MKV_ERR_CUDA;
+    if (cudaMemcpy(head, workspace, sizeof head, cudaMemcpyDeviceToHost) != cudaSuccess) return MKV_ERR_CUDA;
+    bool clean = true;
+    for (uint32_t x : head) clean = clean && x == 0;
+    if (!clean && cudaMemset(workspace, 0, sizeof head) != cudaSuccess) return MKV_ERR_CUDA;
+    const uint32_t word = head[0];
     if (bits) *bits = word;
     return word ? MKV_ERR_DEVICE : MKV_OK;
 }

@@ -16,8 +16,8 @@
 // has its own ring of cp.async stages (16 bytes per lane, the block's page
 // entries read one block ahead), so the walk over a tile has no CTA barrier;
 // the warps' (m, l, O) meet in shared memory at its end. The line of blocks is
-// cut over 152 CTAs (mkv_attention.cuh); k_attend_combine joins the parts of
-// cut tiles. mkv_attention_chunk.cu is the form for many rows.
+// cut over 152 CTAs (mkv_attention.cuh); of the CTAs with a part of a cut tile
+// the one that comes last joins the parts, always in the same order. mkv_attention_chunk.cu is the form for many rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -37,7 +37,6 @@ using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
 constexpr int64_t kAgainBytes = 28000000;  // see takes_chunks
-constexpr int kJoinWarps = 4;  // warps that share the parts of a row in the join
 constexpr float kLag = 8.f;    // log2 of how far a row's maximum may lag
 
 // Shape of one instantiation.
@@ -145,9 +144,63 @@ __device__ __forceinline__ uint32_t at_rows2(int r, int c)
     return (uint32_t)(r * CPR + (c ^ (CPR >= 8 ? (r & 1) << 2 : 0))) * 16u;
 }
 
+// One row of a tile whose parts the CTAs c0 .. c1 left (c0's second, the first
+// of the others): a warp, eight parts' loads in flight. Parts were written by
+// other CTAs of this launch: loads through L2.
+template <int D>
+__device__ __forceinline__ void join_row(const AttnArgs &a, int c0, int c1, int r, int64_t token, int head)
+{
+    constexpr int E = D / 32, U = 8;
+    const int lane = threadIdx.x & 31;
+    float sum[E], l = 0.f, M = -CUDART_INF_F;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.f;
+    for (int s0 = c0; s0 <= c1; s0 += U) {
+        float2 ml[U], v[U][E / 2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u;
+            ml[u] = make_float2(-CUDART_INF_F, 0.f);
+            if (s <= c1) {
+                const int64_t at = ((int64_t)s * 2 + (s == c0 ? 1 : 0)) * kRows + r;
+                ml[u] = __ldcg(a.part_ml + at);
+                const float2 *src = reinterpret_cast<const float2 *>(a.part_o + at * D + lane * E);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) v[u][e] = __ldcg(src + e);
+            }
+        }
+        float best = M;
+#pragma unroll
+        for (int u = 0; u < U; ++u) best = fmaxf(best, ml[u].x);
+        if (best == -CUDART_INF_F) continue;
+        const float f0 = M == -CUDART_INF_F ? 0.f : exp2_approx(M - best);
+        M = best;
+        l *= f0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[e] *= f0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (ml[u].x == -CUDART_INF_F) continue;  // none, or it saw nothing
+            const float f = exp2_approx(ml[u].x - M);
+            l += f * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                sum[2 * e] += f * v[u][e].x;
+                sum[2 * e + 1] += f * v[u][e].y;
+            }
+        }
+    }
+    const float inv = l > 0.f ? a.v_scale / l : 0.f;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[2 * e] * inv, sum[2 * e + 1] * inv);
+    if (lane == 0 && a.lse)
+        a.lse[token * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+}
+
 template <int D, int ES>
 __global__ void __launch_bounds__(Attend<D, ES>::THREADS, 1)
-k_attend(const AttnArgs a, LineInfo *info)
+k_attend(const AttnArgs a)
 {
     using A = Attend<D, ES>;
     constexpr int KT = A::KT, NT = KT / 8, KS = D / 16;  // key tiles of 8, dim steps of 16
@@ -157,16 +210,16 @@ k_attend(const AttnArgs a, LineInfo *info)
     __shared__ __align__(16) uint8_t s_q[Q_REGS ? 16 : kRows * QS];
     __shared__ float s_up[kRows];
     __shared__ LineScratch s_line;
+    __shared__ int4 s_join[2];  // tiles to join: tile, first and last CTA with a part
     __shared__ float2 s_ml[A::WARPS][kRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
-    pdl_trigger();
     Walk w = cut_line<A::KEYS, A::THREADS>(a, kRows, 1, s_line);
-    LineInfo ci = {-1, 0};
+    int at_unit = w.begin;  // of the line
+    if (threadIdx.x < 2) s_join[threadIdx.x].x = -1;
     while (w.next<A::KEYS>(a, kRows)) {
         const Tile &t = w.t;
         const int first = w.from(), last = w.to();
         const int64_t list = (int64_t)t.b * a.heads + t.j;
-        note_segment(w, ci);
         const int32_t *table = a.table + list * a.max_pages;
         const int page_mask = a.page_size - 1;
 
@@ -481,92 +534,32 @@ k_attend(const AttnArgs a, LineInfo *info)
                 a.lse[(int64_t)(qrow0 + i) * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
         }
         __syncthreads();  // the next segment's copies may overwrite the results
-    }
-    if (threadIdx.x == 0) info[blockIdx.x] = ci;
-}
-
-// One CTA per row of the tile that CTA blockIdx.y opened, if it did: its warps
-// take the tile's parts in turn, four loads of a part's row in flight per
-// lane, and meet in shared memory. Always the same order.
-template <int D, int KEYS>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-k_attend_combine(const AttnArgs a, const LineInfo *__restrict__ info)
-{
-    constexpr int E = D / 32, U = 4;
-    __shared__ float s_o[kJoinWarps][D];
-    __shared__ float2 s_ml[kJoinWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = (int)blockIdx.x, c0 = (int)blockIdx.y;
-    pdl_wait();
-    int c1;
-    const int tile = opened_tile(info, c0, (int)gridDim.y, c1);
-    if (tile < 0) return;
-    const Tile t = make_tile<KEYS>(a, tile, kRows, false);
-    if (r >= t.rows) return;
-    const int R = t.row0 + r, i = a.by_group(R), head = t.j * a.group + R - i * a.group;
-    const int64_t token = a.q_start[t.b] + i;
-    float sum[E], l = 0.f, M = -CUDART_INF_F;
-#pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] = 0.f;
-    for (int s0 = c0 + warp; s0 <= c1; s0 += U * kJoinWarps) {
-        float2 ml[U];
-        float v[U][E];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * kJoinWarps;
-            ml[u] = make_float2(-CUDART_INF_F, 0.f);
-            if (s <= c1) {
-                const int64_t at = ((int64_t)s * 2 + (s == c0 ? 1 : 0)) * kRows + r;
-                ml[u] = a.part_ml[at];
-                const float *src = a.part_o + at * D + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(&v[u][e]) = *reinterpret_cast<const float2 *>(src + e);
+        if (!w.whole() && threadIdx.x == 0) {
+            // Parts of a tile count themselves in a byte of the workspace's head,
+            // which the last one takes back to zero; it joins the parts below.
+            const int unit0 = at_unit - w.first, c0 = cta_of(unit0, s_line), c1 = cta_of(unit0 + w.units - 1, s_line);
+            uint32_t *word = a.counts + c0 / 4;
+            const int shift = c0 % 4 * 8;
+            __threadfence();
+            if ((int)(atomicAdd(word, 1u << shift) >> shift & 255u) == c1 - c0) {
+                atomicSub(word, (uint32_t)(c1 - c0 + 1) << shift);
+                s_join[w.first > 0 ? 0 : 1] = make_int4(w.tile - 1, c0, c1, 0);
             }
         }
-        float best = M;
-#pragma unroll
-        for (int u = 0; u < U; ++u) best = fmaxf(best, ml[u].x);
-        if (best == -CUDART_INF_F) continue;
-        const float f0 = M == -CUDART_INF_F ? 0.f : exp2_approx(M - best);
-        M = best;
-        l *= f0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] *= f0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (ml[u].x == -CUDART_INF_F) continue;
-            const float f = exp2_approx(ml[u].x - M);
-            l += f * ml[u].y;
-#pragma unroll
-            for (int e = 0; e < E; ++e) sum[e] += f * v[u][e];
-        }
+        at_unit += w.last - w.first;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = sum[e];
-    if (lane == 0) s_ml[warp] = make_float2(M, l);
     __syncthreads();
-    M = -CUDART_INF_F;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_ml[w].x);
-    float f[kJoinWarps];
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        f[w] = s_ml[w].x == -CUDART_INF_F ? 0.f : exp2_approx(s_ml[w].x - M);
-        l += f[w] * s_ml[w].y;
-    }
-    const float inv = l > 0.f ? a.v_scale / l : 0.f;
-    if (threadIdx.x < D / 2) {
-        float x = 0.f, y = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            x += f[w] * s_o[w][2 * threadIdx.x];
-            y += f[w] * s_o[w][2 * threadIdx.x + 1];
+    for (int k = 0; k < 2; ++k) {  // (a CTA's first segment and its last one)
+        const int4 j = s_join[k];
+        if (j.x < 0) continue;
+        __threadfence();
+        const Tile t = make_tile<A::KEYS>(a, j.x, kRows, false);
+        const int64_t token0 = a.q_start[t.b];
+        for (int r = warp; r < t.rows; r += A::WARPS) {
+            const int R = t.row0 + r, i = a.by_group(R);
+            join_row<D>(a, j.y, j.z, r, token0 + i, t.j * a.group + R - i * a.group);
         }
-        reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D))[threadIdx.x] =
-            pack_bf16(x * inv, y * inv);
     }
-    if (threadIdx.x == 0 && a.lse)
-        a.lse[token * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
 }
 
 template <int D, int ES>
@@ -575,19 +568,8 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
     using A = Attend<D, ES>;
     cudaError_t e = cudaFuncSetAttribute(k_attend<D, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
     if (e != cudaSuccess) return e;
-    LineInfo *info = reinterpret_cast<LineInfo *>(a.part_ml + (int64_t)a.ctas * 2 * kRows);
-    k_attend<D, ES><<<a.ctas, A::THREADS, A::SMEM, st>>>(a, info);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kRows, (unsigned)a.ctas);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attend_combine<D, A::KEYS>, a, (const LineInfo *)info);
+    k_attend<D, ES><<<a.ctas, A::THREADS, A::SMEM, st>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -88,6 +88,7 @@ __device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max
 struct Walk {
     int tile, left;  // the next tile, units left
     int skip;        // units of that tile that belong to the CTA before
+    int begin;       // the unit of the line that this CTA's part begins with
     bool have;       // t is that tile already
     Tile t;
     int first, last, units;  // units [first, last) of the tile's
@@ -121,6 +122,7 @@ struct Walk {
 // host has checked that the line's length fits 32 bits.)
 struct LineScratch {
     int sum[32], rest[32];
+    int units, parts;  // the line's length, the CTAs that it is cut over
     Walk walk;
 };
 template <int KEYS, int THREADS>
@@ -171,6 +173,11 @@ __device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int m
         return (int)((long long)units * c / parts);
     };
     const int u0 = begin((int)blockIdx.x), u1 = begin((int)blockIdx.x + 1);
+    if (threadIdx.x == 0) {
+        s.units = units;
+        s.parts = parts;
+        s.walk.begin = u0;
+    }
     auto claim = [&](int x, int off) {  // the thread whose tile holds u0 begins the walk
         if (mine > 0 && off <= u0 && u0 < off + mine) {
             s.walk.tile = x;
@@ -203,6 +210,13 @@ __device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int m
     }
     __syncthreads();
     return s.walk;
+}
+
+// The CTA whose part holds a unit of the line: the c with c units / parts
+// (rounded down) <= unit < (c + 1) units / parts.
+__device__ __forceinline__ int cta_of(int unit, const LineScratch &s)
+{
+    return (int)((((long long)unit + 1) * s.parts - 1) / s.units);
 }
 
 // What the joining kernel needs of each CTA.

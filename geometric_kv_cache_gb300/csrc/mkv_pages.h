@@ -92,6 +92,7 @@ struct AttnArgs {
     float *part_o;     // [2 ctas, rows of a tile, head_dim]: parts of cut tiles, before the division
     float2 *part_ml;   // [2 ctas, rows of a tile]: running maximum (log2 units) and sum; the CTAs' LineInfo follows
     uint32_t *status;
+    uint32_t *counts;  // a byte per CTA in the workspace's head, zero between calls: parts of the tile that it opened
 };
 // The launch of a shape, and the workspace bytes behind the status word.
 struct AttnPlan {

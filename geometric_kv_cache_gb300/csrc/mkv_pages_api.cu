@@ -17,6 +17,9 @@ constexpr size_t kAlign = 256;
 // The launches are planned for the 152 SMs of a GB300, so that workspace sizes
 // need no device and results do not depend on one.
 constexpr int kPlanSms = 152;
+// Where the workspace's head holds the counts of cut tiles' parts.
+constexpr size_t kCounts = 64;
+static_assert(kCounts + kPlanSms <= kAlign && kPlanSms < 256, "a byte per CTA");
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -385,6 +388,7 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     a.part_o = region<float>(workspace, kAlign);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + plan.part_rows * d);
     a.status = region<uint32_t>(workspace, 0);
+    a.counts = region<uint32_t>(workspace, kCounts);
     return cuda_status(launch_paged_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -57,7 +57,9 @@
  *   mkv_device_status. No kernel traps or asserts.
  * Workspace. mkv_workspace_size() bytes are enough for every entry point on
  *   that shape and window. The status word must be zero before the first
- *   call (allocate the workspace zeroed, or call mkv_device_status once).
+ *   call (allocate the workspace zeroed, or call mkv_device_status once); for
+ *   mkv_paged_attention so must the workspace's first 256 bytes, which every
+ *   call leaves zero but for the status word (the same two ways).
  *   Calls that share a workspace must not overlap on the GPU.
  * Supported. head_dim 64, 128 or 256 and dtype bf16 or E4M3 (else
  *   MKV_ERR_UNSUPPORTED; the OjaKV scorer needs 128 and bf16); t_max <= 2^30.
@@ -678,7 +680,7 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
                                void *workspace, size_t workspace_bytes, mkv_stream_t stream);
 
 /* Synchronise `stream`, read the status word of `workspace` into *bits (may
- * be NULL) and reset it to zero. MKV_OK if it was zero, MKV_ERR_DEVICE if
+ * be NULL) and reset it (and the workspace's first 256 bytes) to zero. MKV_OK if it was zero, MKV_ERR_DEVICE if
  * not, MKV_ERR_CUDA if the synchronisation or copy failed. */
 mkv_status mkv_device_status(void *workspace, mkv_stream_t stream, uint32_t *bits);
 

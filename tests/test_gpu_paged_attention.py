@@ -225,6 +225,21 @@ def test_long_lists_of_full_and_nearly_empty_tiles(d, dtype, page):
     p.check(O, lse)
 
 
+def test_workspace_of_any_contents_after_one_status_call():
+    p = Problem(15, [1, 1], [[3000, 200], [50, 4000]], 4, 128, 16, BF)
+    dev = lambda x: pu.raw(x).to(DEV).view(x.dtype) if x.dtype in pu.CODES else x.to(DEV)  # noqa: E731
+    Q, k, v, table, lens, start = (dev(x) for x in (p.Q, p.k, p.v, p.table, p.lens, p.start))
+    O, lse = torch.zeros_like(Q), torch.zeros(Q.shape[:2], device=DEV)
+    ws = torch.full_like(mkv.attention_workspace_for(Q, k, table, 1, 4000), 0xA7)
+    assert mkv.mkv_device_status(ws) == 0xA7A7A7A7
+    for _ in range(3):
+        O.fill_(7.0)
+        mkv.mkv_paged_attention(Q, k, v, table, lens, start, 1, 4000, O, ws, lse=lse)
+        assert int(ws[:256].sum()) == 0
+        p.check(O.cpu(), lse.cpu())
+    assert mkv.mkv_device_status(ws) == 0
+
+
 @pytest.mark.parametrize("counts", [[1, 1], [90, 1]])
 def test_same_bits_on_every_call(counts):
     p = Problem(11, counts, [[2000, 200], [50, 1500]], 4, 128, 16, BF)
