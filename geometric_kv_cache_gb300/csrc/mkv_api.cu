@@ -960,8 +960,8 @@ const char *mkv_status_string(int32_t status)
     case MKV_ERR_INVALID_ARG: return "MKV_ERR_INVALID_ARG: bad argument (null or misaligned pointer, size, ratio, window or stride)";
     case MKV_ERR_UNSUPPORTED:
         return "MKV_ERR_UNSUPPORTED: head_dim must be 64, 128 or 256, dtype bf16 or fp8 E4M3 (bf16 and 128 dims for "
-               "the OjaKV scorer) and t_max at most 2^30";
-    case MKV_ERR_WORKSPACE: return "MKV_ERR_WORKSPACE: workspace missing, misaligned or smaller than mkv_workspace_size";
+               "the OjaKV scorer) and t_max at most 2^30 (paged caches: page_size 16, 32, 64 or 128, the other limits in mkv.h)";
+    case MKV_ERR_WORKSPACE: return "MKV_ERR_WORKSPACE: workspace missing, misaligned or smaller than its size function gives";
     case MKV_ERR_CUDA: return "MKV_ERR_CUDA: a CUDA call or kernel launch failed";
     case MKV_ERR_DEVICE: return "MKV_ERR_DEVICE: a kernel reported bad device-side input (see the status bits)";
     default: return "unknown mkv_status";

@@ -25,6 +25,13 @@
 // The line of blocks is cut over 152 CTAs (mkv_attention.cuh);
 // k_chunk_combine joins the parts of cut tiles.
 //
+// Measured: 2048 new tokens of 32 query heads (8 KV heads of 128 dims) over 32768
+// bf16 tokens 0.72 ms, 1.48 PFLOP/s, 0.77 of the measured cuBLAS rate; the tensor
+// pipe is busy 67% of the time. Without the softmax (weights left as they are)
+// the same loop takes 0.63 ms, without copies too 0.57: what is left is the chain
+// scores -> weights -> product of each sub-tile, of which two overlap. E4M3 at
+// the same size 1.0 ms: expanding the codes takes the larger part.
+//
 // Every wait is bounded (1 s); when one runs out the CTA reports
 // MKV_DEV_TIMEOUT, its roles leave their loops, the copies and MMAs in flight
 // are waited for (bounded) and the TMEM is freed.
@@ -51,7 +58,7 @@ using namespace dev;
 constexpr int kSubRows = 128;                // rows per sub-tile: the MMA's M, the TMEM lanes
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLag = 8.f;                  // log2 of how far a row's maximum may lag
-constexpr int kMinBlocks = 4;                // blocks that make a CTA worth its start
+constexpr int kMinBlocks = 4;                // least blocks of a CTA's part: fewer make more parts to join, not less time
 
 template <int D, int ES>
 struct Chunk {
@@ -83,10 +90,6 @@ struct Chunk {
     static constexpr int O_COL = NSUB * KEYS;      // S of the sub-tiles, then O
 };
 
-__device__ __forceinline__ uint32_t saddr(const void *p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 __device__ __forceinline__ void bar_init(uint64_t *b, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(count) : "memory");
@@ -242,12 +245,6 @@ __device__ __forceinline__ uint32_t low_bits(int n)
     return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Two fp32 operations in one instruction: (a.x b.x + c.x, a.y b.y + c.y).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -266,27 +263,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint4 v)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-
 template <int D, int ES>
 __global__ void __launch_bounds__(Chunk<D, ES>::THREADS, 1)
 k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
