@@ -689,6 +689,8 @@ def mkv_paged_attention(Q, k_pages, v_pages, table, lens, q_start, max_q: int, m
     n, hq, d = Q.shape[0], Q.shape[1], pool.head_dim
     qs, os_ = _token_rows(Q, hq, d, n, "Q"), _token_rows(O, hq, d, n, "O")
     _int32(q_start, (lists.batch + 1,), "q_start")
+    if max(max_q, max_len, window, sinks) > 0x7FFFFFFF:
+        raise ValueError("max_q, max_len, window and sinks are 32-bit numbers")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 tensor [n_tokens, q_heads]")
     _workspace(workspace)

@@ -41,7 +41,7 @@ namespace {
 using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
-constexpr int64_t kAgainBytes = 28000000;  // see takes_chunks
+constexpr double kAgainBytes = 28e6;  // see takes_chunks
 constexpr float kLag = 8.f;    // log2 of how far a row's maximum may lag
 
 // Shape of one instantiation.
@@ -559,7 +559,7 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 bool takes_chunks(int64_t lists, int64_t rows, int64_t max_len, int32_t head_dim, int32_t es)
 {
     const int64_t again = (rows + kRows - 1) / kRows - (es == 1 ? 2 : 1);
-    return again > 0 && lists * max_len * again > kAgainBytes / (head_dim * es);
+    return again > 0 && (double)lists * (double)max_len * (double)again * head_dim * es > kAgainBytes;
 }
 
 AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int32_t es,

@@ -58,10 +58,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 // codes where bf16 would take five instructions: a row of queries is scaled by
 // the power of two that brings its largest magnitude into [1, 2). Elements
 // from 2^-14 of that on keep all their bits; smaller ones are off by at most
-// 2^-25 of the largest. E: the biased exponent of the largest magnitude.
+// 2^-25 of the largest. E: the biased exponent of the largest magnitude (at
+// least 2^-63: smaller queries make no difference to any score, and the
+// factor that takes the scaling back stays far from the smallest numbers).
 __device__ __forceinline__ int row_exponent(float largest)
 {
-    return min(max((int)(__float_as_uint(largest) >> 23), 1), 253);
+    return min(max((int)(__float_as_uint(largest) >> 23), 64), 253);
 }
 __device__ __forceinline__ float down_by(int E) { return __uint_as_float((uint32_t)(254 - E) << 23); }  // 2^(127 - E)
 __device__ __forceinline__ float up_by(int E) { return __uint_as_float((uint32_t)E << 23); }            // 2^(E - 127)

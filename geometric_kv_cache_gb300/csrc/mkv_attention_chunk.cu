@@ -30,7 +30,9 @@
 // pipe is busy 67% of the time. Without the softmax (weights left as they are)
 // the same loop takes 0.63 ms, without copies too 0.57: what is left is the chain
 // scores -> weights -> product of each sub-tile, of which two overlap. E4M3 at
-// the same size 1.0 ms: expanding the codes takes the larger part.
+// the same size 0.88 ms (0.99 with three slots and three blocks of codes instead
+// of four and two); the conversions themselves cost nothing, the traffic of
+// codes and their expansion through shared memory does.
 //
 // Every wait is bounded (1 s); when one runs out the CTA reports
 // MKV_DEV_TIMEOUT, its roles leave their loops, the copies and MMAs in flight
@@ -40,6 +42,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -71,8 +74,8 @@ struct Chunk {
     static constexpr int BOX = KEYS * 128;          // 64 dims of a block: rows of 128 bytes
     static constexpr int SLOT = BOXES * BOX;        // one block of K or of V as the MMA reads it
     static constexpr int RAW = KEYS * D;            // ... as E4M3 codes
-    static constexpr int RAWS = ES == 2 ? 0 : D == 256 ? 2 : 3;
-    static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 5) : (D == 64 ? 9 : D == 128 ? 3 : 4);
+    static constexpr int RAWS = ES == 2 ? 0 : D == 64 ? 3 : 2;
+    static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 5) : (D == 64 ? 9 : 4);
     static constexpr int QBOX = kSubRows * 128;
     static constexpr int QBYTES = BOXES * QBOX;     // one sub-tile of queries
     static constexpr int SMEM = NSUB * QBYTES + SLOTS * SLOT + RAWS * RAW + 1024;
@@ -275,8 +278,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     uint8_t *q_smem = smem;                      // NSUB x [D / 64 boxes][128 rows x 128 B]
     uint8_t *ring = smem + NSUB * C::QBYTES;     // SLOTS blocks: K, V, K, V, ...
     uint8_t *raws = ring + SLOTS * C::SLOT;      // RAWS blocks of E4M3 codes, in the same order
-    __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], raw_full[RAWS + 1], raw_empty[RAWS + 1], s_full[2], p_ready[2], o_done[2], o_free[2], q_full[2],
-        drain[2];
+    __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], raw_full[RAWS + 1], raw_empty[RAWS + 1], s_full[2],
+        p_ready[2], o_done[2], o_free[2], q_full[2], drain[2];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t abort_flag;
     __shared__ Walk s_walk[C::THREADS / 32];
@@ -519,9 +522,11 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         const int t = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;  // sub-tile, row of it
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + t * kKeys, o_addr = tmem + lanes + C::O_COL + t * D;
-        // scores c x_s with c > 0: the queries take the sign, and all zeros for c = 0
-        const float c_all = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
-        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u, keep = a.scale_log2 == 0.f ? 0u : ~0u;
+        // scores c x_s with c > 0: the queries take the sign, and a factor of zero
+        // becomes the smallest normal number, which makes every score as good as zero
+        // (zero times a masked score's -inf would be NaN)
+        const float c_all = fmaxf(fabsf(a.scale_log2), FLT_MIN);
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
         uint32_t n_s = 0, n_o = 0;  // blocks, segments with blocks so far
         bool ok = true;
         while (ok && next_segment()) {
@@ -551,7 +556,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         }
                     const int E = row_exponent(largest);
                     down = down_by(E);
-                    c = c_all * up_by(E);
+                    c = fmaxf(c_all * up_by(E), FLT_MIN);
                 }
 #pragma unroll 8
                 for (int x = 0; x < D / 8; ++x) {
@@ -562,10 +567,10 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         v = make_uint4(pack_f16(f[0] * down, f[1] * down), pack_f16(f[2] * down, f[3] * down),
                                        pack_f16(f[4] * down, f[5] * down), pack_f16(f[6] * down, f[7] * down));
                     }
-                    v.x = (v.x ^ flip) & keep;
-                    v.y = (v.y ^ flip) & keep;
-                    v.z = (v.z ^ flip) & keep;
-                    v.w = (v.w ^ flip) & keep;
+                    v.x ^= flip;
+                    v.y ^= flip;
+                    v.z ^= flip;
+                    v.w ^= flip;
                     sts16(dst + (x >> 3) * C::QBOX + (((x & 7) ^ (row & 7)) << 4), v);
                 }
                 fence_async();
@@ -668,8 +673,9 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 if (real && whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
-                        dst[(x + e) >> 3] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                                       pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+                        dst[(x + e) >> 3] =
+                            make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                       pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
                 } else if (real) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) dst_part[(x + e) >> 2] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);

@@ -558,8 +558,9 @@ typedef struct {
 
 /* New tokens of a step, packed row after row: row b's are tokens
  * [q_start[b], q_start[b + 1]) (q_start: device int32 [batch + 1], not
- * decreasing, within [0, n_tokens]); a row may have none. Tokens outside
- * every row (padding) are neither read nor written. The lists already count
+ * decreasing, within [0, n_tokens]); a row may have none. What stands in
+ * tokens outside every row (padding) does not matter, and nothing is written
+ * for them. The lists already count
  * them: the n new tokens of row b are the last n of each of its lists. */
 typedef struct {
     int32_t n_tokens;

@@ -136,6 +136,36 @@ def test_flat_and_sharp_softmax(dtype, q_scale):
     p.check(O, lse, scale=-0.3)
 
 
+@pytest.mark.parametrize("d,dtype", [(128, BF), (128, F8), (64, BF)])
+@pytest.mark.parametrize("most", [1, 600])
+def test_more_lists_than_threads(d, dtype, most):
+    # decode and chunk forms over hundreds to thousands of tiles, most of them without rows or with few keys
+    rng = random.Random(most)
+    counts = [rng.choice([0, 1, 1]) for _ in range(260)]
+    counts[37] = most
+    counts[200] = min(most, 40)
+    lens = [[c + rng.choice([0, 1, 30]) for _ in range(3)] for c in counts]
+    lens[90][1] = lens[251][2] = 900
+    p = Problem(16, counts, lens, 2, d, 16, dtype, pad=3)
+    O, lse = p.run()
+    assert p.status == 0
+    p.check(O, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("counts", [[1, 1], [70, 2]])
+def test_queries_of_zero_and_tiny_and_large_ones(dtype, counts):
+    p = Problem(17, counts, [[counts[0] + 100, counts[0]], [40, 300]], 4, 128, 16, dtype)
+    p.Q[0] = 0
+    p.Q[-1] = 0
+    if counts[0] > 1:
+        for t, e in ((1, -120), (2, -70), (3, -30), (4, 8)):
+            p.Q[t] = (p.Q[t].double() * 2.0 ** e).to(BF)
+    for scale in (None, 0.0, 1e-30, -1e-37):
+        O, lse = p.run(scale=scale)
+        p.check(O, lse, scale=scale)
+
+
 def test_one_long_list_among_short_ones():
     p = Problem(4, [1, 1, 1], [[9000, 3], [1, 0], [64, 4097]], 4, 128, 16, BF)
     O, lse = p.run()

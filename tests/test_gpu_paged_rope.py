@@ -126,6 +126,16 @@ def test_far_positions_and_fast_pairs():
         _check(p, res, 2, 2, 128, layout, 1.0, (1.0, 1.0))
 
 
+@pytest.mark.parametrize("rows", [33, 1100])
+def test_many_rows(rows):
+    rng = random.Random(rows)
+    counts = [rng.choice([0, 0, 1, 2]) for _ in range(rows)]
+    p = _problem(10, counts, 1, 1, 64, 16, BF, pad_front=2, pad_back=3)
+    res = _run(p, 1, 1, 64, "half")
+    assert res[3] == 0
+    _check(p, res, 1, 1, 64, "half", 1.0, (1.0, 1.0))
+
+
 def test_queries_in_place():
     p = _problem(6, [3, 20], 2, 4, 128, 16, BF)
     res = _run(p, 2, 4, 64, "half", 1.0, in_place=True)
