@@ -617,9 +617,10 @@ def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, 
     if (K is None) != (V is None) or (K is None and seq_lens is not None):
         raise ValueError("K and V come together (and seq_lens only with them)")
     if K is not None:
-        _cache_types(K, V, k_pages)
+        if K.dtype is not k_pages.dtype or V.dtype is not k_pages.dtype:
+            raise ValueError("K, V and the pages must share one dtype: bf16 or float8_e4m3fn")
         t_max = K.shape[2] if K.dim() == 4 else 0
-        if tuple(K.shape) != (src.batch, src.heads, t_max, pool.head_dim) or K.shape != V.shape:
+        if K.shape != (src.batch, src.heads, t_max, pool.head_dim) or V.shape != K.shape:
             raise ValueError("K and V must be [batch, heads, t_max, head_dim] of the lists' sizes")
         if not (K.is_contiguous() and V.is_contiguous()):
             raise ValueError("tensors passed to the CUDA library must be contiguous")
