@@ -23,7 +23,8 @@
 // 6.8 TB/s, the measured copy peak; two rows of 60K-65K E4M3 tokens (10 KV heads)
 // 64 us, 5.0 TB/s (55 us without any arithmetic: start, first and last copies);
 // one row of 2K tokens 9 us, latency. The first form, with a fixed number of parts
-// per list, took 213, 101 and 7 us. #include <cuda_bf16.h>
+// per list, took 213, 101 and 7 us.
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -42,6 +43,7 @@ using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
 constexpr double kAgainBytes = 28e6;  // see takes_chunks
+constexpr int kSlack = 3;      // see cut_line
 constexpr float kLag = 8.f;    // log2 of how far a row's maximum may lag
 
 // Shape of one instantiation.
@@ -188,7 +190,7 @@ k_attend(const AttnArgs a)
     __shared__ int4 s_join[2];  // tiles to join: tile, first and last CTA with a part
     __shared__ float2 s_ml[A::WARPS][kRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
-    Walk w = cut_line<A::KEYS, A::THREADS>(a, kRows, 1, s_line);
+    Walk w = cut_line<A::KEYS, A::THREADS>(a, kRows, 1, kSlack, s_line);
     int at_unit = w.begin;  // of the line
     if (threadIdx.x < 2) s_join[threadIdx.x].x = -1;
     while (w.next<A::KEYS>(a, kRows)) {

@@ -153,27 +153,40 @@ struct Walk {
 };
 
 // This CTA's part of the line; every thread of the CTA must call it. (The
-// host has checked that the line's length fits 32 bits.)
+// host has checked that the line's length fits 32 bits.) There are fewer parts
+// than CTAs where a part would have less than min_units units and there are
+// not that many tiles either. Where whole tiles, of which some CTAs get one
+// more than others, cost a CTA less than `slack` units more than equal parts
+// do, a cut moves to the nearer end of its tile (not in tiles that are much
+// longer than a part): the parts of cut tiles have to be written, read and
+// joined. Measured (us, equal parts / whole tiles, 128 dims, bf16): 128 tiles of
+// 8 blocks, 16 rows 21 / 15.5, 256 rows 49 / 30; 512 tiles of 8, 16 rows 61 / 66.5
+// (5 blocks more), 256 rows 113 / 102; 32 tiles of 16, 256 rows 30 / 44 (12 more).
 struct LineScratch {
-    int sum[32], rest[32];
+    int sum[32], rest[32], live[32];
     int units, parts;  // the line's length, the CTAs that it is cut over
+    int last;          // where this CTA's part ends
     Walk walk;
 };
 template <int KEYS, int THREADS>
-__device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int min_units, LineScratch &s)
+__device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int min_units, int slack, LineScratch &s)
 {
     constexpr int WARPS = THREADS / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_tiles = a.batch * a.heads * a.tiles;
     // the first THREADS tiles, one per thread, and the sum of the others
     Tile t;
-    int mine = 0, rest = 0;
+    int mine = 0, rest = 0, live = 0;
     if ((int)threadIdx.x < n_tiles) {
         t = make_tile<KEYS>(a, threadIdx.x, tile_rows, blockIdx.x == 0);
         mine = units_of(t);
+        live = mine > 0;
     }
-    for (int x = threadIdx.x + THREADS; x < n_tiles; x += THREADS)
-        rest += units_of(make_tile<KEYS>(a, x, tile_rows, blockIdx.x == 0));
+    for (int x = threadIdx.x + THREADS; x < n_tiles; x += THREADS) {
+        const int u = units_of(make_tile<KEYS>(a, x, tile_rows, blockIdx.x == 0));
+        rest += u;
+        live += u > 0;
+    }
     auto scan = [&](int v) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -184,22 +197,28 @@ __device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int m
     };
     int upto = scan(mine);
     if (n_tiles > THREADS) rest = __reduce_add_sync(kFull, rest);
+    live = __reduce_add_sync(kFull, live);
     if (lane == 31) {
         s.sum[warp] = upto;
         s.rest[warp] = rest;
+        s.live[warp] = live;
     }
-    if (threadIdx.x == 0) s.walk.left = 0;
     __syncthreads();
-    int before = 0, units = 0;
+    int before = 0, units = 0, tiles = 0;
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) {
         before += i < warp ? s.sum[i] : 0;
         units += s.sum[i];
+        tiles += s.live[i];
     }
     int seen = units;  // in the tiles looked at so far
     if (n_tiles > THREADS)
         for (int i = 0; i < WARPS; ++i) units += s.rest[i];
-    const int parts = max(1, min((int)gridDim.x, units / min_units));
+    const int parts = max(1, min((int)gridDim.x, max(units / min_units, tiles)));
+    // ceil(tiles / parts) average tiles less units / parts, against the slack (less where fewer parts would be joined)
+    const int idle = (tiles + parts - 1) / parts * parts - tiles;  // places for a tile that stay empty
+    const bool move = (long long)idle * units * (int)gridDim.x < (long long)slack * tiles * parts * parts;
+    const int whole = move ? units / parts + slack : 0;  // tiles of up to so many units are not cut
     // part c begins at c units / parts, rounded down (in 32 bits where they do)
     auto begin = [&](int c) -> int {
         c = min(c, parts);
@@ -210,20 +229,24 @@ __device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int m
     if (threadIdx.x == 0) {
         s.units = units;
         s.parts = parts;
-        s.walk.begin = u0;
     }
-    auto claim = [&](int x, int off) {  // the thread whose tile holds u0 begins the walk
-        if (mine > 0 && off <= u0 && u0 < off + mine) {
-            s.walk.tile = x;
-            s.walk.skip = u0 - off;
-            s.walk.have = true;
+    // The threads whose tiles hold the part's first unit and the next part's: its ends.
+    auto claim = [&](int x, int off) {
+        if (mine == 0) return;
+        auto edge = [&](int u) -> int { return mine > whole ? u : 2 * (u - off) < mine ? off : off + mine; };
+        if (off <= u0 && u0 < off + mine) {
+            const int at = edge(u0);
+            s.walk.begin = at;
+            s.walk.have = at < off + mine;
+            s.walk.tile = at < off + mine ? x : x + 1;
+            s.walk.skip = at < off + mine ? at - off : 0;
             s.walk.t = t;
-            s.walk.left = u1 - u0;
         }
+        if (off <= u1 && u1 < off + mine) s.last = edge(u1);
     };
     if (u1 > u0) {
         claim(threadIdx.x, before + upto - mine);
-        for (int x0 = THREADS; x0 < n_tiles && seen <= u0; x0 += THREADS) {
+        for (int x0 = THREADS; x0 < n_tiles && seen <= (u1 < units ? u1 : u0); x0 += THREADS) {
             const int x = x0 + threadIdx.x;
             mine = 0;
             if (x < n_tiles) {
@@ -243,11 +266,14 @@ __device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int m
         }
     }
     __syncthreads();
-    return s.walk;
+    Walk w = s.walk;
+    w.left = u1 > u0 ? (u1 < units ? s.last : units) - w.begin : 0;
+    return w;
 }
 
-// The CTA whose part holds a unit of the line: the c with c units / parts
-// (rounded down) <= unit < (c + 1) units / parts.
+// The CTA whose part holds the first or last unit of a cut tile: the c with
+// c units / parts (rounded down) <= unit < (c + 1) units / parts. (A cut that
+// further than its tile's ends.)
 __device__ __forceinline__ int cta_of(int unit, const LineScratch &s)
 {
     return (int)((((long long)unit + 1) * s.parts - 1) / s.units);

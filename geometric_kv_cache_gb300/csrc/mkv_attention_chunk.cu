@@ -61,6 +61,7 @@ using namespace dev;
 constexpr int kSubRows = 128;                // rows per sub-tile: the MMA's M, the TMEM lanes
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kLag = 8.f;                  // log2 of how far a row's maximum may lag
+constexpr int kSlackKeys = 768;              // see cut_line
 constexpr int kMinBlocks = 4;                // least blocks of a CTA's part: fewer make more parts to join, not less time
 
 template <int D, int ES>
@@ -315,7 +316,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     {
-        const Walk start = cut_line<kKeys, C::THREADS>(a, C::ROWS, kMinBlocks, s_line);
+        const Walk start = cut_line<kKeys, C::THREADS>(a, C::ROWS, kMinBlocks, kSlackKeys / kKeys, s_line);
         if (lane == 0) s_walk[warp] = start;
     }
     // A warp's walk lies in shared memory: registers are for the loops.
