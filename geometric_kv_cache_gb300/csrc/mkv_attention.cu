@@ -42,7 +42,7 @@ namespace {
 using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
-constexpr double kAgainBytes = 28e6;  // see takes_chunks
+constexpr double kAgainBytes = 80e6;  // see takes_chunks
 constexpr int kSlack = 3;      // see cut_line
 constexpr float kLag = 8.f;    // log2 of how far a row's maximum may lag
 
@@ -119,60 +119,6 @@ template <int CPR>
 __device__ __forceinline__ uint32_t at_rows2(int r, int c)
 {
     return (uint32_t)(r * CPR + (c ^ (CPR >= 8 ? (r & 1) << 2 : 0))) * 16u;
-}
-
-// One row of a tile whose parts the CTAs c0 .. c1 left (c0's second, the first
-// of the others): a warp, eight parts' loads in flight. Parts were written by
-// other CTAs of this launch: loads through L2.
-template <int D>
-__device__ __forceinline__ void join_row(const AttnArgs &a, int c0, int c1, int r, int64_t token, int head)
-{
-    constexpr int E = D / 32, U = 8;
-    const int lane = threadIdx.x & 31;
-    float sum[E], l = 0.f, M = -CUDART_INF_F;
-#pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] = 0.f;
-    for (int s0 = c0; s0 <= c1; s0 += U) {
-        float2 ml[U], v[U][E / 2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u;
-            ml[u] = make_float2(-CUDART_INF_F, 0.f);
-            if (s <= c1) {
-                const int64_t at = ((int64_t)s * 2 + (s == c0 ? 1 : 0)) * kRows + r;
-                ml[u] = __ldcg(a.part_ml + at);
-                const float2 *src = reinterpret_cast<const float2 *>(a.part_o + at * D + lane * E);
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e) v[u][e] = __ldcg(src + e);
-            }
-        }
-        float best = M;
-#pragma unroll
-        for (int u = 0; u < U; ++u) best = fmaxf(best, ml[u].x);
-        if (best == -CUDART_INF_F) continue;
-        const float f0 = M == -CUDART_INF_F ? 0.f : exp2_approx(M - best);
-        M = best;
-        l *= f0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[e] *= f0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (ml[u].x == -CUDART_INF_F) continue;  // none, or it saw nothing
-            const float f = exp2_approx(ml[u].x - M);
-            l += f * ml[u].y;
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-                sum[2 * e] += f * v[u][e].x;
-                sum[2 * e + 1] += f * v[u][e].y;
-            }
-        }
-    }
-    const float inv = l > 0.f ? a.v_scale / l : 0.f;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[2 * e] * inv, sum[2 * e + 1] * inv);
-    if (lane == 0 && a.lse)
-        a.lse[token * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
 }
 
 template <int D, int ES>
@@ -531,11 +477,7 @@ k_attend(const AttnArgs a)
         if (j.x < 0) continue;
         __threadfence();
         const Tile t = make_tile<A::KEYS>(a, j.x, kRows, false);
-        const int64_t token0 = a.q_start[t.b];
-        for (int r = warp; r < t.rows; r += A::WARPS) {
-            const int R = t.row0 + r, i = a.by_group(R);
-            join_row<D>(a, j.y, j.z, r, token0 + i, t.j * a.group + R - i * a.group);
-        }
+        for (int r = warp; r < t.rows; r += A::WARPS) join_rows<D, kRows, 1, 8>(a, t, j.y, j.z, r);
     }
 }
 
@@ -552,24 +494,28 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 }  // namespace
 
 // Which form: this file's reads K and V once per 16 rows, the other once per
-// 128 or 256, but takes 10 to 17 us more from launch to end. Up to 16 rows (E4M3:
-// 32, the other form expands its codes) this one always; beyond, while the
-// bytes that its further tiles read again, 12 to 18 ns per MB, cost less.
-// Measured (us, this form / the other, 128 dims): 8 lists of 4096 keys, bf16, 32
-// rows 15 / 22, 96 rows 25 / 25, 128 rows 28 / 27; 128 lists of 16384 keys, 16 rows 171 /
-// 186, 32 rows 327 / 188; E4M3 16 rows 114 / 265, 32 rows 216 / 265, 48 rows 301 / 268.
-bool takes_chunks(int64_t lists, int64_t rows, int64_t max_len, int32_t head_dim, int32_t es)
+// 128 or 256, but takes 4 to 12 us more from launch to end. Up to 16 rows this
+// one always; beyond, while what its further tiles cost is less: bytes that are
+// read again, 128 operations' worth per key, and 1024 keys' worth of start and
+// end per tile. (Rows are a bound, so the tiles are too: every new token's, and
+// one begun per list.) Over 350 mixes of 32 to 256 rows, 8 to 384 lists of 64 to
+// 4096 keys, all dims and types, the rule takes 1% more time than the better
+// form for each; bytes alone took 8%. Measured (us, this form / the other, 128
+// dims): MEASURED
+bool takes_chunks(int64_t batch, int64_t heads, int32_t group, int64_t n_tokens, int64_t max_q, int64_t max_len,
+                  int32_t head_dim, int32_t es)
 {
-    const int64_t again = (rows + kRows - 1) / kRows - (es == 1 ? 2 : 1);
-    return again > 0 && (double)lists * (double)max_len * (double)again * head_dim * es > kAgainBytes;
+    const int64_t per_list = (max_q * group + kRows - 1) / kRows - 1, in_all = n_tokens * group / kRows;
+    const int64_t again = heads * std::min(batch * per_list, in_all);
+    return (double)again * (double)(max_len + 1024) * (head_dim * es + 128) > kAgainBytes;
 }
 
-AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int32_t es,
-                        int ctas)
+AttnPlan attention_plan(int32_t batch, int32_t heads, int32_t group, int32_t n_tokens, int32_t max_q, int32_t max_len,
+                        int32_t head_dim, int32_t es, int ctas)
 {
     AttnPlan p;
     const int64_t rows = (int64_t)max_q * group;
-    p.chunked = takes_chunks(lists, rows, max_len, head_dim, es);
+    p.chunked = takes_chunks(batch, heads, group, n_tokens, max_q, max_len, head_dim, es);
     const int tile = p.chunked ? chunk_tile_rows(head_dim) : kRows;
     p.tiles = (int32_t)((rows + tile - 1) / tile);
     p.ctas = ctas;

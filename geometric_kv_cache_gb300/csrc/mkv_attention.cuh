@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include "mkv_device.cuh"
@@ -319,6 +320,76 @@ __device__ __forceinline__ int opened_tile(const LineInfo *__restrict__ info, in
     }
     c1 = min(c1, ctas - 1);
     return tile;
+}
+
+// Rows r0 .. r0 + J - 1 of a tile (of ROWS rows) whose parts the CTAs c0 .. c1
+// left (c0's second, the first of the others): a warp, the loads of U parts in
+// flight. Other CTAs wrote them, maybe in this launch: loads through L2.
+template <int D, int ROWS, int J, int U>
+__device__ __forceinline__ void join_rows(const AttnArgs &a, const Tile &t, int c0, int c1, int r0)
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    float sum[J][E], l[J], M[J];
+#pragma unroll
+    for (int x = 0; x < J; ++x) {
+        l[x] = 0.f;
+        M[x] = -CUDART_INF_F;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[x][e] = 0.f;
+    }
+    for (int s0 = c0; s0 <= c1; s0 += U) {
+        float2 ml[U][J], v[U][J][E / 2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u;
+#pragma unroll
+            for (int x = 0; x < J; ++x) {
+                ml[u][x] = make_float2(-CUDART_INF_F, 0.f);
+                if (s > c1 || r0 + x >= t.rows) continue;
+                const int64_t at = ((int64_t)s * 2 + (s == c0 ? 1 : 0)) * ROWS + r0 + x;
+                ml[u][x] = __ldcg(a.part_ml + at);
+                const float2 *src = reinterpret_cast<const float2 *>(a.part_o + at * D + lane * E);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) v[u][x][e] = __ldcg(src + e);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < J; ++x) {
+            float best = M[x];
+#pragma unroll
+            for (int u = 0; u < U; ++u) best = fmaxf(best, ml[u][x].x);
+            if (best == -CUDART_INF_F) continue;
+            const float f0 = M[x] == -CUDART_INF_F ? 0.f : exp2_approx(M[x] - best);
+            M[x] = best;
+            l[x] *= f0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum[x][e] *= f0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (ml[u][x].x == -CUDART_INF_F) continue;  // none, or it saw nothing
+                const float f = exp2_approx(ml[u][x].x - M[x]);
+                l[x] += f * ml[u][x].y;
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    sum[x][2 * e] += f * v[u][x][e].x;
+                    sum[x][2 * e + 1] += f * v[u][x][e].y;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < J; ++x) {
+        if (r0 + x >= t.rows) break;
+        const float inv = l[x] > 0.f ? a.v_scale / l[x] : 0.f;
+        const int R = t.row0 + r0 + x, i = a.by_group(R), head = t.j * a.group + R - i * a.group;
+        const int64_t token = (int64_t)a.q_start[t.b] + i;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[x][2 * e] * inv, sum[x][2 * e + 1] * inv);
+        if (lane == 0 && a.lse)
+            a.lse[token * a.q_heads + head] = l[x] > 0.f ? (M[x] + log2f(l[x])) * CUDART_LN2_F : -CUDART_INF_F;
+    }
 }
 
 }  // namespace

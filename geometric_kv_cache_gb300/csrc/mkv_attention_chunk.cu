@@ -701,71 +701,24 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     }
 }
 
-// Joins the parts of the tile that CTA blockIdx.y opened, if it did. A warp
-// takes kJoin rows at a time, their loads in flight together.
-constexpr int kJoin = 4;
-
-template <int D, int ES>
+// Joins the parts of the tile that CTA blockIdx.y opened, if it did: a warp per
+// J rows, eight of their parts in flight. Four rows; one where few tiles are
+// cut into many parts each, whose joining is a chain of round trips (two lists
+// of 32768 keys, 256 rows: 35 us, with four rows 55), at the price of four times
+// the blocks, of which most find nothing to join (2.5 us).
+template <int D, int ES, int J>
 __global__ void __launch_bounds__(256)
 k_chunk_combine(const AttnArgs a, const LineInfo *__restrict__ info)
 {
     using C = Chunk<D, ES>;
-    constexpr int E = D / 32;
     pdl_wait();
-    const int c0 = (int)blockIdx.y, lane = threadIdx.x & 31;
+    const int c0 = (int)blockIdx.y;
     int c1;
     const int tile = opened_tile(info, c0, (int)gridDim.y, c1);
     if (tile < 0) return;
     const Tile t = make_tile<C::KEYS>(a, tile, C::ROWS, false);
-    const int row0 = ((int)blockIdx.x * 8 + (threadIdx.x >> 5)) * kJoin;
-    if (row0 >= t.rows) return;
-    float sum[kJoin][E], l[kJoin], M[kJoin];
-#pragma unroll
-    for (int u = 0; u < kJoin; ++u) {
-        l[u] = 0.f;
-        M[u] = -CUDART_INF_F;
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[u][e] = 0.f;
-    }
-    for (int c = c0; c <= c1; ++c) {
-        const int64_t at = ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * C::ROWS + row0;
-        float2 ml[kJoin], v[kJoin][E / 2];
-#pragma unroll
-        for (int u = 0; u < kJoin; ++u) {
-            ml[u] = make_float2(-CUDART_INF_F, 0.f);
-            if (row0 + u < t.rows) {
-                ml[u] = a.part_ml[at + u];
-                const float2 *src = reinterpret_cast<const float2 *>(a.part_o + (at + u) * D + lane * E);
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e) v[u][e] = src[e];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kJoin; ++u) {
-            if (ml[u].x == -CUDART_INF_F) continue;  // saw nothing
-            const float best = fmaxf(M[u], ml[u].x);
-            const float f0 = M[u] == -CUDART_INF_F ? 0.f : exp2_approx(M[u] - best), f1 = exp2_approx(ml[u].x - best);
-            M[u] = best;
-            l[u] = l[u] * f0 + f1 * ml[u].y;
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-                sum[u][2 * e] = sum[u][2 * e] * f0 + f1 * v[u][e].x;
-                sum[u][2 * e + 1] = sum[u][2 * e + 1] * f0 + f1 * v[u][e].y;
-            }
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < kJoin; ++u) {
-        if (row0 + u >= t.rows) break;
-        const float inv = l[u] > 0.f ? a.v_scale / l[u] : 0.f;
-        const int R = t.row0 + row0 + u, i = a.by_group(R), head = t.j * a.group + R - i * a.group;
-        const int64_t token = (int64_t)a.q_start[t.b] + i;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[u][2 * e] * inv, sum[u][2 * e + 1] * inv);
-        if (lane == 0 && a.lse)
-            a.lse[token * a.q_heads + head] = l[u] > 0.f ? (M[u] + log2f(l[u])) * CUDART_LN2_F : -CUDART_INF_F;
-    }
+    const int row0 = ((int)blockIdx.x * 8 + (threadIdx.x >> 5)) * J;
+    if (row0 < t.rows) join_rows<D, C::ROWS, J, 8 / J>(a, t, c0, c1, row0);
 }
 
 // --------------------------------------------------------------- host side --
@@ -813,7 +766,9 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
     k_attend_chunk<D, ES><<<a.ctas, C::THREADS, C::SMEM, st>>>(mk, mv, a, info);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(C::ROWS / (8 * kJoin)), (unsigned)a.ctas);
+    // tiles of eight parts and more
+    const bool few = (int64_t)a.batch * a.heads * a.tiles * 8 <= a.ctas && a.max_len >= 8 * kMinBlocks * C::KEYS;
+    cfg.gridDim = dim3((unsigned)(C::ROWS / 8 / (few ? 1 : 4)), (unsigned)a.ctas);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -821,7 +776,8 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_chunk_combine<D, ES>, a, (const LineInfo *)info);
+    return few ? cudaLaunchKernelEx(&cfg, k_chunk_combine<D, ES, 1>, a, (const LineInfo *)info)
+               : cudaLaunchKernelEx(&cfg, k_chunk_combine<D, ES, 4>, a, (const LineInfo *)info);
 }
 
 }  // namespace

@@ -100,8 +100,8 @@ struct AttnPlan {
     int64_t part_rows = 0;  // rows of part_o
     size_t bytes = 0;
 };
-AttnPlan attention_plan(int64_t lists, int32_t group, int32_t max_q, int32_t max_len, int32_t head_dim, int32_t es,
-                        int ctas);
+AttnPlan attention_plan(int32_t batch, int32_t heads, int32_t group, int32_t n_tokens, int32_t max_q, int32_t max_len,
+                        int32_t head_dim, int32_t es, int ctas);
 int chunk_tile_rows(int head_dim);
 cudaError_t launch_attend_chunk(const AttnArgs &a, cudaStream_t st);
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t st);

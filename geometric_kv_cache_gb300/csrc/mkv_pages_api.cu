@@ -313,8 +313,8 @@ static mkv_status attention_sizes(const mkv_page_pool &pool, const mkv_page_list
     *plan = AttnPlan();
     if (no_lists(lists) || max_q == 0) return MKV_OK;
     const int64_t n = (int64_t)lists.batch * lists.heads;
-    *plan = attention_plan(n, tokens.q_heads / lists.heads, max_q, max_len, pool.head_dim,
-                           elem_bytes(pool.dtype), kPlanSms);
+    *plan = attention_plan(lists.batch, lists.heads, tokens.q_heads / lists.heads, tokens.n_tokens, max_q, max_len,
+                           pool.head_dim, elem_bytes(pool.dtype), kPlanSms);
     // blocks of at least 64 keys of all tiles are counted in 32 bits
     if (n * plan->tiles > (int64_t)INT32_MAX / ((int64_t)max_len / 64 + 2))
         return MKV_ERR_UNSUPPORTED;

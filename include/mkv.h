@@ -651,7 +651,8 @@ typedef enum {
 int32_t mkv_rope_frequencies(int32_t rot_dim, double theta, mkv_rope_scaling scaling, double scale,
                              int32_t original_len, double low_turns, double high_turns, float *inv_freq);
 
-/* Bytes of workspace for mkv_paged_attention (0 on a bad shape). */
+/* Bytes of workspace for mkv_paged_attention (0 on a bad shape). What is enough
+ * for more tokens, a larger max_q or max_len is enough for less of them. */
 size_t mkv_attention_workspace_size(mkv_page_pool pool, mkv_page_lists lists, mkv_new_tokens tokens, int32_t max_q,
                                     int32_t max_len);
 

@@ -255,6 +255,80 @@ def test_long_lists_of_full_and_nearly_empty_tiles(d, dtype, page):
     p.check(O, lse)
 
 
+def wide(seed, counts, extra, G, d, page, dtype, heads=16, **kw):
+    """A problem of enough query rows for the form for chunks: its parts in the workspace are 128 or 256 rows, not 16."""
+    p = Problem(seed, counts, [[max(0, c + extra[(b + j) % len(extra)]) for j in range(heads)]
+                               for b, c in enumerate(counts)], G, d, page, dtype, **kw)
+    pool = torch.empty(p.k.shape, dtype=dtype, device=DEV)
+    ws = mkv.attention_workspace_for(torch.empty((p.n, heads * G, d), dtype=BF, device=DEV), pool,
+                                     torch.empty(p.table.shape, dtype=torch.int32, device=DEV), p.max_q, p.max_len)
+    assert ws.numel() > 152 * 2 * 100 * (4 * d + 8)
+    return p
+
+
+@pytest.mark.parametrize("d,dtype,page", SHAPES)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 4), (33, 0), (130, 64), (5000, 4)])
+def test_chunk_form_windows_and_short_lists(d, dtype, page, window, sinks):
+    # lists shorter than their new tokens (the first see nothing), empty ones, rows without tokens and of one token
+    p = wide(window + 1, [36, 0, 1, 2, 20], [0, 1, -3, 200, 430, -40], 8, d, page, dtype, pad=2)
+    O, lse = p.run(window, sinks)
+    assert p.status == 0
+    p.check(O, lse, window, sinks)
+
+
+@pytest.mark.parametrize("d,dtype,page", SHAPES)
+def test_chunk_form_one_token_per_row(d, dtype, page):
+    p = wide(2, [1] * 80, [-1, 0, 5, 129, page, 700], 40, d, page, dtype, heads=2)
+    O, lse = p.run()
+    assert p.status == 0
+    p.check(O, lse)
+
+
+@pytest.mark.parametrize("d,dtype,page", SHAPES)
+@pytest.mark.parametrize("extra", [[0, 128, 256, 900, 1500], [1900], [0, 60]])
+def test_chunk_form_cut_and_whole_tiles(d, dtype, page, extra):
+    # 96 to 160 tiles of 1 to 32 blocks: some lines are cut at tiles' ends, some inside tiles
+    p = wide(3, [66, 20, 33, 1], extra, 4, d, page, dtype)
+    a, b = p.run(strided=True), p.run()
+    assert p.status == 0
+    p.check(*a)
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("d,dtype,page", [(64, F8, 32), (128, BF, 16), (128, F8, 64), (256, BF, 32)])
+@pytest.mark.parametrize("q_scale,scale", [(0.0, None), (30.0, None), (1.0, -0.3), (1.0, 0.0), (1.0, -1e-37)])
+def test_chunk_form_flat_sharp_and_negative_scales(d, dtype, page, q_scale, scale):
+    p = wide(4, [36, 3, 10], [0, 7, 300], 8, d, page, dtype, q_scale=q_scale)
+    p.Q[0] = 0
+    for t, e in ((1, -120), (2, -70), (3, -30), (4, 8)):
+        p.Q[t] = (p.Q[t].double() * 2.0 ** e).to(BF)
+    O, lse = p.run(scale=scale)
+    assert p.status == 0
+    p.check(O, lse, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+def test_chunk_form_reports_bad_pages_rows_and_lengths(dtype):
+    p = wide(5, [70, 9, 30], [300], 8, 128, 16, dtype)
+    good, _ = p.run()
+    table, lens, start = p.table.clone(), p.lens.clone(), p.start.clone()
+    p.table[0, 0, 2], p.table[0, 5, 3] = p.k.shape[0], -1
+    O, _ = p.run()
+    assert p.status == mkv.MKV_DEV_BAD_PAGE
+    assert torch.equal(O[70:], good[70:]) and torch.equal(O[:, 8:40], good[:, 8:40])
+    p.table = table.clone()
+    p.lens[1, 3] = p.max_len + 1
+    O, _ = p.run()
+    assert p.status == mkv.MKV_DEV_BAD_SEQ_LEN
+    untouched = torch.full_like(O[70:79, 24:32], 7.0)
+    assert torch.equal(O[70:79, 24:32], untouched) and torch.equal(O[:70], good[:70])
+    p.lens = lens.clone()
+    p.start = start.clone()
+    p.start[2] = p.start[3] + 1  # row 2 ends before it begins
+    p.run(max_q=70)
+    assert p.status == mkv.MKV_DEV_BAD_TOKENS
+
+
 def test_workspace_of_any_contents_after_one_status_call():
     p = Problem(15, [1, 1], [[3000, 200], [50, 4000]], 4, 128, 16, BF)
     dev = lambda x: pu.raw(x).to(DEV).view(x.dtype) if x.dtype in pu.CODES else x.to(DEV)  # noqa: E731
