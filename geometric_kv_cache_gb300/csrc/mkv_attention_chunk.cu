@@ -4,7 +4,7 @@
 // few).
 //
 // A tile is NSUB x 128 packed rows (new token, query head of the KV head's
-// group) of one list; a block is 128 keys. Per block and sub-tile
+// group) of one list; a block is 128 keys (64 at 256 dims). Per block and sub-tile
 //     S = Q K^T          tcgen05.mma, M = 128, N = 128, fp32 in TMEM
 //     P = 2^(S c - m)    one thread per row, P rounded to 16 bits over S in TMEM
 //     O += P V           tcgen05.mma with P as the A operand from TMEM
@@ -267,9 +267,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+// (Not inlined: its registers would change how the kernel's loops are compiled.)
+// Not inlined: the kernel's loops are then compiled with fewer spills (2048
+// tokens of 32 query heads over 32768 bf16 tokens 712 us, inlined 755; a call with nearly
+// nothing to do takes 0.7 us more).
+template <int KEYS, int THREADS>
+__device__ __noinline__ void cut_for_warps(const AttnArgs &a, int tile_rows, int min_units, int slack, LineScratch &s,
+                                           Walk *walks)
+{
+    const Walk start = cut_line<KEYS, THREADS>(a, tile_rows, min_units, slack, s);
+    if ((threadIdx.x & 31) == 0) walks[threadIdx.x >> 5] = start;
+}
+
 template <int D, int ES>
 __global__ void __launch_bounds__(Chunk<D, ES>::THREADS, 1)
-k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
+k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs a,
                LineInfo *info)
 {
     using C = Chunk<D, ES>;
@@ -315,10 +327,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    {
-        const Walk start = cut_line<kKeys, C::THREADS>(a, C::ROWS, kMinBlocks, kSlackKeys / kKeys, s_line);
-        if (lane == 0) s_walk[warp] = start;
-    }
+    cut_for_warps<kKeys, C::THREADS>(a, C::ROWS, kMinBlocks, kSlackKeys / kKeys, s_line, s_walk);
     // A warp's walk lies in shared memory: registers are for the loops.
     const Walk &w = s_walk[warp];
     auto next_segment = [&]() -> bool {
@@ -530,16 +539,16 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
         uint32_t n_s = 0, n_o = 0;  // blocks, segments with blocks so far
         bool ok = true;
-        while (ok && next_segment()) {
-            if (t * kSubRows >= w.t.rows) continue;
+        // The next segment with rows for this sub-tile, its queries on their way
+        // to the MMAs. (Every wait for the last block of the segment before has
+        // ended: Q is free.)
+        float c_row = c_all;
+        auto begin = [&]() -> bool {
+            do {
+                if (!next_segment()) return false;
+            } while (t * kSubRows >= w.t.rows);
             const bool real = t * kSubRows + row < w.t.rows;
-            const int first = w.from(), nb = w.to() - first;
-            const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
-            // the row's own key (of rows that are not there: the first row's)
-            const int p = w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows + (real ? row : 0));
-            float c = c_all;
-            // (every wait for this sub-tile's last block of the segment before has ended: Q is free)
-            if (nb > 0) {
+            if (w.to() > w.from()) {
                 const int R = w.t.row0 + t * kSubRows + row, i = a.by_group(R), head = w.t.j * a.group + R - i * a.group;
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     a.Q + 2 * (((int64_t)a.q_start[w.t.b] + i) * a.q_stride + (int64_t)head * D));
@@ -557,7 +566,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         }
                     const int E = row_exponent(largest);
                     down = down_by(E);
-                    c = fmaxf(c_all * up_by(E), FLT_MIN);
+                    c_row = fmaxf(c_all * up_by(E), FLT_MIN);
                 }
 #pragma unroll 8
                 for (int x = 0; x < D / 8; ++x) {
@@ -578,6 +587,15 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) bar_arrive(&q_full[t]);
             }
+            return true;
+        };
+        while (begin()) {
+            const bool real = t * kSubRows + row < w.t.rows;
+            const int first = w.from(), nb = w.to() - first;
+            const float c = ES == 1 ? c_row : c_all;
+            // the row's own key (of rows that are not there: the first row's)
+            const int p = w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows + (real ? row : 0));
+            const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
             // the first and last place that is visible to every row: blocks inside need no mask
             const int r_last = min(w.t.rows, (t + 1) * kSubRows) - 1;
             const int whole_to = w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows);
@@ -661,6 +679,9 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const float inv = l > 0.f ? a.v_scale / l : 0.f;
             uint4 *dst = reinterpret_cast<uint4 *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D));
             float4 *dst_part = reinterpret_cast<float4 *>(a.part_o + part * D);
+            if (real && whole && a.lse)
+                a.lse[token * a.q_heads + head] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+            if (real && !whole) a.part_ml[part] = make_float2(m, l);
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 float o[32];
@@ -683,9 +704,6 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 }
                 __syncwarp();
             }
-            if (real && whole && a.lse)
-                a.lse[token * a.q_heads + head] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
-            if (real && !whole) a.part_ml[part] = make_float2(m, l);
             if (nb > 0) {
                 fence_before();
                 __syncwarp();
