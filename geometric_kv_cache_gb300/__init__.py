@@ -654,7 +654,8 @@ def mkv_rope_append(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens,
     if Q.dim() != 3:
         raise ValueError("Q must be a bf16 tensor [n_tokens, q_heads, head_dim]")
     n, hq, d = Q.shape[0], Q.shape[1], pool.head_dim
-    qs, ks, vs = _token_rows(Q, hq, d, n, "Q"), _token_rows(K, lists.heads, d, n, "K"), _token_rows(V, lists.heads, d, n, "V")
+    qs = _token_rows(Q, hq, d, n, "Q")
+    ks, vs = _token_rows(K, lists.heads, d, n, "K"), _token_rows(V, lists.heads, d, n, "V")
     _token_rows(Q_out, hq, d, n, "Q_out")
     if not Q_out.is_contiguous():
         raise ValueError("Q_out must be contiguous")

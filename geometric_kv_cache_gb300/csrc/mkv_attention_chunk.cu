@@ -30,7 +30,7 @@
 // pipe is busy 67% of the time. Without the softmax (weights left as they are)
 // the same loop takes 0.63 ms, without copies too 0.57: what is left is the chain
 // scores -> weights -> product of each sub-tile, of which two overlap. E4M3 at
-// the same size 0.88 ms (0.99 with three slots and three blocks of codes instead
+// the same size 0.86 ms (0.99 with three slots and three blocks of codes instead
 // of four and two); the conversions themselves cost nothing, the traffic of
 // codes and their expansion through shared memory does.
 //
@@ -77,6 +77,11 @@ struct Chunk {
     static constexpr int RAW = KEYS * D;            // ... as E4M3 codes
     static constexpr int RAWS = ES == 2 ? 0 : D == 64 ? 3 : 2;
     static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 5) : (D == 64 ? 9 : 4);
+    // The next tile's queries go to the MMAs before this one's output is written
+    // (384 lists of 64 keys, 256 rows: E4M3 at 128 dims 43.5 us, else 44.7; bf16 at 256
+    // dims 63 / 66; 160 lists of 2048, 1024 rows, E4M3 at 64 dims 148 / 153). Of bf16 at 64
+    // and 128 dims it takes registers from the loop: 8192 rows over 32768 keys 725 / 712.
+    static constexpr bool EARLY = ES == 1 || D == 256;
     static constexpr int QBOX = kSubRows * 128;
     static constexpr int QBYTES = BOXES * QBOX;     // one sub-tile of queries
     static constexpr int SMEM = NSUB * QBYTES + SLOTS * SLOT + RAWS * RAW + 1024;
@@ -281,8 +286,8 @@ __device__ __noinline__ void cut_for_warps(const AttnArgs &a, int tile_rows, int
 
 template <int D, int ES>
 __global__ void __launch_bounds__(Chunk<D, ES>::THREADS, 1)
-k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ AttnArgs a,
-               LineInfo *info)
+k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+               const __grid_constant__ AttnArgs a, LineInfo *info)
 {
     using C = Chunk<D, ES>;
     constexpr int NSUB = C::NSUB, SLOTS = C::SLOTS, RAWS = C::RAWS, kKeys = C::KEYS, kBoxBytes = C::BOX;
@@ -589,7 +594,8 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             }
             return true;
         };
-        while (begin()) {
+        bool have = C::EARLY && begin();
+        while (C::EARLY ? have : begin()) {
             const bool real = t * kSubRows + row < w.t.rows;
             const int first = w.from(), nb = w.to() - first;
             const float c = ES == 1 ? c_row : c_all;
@@ -682,29 +688,31 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             if (real && whole && a.lse)
                 a.lse[token * a.q_heads + head] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
             if (real && !whole) a.part_ml[part] = make_float2(m, l);
+            const bool write = real, seen = nb > 0;
+            if (C::EARLY) have = begin();
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 float o[32];
-                if (nb > 0) {
+                if (seen) {
                     tmem_ld32(o_addr + x, o);
                     wait_ld();
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0.f;
                 }
-                if (real && whole) {
+                if (write && whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         dst[(x + e) >> 3] =
                             make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
                                        pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-                } else if (real) {
+                } else if (write) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) dst_part[(x + e) >> 2] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
                 __syncwarp();
             }
-            if (nb > 0) {
+            if (seen) {
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(&o_free[t]);

@@ -453,7 +453,8 @@ template <int LPR>
 __global__ void __launch_bounds__(kPageThreads, 3)
 k_page_compact(const PageArgs a, int list_ctas)
 {
-    constexpr int RB = LPR * 16, RPS = 32 / LPR, STEPS = kItem / RPS, B = STEPS < 4 ? STEPS : 4;  // rows per step, steps per batch
+    constexpr int RB = LPR * 16, RPS = 32 / LPR;  // bytes of a row, rows per step
+    constexpr int STEPS = kItem / RPS, B = STEPS < 4 ? STEPS : 4;  // steps, and of a batch
     pdl_wait();
     const bool bad = a.verdict[0] != 0;
     const int64_t lists = (int64_t)a.batch * a.heads;

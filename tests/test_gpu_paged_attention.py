@@ -255,6 +255,18 @@ def test_long_lists_of_full_and_nearly_empty_tiles(d, dtype, page):
     p.check(O, lse)
 
 
+@pytest.mark.parametrize("d,dtype,page", [(64, BF, 16), (128, BF, 64), (128, F8, 32), (256, BF, 32)])
+@pytest.mark.parametrize("extra", [[255], [700, 29], [-1, 59, 3899], [1999]])
+def test_many_short_lists_and_a_few_long_ones(d, dtype, page, extra):
+    # 140 tiles over 152 CTAs: cuts move to the ends of short tiles, long ones among them are cut all the same
+    p = Problem(18, [1] * 70, [[1 + extra[b % len(extra)], 1 + extra[(b + 1) % len(extra)]] for b in range(70)], 2, d,
+                page, dtype, pad=1)
+    a, b = p.run(), p.run()
+    assert p.status == 0
+    p.check(*a)
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
 def wide(seed, counts, extra, G, d, page, dtype, heads=16, **kw):
     """A problem of enough query rows for the form for chunks: its parts in the workspace are 128 or 256 rows, not 16."""
     p = Problem(seed, counts, [[max(0, c + extra[(b + j) % len(extra)]) for j in range(heads)]
