@@ -435,7 +435,7 @@ k_attend(const AttnArgs a)
 #pragma unroll
             for (int y = 0; y < A::WARPS; ++y) {
                 const float2 ml = s_ml[y][r];
-                const float f = ml.x == -CUDART_INF_F ? 0.f : exp2_approx(ml.x - M);
+                const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - M);
                 const float4 v = reinterpret_cast<const float4 *>(smem)[(y * kRows + r) * (D / 4) + c];
                 sum.x += f * v.x;
                 sum.y += f * v.y;
@@ -449,12 +449,11 @@ k_attend(const AttnArgs a)
                 if (c == 0) a.part_ml[part] = make_float2(M, l);
                 continue;
             }
-            const float inv = l > 0.f ? a.v_scale / l : 0.f;
+            const float inv = inverse_sum(l, a.v_scale);
             const int R = t.row0 + r, i = a.by_group(R), head = t.j * a.group + R - i * a.group;
             *reinterpret_cast<uint2 *>(a.O + 2 * ((int64_t)(qrow0 + i) * a.o_stride + (int64_t)head * D + 4 * c)) =
                 make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-            if (c == 0 && a.lse)
-                a.lse[(int64_t)(qrow0 + i) * a.q_heads + head] = l > 0.f ? (M + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+            if (c == 0 && a.lse) a.lse[(int64_t)(qrow0 + i) * a.q_heads + head] = log_sum(M, l);
         }
         __syncthreads();  // the next segment's copies may overwrite the results
         if (!w.whole() && threadIdx.x == 0) {

@@ -119,6 +119,16 @@ __device__ __forceinline__ int block_key(const Tile &t, int blk)
 // Units of a tile on the line: its blocks; one for a tile whose rows see nothing.
 __device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max(t.blocks, 1) : 0; }
 
+// What a row's sum l of weights makes of it. l is 0 only for a row that has seen
+// nothing (or scores of -inf alone); a NaN among its scores (queries may hold
+// anything) makes l NaN, also where the maximum, which passes over NaN, is
+// still -inf. Such a row's O and lse are NaN; no part of it may pass as empty.
+__device__ __forceinline__ float inverse_sum(float l, float v_scale) { return l == 0.f ? 0.f : v_scale / l; }
+__device__ __forceinline__ float log_sum(float m, float l)
+{
+    return l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * CUDART_LN2_F;
+}
+
 // A CTA's walk over its part of the line.
 struct Walk {
     int tile, left;  // the next tile, units left
@@ -359,7 +369,6 @@ __device__ __forceinline__ void join_rows(const AttnArgs &a, const Tile &t, int 
             float best = M[x];
 #pragma unroll
             for (int u = 0; u < U; ++u) best = fmaxf(best, ml[u][x].x);
-            if (best == -CUDART_INF_F) continue;
             const float f0 = M[x] == -CUDART_INF_F ? 0.f : exp2_approx(M[x] - best);
             M[x] = best;
             l[x] *= f0;
@@ -367,7 +376,7 @@ __device__ __forceinline__ void join_rows(const AttnArgs &a, const Tile &t, int 
             for (int e = 0; e < E; ++e) sum[x][e] *= f0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (ml[u][x].x == -CUDART_INF_F) continue;  // none, or it saw nothing
+                if (ml[u][x].y == 0.f) continue;  // none, or it saw nothing
                 const float f = exp2_approx(ml[u][x].x - M[x]);
                 l[x] += f * ml[u][x].y;
 #pragma unroll
@@ -381,14 +390,13 @@ __device__ __forceinline__ void join_rows(const AttnArgs &a, const Tile &t, int 
 #pragma unroll
     for (int x = 0; x < J; ++x) {
         if (r0 + x >= t.rows) break;
-        const float inv = l[x] > 0.f ? a.v_scale / l[x] : 0.f;
+        const float inv = inverse_sum(l[x], a.v_scale);
         const int R = t.row0 + r0 + x, i = a.by_group(R), head = t.j * a.group + R - i * a.group;
         const int64_t token = (int64_t)a.q_start[t.b] + i;
         uint32_t *dst = reinterpret_cast<uint32_t *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D + lane * E));
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(sum[x][2 * e] * inv, sum[x][2 * e + 1] * inv);
-        if (lane == 0 && a.lse)
-            a.lse[token * a.q_heads + head] = l[x] > 0.f ? (M[x] + log2f(l[x])) * CUDART_LN2_F : -CUDART_INF_F;
+        if (lane == 0 && a.lse) a.lse[token * a.q_heads + head] = log_sum(M[x], l[x]);
     }
 }
 

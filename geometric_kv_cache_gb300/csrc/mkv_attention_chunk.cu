@@ -682,11 +682,10 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             const int64_t token = (int64_t)a.q_start[w.t.b] + i;
             const bool whole = w.whole();
             const int64_t part = part_row(w, C::ROWS) + t * kSubRows + row;
-            const float inv = l > 0.f ? a.v_scale / l : 0.f;
+            const float inv = inverse_sum(l, a.v_scale);
             uint4 *dst = reinterpret_cast<uint4 *>(a.O + 2 * (token * a.o_stride + (int64_t)head * D));
             float4 *dst_part = reinterpret_cast<float4 *>(a.part_o + part * D);
-            if (real && whole && a.lse)
-                a.lse[token * a.q_heads + head] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+            if (real && whole && a.lse) a.lse[token * a.q_heads + head] = log_sum(m, l);
             if (real && !whole) a.part_ml[part] = make_float2(m, l);
             const bool write = real, seen = nb > 0;
             if (C::EARLY) have = begin();
