@@ -621,10 +621,14 @@ typedef enum {
  * head_dim], contiguous; may be Q itself when Q is contiguous. E4M3 pools
  * store round(value * (1 / k_scale)) (keys) and round(value * (1 / v_scale))
  * (values), saturated at 448, the reciprocals in fp32 (they must be finite);
- * for bf16 pools the scales must be 1. A token whose list
- * or page is invalid is not written (MKV_DEV_BAD_SEQ_LEN when the list is
- * shorter than the row's new tokens or longer than its capacity,
- * MKV_DEV_BAD_PAGE, MKV_DEV_BAD_TOKENS); its query is written all the same. */
+ * for bf16 pools the scales must be 1. A token whose list or page is invalid
+ * is not written into it (MKV_DEV_BAD_SEQ_LEN when the list is shorter than the
+ * row's new tokens or longer than its capacity, MKV_DEV_BAD_PAGE), nor is a
+ * token of a row whose range leaves [0, n_tokens]; its query is written all
+ * the same. q_start is checked as a whole: an entry outside [0, n_tokens] or
+ * below the one before it sets MKV_DEV_BAD_TOKENS. If entries decrease, which
+ * tokens are found in a row is unspecified; no query outside every row's range
+ * and no place but those of valid rows' new tokens is written even then. */
 mkv_status mkv_rope_append(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V,
                            int64_t v_stride, mkv_new_tokens tokens, const int32_t *positions, const float *inv_freq,
                            int32_t rot_dim, mkv_rope_layout layout, float factor, void *Q_out, mkv_page_pool pool,

@@ -69,3 +69,47 @@ def test_chunk_form_queries_that_are_not_finite(d, dtype, extra):
     O, lse = p.run()
     assert p.status == 0
     _check_with_nans(p, O, lse)
+
+
+@pytest.mark.parametrize("rows,start", [(3, [0, 5, 3, 9]), (3, [-2, 1, 3, 9]), (3, [0, 3, 6, 1000]), (3, [9, 6, 3, 0]),
+                                        (3, [0, 3, 2 ** 31 - 1, -2 ** 31]), (300, None), (40, None)])
+def test_rope_reports_every_bad_row_start(rows, start):
+    # what is written stays within the queries and the places of the lists' new tokens
+    n, H, G, d, page = 9 if start else 2 * rows, 1, 2, 64, 16
+    rng = random.Random(rows)
+    if start is None:  # one step back among many rows
+        start = [2 * b for b in range(rows + 1)]
+        start[rows - 7] = start[rows - 8] - 1
+    lens = [[rng.randint(n, n + 40)] for _ in range(rows)]
+    need = sum(pu.pages_of(r[0], page) for r in lens)
+    table, lens, _ = pu.random_lists(rng, lens, page, need + 3, pu.pages_of(n + 40, page))
+    k, v = pu.random_pool(rows, need + 3, page, d, BF)
+    qkv = torch.randn((n, H * (G + 2), d), generator=torch.Generator().manual_seed(rows)).to(BF)
+    positions, inv_freq = torch.arange(n, dtype=torch.int32) * 7, mkv.mkv_rope_frequencies(d, 10000.0)
+    kd, vd, x = k.to(DEV), v.to(DEV), qkv.to(DEV)
+    Q_out = torch.full((n, H * G, d), 7.0, dtype=BF, device=DEV)
+    ws = mkv.page_workspace_for(kd, table.to(DEV))
+    mkv.mkv_rope_append(x[:, :H * G], x[:, H * G:H * (G + 1)], x[:, H * (G + 1):], positions.to(DEV), inv_freq.to(DEV), kd,
+                        vd, table.to(DEV), lens.to(DEV), torch.tensor(start, dtype=torch.int32, device=DEV), Q_out, ws)
+    assert mkv.mkv_device_status(ws) == mkv.MKV_DEV_BAD_TOKENS
+    y = pu.rotate(qkv, positions, inv_freq, d, "half", 1.0)[:, :H * G]
+    near = (Q_out.cpu().double() - y).abs() <= 2.0 ** -8 * y.abs() * (1 + 2.0 ** -7) + 2.0 ** -18
+    turned, left = near.all(-1).all(-1), (Q_out.cpu() == 7.0).all(-1).all(-1)
+    assert (turned | left).all()
+    # a token inside the range of exactly one row has its query turned, also where that range leaves [0, n]
+    inside = torch.tensor([sum(start[b] <= t < start[b + 1] for b in range(rows)) for t in range(n)])
+    steady = all(start[b] <= start[b + 1] for b in range(rows))
+    if steady:
+        assert torch.equal(turned, inside == 1)
+    assert left[inside == 0].all()
+    # the lists' last places, and of rows with an invalid range none
+    may = torch.zeros(k.shape[:2], dtype=torch.bool)
+    for b in range(rows):
+        if 0 <= start[b] <= start[b + 1] <= n:
+            L = int(lens[b, 0])
+            for s in range(L - (start[b + 1] - start[b]), L):
+                may[int(table[b, 0, s // page]), s % page] = True
+    for pool, old in ((kd.cpu(), k), (vd.cpu(), v)):
+        assert torch.equal(pu.raw(pool)[~may], pu.raw(old)[~may])
+        if steady:  # the tokens of the valid rows are there
+            assert (pu.raw(pool)[may] != pu.raw(old)[may]).any(-1).all()
