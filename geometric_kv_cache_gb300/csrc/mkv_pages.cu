@@ -379,7 +379,7 @@ k_page_update(const PageArgs a)
     const int64_t h = ((int64_t)blockIdx.x * kPageThreads + threadIdx.x) >> 5;
     if (h >= (int64_t)a.batch * a.heads) return;
     const int b = (int)(h / a.heads), j = (int)(h - (int64_t)b * a.heads);
-    const bool in_place = a.table_out == a.table;
+    const bool in_place = a.lens_out == a.lens;  // (lists without capacity may have no tables at all)
     const int32_t *mine = a.table + h * a.max_pages;
     int32_t *out = a.table_out + h * a.max_pages;
     // (read together; the last two mean nothing after a bad verdict)

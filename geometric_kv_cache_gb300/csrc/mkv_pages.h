@@ -20,7 +20,7 @@ struct PageLayout {
 };
 
 // What the page calls share. Pointers of `in` and `out` lists; in place when
-// table_out == table.
+// lens_out == lens (and then table_out == table).
 struct PageArgs {
     int32_t n_pages, page_size, page_shift, batch, heads, max_pages;
     int64_t row_bytes;

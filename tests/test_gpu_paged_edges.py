@@ -113,3 +113,16 @@ def test_rope_reports_every_bad_row_start(rows, start):
         assert torch.equal(pu.raw(pool)[~may], pu.raw(old)[~may])
         if steady:  # the tokens of the valid rows are there
             assert (pu.raw(pool)[may] != pu.raw(old)[may]).any(-1).all()
+
+
+def test_failed_update_without_capacity_gives_the_lists_as_they_were():
+    # lists of no pages: both tables may be the same (no) memory, the lengths are not
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=DEV)  # noqa: E731
+    k = torch.zeros((4, 16, 64), dtype=BF, device=DEV)
+    ws = mkv.page_workspace_for(k, i32(2, 3, 0))
+    for n_new, status in ((1, mkv.MKV_DEV_BAD_PARENT), (0, 0)):
+        lens_out, refs_out = i32(2, 3) + 9, i32(4) + 9
+        mkv.mkv_page_update(k, k.clone(), i32(2, 3, 0), i32(2, 3), i32(4) + 3, i32(2, 3, 0), lens_out, refs_out, ws,
+                            n_new=i32(2) + n_new)
+        assert mkv.mkv_device_status(ws) == status
+        assert lens_out.tolist() == [[0] * 3] * 2 and refs_out.tolist() == [3] * 4
