@@ -602,7 +602,7 @@ def mkv_page_update(k_pages, v_pages, table, lens, refs, table_out, lens_out, re
 def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K=None,
                      V=None, seq_lens=None, stream=None):
     """Compaction in pages: list h keeps its tokens idx[h][:kept[h]] in new pages, its old pages lose a holder. idx
-    int32 [batch, heads, n] (None: the first kept tokens), kept int32 [batch, heads], as mkv_compress writes them.
+    int32 [batch, heads, n] (None: the first kept tokens, not the same as n = 0), kept int32 [batch, heads], as mkv_compress writes them.
     With K and V [batch, heads, t_max, head_dim] (and seq_lens) the tokens come from that contiguous cache instead."""
     dev = _on_device((k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K, V,
                       seq_lens))
@@ -625,8 +625,12 @@ def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, 
         if not (K.is_contiguous() and V.is_contiguous()):
             raise ValueError("tensors passed to the CUDA library must be contiguous")
         _int32(seq_lens, (src.batch,), "seq_lens")
-    _check((_lib or load()).mkv_page_compact(pool, src, refs.data_ptr(), _at(idx), 0 if idx is None else idx.shape[-1],
-                                             kept.data_ptr(), _at(K), _at(V), t_max, _at(seq_lens), dst,
+    # (a tensor without elements has no address, and to the library NULL means that there is none at all)
+    some = workspace.data_ptr()
+    _check((_lib or load()).mkv_page_compact(pool, src, refs.data_ptr(), None if idx is None else idx.data_ptr() or some,
+                                             0 if idx is None else idx.shape[-1], kept.data_ptr(),
+                                             None if K is None else K.data_ptr() or some,
+                                             None if V is None else V.data_ptr() or some, t_max, _at(seq_lens), dst,
                                              refs_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                              _raw_stream(stream, dev)), "mkv_page_compact")
 

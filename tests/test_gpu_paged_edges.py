@@ -126,3 +126,26 @@ def test_failed_update_without_capacity_gives_the_lists_as_they_were():
                             n_new=i32(2) + n_new)
         assert mkv.mkv_device_status(ws) == status
         assert lens_out.tolist() == [[0] * 3] * 2 and refs_out.tolist() == [3] * 4
+
+
+def test_compaction_of_no_indices_and_of_an_empty_cache_is_not_that_of_the_lists():
+    # an index tensor without columns, or a cache without tokens, holds nothing to keep
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=DEV)  # noqa: E731
+    k = torch.zeros((9, 16, 64), dtype=BF, device=DEV)
+    v = k.clone()
+    table, lens, refs = i32(1, 2, 2), i32(1, 2) + 20, i32(9)
+    table.view(-1).copy_(torch.arange(4))
+    refs[:4] = 1
+    ws = mkv.page_workspace_for(k, table)
+    empty = torch.zeros((1, 2, 0, 64), dtype=BF, device=DEV)
+    for extra in (dict(idx=i32(1, 2, 0)), dict(idx=i32(1, 2, 0), K=empty, V=empty), dict(idx=None, K=empty, V=empty)):
+        for kept in (1, 0):
+            out = i32(1, 2, 2) - 1, i32(1, 2) - 1, i32(9) - 1
+            mkv.mkv_page_compact(k, v, table, lens, refs, kept=i32(1, 2) + kept, table_out=out[0], lens_out=out[1],
+                                 refs_out=out[2], workspace=ws, **extra)
+            if kept:  # refused: the lists as they were
+                assert mkv.mkv_device_status(ws) == mkv.MKV_DEV_BAD_N_KEEP
+                assert torch.equal(out[0], table) and torch.equal(out[1], lens) and torch.equal(out[2], refs)
+            else:
+                assert mkv.mkv_device_status(ws) == 0
+                assert int(out[1].abs().sum()) == 0 and int(out[2].abs().sum()) == 0
