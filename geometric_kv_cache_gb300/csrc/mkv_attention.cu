@@ -8,7 +8,8 @@
 // packed 16 to a tile, with scores x_s = scale q.k_s over the visible tokens:
 //     m = max x, l = sum 2^(x - m), O = sum 2^(x - m) v / l
 // kept as running values over blocks of keys (m, l and O in fp32; a new maximum
-// multiplies l and O by 2^(m_old - m_new)).
+// multiplies l and O by 2^(m_old - m_new); any m near the maximum will do, see
+// kBase).
 //
 // This file: the form for few rows, whose bound is the bytes of K and V. A
 // tile is 16 rows (the M of mma.sync m16n8k16; a decode step of a group of 4
@@ -44,7 +45,6 @@ using namespace dev;
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
 constexpr double kAgainBytes = 80e6;  // see takes_chunks
 constexpr int kSlack = 3;      // see cut_line
-constexpr float kLag = 8.f;    // log2 of how far a row's maximum may lag
 
 // Shape of one instantiation.
 template <int D, int ES>
@@ -337,9 +337,8 @@ k_attend(const AttnArgs a)
             x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 1));
             x0 = fmaxf(x0, __shfl_xor_sync(kFull, x0, 2));
             x1 = fmaxf(x1, __shfl_xor_sync(kFull, x1, 2));
-            // The maximum may lag by 2^8 (weights stay below 256): rescaling O is rare.
-            if (__any_sync(kFull, x0 > m0 + kLag || x1 > m1 + kLag)) {
-                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            if (__any_sync(kFull, x0 - m0 > kLag<ES> || x1 - m1 > kLag<ES>)) {
+                const float n0 = fmaxf(m0, x0 - kBase<ES>), n1 = fmaxf(m1, x1 - kBase<ES>);
                 // (a row that has seen nothing yet has l = 0 and O = 0: any finite factor)
                 const float f0 = m0 == -CUDART_INF_F ? 0.f : exp2_approx(m0 - n0);
                 const float f1 = m1 == -CUDART_INF_F ? 0.f : exp2_approx(m1 - n1);
@@ -363,11 +362,8 @@ k_attend(const AttnArgs a)
                 const float e2 = exp2_approx(s[i][2] - b1), e3 = exp2_approx(s[i][3] - b1);
                 l0 += e0 + e1;
                 l1 += e2 + e3;
-                // the weights rounded for the product with V: to bf16, the MMA's
-                // type next to bf16 values; to fp16 (11 bits) next to E4M3 ones,
-                // which fp16 holds exactly
-                p[i][0] = ES == 2 ? pack_bf16(e0, e1) : pack_f16(e0, e1);
-                p[i][1] = ES == 2 ? pack_bf16(e2, e3) : pack_f16(e2, e3);
+                p[i][0] = pack_weights<ES>(e0, e1);
+                p[i][1] = pack_weights<ES>(e2, e3);
             }
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk) {

@@ -119,6 +119,30 @@ __device__ __forceinline__ int block_key(const Tile &t, int blk)
 // Units of a tile on the line: its blocks; one for a tile whose rows see nothing.
 __device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max(t.blocks, 1) : 0; }
 
+// The reference point m of a row's weights 2^(x - m): its running maximum,
+// which may lag by 2^8 (weights stay below 256, and rescaling O is rare), less
+// kBase. Weights next to E4M3 values are fp16, which ends at 2^-25: put 2^7
+// higher they are at most 2^15, still in range, and what is lost, while the sum
+// l in fp32 keeps it, is below 2^-32 of the maximum each (without, a flat tail of
+// a million keys could lose 3% of the output).
+template <int ES>
+constexpr float kBase = ES == 1 ? 7.f : 0.f;
+template <int ES>
+constexpr float kLag = 8.f + kBase<ES>;
+
+// Two weights rounded for the product with V: to bf16, the MMA's type next to
+// bf16 values; to fp16 (11 bits) next to E4M3 ones, which fp16 holds exactly.
+// (Scores from 2^24 on, whose steps are whole powers of two, may come out above
+// 2^16: they saturate, so that nothing turns infinite that was not.)
+template <int ES>
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi)
+{
+    if constexpr (ES == 2) return pack_bf16(lo, hi);
+    uint32_t v;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+
 // What a row's sum l of weights makes of it. l is 0 only for a row that has seen
 // nothing (or scores of -inf alone); a NaN among its scores (queries may hold
 // anything) makes l NaN, also where the maximum, which passes over NaN, is

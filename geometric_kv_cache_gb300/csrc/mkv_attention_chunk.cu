@@ -10,7 +10,8 @@
 //     O += P V           tcgen05.mma with P as the A operand from TMEM
 // with the row's maximum m allowed to lag: O is multiplied by 2^(m_old - m_new)
 // only when the maximum has grown by more than 2^8, so weights stay below 256
-// and the rescaling, which has to wait for the tensor core, is rare.
+// (next to E4M3 values 2^15, see kBase) and the rescaling, which has to wait for
+// the tensor core, is rare.
 //
 // Roles (one CTA per SM): warps 0 and 3 bring the pages of K and of V blocks
 // into a ring of shared-memory slots (TMA, 128-byte swizzle, one box of 64 dims
@@ -60,7 +61,6 @@ using namespace dev;
 
 constexpr int kSubRows = 128;                // rows per sub-tile: the MMA's M, the TMEM lanes
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr float kLag = 8.f;                  // log2 of how far a row's maximum may lag
 constexpr int kSlackKeys = 768;              // see cut_line
 constexpr int kMinBlocks = 4;                // least blocks of a CTA's part: fewer make more parts to join, not less time
 
@@ -631,12 +631,13 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 for (int x = 4; x < kKeys; ++x) mx[x & 3] = fmaxf(mx[x & 3], s[x]);
                 const float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 uint32_t pk[16];
-                const bool grow = best > m + kLag;
+                const bool grow = best - m > kLag<ES>;
                 if (blk == 0) {
-                    m = best;
+                    m = best - kBase<ES>;
                 } else if (__any_sync(kFull, grow)) {
-                    const float f = !grow ? 1.f : m == -CUDART_INF_F ? 0.f : exp2_approx(m - best);
-                    if (grow) m = best;
+                    const float to = best - kBase<ES>;
+                    const float f = !grow ? 1.f : m == -CUDART_INF_F ? 0.f : exp2_approx(m - to);
+                    if (grow) m = to;
                     l *= f;
                     // (O is complete up to the block before: its MMAs came before the ones of these scores)
 #pragma unroll
@@ -648,8 +649,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         tmem_st16(o_addr + x, pk);
                     }
                 }
-                // the weights under the maximum m, rounded to the type of the values in the
-                // product: bf16, or fp16 (11 bits)
+                // the weights above the reference point m
                 const float base = m == -CUDART_INF_F ? 0.f : m;
                 const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -661,7 +661,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         v.x = exp2_approx(v.x);
                         v.y = exp2_approx(v.y);
                         sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], v);
-                        pk[e >> 1] = ES == 2 ? pack_bf16(v.x, v.y) : pack_f16(v.x, v.y);
+                        pk[e >> 1] = pack_weights<ES>(v.x, v.y);
                     }
                     tmem_st16(s_addr + (x >> 1), pk);
                 }

@@ -149,3 +149,74 @@ def test_compaction_of_no_indices_and_of_an_empty_cache_is_not_that_of_the_lists
             else:
                 assert mkv.mkv_device_status(ws) == 0
                 assert int(out[1].abs().sum()) == 0 and int(out[2].abs().sum()) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 48])
+def test_weights_far_below_the_largest_add_up_next_to_e4m3_values(d, new):
+    # 12 keys (one for every warp of a CTA) score 26 powers of two above the 2^18 others, whose values are 1 where theirs
+    # are 0: the others together weigh 2^-8, although each alone is below fp16's smallest number relative to the largest.
+    # (152 lists, a CTA each, that share their pages.)
+    n, page, lists, top = 2 ** 18, 128, 152, 12
+    k = torch.zeros((n // page, page, d), dtype=torch.uint8).to(F8)
+    v = torch.ones((n // page, page, d)).to(F8)
+    for i in range(top):
+        k[16 * i // page, 16 * i % page, 0] = 1.0
+        pu.raw(v)[16 * i // page, 16 * i % page] = 0
+    Q = torch.zeros((new * lists, 1, d), dtype=BF)
+    Q[:, 0, 0] = 1.0
+    dev = lambda x: pu.raw(x).to(DEV).view(x.dtype) if x.dtype in pu.CODES else x.to(DEV)  # noqa: E731
+    kd, vd, Qd = dev(k), dev(v), dev(Q)
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV).expand(lists, 1, -1).contiguous()
+    lens = torch.full((lists, 1), n, dtype=torch.int32, device=DEV)
+    start = torch.arange(lists + 1, dtype=torch.int32, device=DEV) * new
+    O, lse = torch.empty_like(Qd), torch.empty((new * lists, 1), device=DEV)
+    ws = mkv.attention_workspace_for(Qd, kd, table, new, n)
+    assert (ws.numel() > 152 * 2 * 100 * (4 * d + 8)) == (new > 1)  # the form for chunks, the one for few rows
+    scale = 26 * math.log(2)
+    mkv.mkv_paged_attention(Qd, kd, vd, table, lens, start, new, n, O, ws, scale=scale, lse=lse)
+    assert mkv.mkv_device_status(ws) == 0
+    small = (n - top - new + 1 + torch.arange(new, dtype=torch.float64)) * 2.0 ** -26  # visible keys but the large ones
+    want = (small / (top + small)).repeat(lists)
+    # scale * log2(e) is an fp32 number: 26 is off by at most 26 x 2^-23, a weight by 2^-18.7 relative, 2^x by 2^-22.
+    # Such a weight times 2^7 lies next to 2^-19, a multiple of fp16's smallest step 2^-24, and rounds to it. At most
+    # 2^18 / 16 additions of equal positive numbers in fp32: 2^-10. The sum of weights may lose all the small ones, each
+    # below half a step of it: small / top. Then bf16's half step.
+    off = 2.0 ** -18 + 2.0 ** -10 + (small / top).repeat(lists)
+    tol = want * (off + 2.0 ** -8 * (1 + 2.0 ** -8))
+    err = (O[:, 0].double().cpu() - want[:, None]).abs()
+    assert (err <= tol[:, None]).all(), (float(O[0, 0, 0]), float(want[0]))
+    exact = scale + torch.log(top + small).repeat(lists)
+    assert ((lse[:, 0].double().cpu() - exact).abs() <= off + 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 48])
+def test_scores_of_many_powers_of_two_stay_finite_next_to_e4m3_values(d, new):
+    # Scores up to 2^28 and beyond, of which fp32 holds no fractions: the weights mean little then, but nothing turns into
+    # NaN, and up to 2^28 O stays inside the range of the values.
+    n, page = 3000, 16
+    k, v = pu.random_pool(d + new, pu.pages_of(n, page), page, d, F8)
+    dev = lambda x: pu.raw(x).to(DEV).view(x.dtype) if x.dtype in pu.CODES else x.to(DEV)  # noqa: E731
+    kd, vd = dev(k), dev(v)
+    table = torch.arange(len(k), dtype=torch.int32, device=DEV).expand(16, 1, -1).contiguous()
+    lens, start = torch.full((16, 1), n, dtype=torch.int32, device=DEV), torch.arange(17, dtype=torch.int32, device=DEV) * new
+    top = v.double().flatten(0, 1)[:n].abs().amax(0)
+    for e in (12, 16, 18, 20):
+        Q = (torch.randn((16 * new, 32, d), generator=torch.Generator().manual_seed(e)) * 2.0 ** e).to(BF)
+        O, lse = torch.empty_like(dev(Q)), torch.empty(Q.shape[:2], device=DEV)
+        ws = mkv.attention_workspace_for(O, kd, table, new, n)
+        assert (ws.numel() > 152 * 2 * 100 * (4 * d + 8)) == (new > 1)
+        mkv.mkv_paged_attention(dev(Q), kd, vd, table, lens, start, new, n, O, ws, scale=1.0, lse=lse)
+        assert mkv.mkv_device_status(ws) == 0
+        assert bool(lse.isfinite().all()) and bool(O.isfinite().all())
+        # Below 2^28 a score in log2 units is below 2^28.53, where an fp32 step is 32, so the reference point is off by at
+        # most 16 and the largest weight, 2^7 to 2^15 above it, lies in [2^-9, 2^31]: it saturates, which only makes O
+        # smaller, or is a normal fp16 number. O is then an average of the values with weights off by 2^-11 relative, or
+        # 2^-25 absolute against a sum of at least 2^-9, and is rounded to bf16.
+        K = kd.double().flatten(0, 1)[:n]
+        most = torch.cat([(x.double() @ K.T).abs().amax(1) for x in dev(Q).flatten(0, 1).split(4096)])
+        inside = (most < 2.0 ** 28).cpu()
+        assert e > 16 or bool(inside.all())
+        slack = 2.0 ** -8 + 2.0 ** -10 + n * 2.0 ** -16
+        assert (O.flatten(0, 1).double().cpu().abs() <= top * (1 + slack))[inside].all()
