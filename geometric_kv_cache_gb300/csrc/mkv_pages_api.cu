@@ -341,6 +341,8 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     if (!isfinite(scale) || !isfinite(k_scale) || !isfinite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f))
         return MKV_ERR_INVALID_ARG;
     if (elem_bytes(pool.dtype) == 2 && (k_scale != 1.f || v_scale != 1.f)) return MKV_ERR_INVALID_ARG;
+    const float scale_log2 = (float)((double)scale * (double)k_scale * M_LOG2E);
+    if (!isfinite(scale_log2)) return MKV_ERR_INVALID_ARG;  // (infinity times a score of 0 would be NaN)
     const int d = pool.head_dim;
     const bool none = tokens.n_tokens == 0 || no_lists(lists) || max_q == 0;
     if (!none) {
@@ -377,7 +379,7 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     a.max_len = max_len;
     a.window = std::min(window, std::max(max_len, 1));  // no list is longer
     a.sinks = sinks;
-    a.scale_log2 = (float)((double)scale * (double)k_scale * M_LOG2E);
+    a.scale_log2 = scale_log2;
     a.v_scale = v_scale;
     a.tiles = plan.tiles;
     a.ctas = plan.ctas;

@@ -665,8 +665,9 @@ size_t mkv_attention_workspace_size(mkv_page_pool pool, mkv_page_lists lists, mk
  * sees the tokens s <= p of the list, with window > 0 only those with
  * s > p - window or s < sinks (positions are places in the list, also after
  * compression). O = sum_s softmax_s(scale * q.k_s) v_s, with keys and values
- * times k_scale and v_scale; lse = log sum_s exp(scale * q.k_s) (natural log;
- * may be NULL), fp32 [n_tokens, q_heads]. A token that sees nothing gives O =
+ * times k_scale and v_scale (positive; scale * k_scale * log2(e) finite in
+ * fp32); lse = log sum_s exp(scale * q.k_s) (natural log; may be NULL), fp32
+ * [n_tokens, q_heads]. A token that sees nothing gives O =
  * 0 and lse = -inf; one whose scores hold a NaN (a NaN or infinite query)
  * gives NaN for both. One new token per row is a decode step; max_q bounds the
  * rows' new tokens and max_len their lists (both host values that size the
