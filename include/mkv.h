@@ -525,9 +525,15 @@ mkv_status mkv_inject_stalled_windows(const void *K, const void *V, mkv_shape sh
  * Order. New pages are the free pages (refs 0 before the call) in ascending
  * order, given to the lists in (row, head, position) order: results do not
  * depend on the GPU. Pages that a call releases can be taken from the next
- * call on. If the free pages do not suffice (MKV_DEV_NO_PAGES), or an argument
- * on the device is invalid, the call changes nothing: the output lists and
- * counts are those of the input.
+ * call on. If the free pages do not suffice (MKV_DEV_NO_PAGES), or a length, a
+ * kept count, a parent or an n_new on the device is invalid, the call changes
+ * nothing: the output lists and counts are those of the input. Table entries
+ * and kept indices are read only where pages are counted and rows copied, when
+ * the call goes through. A page number outside the pool (MKV_DEV_BAD_PAGE) is
+ * then not counted; a list that shares the page carries the entry on; and rows
+ * that would be copied from it, as from an index outside its list
+ * (MKV_DEV_BAD_INDEX), have their place in a new page, whose contents stay what
+ * they were.
  *
  * Input and output lists are distinct buffers (a program keeps two and swaps
  * them), of the same sizes; refs_out may be refs itself. mkv_page_update with

@@ -220,3 +220,79 @@ def test_scores_of_many_powers_of_two_stay_finite_next_to_e4m3_values(d, new):
         assert e > 16 or bool(inside.all())
         slack = 2.0 ** -8 + 2.0 ** -10 + n * 2.0 ** -16
         assert (O.flatten(0, 1).double().cpu().abs() <= top * (1 + slack))[inside].all()
+
+
+def test_update_over_pages_outside_the_pool():
+    # what the header promises: such an entry is carried over and not counted, and a tail that would have been copied from
+    # it has a new page whose contents stay
+    rng = random.Random(61)
+    page, M, P = 16, 5, 40
+    table, lens, refs = pu.random_lists(rng, [[33, 20], [33, 20], [40, 5]], page, P, M)
+    k, v = pu.random_pool(61, P, page, 64, BF)
+    bad = {(1, 0, 0): P, (1, 0, 2): -3, (2, 1, 0): 2 ** 31 - 1}
+    # the same lists with three pages more in the bad ones' place
+    more, n = table.clone(), P
+    for at in bad:
+        more[at] = n
+        n += 1
+    pad = lambda x: torch.cat([x, torch.zeros((3,) + tuple(x.shape[1:]), dtype=x.dtype)])  # noqa: E731
+    refs_more = pad(refs)
+    refs_more[P:] = 9
+    want = pu.page_update(pad(k), pad(v), more, lens, refs_more, [0, 1, 1], [1, 1, 1], page)
+    for at, x in bad.items():
+        table[at] = x
+    g = [x.to(DEV) for x in (k, v, table, lens, refs)]
+    out = [g[2].clone(), torch.zeros_like(g[3]), torch.zeros_like(g[4])]
+    ws = mkv.page_workspace_for(g[0], g[2])
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    mkv.mkv_page_update(*g, *out, ws, parent=i32([0, 1, 1]), n_new=i32([1, 1, 1]))
+    assert mkv.mkv_device_status(ws) == mkv.MKV_DEV_BAD_PAGE
+    carried = want[0].clone()
+    for i, x in enumerate(bad.values()):
+        carried[want[0] == P + i] = x
+    live = torch.arange(M)[None, None] < ((want[1] + page - 1) // page)[..., None]
+    assert torch.equal(out[0].cpu()[live], carried[live])
+    assert torch.equal(out[1].cpu(), want[1]) and torch.equal(out[2].cpu(), want[2][:P])
+    new = int(want[0][2, 0, 2])  # the tail of row 1's first list, which row 2 could not copy
+    assert new < P
+    for pool, old, w in ((g[0], k, want[3]), (g[1], v, want[4])):
+        expect = w[:P].clone()
+        expect[new] = old[new]
+        assert torch.equal(pu.raw(pool).cpu(), pu.raw(expect))
+
+
+def test_compaction_over_pages_outside_the_pool():
+    rng = random.Random(67)
+    page, M, P = 16, 4, 30
+    table, lens, refs = pu.random_lists(rng, [[50, 17], [33, 64]], page, P, M)
+    k, v = pu.random_pool(67, P, page, 64, BF)
+    kept = torch.tensor([[20, 17], [33, 7]], dtype=torch.int32)
+    idx = torch.stack([torch.stack([torch.randperm(max(int(lens[b, j]), 33), generator=torch.Generator().manual_seed(b))[:33]
+                                    for j in range(2)]) for b in range(2)]).to(torch.int32)
+    for b in range(2):
+        for j in range(2):
+            idx[b, j, :kept[b, j]] %= int(lens[b, j])
+    bad = {(0, 0, 1): P, (1, 1, 3): -1}
+    more, n = table.clone(), P
+    for at in bad:
+        more[at] = n
+        n += 1
+    mark = torch.full((2, page, 64), 77.0, dtype=BF)
+    refs_more = torch.cat([refs, torch.full((2,), 9, dtype=torch.int32)])
+    want = pu.page_compact(torch.cat([k, mark]), torch.cat([v, mark]), more, lens, refs_more, idx, kept, page)
+    for at, x in bad.items():
+        table[at] = x
+    g = [x.to(DEV) for x in (k, v, table, lens, refs)]
+    out = [g[2].clone(), torch.zeros_like(g[3]), torch.zeros_like(g[4])]
+    ws = mkv.page_workspace_for(g[0], g[2])
+    mkv.mkv_page_compact(*g, idx.to(DEV), kept.to(DEV), *out, ws)
+    assert mkv.mkv_device_status(ws) == mkv.MKV_DEV_BAD_PAGE
+    live = torch.arange(M)[None, None] < ((kept + page - 1) // page)[..., None]
+    assert torch.equal(out[0].cpu()[live], want[0][live])
+    assert torch.equal(out[1].cpu(), kept) and torch.equal(out[2].cpu(), want[2][:P])
+    skipped = 0
+    for pool, old, w in ((g[0], k, want[3]), (g[1], v, want[4])):
+        expect = torch.where(w[:P] == 77.0, old, w[:P])  # rows that have no source stay
+        skipped += int((w[:P] == 77.0).any(-1).sum())
+        assert torch.equal(pu.raw(pool).cpu(), pu.raw(expect))
+    assert skipped > 0
