@@ -677,15 +677,16 @@ size_t mkv_attention_workspace_size(mkv_page_pool pool, mkv_page_lists lists, mk
  * 0 and lse = -inf; one whose scores hold a NaN (a NaN or infinite query)
  * gives NaN for both. One new token per row is a decode step; max_q bounds the
  * rows' new tokens and max_len their lists (both host values that size the
- * launch; larger ones cost time only; max_len at most max_pages * page_size).
+ * launch; larger ones cost time only; max_len at most max_pages * page_size;
+ * max_q 0 says that no row has any, and nothing is launched).
  * A row with more than max_q tokens sets MKV_DEV_BAD_TOKENS, a list longer
  * than max_len or shorter than 0 MKV_DEV_BAD_SEQ_LEN, and nothing is written
  * for it; a page outside the pool sets MKV_DEV_BAD_PAGE (its tokens count as
  * zeros). Q, O: bf16 [n_tokens, q_heads, head_dim], token t at element
  * t * stride (a multiple of 8, at least q_heads * head_dim), 16-byte aligned,
- * distinct. With tokens to attend, the pool has at least one page; the launch
- * counts blocks of keys in 32 bits: batch * q_heads * max_q * max_len / 1024
- * beyond 2^31 is MKV_ERR_UNSUPPORTED.
+ * distinct. With tokens to attend, the pool has at least one page. Blocks of
+ * keys are counted in 32 bits: batch * heads * ceil(max_q * (q_heads / heads) /
+ * 16) * (max_len / 64 + 2) beyond 2^31 may be MKV_ERR_UNSUPPORTED.
  * Scores, sums and accumulators are fp32; the softmax weights are rounded to
  * 16 bits for the product with the values (bf16; fp16 next to E4M3 values, where
  * a weight below 2^-32 of its row's largest counts as 0). Scores are to stay

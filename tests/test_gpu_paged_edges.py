@@ -24,19 +24,43 @@ def _cuda():
     torch.cuda.empty_cache()
 
 
-def _check_with_nans(p, O, lse):
-    """NaN exactly where the definition has it, the rest within the bounds."""
-    ref, ref_lse, A, W, E = pu.attention(p.Q, p.k, p.v, p.table, p.lens, p.start, p.page, p.d ** -0.5, *p.scales)
+def _definition(p):
+    """pu.attention without windows, list by list in matrices: O, lse and their bounds."""
+    n, hq, d = p.Q.shape
+    O, A, W = (torch.zeros((n, hq, d), dtype=torch.float64) for _ in range(3))
+    lse, E = torch.full((n, hq), -math.inf, dtype=torch.float64), torch.zeros((n, hq), dtype=torch.float64)
+    for b in range(p.lens.shape[0]):
+        t0, t1 = int(p.start[b]), int(p.start[b + 1])
+        for j in range(p.lens.shape[1]):
+            L, h = int(p.lens[b, j]), slice(j * p.G, (j + 1) * p.G)
+            K, V = (pu.rows_of(x, p.table[b, j], L, p.page) * s for x, s in zip((p.k, p.v), p.scales))
+            hidden = torch.arange(L)[None] > (L - (t1 - t0) + torch.arange(t1 - t0))[:, None]  # [tokens, keys]
+            some = ~hidden.all(1)
+            if not some.any():
+                continue
+            hidden, q = hidden[some][:, None], p.Q[t0:t1, h].double()[some]
+            x = (q @ K.T * d ** -0.5).masked_fill(hidden, -math.inf)
+            w = torch.exp(x - x.amax(-1, keepdim=True)).masked_fill(hidden, 0.0)
+            l = w.sum(-1, keepdim=True)
+            at = torch.arange(t0, t1)[some]
+            O[at, h], A[at, h], W[at, h] = w @ V / l, w @ V.abs() / l, (~hidden).double() @ V.abs() / l
+            lse[at, h] = x.amax(-1) + torch.log(l[..., 0])
+            E[at, h] = (q.abs() @ K.abs().T * d ** -0.5).masked_fill(hidden, 0.0).amax(-1)
+    return O, lse, *pu.attention_bounds(O, lse, A, W, E, d, p.dtype)
+
+
+def _check(p, O, lse, nans=False):
+    """NaN exactly where the definition has it, the rest within the bounds, tokens of no row as they were."""
+    ref, ref_lse, tol, tol_lse = _definition(p)
     n = int(p.start[-1])
-    assert bool(ref_lse[:n].isnan().any()) and not bool(ref_lse[:n].isnan().all())
-    assert torch.equal(lse[:n].isnan(), ref_lse[:n].isnan())
-    assert torch.equal(O[:n].isnan(), ref[:n].isnan())
-    tol, tol_lse = pu.attention_bounds(ref, ref_lse, A, W, E, p.d, p.dtype)
-    fine = ~ref_lse[:n].isnan()
-    assert ((O[:n].double() - ref[:n]).abs() <= tol[:n])[fine].all()
-    assert torch.equal(torch.isinf(lse[:n]), torch.isinf(ref_lse[:n]))
-    some = fine & torch.isfinite(ref_lse[:n])
-    assert ((lse[:n].double() - ref_lse[:n]).abs() <= tol_lse[:n])[some].all()
+    assert torch.equal(O[n:], torch.full_like(O[n:], 7.0)) and torch.equal(lse[n:], torch.full_like(lse[n:], 7.0))
+    O, lse, ref, ref_lse, tol, tol_lse = (x[:n] for x in (O, lse, ref, ref_lse, tol, tol_lse))
+    assert bool(ref_lse.isnan().any()) == nans and not bool(ref_lse.isnan().all())
+    assert torch.equal(lse.isnan(), ref_lse.isnan()) and torch.equal(O.isnan(), ref.isnan())
+    assert torch.equal(torch.isinf(lse), torch.isinf(ref_lse))
+    fine = ~ref_lse.isnan()
+    assert ((O.double() - ref).abs() <= tol)[fine].all()
+    assert ((lse.double() - ref_lse).abs() <= tol_lse)[torch.isfinite(ref_lse)].all()
 
 
 def _spoil(p, tokens):
@@ -58,7 +82,7 @@ def test_queries_that_are_not_finite(d, dtype, counts):
     _spoil(p, [0, counts[0]])
     O, lse = p.run()
     assert p.status == 0
-    _check_with_nans(p, O, lse)
+    _check(p, O, lse, nans=True)
 
 
 @pytest.mark.parametrize("d,dtype", [(64, BF), (64, F8), (128, BF), (128, F8), (256, BF), (256, F8)])
@@ -68,7 +92,35 @@ def test_chunk_form_queries_that_are_not_finite(d, dtype, extra):
     _spoil(p, [0, 40, 70, 119])
     O, lse = p.run()
     assert p.status == 0
-    _check_with_nans(p, O, lse)
+    _check(p, O, lse, nans=True)
+
+
+def _with_zero_page(p, bad):
+    """The same problem with a page of zeros more, which the table entries `bad` name."""
+    zero = torch.zeros((1,) + tuple(p.k.shape[1:]), dtype=torch.uint8).to(p.dtype)
+    k, v = (torch.cat([pu.raw(x), pu.raw(zero)]).view(p.dtype) for x in (p.k, p.v))
+    table = p.table.clone()
+    for at in bad:
+        table[at] = p.k.shape[0]
+    return k, v, table
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("form", ["few", "chunk"])
+def test_tokens_of_pages_outside_the_pool_count_as_zeros(form, dtype):
+    if form == "few":
+        p = Problem(23, [1, 3], [[600, 200], [90, 9]], 4, 128, 16, dtype)
+        bad = [(0, 0, 2), (0, 0, 3), (0, 1, 0), (1, 0, 5)]
+    else:
+        p = wide(23, [70, 9, 30], [300], 8, 128, 16, dtype)
+        bad = [(0, 0, 2), (0, 0, 3), (0, 5, 0), (2, 7, 20)]
+    k, v, table = _with_zero_page(p, bad)
+    for i, at in enumerate(bad):
+        p.table[at] = [p.k.shape[0], -1, 2 ** 31 - 1, -2 ** 31][i]
+    O, lse = p.run()
+    assert p.status == mkv.MKV_DEV_BAD_PAGE
+    p.k, p.v, p.table = k, v, table
+    _check(p, O, lse)
 
 
 @pytest.mark.parametrize("rows,start", [(3, [0, 5, 3, 9]), (3, [-2, 1, 3, 9]), (3, [0, 3, 6, 1000]), (3, [9, 6, 3, 0]),
@@ -296,3 +348,97 @@ def test_compaction_over_pages_outside_the_pool():
         skipped += int((w[:P] == 77.0).any(-1).sum())
         assert torch.equal(pu.raw(pool).cpu(), pu.raw(expect))
     assert skipped > 0
+
+
+@pytest.mark.parametrize("d,dtype", [(64, BF), (64, F8), (256, BF), (256, F8)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 5)])
+def test_chunk_form_pages_of_128_tokens(d, dtype, window, sinks):
+    # at 256 dims a page spans two blocks of keys
+    p = wide(24, [40, 20, 33, 1], [0, 64, 129, 700], 4, d, 128, dtype)
+    O, lse = p.run(window, sinks)
+    assert p.status == 0
+    p.check(O, lse, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF, F8])
+@pytest.mark.parametrize("rows", [19, 38])
+def test_ragged_lists_as_many_as_the_sms(rows, dtype):
+    # 152 and 304 lists whose lengths differ fourfold: cuts at tiles' ends would make parts of uneven length
+    rng = random.Random(rows)
+    p = Problem(25, [1] * rows, [[rng.randint(300, 1300) for _ in range(8)] for _ in range(rows)], 2, 64, 16, dtype)
+    a, b = p.run(), p.run()
+    assert p.status == 0
+    _check(p, *a)
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, BF), (128, F8), (256, BF)])
+@pytest.mark.parametrize("counts,heads", [([608], 8), ([40, 300, 1, 77, 210], 9)])
+def test_fresh_prompts(counts, heads, d, dtype):
+    # lists of the new tokens alone: the tiles of a list see ever more keys
+    p = wide(26, counts, [0], 8, d, 16, dtype, heads=heads)
+    a, b = p.run(), p.run()
+    assert p.status == 0
+    _check(p, *a)
+    assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+def test_two_streams_with_a_workspace_each():
+    ps = [Problem(27, [1, 1, 1], [[5000, 50], [70, 3000], [60, 900]], 4, 128, 16, BF),
+          wide(28, [66, 20, 33, 1], [2500, 900], 4, 128, 16, BF),
+          Problem(29, [3, 1], [[9000, 50], [70, 7000]], 4, 128, 16, F8)]
+    dev = lambda x: pu.raw(x).to(DEV).view(x.dtype) if x.dtype in pu.CODES else x.to(DEV)  # noqa: E731
+    runs = []
+    for p in ps:
+        Q, k, v, table, lens, start = (dev(x) for x in (p.Q, p.k, p.v, p.table, p.lens, p.start))
+        runs.append((p, (Q, k, v, table, lens, start, p.max_q, p.max_len), torch.empty_like(Q),
+                     torch.empty(Q.shape[:2], device=DEV), mkv.attention_workspace_for(Q, k, table, p.max_q, p.max_len),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for p, args, O, lse, ws, stream in runs:
+            mkv.mkv_paged_attention(*args, O, ws, k_scale=p.scales[0], v_scale=p.scales[1], lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    for p, args, O, lse, ws, stream in runs:
+        alone = p.run()
+        assert mkv.mkv_device_status(ws) == 0
+        assert torch.equal(O.cpu().view(torch.int16), alone[0].view(torch.int16)) and torch.equal(lse.cpu(), alone[1])
+        _check(p, *alone)
+
+
+@pytest.mark.parametrize("dtype,new", [(BF, 1), (F8, 1), (BF, 48), (F8, 48)])
+def test_lists_beyond_64k_tokens(dtype, new):
+    # (the reference in fp64 on the GPU: the lists are long, the rows few)
+    n, d, page, G = 140001, 64, 64, 2
+    rng = random.Random(new)
+    pages = pu.pages_of(n, page)
+    g = torch.Generator().manual_seed(new)
+    ids = torch.randperm(pages, generator=g).to(torch.int32)
+    k, v = pu.random_pool(new, pages, page, d, dtype)
+    pu.raw(k)[int(ids[-1]), n % page:] = pu.raw(v)[int(ids[-1]), n % page:] = -1 if dtype == BF else 255
+    Q = torch.randn((new, G, d), generator=g).to(BF)
+    dev = lambda x: pu.raw(x).to(DEV).view(x.dtype) if x.dtype in pu.CODES else x.to(DEV)  # noqa: E731
+    kd, vd, Qd, table = dev(k), dev(v), dev(Q), ids.view(1, 1, -1).to(DEV)
+    lens, start = torch.tensor([[n]], dtype=torch.int32, device=DEV), torch.tensor([0, new], dtype=torch.int32, device=DEV)
+    O, lse = torch.empty_like(Qd), torch.empty((new, G), device=DEV)
+    ws = mkv.attention_workspace_for(Qd, kd, table, new, n)
+    mkv.mkv_paged_attention(Qd, kd, vd, table, lens, start, new, n, O, ws, lse=lse)
+    assert mkv.mkv_device_status(ws) == 0
+    K, V = (x[table[0, 0].long()].view(-1, d)[:n].view(dtype).double() for x in (pu.raw(kd), pu.raw(vd)))
+    at, E = torch.arange(n, device=DEV), torch.zeros((new, G), dtype=torch.float64)
+    ref, A, W = (torch.zeros((new, G, d), dtype=torch.float64) for _ in range(3))
+    ref_lse = torch.zeros((new, G), dtype=torch.float64)
+    for t in range(new):
+        q = Qd[t].double()
+        x = (q @ K.T * d ** -0.5).masked_fill(at > n - new + t, -math.inf)
+        w = torch.exp(x - x.amax(1, keepdim=True))
+        l = w.sum(1, keepdim=True)
+        seen = (at <= n - new + t).double()
+        ref[t], A[t], W[t] = (w @ V / l).cpu(), (w @ V.abs() / l).cpu(), ((seen @ V.abs())[None] / l).cpu()
+        ref_lse[t] = torch.logsumexp(x, 1).cpu()
+        E[t] = ((q.abs() @ K.abs().T) * d ** -0.5).amax(1).cpu()
+    tol, tol_lse = pu.attention_bounds(ref, ref_lse, A, W, E, d, dtype)
+    # beyond 2^13 keys the sum's fp32 error grows past the bound's 2^-18: (keys / 8) 2^-24 for both sums
+    tol = tol + 2 * (n / 8) * 2.0 ** -24 * A
+    assert ((O.cpu().double() - ref).abs() <= tol).all()
+    assert ((lse.cpu().double() - ref_lse).abs() <= tol_lse + (n / 8) * 2.0 ** -24).all()
