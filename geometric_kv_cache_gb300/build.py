@@ -21,7 +21,7 @@ SOURCES = ["mkv_kernels.cu", "mkv_gather.cu", "mkv_inplace.cu", "mkv_summaries.c
            "mkv_pages_api.cu"]
 HEADERS = [os.path.join(CSRC, "mkv_internal.h"), os.path.join(CSRC, "mkv_device.cuh"),
            os.path.join(CSRC, "mkv_select.cuh"), os.path.join(CSRC, "mkv_gather.cuh"),
-           os.path.join(CSRC, "mkv_pages.h"), os.path.join(CSRC, "mkv_attention.cuh"),
+           os.path.join(CSRC, "mkv_pages.h"), os.path.join(CSRC, "mkv_line.h"), os.path.join(CSRC, "mkv_attention.cuh"),
            os.path.join(os.path.dirname(PKG_DIR), "include", "mkv.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -44,7 +44,7 @@ using namespace dev;
 
 constexpr int kRows = 16;  // rows per tile (the MMA's M)
 constexpr double kAgainBytes = 80e6;  // see takes_chunks
-constexpr int kSlack = 3;      // see cut_line
+constexpr LineRule kLine = {1, 3, 3};  // see mkv_line.h
 
 // Shape of one instantiation.
 template <int D, int ES>
@@ -133,10 +133,11 @@ k_attend(const AttnArgs a)
     __shared__ __align__(16) uint8_t s_q[Q_REGS ? 16 : kRows * QS];
     __shared__ float s_up[kRows];
     __shared__ LineScratch s_line;
+    __shared__ int s_shift[kLineShifts];
     __shared__ int4 s_join[2];  // tiles to join: tile, first and last CTA with a part
     __shared__ float2 s_ml[A::WARPS][kRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
-    Walk w = cut_line<A::KEYS, A::THREADS>(a, kRows, 1, kSlack, s_line);
+    Walk w = cut_line<A::KEYS, A::THREADS>(a, kRows, kLine, s_line, s_shift);
     int at_unit = w.begin;  // of the line
     if (threadIdx.x < 2) s_join[threadIdx.x].x = -1;
     while (w.next<A::KEYS>(a, kRows)) {

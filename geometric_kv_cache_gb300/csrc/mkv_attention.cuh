@@ -5,8 +5,8 @@
 // The rows (new token, query head of the KV head's group) of a list are packed
 // token by token into tiles; a tile walks the blocks of KEYS keys that any of
 // its rows sees. The blocks of all tiles of all lists form one line, cut into
-// equal parts, one per CTA: no CTA idles behind a long list or an uneven
-// number of tiles. A tile that is cut leaves its parts (O before the division,
+// one part per CTA (mkv_line.h: equal parts, or nearly equal ones of whole tiles):
+// no CTA idles behind a long list or an uneven number of tiles. A tile that is cut leaves its parts (O before the division,
 // m, l) in the workspace, at most two per CTA, and they are joined in order.
 #pragma once
 
@@ -17,6 +17,7 @@
 #include <stdint.h>
 
 #include "mkv_device.cuh"
+#include "mkv_line.h"
 #include "mkv_pages.h"
 
 namespace mkv {
@@ -187,28 +188,24 @@ struct Walk {
     __device__ __forceinline__ int to() const { return min(last, t.blocks); }
 };
 
-// This CTA's part of the line; every thread of the CTA must call it. (The
-// host has checked that the line's length fits 32 bits.) There are fewer parts
-// than CTAs where a part would have less than min_units units and there are
-// not that many tiles either. Where whole tiles, of which some CTAs get one
-// more than others, cost a CTA less than `slack` units more than equal parts
-// do, a cut moves to the nearer end of its tile (not in tiles that are much
-// longer than a part): the parts of cut tiles have to be written, read and
-// joined. Measured (us, equal parts / whole tiles, 128 dims, bf16): 128 tiles of
-// 8 blocks, 16 rows 21 / 15.5, 256 rows 49 / 30; 512 tiles of 8, 16 rows 61 / 66.5
-// (5 blocks more), 256 rows 113 / 102; 32 tiles of 16, 256 rows 30 / 44 (12 more).
+// This CTA's part of the line; every thread of the CTA must call it. (The host
+// has checked that the line's length fits 32 bits.) mkv_line.h has the rule.
 struct LineScratch {
     int sum[32], rest[32], live[32];
-    int units, parts;  // the line's length, the CTAs that it is cut over
-    int last;          // where this CTA's part ends
+    LineCut cut;
+    int off;   // where the tile begins that holds the first unit of this CTA's equal part
     Walk walk;
 };
+constexpr int kLineShifts = kPlanSms + 1;
+// shift: kLineShifts integers of shared memory, by how much each part's begin
+// would move; free again after the caller's next barrier.
 template <int KEYS, int THREADS>
-__device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int min_units, int slack, LineScratch &s)
+__device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, LineRule rule, LineScratch &s, int *shift)
 {
     constexpr int WARPS = THREADS / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_tiles = a.batch * a.heads * a.tiles;
+    for (int x = threadIdx.x; x < kLineShifts; x += THREADS) shift[x] = 0;
     // the first THREADS tiles, one per thread, and the sum of the others
     Tile t;
     int mine = 0, rest = 0, live = 0;
@@ -249,70 +246,68 @@ __device__ __forceinline__ Walk cut_line(const AttnArgs &a, int tile_rows, int m
     int seen = units;  // in the tiles looked at so far
     if (n_tiles > THREADS)
         for (int i = 0; i < WARPS; ++i) units += s.rest[i];
-    const int parts = max(1, min((int)gridDim.x, max(units / min_units, tiles)));
-    // ceil(tiles / parts) average tiles less units / parts, against the slack (less where fewer parts would be joined)
-    const int idle = (tiles + parts - 1) / parts * parts - tiles;  // places for a tile that stay empty
-    const bool move = (long long)idle * units * (int)gridDim.x < (long long)slack * tiles * parts * parts;
-    const int whole = move ? units / parts + slack : 0;  // tiles of up to so many units are not cut
-    // part c begins at c units / parts, rounded down (in 32 bits where they do)
-    auto begin = [&](int c) -> int {
-        c = min(c, parts);
-        if (units < (1 << 23)) return (int)((uint32_t)units * (uint32_t)c / (uint32_t)parts);  // (at most 512 CTAs)
-        return (int)((long long)units * c / parts);
-    };
-    const int u0 = begin((int)blockIdx.x), u1 = begin((int)blockIdx.x + 1);
-    if (threadIdx.x == 0) {
-        s.units = units;
-        s.parts = parts;
-    }
-    // The threads whose tiles hold the part's first unit and the next part's: its ends.
-    auto claim = [&](int x, int off) {
+    const LineCut cut = LineCut::make(units, tiles, (int)gridDim.x, rule);
+    const int me = (int)blockIdx.x, u0 = cut.begin(me), u1 = cut.begin(me + 1);
+    const bool move = cut.hopeful();
+    if (threadIdx.x == 0) s.cut = cut;
+    // The thread whose tile holds the part's first unit, and those whose tiles hold cuts that may move.
+    auto look = [&](int x, int off) {
         if (mine == 0) return;
-        auto edge = [&](int u) -> int { return mine > whole ? u : 2 * (u - off) < mine ? off : off + mine; };
         if (off <= u0 && u0 < off + mine) {
-            const int at = edge(u0);
-            s.walk.begin = at;
-            s.walk.have = at < off + mine;
-            s.walk.tile = at < off + mine ? x : x + 1;
-            s.walk.skip = at < off + mine ? at - off : 0;
+            s.off = off;
+            s.walk.tile = x;
             s.walk.t = t;
         }
-        if (off <= u1 && u1 < off + mine) s.last = edge(u1);
+        if (move && cut.movable(mine))
+            for (int c = cut.part_from(off); c < cut.parts; ++c) {
+                const int u = cut.begin(c);
+                if (u >= off + mine) break;
+                shift[c] = LineCut::moved(u, off, mine) - u;
+            }
     };
-    if (u1 > u0) {
-        claim(threadIdx.x, before + upto - mine);
-        for (int x0 = THREADS; x0 < n_tiles && seen <= (u1 < units ? u1 : u0); x0 += THREADS) {
-            const int x = x0 + threadIdx.x;
-            mine = 0;
-            if (x < n_tiles) {
-                t = make_tile<KEYS>(a, x, tile_rows, false);
-                mine = units_of(t);
-            }
-            upto = scan(mine);
-            __syncthreads();
-            if (lane == 31) s.sum[warp] = upto;
-            __syncthreads();
-            before = seen;
-            for (int i = 0; i < WARPS; ++i) {
-                before += i < warp ? s.sum[i] : 0;
-                seen += s.sum[i];
-            }
-            claim(x, before + upto - mine);
+    look(threadIdx.x, before + upto - mine);
+    for (int x0 = THREADS; x0 < n_tiles && (move ? seen < units : seen <= u0); x0 += THREADS) {
+        const int x = x0 + threadIdx.x;
+        mine = 0;
+        if (x < n_tiles) {
+            t = make_tile<KEYS>(a, x, tile_rows, false);
+            mine = units_of(t);
         }
+        upto = scan(mine);
+        __syncthreads();
+        if (lane == 31) s.sum[warp] = upto;
+        __syncthreads();
+        before = seen;
+        for (int i = 0; i < WARPS; ++i) {
+            before += i < warp ? s.sum[i] : 0;
+            seen += s.sum[i];
+        }
+        look(x, before + upto - mine);
     }
     __syncthreads();
-    Walk w = s.walk;
-    w.left = u1 > u0 ? (u1 < units ? s.last : units) - w.begin : 0;
+    int begin = u0, end = u1;
+    if (move) {
+        int longest = 0;
+        for (int c = lane; c < cut.parts; c += 32)
+            longest = max(longest, cut.begin(c + 1) + shift[c + 1] - cut.begin(c) - shift[c]);
+        if (cut.fits(__reduce_max_sync(kFull, longest))) {
+            begin += shift[me];
+            end += shift[me + 1];
+        }
+    }
+    Walk w = s.walk;  // (of no use where the part is empty)
+    w.have = begin < s.off + units_of(w.t);
+    w.tile += w.have ? 0 : 1;
+    w.skip = w.have ? begin - s.off : 0;
+    w.begin = begin;
+    w.left = end - begin;
     return w;
 }
 
-// The CTA whose part holds the first or last unit of a cut tile: the c with
-// c units / parts (rounded down) <= unit < (c + 1) units / parts. (A cut that
-// further than its tile's ends.)
-__device__ __forceinline__ int cta_of(int unit, const LineScratch &s)
-{
-    return (int)((((long long)unit + 1) * s.parts - 1) / s.units);
-}
+// The CTA whose part holds the first or last unit of a cut tile: the one whose
+// equal part does. (A cut that moves goes no further than the ends of its tile,
+// which is not cut then.)
+__device__ __forceinline__ int cta_of(int unit, const LineScratch &s) { return s.cut.part_of(unit); }
 
 // What the joining kernel needs of each CTA.
 struct LineInfo {

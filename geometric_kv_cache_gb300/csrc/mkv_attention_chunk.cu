@@ -61,7 +61,7 @@ using namespace dev;
 
 constexpr int kSubRows = 128;                // rows per sub-tile: the MMA's M, the TMEM lanes
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int kSlackKeys = 768;              // see cut_line
+constexpr int kSlackKeys = 768, kUnevenKeys = 4096;  // see mkv_line.h
 constexpr int kMinBlocks = 4;                // least blocks of a CTA's part: fewer make more parts to join, not less time
 
 template <int D, int ES>
@@ -277,10 +277,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 // tokens of 32 query heads over 32768 bf16 tokens 712 us, inlined 755; a call with nearly
 // nothing to do takes 0.7 us more).
 template <int KEYS, int THREADS>
-__device__ __noinline__ void cut_for_warps(const AttnArgs &a, int tile_rows, int min_units, int slack, LineScratch &s,
+__device__ __noinline__ void cut_for_warps(const AttnArgs &a, int tile_rows, LineRule rule, LineScratch &s, int *shift,
                                            Walk *walks)
 {
-    const Walk start = cut_line<KEYS, THREADS>(a, tile_rows, min_units, slack, s);
+    const Walk start = cut_line<KEYS, THREADS>(a, tile_rows, rule, s, shift);
     if ((threadIdx.x & 31) == 0) walks[threadIdx.x >> 5] = start;
 }
 
@@ -332,7 +332,9 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    cut_for_warps<kKeys, C::THREADS>(a, C::ROWS, kMinBlocks, kSlackKeys / kKeys, s_line, s_walk);
+    // (the queries' place lends its memory: nothing is there before the barrier below)
+    cut_for_warps<kKeys, C::THREADS>(a, C::ROWS, {kMinBlocks, kSlackKeys / kKeys, kUnevenKeys / kKeys}, s_line,
+                                     reinterpret_cast<int *>(q_smem), s_walk);
     // A warp's walk lies in shared memory: registers are for the loops.
     const Walk &w = s_walk[warp];
     auto next_segment = [&]() -> bool {

@@ -10,6 +10,9 @@
 
 namespace mkv {
 
+// The launches are planned for the 152 SMs of a GB300, so that workspace sizes
+// need no device and results do not depend on one.
+constexpr int kPlanSms = 152;
 constexpr int kPlanPages = 4096;  // pages of refs per CTA of the plan kernels (256 threads x 16)
 constexpr int kPlanRows = 8;      // batch rows per CTA of the plan kernels (one warp each)
 

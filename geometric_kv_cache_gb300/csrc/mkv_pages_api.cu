@@ -14,9 +14,6 @@ namespace mkv {
 namespace {
 
 constexpr size_t kAlign = 256;
-// The launches are planned for the 152 SMs of a GB300, so that workspace sizes
-// need no device and results do not depend on one.
-constexpr int kPlanSms = 152;
 // Where the workspace's head holds the counts of cut tiles' parts.
 constexpr size_t kCounts = 64;
 static_assert(kCounts + kPlanSms <= kAlign && kPlanSms < 256, "a byte per CTA");
