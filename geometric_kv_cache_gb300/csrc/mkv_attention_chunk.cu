@@ -272,7 +272,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-// (Not inlined: its registers would change how the kernel's loops are compiled.)
 // Not inlined: the kernel's loops are then compiled with fewer spills (2048
 // tokens of 32 query heads over 32768 bf16 tokens 712 us, inlined 755; a call with nearly
 // nothing to do takes 0.7 us more).

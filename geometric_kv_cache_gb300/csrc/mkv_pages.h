@@ -61,9 +61,10 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t st);
 
-// Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiplication: with l =
-// ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d is the high word of
-// m n, plus n, shifted right by l.
+// Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiplication (Granlund and
+// Montgomery, "Division by Invariant Integers using Multiplication", PLDI 1994,
+// figure 4.1): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d is
+// the high word of m n, plus n, shifted right by l.
 struct FastDiv {
     uint32_t d = 1, m = 1, l = 0;
     FastDiv() = default;
