@@ -20,11 +20,12 @@
 // cut over 152 CTAs (mkv_attention.cuh); of the CTAs with a part of a cut tile
 // the one that comes last joins the parts, always in the same order.
 //
-// Measured: 32 rows of 4K-16K bf16 tokens (8 KV heads of 128 dims, group 4) 197 us,
-// 6.8 TB/s, the measured copy peak; two rows of 60K-65K E4M3 tokens (10 KV heads)
-// 64 us, 5.0 TB/s (55 us without any arithmetic: start, first and last copies);
-// one row of 2K tokens 9 us, latency. The first form, with a fixed number of parts
-// per list, took 213, 101 and 7 us.
+// Measured: 32 rows of 4K-16K bf16 tokens (8 KV heads of 128 dims, group 4) 200 us,
+// 6.4 TB/s, 0.95 of the measured copy rate, 19 such rows 130 us; two rows of 60K-65K
+// E4M3 tokens (10 KV heads) 64 us, 5.0 TB/s (55 us without any arithmetic: start,
+// first and last copies); one row of 2K tokens 9 us, latency. The first form, with a
+// fixed number of parts per list, took 213 us for the 32 rows, 101 for the two and 7
+// for the one, which pays for the cut of the line and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -15,7 +15,7 @@
 // are few, a share of one token's heads) with no shared memory and no
 // barrier: a lane always has the same 16 dims of a head, so the 8 pairs of
 // sine and cosine that it needs stay in its registers for all heads. 16384
-// tokens of 32 + 2 x 8 heads of 128 dims take 71 us, 5.7 TB/s, 0.84 of the
+// tokens of 32 + 2 x 8 heads of 128 dims take 71 us, 5.7 TB/s, 0.83 of the
 // measured copy peak; the form with a CTA per group of tokens and the angles in
 // shared memory took 82 us, one without loads ahead of the angles 93.
 #include <cuda_bf16.h>

@@ -689,8 +689,10 @@ size_t mkv_attention_workspace_size(mkv_page_pool pool, mkv_page_lists lists, mk
  * 16) * (max_len / 64 + 2) beyond 2^31 may be MKV_ERR_UNSUPPORTED.
  * Scores, sums and accumulators are fp32; the softmax weights are rounded to
  * 16 bits for the product with the values (bf16; fp16 next to E4M3 values, where
- * a weight below 2^-32 of its row's largest counts as 0). Scores are to stay
- * below 2^28 in magnitude: fp32 steps are of 16 and more there. */
+ * a weight below 2^-32 of its row's largest counts as 0). Next to E4M3 keys a
+ * query row is fp16 times a power of two: elements below 2^-14 of its largest are
+ * off by at most 2^-25 of that. Scores are to stay below 2^28 in magnitude: fp32
+ * steps are of 16 and more there. */
 mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens tokens, int32_t max_q,
                                mkv_page_pool pool, mkv_page_lists lists, int32_t max_len, float scale, float k_scale,
                                float v_scale, int32_t window, int32_t sinks, void *O, int64_t o_stride, float *lse,
