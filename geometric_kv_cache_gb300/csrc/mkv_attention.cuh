@@ -5,9 +5,10 @@
 // The rows (new token, query head of the KV head's group) of a list are packed
 // token by token into tiles; a tile walks the blocks of KEYS keys that any of
 // its rows sees. The blocks of all tiles of all lists form one line, cut into
-// one part per CTA (mkv_line.h: equal parts, or nearly equal ones of whole tiles):
-// no CTA idles behind a long list or an uneven number of tiles. A tile that is cut leaves its parts (O before the division,
-// m, l) in the workspace, at most two per CTA, and they are joined in order.
+// one part per CTA (mkv_line.h: equal parts, or nearly equal ones of whole
+// tiles): no CTA idles behind a long list or an uneven number of tiles. A tile
+// that is cut leaves its parts (O before the division, m, l) in the workspace,
+// at most two per CTA, and they are joined in order.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -122,8 +123,8 @@ __device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max
 
 // The reference point m of a row's weights 2^(x - m): its running maximum,
 // which may lag by 2^8 (weights stay below 256, and rescaling O is rare), less
-// kBase. Weights next to E4M3 values are fp16, which ends at 2^-25: put 2^7
-// higher they are at most 2^15, still in range, and what is lost, while the sum
+// kBase. Weights next to E4M3 values are fp16, which rounds what is below 2^-25
+// to 0: put 2^7 higher they are at most 2^15, still in range, and what is lost, while the sum
 // l in fp32 keeps it, is below 2^-32 of the maximum each (without, a flat tail of
 // a million keys could lose 3% of the output).
 template <int ES>
