@@ -124,9 +124,9 @@ __device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max
 // The reference point m of a row's weights 2^(x - m): its running maximum,
 // which may lag by 2^8 (weights stay below 256, and rescaling O is rare), less
 // kBase. Weights next to E4M3 values are fp16, which rounds what is below 2^-25
-// to 0: put 2^7 higher they are at most 2^15, still in range, and what is lost, while the sum
-// l in fp32 keeps it, is below 2^-32 of the maximum each (without, a flat tail of
-// a million keys could lose 3% of the output).
+// to 0: put 2^7 higher they are at most 2^15, still in range, and what is lost,
+// while the sum l in fp32 keeps it, is below 2^-32 of the maximum each (without,
+// a flat tail of a million keys could lose 3% of the output).
 template <int ES>
 constexpr float kBase = ES == 1 ? 7.f : 0.f;
 template <int ES>
