@@ -9,7 +9,7 @@ negatives) and an E4M3 scale per 16 dims; an element is code * scale times the p
     s = e4m3(max|x| * (1 / (6 scale))),  codes e2m1(x * ((1 / scale) / s)),  all codes 0 where s is 0,
 
 each step one fp32 operation (1 / (6 scale) and 1 / scale are rounded once), rounded to nearest, ties to the even code,
-saturating at 448 and 6. Keys are the exact rotated values, rounded once to fp32, before that. So the bytes of a page
+saturating at 448 and 6, zero without a sign. Keys are the exact rotated values, rounded once to fp32, before that. So the bytes of a page
 are settled by the rule, and are compared as they are.
 
 Pools, page lists and their counts are otherwise those of the 8- and 16-bit caches: table int32 [batch, heads,
@@ -150,7 +150,7 @@ def _encode(x, scale):
     # passed borders between neighbouring values, those of odd codes' lower ends included: ties go to the even code
     c = sum((a > b).to(torch.uint8) if i % 2 == 0 else (a >= b).to(torch.uint8)
             for i, b in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)))
-    c = (c | ((t < 0).to(torch.uint8) << 3)).flatten(-2)
+    c = (c | (((t < 0) & (c > 0)).to(torch.uint8) << 3)).flatten(-2)  # zero has one code
     return c[..., 0::2] | (c[..., 1::2] << 4), s8.view(torch.uint8)
 
 
