@@ -38,6 +38,7 @@ MKV_DEV_NO_PAGES = 0x20
 MKV_DEV_BAD_PARENT = 0x40
 MKV_DEV_BAD_TOKENS = 0x80
 MKV_DEV_BAD_INDEX = 0x100
+MKV_DEV_BAD_AXIS = 0x200
 
 MKV_MODE_L2 = 0
 MKV_MODE_COSINE = 1
@@ -62,7 +63,7 @@ EXPORTED = (
     "mkv_compress_inplace", "mkv_set_head_groups", "mkv_set_fused", "mkv_centroid_score",
     "mkv_inject_stalled_fused", "mkv_set_head_group_ring", "mkv_head_group_plan", "mkv_set_oja_pair",
     "mkv_page_workspace_size", "mkv_page_update", "mkv_page_compact", "mkv_rope_append", "mkv_rope_frequencies",
-    "mkv_attention_workspace_size", "mkv_paged_attention",
+    "mkv_attention_workspace_size", "mkv_paged_attention", "mkv_page_quantize", "mkv_rope_append_axes", "mkv_rope_axes",
 )
 
 
@@ -87,6 +88,8 @@ class MkvNewTokens(ctypes.Structure):
 
 # mkv_dtype of each supported cache element type
 DTYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+# ... and of 4-bit pages, which torch holds as bytes: head_dim * 9 / 16 of them per token
+E2M1 = 4
 
 
 class MKVError(RuntimeError):
@@ -161,6 +164,11 @@ def load(build_if_missing: bool = True):
                                        vp, sz, vp]),
             "mkv_rope_append": (i32, [vp, i64, vp, i64, vp, i64, MkvNewTokens, vp, vp, i32, i32, f32, vp, MkvPagePool,
                                       MkvPageLists, f32, f32, vp, sz, vp]),
+            "mkv_page_quantize": (i32, [MkvPagePool, MkvPageLists, vp, vp, i32, vp, vp, vp, i32, vp, f32, f32, MkvPageLists,
+                                        vp, vp, sz, vp]),
+            "mkv_rope_append_axes": (i32, [vp, i64, vp, i64, vp, i64, MkvNewTokens, vp, i32, vp, vp, i32, i32, f32, vp,
+                                           MkvPagePool, MkvPageLists, f32, f32, vp, sz, vp]),
+            "mkv_rope_axes": (i32, [i32, i32, vp, i32, vp]),
             "mkv_rope_frequencies": (i32, [i32, f64, i32, f64, i32, f64, f64, vp]),
             "mkv_attention_workspace_size": (sz, [MkvPagePool, MkvPageLists, MkvNewTokens, i32, i32]),
             "mkv_paged_attention": (i32, [vp, i64, MkvNewTokens, i32, MkvPagePool, MkvPageLists, i32, f32, f32, f32,
@@ -540,16 +548,26 @@ def _workspace(ws):
 
 
 def pool_of(k_pages: torch.Tensor, v_pages: torch.Tensor) -> MkvPagePool:
-    """mkv_page_pool of two [n_pages, page_size, head_dim] bf16 or float8_e4m3fn tensors."""
+    """mkv_page_pool of two [n_pages, page_size, head_dim] bf16 or float8_e4m3fn tensors, or of two uint8 tensors
+    [n_pages, page_size, head_dim * 9 / 16]: 4-bit pages (codes of all tokens, then their scales: see mkv.h)."""
     dtype, shape = DTYPES.get(k_pages.dtype), k_pages.shape
-    if len(shape) != 3 or dtype is None:
-        raise ValueError("k_pages must be a bf16 or float8_e4m3fn tensor [n_pages, page_size, head_dim]")
+    four = k_pages.dtype is torch.uint8
+    if len(shape) != 3 or (dtype is None and not (four and shape[2] % 9 == 0)):
+        raise ValueError("k_pages must be a bf16 or float8_e4m3fn tensor [n_pages, page_size, head_dim], or uint8 "
+                         "[n_pages, page_size, head_dim * 9 / 16]")
     if v_pages.shape != shape or v_pages.dtype is not k_pages.dtype:
         raise ValueError("k_pages and v_pages must have one shape and dtype")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous()):
         raise ValueError("k_pages and v_pages must be contiguous")
     n, p, d = shape
+    if four:
+        d, dtype = d * 16 // 9, E2M1
     return MkvPagePool(n, p, d, dtype, k_pages.data_ptr(), v_pages.data_ptr())
+
+
+def e2m1_pages(n_pages: int, page_size: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """Zeroed 4-bit pages: uint8 [n_pages, page_size, head_dim * 9 / 16]."""
+    return torch.zeros((n_pages, page_size, head_dim * 9 // 16), dtype=torch.uint8, device=device)
 
 
 def lists_of(table: torch.Tensor, lens: Optional[torch.Tensor] = None) -> MkvPageLists:
@@ -576,7 +594,8 @@ def _token_rows(t, heads, d, n_tokens, what):
 
 
 def page_workspace_for(k_pages: torch.Tensor, table: torch.Tensor) -> torch.Tensor:
-    """A zeroed workspace for mkv_page_update, mkv_page_compact and mkv_rope_append."""
+    """A zeroed workspace for mkv_page_update, mkv_page_compact, mkv_page_quantize, mkv_rope_append and
+    mkv_rope_append_axes."""
     n = int(load().mkv_page_workspace_size(pool_of(k_pages, k_pages), lists_of(table)))
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=k_pages.device)
 
@@ -599,11 +618,10 @@ def mkv_page_update(k_pages, v_pages, table, lens, refs, table_out, lens_out, re
            "mkv_page_update")
 
 
-def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K=None,
-                     V=None, seq_lens=None, stream=None):
-    """Compaction in pages: list h keeps its tokens idx[h][:kept[h]] in new pages, its old pages lose a holder. idx
-    int32 [batch, heads, n] (None: the first kept tokens, not the same as n = 0), kept int32 [batch, heads], as mkv_compress writes them.
-    With K and V [batch, heads, t_max, head_dim] (and seq_lens) the tokens come from that contiguous cache instead."""
+def _compaction(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K, V, seq_lens,
+                dtype):
+    """What mkv_page_compact and mkv_page_quantize check: the device, the pool, both lists, and t_max of K and V (of
+    `dtype`)."""
     dev = _on_device((k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K, V,
                       seq_lens))
     pool, src, dst = pool_of(k_pages, v_pages), lists_of(table, lens), lists_of(table_out, lens_out)
@@ -617,14 +635,28 @@ def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, 
     if (K is None) != (V is None) or (K is None and seq_lens is not None):
         raise ValueError("K and V come together (and seq_lens only with them)")
     if K is not None:
-        if K.dtype is not k_pages.dtype or V.dtype is not k_pages.dtype:
-            raise ValueError("K, V and the pages must share one dtype: bf16 or float8_e4m3fn")
+        if K.dtype is not dtype or V.dtype is not dtype:
+            raise ValueError("K and V must be bf16" if dtype is not k_pages.dtype else
+                             "K, V and the pages must share one dtype: bf16 or float8_e4m3fn")
         t_max = K.shape[2] if K.dim() == 4 else 0
         if K.shape != (src.batch, src.heads, t_max, pool.head_dim) or V.shape != K.shape:
             raise ValueError("K and V must be [batch, heads, t_max, head_dim] of the lists' sizes")
         if not (K.is_contiguous() and V.is_contiguous()):
             raise ValueError("tensors passed to the CUDA library must be contiguous")
         _int32(seq_lens, (src.batch,), "seq_lens")
+    return dev, pool, src, dst, t_max
+
+
+def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out, refs_out, workspace, K=None,
+                     V=None, seq_lens=None, stream=None):
+    """Compaction in pages: list h keeps its tokens idx[h][:kept[h]] in new pages, its old pages lose a holder. idx
+    int32 [batch, heads, n] (None: the first kept tokens, not the same as n = 0), kept int32 [batch, heads], as mkv_compress writes them.
+    With K and V [batch, heads, t_max, head_dim] (and seq_lens) the tokens come from that contiguous cache instead (of the
+    pages' type; into 4-bit pages mkv_page_quantize writes)."""
+    if K is not None and k_pages.dtype is torch.uint8:
+        raise ValueError("a contiguous cache becomes 4-bit pages by mkv_page_quantize")
+    dev, pool, src, dst, t_max = _compaction(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out,
+                                             refs_out, workspace, K, V, seq_lens, k_pages.dtype)
     # (a tensor without elements has no address, and to the library NULL means that there is none at all)
     some = workspace.data_ptr()
     _check((_lib or load()).mkv_page_compact(pool, src, refs.data_ptr(), None if idx is None else idx.data_ptr() or some,
@@ -633,6 +665,22 @@ def mkv_page_compact(k_pages, v_pages, table, lens, refs, idx, kept, table_out, 
                                              None if V is None else V.data_ptr() or some, t_max, _at(seq_lens), dst,
                                              refs_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                              _raw_stream(stream, dev)), "mkv_page_compact")
+
+
+def mkv_page_quantize(k_pages, v_pages, table, lens, refs, idx, kept, K, V, table_out, lens_out, refs_out, workspace,
+                      k_scale: float = 1.0, v_scale: float = 1.0, seq_lens=None, stream=None):
+    """mkv_page_compact from a contiguous bf16 cache K, V [batch, heads, t_max, head_dim] into pages of 8 or 4 bits: the
+    kept rows divided by k_scale and v_scale and rounded as mkv_rope_append rounds them."""
+    if K is None or V is None:
+        raise ValueError("K and V are the cache that becomes pages")
+    dev, pool, src, dst, t_max = _compaction(k_pages, v_pages, table, lens, refs, idx, kept, table_out, lens_out,
+                                             refs_out, workspace, K, V, seq_lens, torch.bfloat16)
+    some = workspace.data_ptr()
+    _check((_lib or load()).mkv_page_quantize(pool, src, refs.data_ptr(), None if idx is None else idx.data_ptr() or some,
+                                              0 if idx is None else idx.shape[-1], kept.data_ptr(), K.data_ptr() or some,
+                                              V.data_ptr() or some, t_max, _at(seq_lens), k_scale, v_scale, dst,
+                                              refs_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                              _raw_stream(stream, dev)), "mkv_page_quantize")
 
 
 def mkv_rope_frequencies(rot_dim: int, theta: float, scaling="plain", scale: float = 1.0, original_len: int = 0,
@@ -648,12 +696,22 @@ def mkv_rope_frequencies(rot_dim: int, theta: float, scaling="plain", scale: flo
     return out
 
 
-def mkv_rope_append(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace,
-                    layout="half", factor: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
-    """Rotary positions of a step's new tokens: Q [n_tokens, q_heads, d] turned into Q_out, K [n_tokens, heads, d]
-    turned into the pages, V into the pages (all bf16; tokens may lie apart, as in a fused projection). Row b's tokens
-    are [q_start[b], q_start[b + 1]) and the last ones of its lists. inv_freq fp32 [rot_dim / 2] on the device."""
-    dev = _on_device((Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace))
+def mkv_rope_axes(sections, dealt: bool = False) -> torch.Tensor:
+    """The axis that turns each pair (host helper): int32 [sum(sections)] on the CPU, axis a having sections[a] pairs, in
+    runs or (dealt) given out to the axes in turn, past those that have all of theirs."""
+    sections = [int(n) for n in sections]
+    if not 0 < sum(sections) <= 1 << 20:  # (no head has as many pairs)
+        raise MKVError(MKV_ERR_INVALID_ARG, "mkv_rope_axes")
+    out = torch.empty(sum(sections), dtype=torch.int32)
+    st = load().mkv_rope_axes(2 * sum(sections), len(sections), (ctypes.c_int32 * len(sections))(*sections),
+                              1 if dealt else 0, _ptr(out))
+    if st != 0:
+        raise MKVError(MKV_ERR_INVALID_ARG, "mkv_rope_axes")
+    return out
+
+
+def _rope_args(Q, K, V, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace):
+    """What both rotary calls check: the pool, the lists, tokens, heads and the strides of Q, K and V."""
     pool, lists = pool_of(k_pages, v_pages), lists_of(table, lens)
     if Q.dim() != 3:
         raise ValueError("Q must be a bf16 tensor [n_tokens, q_heads, head_dim]")
@@ -663,15 +721,42 @@ def mkv_rope_append(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens,
     _token_rows(Q_out, hq, d, n, "Q_out")
     if not Q_out.is_contiguous():
         raise ValueError("Q_out must be contiguous")
-    _int32(positions, (n,), "positions")
     _int32(q_start, (lists.batch + 1,), "q_start")
     if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous fp32 tensor [rot_dim / 2]")
     _workspace(workspace)
+    return pool, lists, n, hq, qs, ks, vs
+
+
+def mkv_rope_append(Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace,
+                    layout="half", factor: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """Rotary positions of a step's new tokens: Q [n_tokens, q_heads, d] turned into Q_out, K [n_tokens, heads, d]
+    turned into the pages, V into the pages (all bf16; tokens may lie apart, as in a fused projection). Row b's tokens
+    are [q_start[b], q_start[b + 1]) and the last ones of its lists. inv_freq fp32 [rot_dim / 2] on the device."""
+    dev = _on_device((Q, K, V, positions, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace))
+    pool, lists, n, hq, qs, ks, vs = _rope_args(Q, K, V, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace)
+    _int32(positions, (n,), "positions")
     _check((_lib or load()).mkv_rope_append(
         Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, MkvNewTokens(n, hq, q_start.data_ptr()), positions.data_ptr(),
         inv_freq.data_ptr(), 2 * inv_freq.shape[0], _ROPE_LAYOUTS[layout], factor, Q_out.data_ptr(), pool, lists, k_scale,
         v_scale, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)), "mkv_rope_append")
+
+
+def mkv_rope_append_axes(Q, K, V, positions, axes, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace,
+                         layout="half", factor: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """mkv_rope_append with positions on several axes (time, row, column, ... of image and video patches): positions
+    int32 [n_axes, n_tokens]; pair i turns by positions[axes[i]], axes int32 [rot_dim / 2] (mkv_rope_axes)."""
+    dev = _on_device((Q, K, V, positions, axes, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace))
+    pool, lists, n, hq, qs, ks, vs = _rope_args(Q, K, V, inv_freq, k_pages, v_pages, table, lens, q_start, Q_out, workspace)
+    if positions.dim() != 2:
+        raise ValueError("positions must be a contiguous int32 tensor [n_axes, n_tokens]")
+    _int32(positions, (positions.shape[0], n), "positions")
+    _int32(axes, (inv_freq.shape[0],), "axes")
+    _check((_lib or load()).mkv_rope_append_axes(
+        Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, MkvNewTokens(n, hq, q_start.data_ptr()), positions.data_ptr(),
+        positions.shape[0], axes.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], _ROPE_LAYOUTS[layout], factor,
+        Q_out.data_ptr(), pool, lists, k_scale, v_scale, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev)),
+        "mkv_rope_append_axes")
 
 
 def attention_workspace_for(Q, k_pages, table, max_q: int, max_len: int) -> torch.Tensor:

@@ -507,7 +507,8 @@ bool takes_chunks(int64_t batch, int64_t heads, int32_t group, int64_t n_tokens,
 {
     const int64_t per_list = (max_q * group + kRows - 1) / kRows - 1, in_all = n_tokens * group / kRows;
     const int64_t again = heads * std::min(batch * per_list, in_all);
-    return (double)again * (double)(max_len + 1024) * (head_dim * es + 128) > kAgainBytes;
+    const double row_bytes = es ? head_dim * es : head_dim * 9 / 16;
+    return (double)again * (double)(max_len + 1024) * (row_bytes + 128) > kAgainBytes;
 }
 
 AttnPlan attention_plan(int32_t batch, int32_t heads, int32_t group, int32_t n_tokens, int32_t max_q, int32_t max_len,
@@ -516,7 +517,8 @@ AttnPlan attention_plan(int32_t batch, int32_t heads, int32_t group, int32_t n_t
     AttnPlan p;
     const int64_t rows = (int64_t)max_q * group;
     p.chunked = takes_chunks(batch, heads, group, n_tokens, max_q, max_len, head_dim, es);
-    const int tile = p.chunked ? chunk_tile_rows(head_dim) : kRows;
+    const int tile = p.chunked ? chunk_tile_rows(head_dim) : es == 0 ? e2m1_tile_rows(rows) : kRows;
+    p.tile_rows = tile;
     p.tiles = (int32_t)((rows + tile - 1) / tile);
     p.ctas = ctas;
     p.part_rows = (int64_t)ctas * 2 * tile;
@@ -527,6 +529,7 @@ AttnPlan attention_plan(int32_t batch, int32_t heads, int32_t group, int32_t n_t
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t st)
 {
     if (a.chunked) return launch_attend_chunk(a, st);
+    if (a.es == 0) return launch_attend_e2m1(a, st);
     if (a.es == 2) {
         switch (a.head_dim) {
         case 64: return launch_one<64, 2>(a, st);

@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// Next to E4M3 keys the queries run as fp16, which takes one conversion per two
+// Next to E4M3 (and 4-bit) keys the queries run as fp16, which takes one conversion per two
 // codes where bf16 would take five instructions: a row of queries is scaled by
 // the power of two that brings its largest magnitude into [1, 2). Elements
 // from 2^-14 of that on keep all their bits; smaller ones are off by at most
@@ -123,12 +123,12 @@ __device__ __forceinline__ int units_of(const Tile &t) { return t.rows > 0 ? max
 
 // The reference point m of a row's weights 2^(x - m): its running maximum,
 // which may lag by 2^8 (weights stay below 256, and rescaling O is rare), less
-// kBase. Weights next to E4M3 values are fp16, which rounds what is below 2^-25
+// kBase. Weights next to E4M3 and 4-bit values (ES 1 and 0) are fp16, which rounds what is below 2^-25
 // to 0: put 2^7 higher they are at most 2^15, still in range, and what is lost,
 // while the sum l in fp32 keeps it, is below 2^-32 of the maximum each (without,
 // a flat tail of a million keys could lose 3% of the output).
 template <int ES>
-constexpr float kBase = ES == 1 ? 7.f : 0.f;
+constexpr float kBase = ES == 2 ? 0.f : 7.f;
 template <int ES>
 constexpr float kLag = 8.f + kBase<ES>;
 

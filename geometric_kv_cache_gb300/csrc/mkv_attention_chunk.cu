@@ -52,6 +52,7 @@
 
 #include "mkv_attention.cuh"
 #include "mkv_device.cuh"
+#include "mkv_e2m1.cuh"
 #include "mkv_pages.h"
 
 namespace mkv {
@@ -74,19 +75,20 @@ struct Chunk {
     static constexpr int BOXES = D / 64;
     static constexpr int BOX = KEYS * 128;          // 64 dims of a block: rows of 128 bytes
     static constexpr int SLOT = BOXES * BOX;        // one block of K or of V as the MMA reads it
-    static constexpr int RAW = KEYS * D;            // ... as E4M3 codes
-    static constexpr int RAWS = ES == 2 ? 0 : D == 64 ? 3 : 2;
+    static constexpr int CODES_BYTES = ES == 0 ? KEYS * D / 2 : KEYS * D;   // ... as E4M3 or 4-bit codes
+    static constexpr int RAW = CODES_BYTES + (ES == 0 ? KEYS * D / 16 : 0);  // (and their scales)
+    static constexpr int RAWS = ES == 2 ? 0 : ES == 0 || D == 64 ? 3 : 2;
     static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 5) : (D == 64 ? 9 : 4);
     // The next tile's queries go to the MMAs before this one's output is written
     // (384 lists of 64 keys, 256 rows: E4M3 at 128 dims 43.5 us, else 44.7; bf16 at 256
     // dims 63 / 66; 160 lists of 2048, 1024 rows, E4M3 at 64 dims 148 / 153). Of bf16 at 64
     // and 128 dims it takes registers from the loop: 8192 rows over 32768 keys 725 / 712.
-    static constexpr bool EARLY = ES == 1 || D == 256;
+    static constexpr bool EARLY = ES != 2 || D == 256;
     static constexpr int QBOX = kSubRows * 128;
     static constexpr int QBYTES = BOXES * QBOX;     // one sub-tile of queries
     static constexpr int SMEM = NSUB * QBYTES + SLOTS * SLOT + RAWS * RAW + 1024;
     static constexpr int SOFT = NSUB * 4;                     // softmax warps, from warp 4 on
-    static constexpr int CODES = ES == 2 ? 0 : 4;             // warps that expand E4M3 codes, after them
+    static constexpr int CODES = ES == 2 ? 0 : 4;             // warps that expand codes, after them
     static constexpr int THREADS = (4 + SOFT + CODES) * 32;   // 256, 384 or 512
     // Registers per thread of warps 0-3, the softmax warps and the expanding
     // ones: at most what the launch has (256 x 224, 384 x 168 or 512 x 128).
@@ -153,6 +155,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// `bytes` consecutive ones (a multiple of 16, as are both addresses).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t *src, uint32_t bytes, uint64_t *b)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(saddr(b))
+                 : "memory");
+}
+
 // Shared-memory matrix descriptors, 128-byte swizzle (layout type 2, version
 // 1), 8-row groups 1024 bytes apart. Keys and queries are K-major (the
 // contraction runs along the 128-byte rows; leading offset unused). Values
@@ -198,6 +208,18 @@ __device__ __forceinline__ void mma_commit(uint64_t *b)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(b))
                  : "memory");
+}
+__device__ __forceinline__ uint2 lds8(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
 }
 // One lane of the converged warp. (Issued under this the MMAs go out back to
 // back; under a test of the lane number they took 90 cycles each, more than
@@ -294,7 +316,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *q_smem = smem;                      // NSUB x [D / 64 boxes][128 rows x 128 B]
     uint8_t *ring = smem + NSUB * C::QBYTES;     // SLOTS blocks: K, V, K, V, ...
-    uint8_t *raws = ring + SLOTS * C::SLOT;      // RAWS blocks of E4M3 codes, in the same order
+    uint8_t *raws = ring + SLOTS * C::SLOT;      // RAWS blocks of codes, in the same order
     __shared__ __align__(8) uint64_t full[SLOTS], empty[SLOTS], raw_full[RAWS + 1], raw_empty[RAWS + 1], s_full[2],
         p_ready[2], o_done[2], o_free[2], q_full[2], drain[2];
     __shared__ uint32_t tmem_base;
@@ -383,13 +405,33 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                 int row = lookup(from);
                 for (int blk = from; ok && blk < to; ++blk, seq += 2) {
                     const int next = lookup(blk + 1), s = (int)(seq % N);
-                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, row >= 0)) * D * ES) << box_shift;
+                    bool copied = row >= 0;
+                    // (4-bit pages are copied as they lie, with no tensor map that would fill in for a bad one)
+                    if constexpr (ES == 0) copied = copied && row < a.n_pages << a.page_shift;
+                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, copied)) * (ES ? D * ES : D * 9 / 16)) << box_shift;
                     ok = seq < N || warp_wait(&taken[s], ((seq / N) - 1) & 1u, a.status, &abort_flag);
                     if (!ok) break;
+                    if constexpr (ES == 0) {
+                        if (row >= 0 && !copied) {  // a bad page's elements are zeros: all its scales
+                            const uint32_t dst = saddr(raws + s * C::RAW + C::CODES_BYTES) + ((uint32_t)lane * (D / 16) << box_shift);
+                            for (int o = 0; o < D / 16 << box_shift; o += 16) sts16(dst + o, make_uint4(0u, 0u, 0u, 0u));
+                            fence_async();
+                        }
+                        __syncwarp();
+                    }
                     if (lane == 0) bar_expect(&landed[s], bytes);
                     __syncwarp();
-                    if (row >= 0) {
-                        if constexpr (ES == 2) {
+                    if (copied) {
+                        if constexpr (ES == 0) {
+                            const int in_page = row & (a.page_size - 1);
+                            const uint8_t *page = (kv ? a.v : a.k) + (int64_t)(row >> a.page_shift) * (D * 9 / 16 << a.page_shift);
+                            const uint32_t dst = saddr(raws + s * C::RAW);
+                            bulk_load(dst + ((uint32_t)lane * (D / 2) << box_shift), page + in_page * (D / 2),
+                                      (uint32_t)(D / 2) << box_shift, &landed[s]);
+                            bulk_load(dst + C::CODES_BYTES + ((uint32_t)lane * (D / 16) << box_shift),
+                                      page + (D / 2 << a.page_shift) + in_page * (D / 16), (uint32_t)(D / 16) << box_shift,
+                                      &landed[s]);
+                        } else if constexpr (ES == 2) {
                             const uint32_t dst = saddr(ring + s * C::SLOT) + ((uint32_t)lane * 128u << box_shift);
 #pragma unroll
                             for (int x = 0; x < C::BOXES; ++x)
@@ -492,9 +534,9 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
             }
         }
     } else if (warp >= 4 + C::SOFT) {
-        // -------------------------------------------- E4M3 codes to fp16 (exact) --
+        // ------------------------------------------------- codes to fp16 (exact) --
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CODES));
-        if constexpr (ES == 1) {
+        if constexpr (ES != 2) {
             const int quarter = warp - 4 - C::SOFT;
             uint32_t seq = 0;
             bool ok = true;
@@ -508,10 +550,25 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                              (seq < SLOTS || warp_wait(&empty[s], ((seq / SLOTS) - 1) & 1u, a.status, &abort_flag));
                         if (!ok) break;
                         const uint32_t from = saddr(raws + q * C::RAW), to = saddr(ring + s * C::SLOT);
-                        constexpr int CPR = D / 16;  // 16-byte chunks of codes per row
+                        constexpr int CPR = D / 16;  // groups of 16 codes per row
 #pragma unroll 4
                         for (int o = quarter * 32 + lane; o < kKeys * CPR; o += 128) {
                             const int key = o / CPR, c = o % CPR;
+                            if constexpr (ES == 0) {
+                                const uint32_t row = to + (c >> 2) * kBoxBytes + key * 128, x = (uint32_t)(c & 3) * 2;
+                                uint2 v = lds8(from + o * 8);
+                                uint32_t sc = lds1(from + C::CODES_BYTES + o);
+                                if (key >= live) sc = 0u;
+                                sc = e4m3x2_to_f16x2(sc | sc << 8);
+                                uint32_t h[8];
+                                e2m1x8_to_f16(v.x, *reinterpret_cast<uint32_t(*)[4]>(h));
+                                e2m1x8_to_f16(v.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) h[e] = mul_f16x2(h[e], sc);
+                                sts16(row + ((x ^ (key & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+                                sts16(row + (((x + 1) ^ (key & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+                                continue;
+                            }
                             uint4 v = lds16(from + o * 16);
                             if (key >= live) v = make_uint4(0u, 0u, 0u, 0u);
                             const uint32_t row = to + (c >> 2) * kBoxBytes + key * 128, x = (uint32_t)(c & 3) * 2;
@@ -560,7 +617,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                     a.Q + 2 * (((int64_t)a.q_start[w.t.b] + i) * a.q_stride + (int64_t)head * D));
                 const uint32_t dst = saddr(q_smem + t * C::QBYTES) + row * 128;
                 float down = 1.f;
-                if constexpr (ES == 1) {  // fp16 next to E4M3 keys, the row scaled by a power of two
+                if constexpr (ES != 2) {  // fp16 next to codes, the row scaled by a power of two
                     float largest = 0.f;
                     if (real)
 #pragma unroll 8
@@ -577,7 +634,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 #pragma unroll 8
                 for (int x = 0; x < D / 8; ++x) {
                     uint4 v = real ? src[x] : make_uint4(0u, 0u, 0u, 0u);
-                    if constexpr (ES == 1) {
+                    if constexpr (ES != 2) {
                         float f[8];
                         bf16x8_to_f32(v, f);
                         v = make_uint4(pack_f16(f[0] * down, f[1] * down), pack_f16(f[2] * down, f[3] * down),
@@ -599,7 +656,7 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         while (C::EARLY ? have : begin()) {
             const bool real = t * kSubRows + row < w.t.rows;
             const int first = w.from(), nb = w.to() - first;
-            const float c = ES == 1 ? c_row : c_all;
+            const float c = ES != 2 ? c_row : c_all;
             // the row's own key (of rows that are not there: the first row's)
             const int p = w.t.L - w.t.n + a.by_group(w.t.row0 + t * kSubRows + (real ? row : 0));
             const int sink_blocks = w.t.sink_blocks, past_sinks = w.t.win_block - w.t.sink_blocks;
@@ -784,8 +841,8 @@ template <int D, int ES>
 cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 {
     using C = Chunk<D, ES>;
-    CUtensorMap mk, mv;
-    if (!make_map(&mk, a.k, a, C::KEYS) || !make_map(&mv, a.v, a, C::KEYS)) return cudaErrorUnknown;
+    CUtensorMap mk = {}, mv = {};  // (4-bit pages are copied without)
+    if (ES != 0 && (!make_map(&mk, a.k, a, C::KEYS) || !make_map(&mv, a.v, a, C::KEYS))) return cudaErrorUnknown;
     cudaError_t e = cudaFuncSetAttribute(k_attend_chunk<D, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     LineInfo *info = reinterpret_cast<LineInfo *>(a.part_ml + (int64_t)a.ctas * 2 * C::ROWS);
@@ -812,11 +869,11 @@ int chunk_tile_rows(int head_dim) { return head_dim == 256 ? kSubRows : 2 * kSub
 
 cudaError_t launch_attend_chunk(const AttnArgs &a, cudaStream_t st)
 {
-    const bool bf16 = a.es == 2;
+    const int es = a.es;
     switch (a.head_dim) {
-    case 64: return bf16 ? launch_one<64, 2>(a, st) : launch_one<64, 1>(a, st);
-    case 128: return bf16 ? launch_one<128, 2>(a, st) : launch_one<128, 1>(a, st);
-    case 256: return bf16 ? launch_one<256, 2>(a, st) : launch_one<256, 1>(a, st);
+    case 64: return es == 2 ? launch_one<64, 2>(a, st) : es == 1 ? launch_one<64, 1>(a, st) : launch_one<64, 0>(a, st);
+    case 128: return es == 2 ? launch_one<128, 2>(a, st) : es == 1 ? launch_one<128, 1>(a, st) : launch_one<128, 0>(a, st);
+    case 256: return es == 2 ? launch_one<256, 2>(a, st) : es == 1 ? launch_one<256, 1>(a, st) : launch_one<256, 0>(a, st);
     }
     return cudaErrorInvalidValue;
 }

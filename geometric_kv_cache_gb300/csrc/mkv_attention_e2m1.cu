@@ -1,0 +1,501 @@
+// sm_103a attention of a step's few new tokens over 4-bit pages (the form of
+// mkv_paged_attention for lists with few query rows; see mkv_attention.cu for
+// the definition, mkv_attention_chunk.cu for the form for many).
+//
+// A cached element is code * scale, exact in fp16, so the arithmetic is that of
+// E4M3 caches: queries as fp16 scaled by a power of two per row, fp16 weights,
+// fp32 sums. What is new is the work per byte: 1 KB of HBM holds 1820 elements,
+// each to be expanded (a conversion for two codes, a product with the scale for
+// two) before a tensor core can take it. So the cached side is the MMA's A
+// operand, 16 keys or 16 dims per instruction, and the rows are its 8 columns:
+//     S^T = K Q^T   (16 keys x 8 rows),   O^T += V^T P^T   (16 dims x 8 rows):
+// a tile of 8 rows takes half the instructions that 16 rows would, and a tile of
+// 16 expands every element once for both halves. Keys of a lane's fragment are
+// the bytes that it loads: dims may be contracted in any order, so a lane's dims
+// are those of one 16-byte load and the queries follow; likewise a lane's dims
+// of V are consecutive ones, all under one scale per key.
+//
+// The split of work is that of the other form: tiles of packed rows, the line of
+// key blocks cut over 152 CTAs, a ring of cp.async stages per warp, the parts of
+// cut tiles joined by the CTA that comes last (mkv_attention.cuh).
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "mkv_attention.cuh"
+#include "mkv_device.cuh"
+#include "mkv_e2m1.cuh"
+#include "mkv_pages.h"
+
+namespace mkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kKeys = 16;  // keys of a warp's step: they lie in one page
+constexpr LineRule kLine = {1, 3, 3};  // see mkv_line.h
+
+// Shape of one instantiation: head dims, rows of a tile.
+template <int D, int R>
+struct Attend4 {
+    static constexpr int WARPS = D == 256 ? (R == 8 ? 12 : 8) : D == 128 && R == 16 ? 12 : 16;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int KEYS = WARPS * kKeys;     // keys per block of the CTA
+    static constexpr int CB = D / 2, SB = D / 16;  // bytes of a row's codes and scales
+    static constexpr int CODES = kKeys * CB, SCALES = kKeys * SB;
+    static constexpr int HALF = CODES + SCALES, STAGE = 2 * HALF;
+    static constexpr int STAGES = 220 * 1024 / (WARPS * STAGE) < 6 ? 220 * 1024 / (WARPS * STAGE) : 6;
+    static constexpr int RING = STAGES * STAGE;    // per warp
+    static constexpr int OS = D + 4;               // floats between a result's rows
+    static constexpr int MERGE = WARPS * R * OS * 4;
+    static constexpr int SMEM = WARPS * RING > MERGE ? WARPS * RING : MERGE;
+    static constexpr int NR = R / 8;               // column tiles of rows
+    static constexpr int KW = D / 32;              // 32-bit words of codes per lane and key, K
+    static constexpr int VW = D / 64 ? D / 64 : 1; // ... V: 8 dims to a word
+};
+
+// 16 bytes to shared memory, of which the first n come from src, the others are zeros.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, int n)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("{ .reg .u16 h; ld.shared.u16 h, [%1]; cvt.u32.u16 %0, h; }" : "=r"(v) : "r"(addr));
+    return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w)
+{
+    if constexpr (N == 1) {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    } else {
+        const uint4 v = lds16(addr);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+}
+
+// Where 16-byte chunk c of row r of a step's codes lies. K: a quarter-warp reads
+// two rows of 64 bytes, or half of two rows of 128, one of which has its halves
+// exchanged. V: the lanes that load together have the rows 0, 2, 4, 6 (or the
+// odd ones) and the same quarter of each, which have to be 8 distinct chunks
+// modulo 128 bytes.
+template <int D>
+__device__ __forceinline__ uint32_t k_at(int r, int c)
+{
+    return (uint32_t)(r * (D / 32) + (D == 256 ? c ^ (r & 1) << 2 : c)) * 16u;
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_at(int r, int c)
+{
+    if constexpr (D == 64) return (uint32_t)((r ^ (r >> 2 & 1)) * 2 + c) * 16u;
+    if constexpr (D == 128) return (uint32_t)((r * 4 ^ (r >> 1 & 1) << 2) + (c ^ (r >> 2 & 1) << 1)) * 16u;
+    return (uint32_t)(r * 8 + (c ^ (r >> 1 & 3) << 1)) * 16u;
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(Attend4<D, R>::THREADS, 1)
+k_attend_e2m1(const __grid_constant__ AttnArgs a)
+{
+    using A = Attend4<D, R>;
+    constexpr int NR = A::NR, KW = A::KW, VW = A::VW;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LineScratch s_line;
+    __shared__ int s_shift[kLineShifts];
+    __shared__ int4 s_join[2];  // tiles to join: tile, first and last CTA with a part
+    __shared__ float2 s_ml[A::WARPS][R];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
+    Walk w = cut_line<A::KEYS, A::THREADS>(a, R, kLine, s_line, s_shift);
+    int at_unit = w.begin;  // of the line
+    if (threadIdx.x < 2) s_join[threadIdx.x].x = -1;
+    // this lane's dims of a key: word x holds 8 of them
+    auto k_dim = [&](int x) -> int {
+        return D == 64 ? 16 * tq + 8 * x : D == 128 ? 32 * tq + 8 * x : 128 * (x / 4) + 32 * tq + 8 * (x % 4);
+    };
+    const int page_mask = a.page_size - 1;
+    const int64_t page_bytes = (int64_t)(A::CB + A::SB) << a.page_shift;
+    while (w.next<A::KEYS>(a, R)) {
+        const Tile &t = w.t;
+        const int first = w.from(), last = w.to();
+        const int32_t *table = a.table + ((int64_t)t.b * a.heads + t.j) * a.max_pages;
+        const int qrow0 = a.q_start[t.b];
+
+        // queries: column gr of each column tile, this lane's dims, as fp16 with a power of two taken out
+        uint32_t q[NR][2 * KW][2];
+        float sc[NR][2];  // of this lane's columns of scores, 2 tq and 2 tq + 1
+        int p[NR][2];     // their places in the list
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const int Rq = t.row0 + min(8 * n + gr, t.rows - 1), i = a.by_group(Rq), g = Rq - i * a.group;
+            const uint8_t *src = a.Q + 2 * ((int64_t)(qrow0 + i) * a.q_stride + (int64_t)(t.j * a.group + g) * D);
+            float m = 0.f;
+            uint4 v[KW];
+#pragma unroll
+            for (int x = 0; x < KW; ++x) {
+                v[x] = *reinterpret_cast<const uint4 *>(src + 2 * k_dim(x));
+                float f[8];
+                bf16x8_to_f32(v[x], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+            }
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+            const int E = row_exponent(m);
+            const float down = down_by(E);
+#pragma unroll
+            for (int x = 0; x < KW; ++x) {
+                float f[8];
+                bf16x8_to_f32(v[x], f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q[n][2 * x + (e >> 1)][e & 1] = pack_f16(f[2 * e] * down, f[2 * e + 1] * down);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                sc[n][c] = a.scale_log2 * up_by(__shfl_sync(kFull, E, (2 * tq + c) * 4));
+                p[n][c] = t.L - t.n + a.by_group(t.row0 + min(8 * n + 2 * tq + c, t.rows - 1));
+            }
+        }
+        // places of the tile's first and last row
+        const int p_lo = t.L - t.n + a.by_group(t.row0), p_hi = t.L - t.n + a.by_group(t.row0 + t.rows - 1);
+
+        const uint32_t ring = saddr(smem) + warp * A::RING;
+        auto key0 = [&](int blk) -> int { return block_key<A::KEYS>(t, blk) + warp * kKeys; };
+        // the page entry of a block's keys, -1 where no row sees any of them
+        auto lookup = [&](int blk) -> int {
+            if (blk >= last) return -1;
+            const int s = key0(blk);
+            if (s >= t.end || (a.window > 0 && s + kKeys - 1 <= p_lo - a.window && s >= a.sinks)) return -1;
+            const int id = table[s >> a.page_shift];
+            if ((uint32_t)id < (uint32_t)a.n_pages) return id;
+            if (lane == 0) atomicOr(a.status, MKV_DEV_BAD_PAGE);
+            return -1;
+        };
+        // Scales that are not there (keys behind the list's end, a bad page, keys
+        // that no row sees) arrive as zeros, which makes their elements zeros:
+        // nothing else has to be told apart, codes are finite whatever they are.
+        auto issue = [&](int stage, int blk, int id) {
+            if (blk < last) {
+                const int s = key0(blk);
+                const uint32_t dst = ring + stage * A::STAGE;
+                const int64_t page = max(id, 0) * page_bytes;
+                const int64_t codes = page + (s & page_mask) * A::CB;
+                if (id >= 0) {
+#pragma unroll
+                    for (int o = lane; o < A::CODES / 16; o += 32) {
+                        const int r = o / (D / 32), c = o % (D / 32);
+                        cp16(dst + k_at<D>(r, c), a.k + codes + o * 16, 16);
+                        cp16(dst + A::HALF + v_at<D>(r, c), a.v + codes + o * 16, 16);
+                    }
+                }
+                const int64_t scales = page + (A::CB << a.page_shift) + (s & page_mask) * A::SB;
+                const int there = id < 0 ? 0 : min(kKeys, t.end - s) * A::SB;
+                // chunks of K's scales, then of V's
+                if (lane < 2 * (A::SCALES / 16)) {
+                    const int kv = lane >= A::SCALES / 16, c = lane - kv * (A::SCALES / 16);
+                    cp16(dst + kv * A::HALF + A::CODES + c * 16, (kv ? a.v : a.k) + scales + c * 16,
+                         min(max(there - 16 * c, 0), 16));
+                }
+            }
+            cp_commit();
+        };
+
+        float o[D / 16][NR][4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int n = 0; n < NR; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+        float m[NR][2], l[NR][2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            m[n][0] = m[n][1] = -CUDART_INF_F;
+            l[n][0] = l[n][1] = 0.f;
+        }
+
+        int id = lookup(first);
+#pragma unroll
+        for (int s = 0; s < A::STAGES - 1; ++s) {
+            const int next = lookup(first + s + 1);
+            issue(s, first + s, id);
+            id = next;
+        }
+        for (int blk = first, it = 0; blk < last; ++blk, it = it + 1 == A::STAGES ? 0 : it + 1) {
+            {
+                const int ahead = blk + A::STAGES - 1, next = lookup(ahead + 1);
+                issue(it == 0 ? A::STAGES - 1 : it - 1, ahead, id);
+                id = next;
+            }
+            cp_wait<A::STAGES - 1>();
+            __syncwarp();
+            const uint32_t kb = ring + it * A::STAGE, vb = kb + A::HALF, ks = kb + A::CODES, vs = vb + A::CODES;
+
+            // scores: rows of the MMA are the keys gr and gr + 8
+            float s[NR][4];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            constexpr int WB = KW < 4 ? KW : 4;  // words of a load
+#pragma unroll
+            for (int x0 = 0; x0 < KW; x0 += WB) {
+                uint32_t kw[2][WB], sk[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int key = gr + 8 * h;
+                    if constexpr (D == 64) {
+                        lds_words<WB>(kb + k_at<D>(key, tq >> 1) + 8 * (tq & 1), kw[h]);
+                        const uint32_t f = e4m3x2_to_f16x2(lds_u8(ks + key * A::SB + tq));
+                        sk[h][0] = sk[h][1] = __byte_perm(f, 0, 0x1010);
+                    } else {
+                        lds_words<WB>(kb + k_at<D>(key, tq + x0), kw[h]);
+                        const uint32_t f = e4m3x2_to_f16x2(lds_u16(ks + key * A::SB + 2 * (tq + x0)));
+                        sk[h][0] = __byte_perm(f, 0, 0x1010);
+                        sk[h][1] = __byte_perm(f, 0, 0x3232);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < WB; ++x) {
+                    uint32_t f[2][4];
+                    e2m1x8_to_f16(kw[0][x], f[0]);
+                    e2m1x8_to_f16(kw[1][x], f[1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t k[4] = {mul_f16x2(f[0][2 * e], sk[0][x >> 1]), mul_f16x2(f[1][2 * e], sk[1][x >> 1]),
+                                               mul_f16x2(f[0][2 * e + 1], sk[0][x >> 1]),
+                                               mul_f16x2(f[1][2 * e + 1], sk[1][x >> 1])};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) {
+                            const uint32_t(&b)[2] = q[n][2 * (x0 + x) + e];
+                            mma_f16(s[n], k, b[0], b[1]);
+                        }
+                    }
+                }
+            }
+
+            // mask, reference point, weights
+            const int k0 = key0(blk), k1 = k0 + kKeys - 1;
+            const bool whole = k1 <= p_lo && (a.window <= 0 || k0 > p_hi - a.window || k1 < a.sinks);
+            bool grow = false;
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = s[n][e] * sc[n][e & 1];
+                    if (!whole) {
+                        const int key = k0 + gr + 8 * (e >> 1), at = p[n][e & 1];
+                        const bool seen = (key <= at) & ((a.window <= 0) | (key > at - a.window) | (key < a.sinks));
+                        x = seen ? x : -CUDART_INF_F;
+                    }
+                    s[n][e] = x;
+                    grow |= x - m[n][e & 1] > kLag<1>;
+                }
+            if (__any_sync(kFull, grow)) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float x = fmaxf(s[n][c], s[n][2 + c]);
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+                        const float to = fmaxf(m[n][c], x - kBase<1>);
+                        // (a row that has seen nothing yet has l = 0 and O = 0: any finite factor)
+                        const float f = m[n][c] == -CUDART_INF_F ? 0.f : exp2_approx(m[n][c] - to);
+                        m[n][c] = to;
+                        l[n][c] *= f;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[i][n][c] *= f;
+                            o[i][n][2 + c] *= f;
+                        }
+                    }
+            }
+            uint32_t pw[NR][2];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const float b0 = m[n][0] == -CUDART_INF_F ? 0.f : m[n][0], b1 = m[n][1] == -CUDART_INF_F ? 0.f : m[n][1];
+                const float e0 = exp2_approx(s[n][0] - b0), e1 = exp2_approx(s[n][1] - b1);
+                const float e2 = exp2_approx(s[n][2] - b0), e3 = exp2_approx(s[n][3] - b1);
+                l[n][0] += e0 + e2;
+                l[n][1] += e1 + e3;
+                pw[n][0] = transpose8(pack_weights<1>(e0, e1));
+                pw[n][1] = transpose8(pack_weights<1>(e2, e3));
+            }
+
+            // O^T: rows of the MMA are two of this lane's D / 8 consecutive dims, its contraction the 16 keys
+            uint32_t vw[4][VW], sv[2][2];  // keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
+            uint32_t sb[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int key = 2 * tq + (y & 1) + 8 * (y >> 1);
+                if constexpr (D == 64) {
+                    lds_words<1>(vb + v_at<D>(key, gr >> 2) + 4 * (gr & 3), vw[y]);
+                    sb[y] = lds_u8(vs + key * A::SB + (gr >> 1));
+                } else if constexpr (D == 128) {
+                    lds_words<2>(vb + v_at<D>(key, gr >> 1) + 8 * (gr & 1), vw[y]);
+                    sb[y] = lds_u8(vs + key * A::SB + gr);
+                } else {
+                    lds_words<4>(vb + v_at<D>(key, gr), vw[y]);
+                    sb[y] = lds_u16(vs + key * A::SB + 2 * gr);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sv[h][0] = e4m3x2_to_f16x2(__byte_perm(sb[2 * h], sb[2 * h + 1], 0x40));
+                sv[h][1] = D == 256 ? e4m3x2_to_f16x2(__byte_perm(sb[2 * h], sb[2 * h + 1], 0x51)) : sv[h][0];
+            }
+#pragma unroll
+            for (int x = 0; x < VW; ++x) {
+                uint32_t ev[2][4], od[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // two keys' codes of the same dim side by side: even dims, odd dims
+                    const uint32_t u = vw[2 * h][x], v = vw[2 * h + 1][x];
+                    e2m1x8_to_f16((u & 0x0F0F0F0Fu) | (v << 4 & 0xF0F0F0F0u), ev[h]);
+                    e2m1x8_to_f16((u >> 4 & 0x0F0F0F0Fu) | (v & 0xF0F0F0F0u), od[h]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int hf = x * 8 + 2 * e >= 16 ? 1 : 0;  // the second scale of a lane's 32 dims
+                    const uint32_t f[4] = {mul_f16x2(ev[0][e], sv[0][hf]), mul_f16x2(od[0][e], sv[0][hf]),
+                                           mul_f16x2(ev[1][e], sv[1][hf]), mul_f16x2(od[1][e], sv[1][hf])};
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) mma_f16(o[4 * x + e][n], f, pw[n][0], pw[n][1]);
+                }
+            }
+            __syncwarp();  // the stage is free for the next copies
+        }
+        cp_wait<0>();
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                l[n][c] += __shfl_xor_sync(kFull, l[n][c], 4);
+                l[n][c] += __shfl_xor_sync(kFull, l[n][c], 8);
+                l[n][c] += __shfl_xor_sync(kFull, l[n][c], 16);
+            }
+        __syncthreads();  // every ring is done with: the warps' results take its place
+        float *mine = reinterpret_cast<float *>(smem) + warp * R * A::OS;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = 8 * n + 2 * tq + c;
+                if (gr == 0) s_ml[warp][r] = make_float2(m[n][c], l[n][c]);
+#pragma unroll
+                for (int i = 0; i < D / 16; i += 2)
+                    *reinterpret_cast<float4 *>(mine + r * A::OS + gr * (D / 8) + 2 * i) =
+                        make_float4(o[i][n][c], o[i][n][2 + c], o[i + 1][n][c], o[i + 1][n][2 + c]);
+            }
+        __syncthreads();
+        for (int x = threadIdx.x; x < t.rows * (D / 4); x += A::THREADS) {
+            const int r = x / (D / 4), c = x % (D / 4);
+            float M = -CUDART_INF_F;
+#pragma unroll
+            for (int y = 0; y < A::WARPS; ++y) M = fmaxf(M, s_ml[y][r].x);
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            float total = 0.f;
+#pragma unroll
+            for (int y = 0; y < A::WARPS; ++y) {
+                const float2 ml = s_ml[y][r];
+                const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - M);
+                const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + (y * R + r) * A::OS + 4 * c);
+                sum.x += f * v.x;
+                sum.y += f * v.y;
+                sum.z += f * v.z;
+                sum.w += f * v.w;
+                total += f * ml.y;
+            }
+            if (!w.whole()) {
+                const int64_t part = part_row(w, R) + r;
+                reinterpret_cast<float4 *>(a.part_o)[part * (D / 4) + c] = sum;
+                if (c == 0) a.part_ml[part] = make_float2(M, total);
+                continue;
+            }
+            const float inv = inverse_sum(total, a.v_scale);
+            const int Rq = t.row0 + r, i = a.by_group(Rq), head = t.j * a.group + Rq - i * a.group;
+            *reinterpret_cast<uint2 *>(a.O + 2 * ((int64_t)(qrow0 + i) * a.o_stride + (int64_t)head * D + 4 * c)) =
+                make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+            if (c == 0 && a.lse) a.lse[(int64_t)(qrow0 + i) * a.q_heads + head] = log_sum(M, total);
+        }
+        __syncthreads();  // the next segment's copies may overwrite the results
+        if (!w.whole() && threadIdx.x == 0) {
+            // Parts of a tile count themselves in a byte of the workspace's head,
+            // which the last one takes back to zero; it joins the parts below.
+            const int unit0 = at_unit - w.first, c0 = cta_of(unit0, s_line), c1 = cta_of(unit0 + w.units - 1, s_line);
+            uint32_t *word = a.counts + c0 / 4;
+            const int shift = c0 % 4 * 8;
+            __threadfence();
+            if ((int)(atomicAdd(word, 1u << shift) >> shift & 255u) == c1 - c0) {
+                atomicSub(word, (uint32_t)(c1 - c0 + 1) << shift);
+                s_join[w.first > 0 ? 0 : 1] = make_int4(w.tile - 1, c0, c1, 0);
+            }
+        }
+        at_unit += w.last - w.first;
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {  // (a CTA's first segment and its last one)
+        const int4 j = s_join[k];
+        if (j.x < 0) continue;
+        __threadfence();
+        const Tile t = make_tile<A::KEYS>(a, j.x, R, false);
+        for (int r = warp; r < t.rows; r += A::WARPS) join_rows<D, R, 1, 8>(a, t, j.y, j.z, r);
+    }
+}
+
+template <int D, int R>
+cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
+{
+    using A = Attend4<D, R>;
+    cudaError_t e = cudaFuncSetAttribute(k_attend_e2m1<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM);
+    if (e != cudaSuccess) return e;
+    k_attend_e2m1<D, R><<<a.ctas, A::THREADS, A::SMEM, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Rows of a tile: 8 where a list has no more (a decode step of up to 8 query
+// heads per KV head), else 16.
+int e2m1_tile_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
+cudaError_t launch_attend_e2m1(const AttnArgs &a, cudaStream_t st)
+{
+    const bool small = a.tile_rows == 8;
+    switch (a.head_dim) {
+    case 64: return small ? launch_one<64, 8>(a, st) : launch_one<64, 16>(a, st);
+    case 128: return small ? launch_one<128, 8>(a, st) : launch_one<128, 16>(a, st);
+    case 256: return small ? launch_one<256, 8>(a, st) : launch_one<256, 16>(a, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace mkv

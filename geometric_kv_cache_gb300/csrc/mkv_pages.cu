@@ -29,6 +29,7 @@
 #include <algorithm>
 
 #include "mkv_device.cuh"
+#include "mkv_e2m1.cuh"
 #include "mkv_pages.h"
 
 namespace mkv {
@@ -419,9 +420,17 @@ k_page_update(const PageArgs a)
             if (lane == 0) atomicOr(a.status, MKV_DEV_BAD_PAGE);
             return;
         }
-        const int64_t page_bytes = a.row_bytes << a.page_shift, n = rest * a.row_bytes;
-        const uint8_t *ks = a.k + s * page_bytes, *vs = a.v + s * page_bytes;
-        uint8_t *kd = a.k + d * page_bytes, *vd = a.v + d * page_bytes;
+        const int64_t n = rest * a.row_bytes;
+        const uint8_t *ks = a.k + s * a.page_bytes, *vs = a.v + s * a.page_bytes;
+        uint8_t *kd = a.k + d * a.page_bytes, *vd = a.v + d * a.page_bytes;
+        // 4-bit pages: the rows' scales, behind the codes of the whole page
+        const int64_t sc = a.row_bytes << a.page_shift;
+        for (int o = lane * 4; o < rest * a.scale_bytes; o += 128) {
+            const uint32_t x = *reinterpret_cast<const uint32_t *>(ks + sc + o);
+            const uint32_t y = *reinterpret_cast<const uint32_t *>(vs + sc + o);
+            *reinterpret_cast<uint32_t *>(kd + sc + o) = x;
+            *reinterpret_cast<uint32_t *>(vd + sc + o) = y;
+        }
         // one round trip for 16 rows of 256 bytes
         constexpr int U = 8;
         for (int64_t o = lane * 16; o < n; o += 512 * U) {
@@ -449,12 +458,57 @@ k_page_update(const PageArgs a)
 // An item's owner is read three items ahead, its indices two and its page
 // entries one, so that every row copy (groups of LPR lanes, 16 bytes each, 4
 // rows of K and of V in flight per lane) finds its addresses in registers.
-template <int LPR>
+// ROWS: what a row is. Of 4-bit pages a lane also copies the scales of its own
+// token, with one load of each. Rows that become codes are 32 bytes of bf16 per
+// lane, one group of 16 dims: its largest element never leaves the lane.
+template <int BYTES>
+struct ScaleWord {
+    using type = uint32_t;
+};
+template <>
+struct ScaleWord<8> {
+    using type = uint2;
+};
+template <>
+struct ScaleWord<16> {
+    using type = uint4;
+};
+enum Rows { kCopy, kCopyCodes, kToE4m3, kToE2m1 };
+
+// A group of 16 bf16 as E4M3 codes (16 bytes), or as 4-bit codes (8 bytes) and their scale.
+__device__ __forceinline__ uint4 group_to_e4m3(uint4 lo, uint4 hi, Rounding r)
+{
+    float x[8], y[8];
+    bf16x8_to_f32(lo, x);
+    bf16x8_to_f32(hi, y);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float *f = i < 2 ? x + 4 * i : y + 4 * (i - 2);
+        w[i] = f32x2_to_e4m3(f[0] * r.inv, f[1] * r.inv) | f32x2_to_e4m3(f[2] * r.inv, f[3] * r.inv) << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint2 group_to_e2m1(uint4 lo, uint4 hi, Rounding r, uint32_t &scale)
+{
+    float x[8], y[8];
+    bf16x8_to_f32(lo, x);
+    bf16x8_to_f32(hi, y);
+    scale = f32x2_to_e4m3(max_nan(largest8(x), largest8(y)) * r.inv6, 0.f) & 0xFFu;
+    const float f = code_factor(scale, r.inv);
+    return make_uint2(codes8(x, f), codes8(y, f));
+}
+
+template <int LPR, Rows ROWS>
 __global__ void __launch_bounds__(kPageThreads, 3)
 k_page_compact(const PageArgs a, int list_ctas)
 {
-    constexpr int RB = LPR * 16, RPS = 32 / LPR;  // bytes of a row, rows per step
-    constexpr int STEPS = kItem / RPS, B = STEPS < 4 ? STEPS : 4;  // steps, and of a batch
+    constexpr bool ROUND = ROWS == kToE4m3 || ROWS == kToE2m1;
+    constexpr int RB = LPR * (ROUND ? 32 : 16), RPS = 32 / LPR;  // bytes of a row (read), rows per step
+    constexpr int MOST = ROUND ? 2 : 4;
+    constexpr int STEPS = kItem / RPS, B = STEPS < MOST ? STEPS : MOST;  // steps, and of a batch
+    constexpr int SB = ROWS == kCopyCodes ? LPR * 2 : ROWS == kToE2m1 ? LPR : 0;  // bytes of a row's scales
+    constexpr int WB = ROWS == kToE2m1 ? LPR * 8 : LPR * 16;                      // bytes of a row written, without them
     pdl_wait();
     const bool bad = a.verdict[0] != 0;
     const int64_t lists = (int64_t)a.batch * a.heads;
@@ -520,8 +574,15 @@ k_page_compact(const PageArgs a, int list_ctas)
         }
         to = (a.free_ids[it.rank] << a.page_shift) + (it.i & (a.page_size - 1));
     };
-    const uint8_t *ks = (a.K ? a.K : a.k) + lr * 16, *vs = (a.K ? a.V : a.v) + lr * 16;
-    uint8_t *kd = a.k + lr * 16, *vd = a.v + lr * 16;
+    const uint8_t *ks = (a.K ? a.K : a.k) + lr * (RB / LPR), *vs = (a.K ? a.V : a.v) + lr * (RB / LPR);
+    uint8_t *kd = a.k + lr * (WB / LPR), *vd = a.v + lr * (WB / LPR);
+    // where a row of the pool's codes, and of its scales, lies: each page has both
+    auto codes_at = [&](int64_t row) -> int64_t {
+        return row * WB + (SB ? (row >> a.page_shift << a.page_shift) * SB : 0);
+    };
+    auto scales_at = [&](int64_t row) -> int64_t {
+        return ((row >> a.page_shift) + 1 << a.page_shift) * WB + row * SB;
+    };
     int64_t from;
     int to;
     Item ahead = source(warp, owner(warp));
@@ -535,9 +596,19 @@ k_page_compact(const PageArgs a, int list_ctas)
         places(ahead, next_from, next_to);
         ahead = source(item + 2 * warps, own);
         own = owner(item + 3 * warps);
+        if constexpr (ROWS == kCopyCodes) {  // this lane's token
+            using S = typename ScaleWord<SB>::type;
+            if (to >= 0) {
+                const int64_t s = scales_at(from), d = scales_at(to);
+                const S x = *reinterpret_cast<const S *>(a.k + s), y = *reinterpret_cast<const S *>(a.v + s);
+                *reinterpret_cast<S *>(a.k + d) = x;
+                *reinterpret_cast<S *>(a.v + d) = y;
+            }
+        }
 #pragma unroll
         for (int b0 = 0; b0 < STEPS; b0 += B) {
-            uint4 kr[B], vr[B];
+            constexpr int N = ROUND ? 2 : 1;
+            uint4 kr[B][N], vr[B][N];
             int dst[B];
 #pragma unroll
             for (int u = 0; u < B; ++u) {
@@ -545,15 +616,32 @@ k_page_compact(const PageArgs a, int list_ctas)
                 const int64_t src = __shfl_sync(kFull, from, row);
                 dst[u] = __shfl_sync(kFull, to, row);
                 if (dst[u] >= 0) {
-                    kr[u] = ld_stream(ks + src * RB);
-                    vr[u] = ld_stream(vs + src * RB);
+                    const int64_t at = ROWS == kCopyCodes ? codes_at(src) : src * RB;
+#pragma unroll
+                    for (int x = 0; x < N; ++x) {
+                        kr[u][x] = ld_stream(ks + at + 16 * x);
+                        vr[u][x] = ld_stream(vs + at + 16 * x);
+                    }
                 }
             }
 #pragma unroll
             for (int u = 0; u < B; ++u)
                 if (dst[u] >= 0) {
-                    st_v4(kd + (int64_t)dst[u] * RB, kr[u]);
-                    st_v4(vd + (int64_t)dst[u] * RB, vr[u]);
+                    const int64_t at = codes_at(dst[u]);
+                    if constexpr (ROWS == kToE4m3) {
+                        st_v4(kd + at, group_to_e4m3(kr[u][0], kr[u][N - 1], a.k_round));
+                        st_v4(vd + at, group_to_e4m3(vr[u][0], vr[u][N - 1], a.v_round));
+                    } else if constexpr (ROWS == kToE2m1) {
+                        uint32_t s, z;
+                        *reinterpret_cast<uint2 *>(kd + at) = group_to_e2m1(kr[u][0], kr[u][N - 1], a.k_round, s);
+                        *reinterpret_cast<uint2 *>(vd + at) = group_to_e2m1(vr[u][0], vr[u][N - 1], a.v_round, z);
+                        const int64_t to_scales = scales_at(dst[u]) + lr;
+                        a.k[to_scales] = (uint8_t)s;
+                        a.v[to_scales] = (uint8_t)z;
+                    } else {
+                        st_v4(kd + at, kr[u][0]);
+                        st_v4(vd + at, vr[u][0]);
+                    }
                 }
         }
         from = next_from;
@@ -561,15 +649,23 @@ k_page_compact(const PageArgs a, int list_ctas)
     }
 }
 
-const void *compact_fn(int64_t row_bytes)
+template <Rows ROWS>
+const void *compact_lanes(int64_t lanes)
 {
-    switch (row_bytes) {
-    case 64: return (const void *)k_page_compact<4>;
-    case 128: return (const void *)k_page_compact<8>;
-    case 256: return (const void *)k_page_compact<16>;
-    case 512: return (const void *)k_page_compact<32>;
-    default: return nullptr;
-    }
+    if constexpr (ROWS == kCopyCodes)
+        if (lanes == 2) return (const void *)k_page_compact<2, ROWS>;
+    if constexpr (ROWS != kCopyCodes)
+        if (lanes == 16) return (const void *)k_page_compact<16, ROWS>;
+    if constexpr (ROWS == kCopy)
+        if (lanes == 32) return (const void *)k_page_compact<32, ROWS>;
+    return lanes == 4 ? (const void *)k_page_compact<4, ROWS> : lanes == 8 ? (const void *)k_page_compact<8, ROWS> : nullptr;
+}
+
+const void *compact_fn(const PageArgs &a)
+{
+    if (a.quantize == 1) return compact_lanes<kToE4m3>(a.row_bytes / 16);
+    if (a.quantize == 2) return compact_lanes<kToE2m1>(a.row_bytes / 8);
+    return a.scale_bytes ? compact_lanes<kCopyCodes>(a.row_bytes / 16) : compact_lanes<kCopy>(a.row_bytes / 16);
 }
 
 cudaError_t launch_dependent(const void *fn, int64_t grid, void **args, cudaStream_t st)
@@ -614,7 +710,7 @@ cudaError_t launch_page_call(const PageArgs &pa, cudaStream_t st)
     }
     if (!a.kept)
         return launch_dependent((const void *)k_page_update, (lists * 32 + kPageThreads - 1) / kPageThreads, args, st);
-    const void *fn = compact_fn(a.row_bytes);
+    const void *fn = compact_fn(a);
     if (!fn) return cudaErrorInvalidValue;
     // no more items than the pages that can be taken have
     const int64_t most = a.idx ? std::min((int64_t)a.idx_stride, (int64_t)a.max_pages << a.page_shift)

@@ -14,6 +14,7 @@ namespace mkv {
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int32_t kMaxAxes = 8;
 // Where the workspace's head holds the counts of cut tiles' parts.
 constexpr size_t kCounts = 64;
 static_assert(kCounts + kPlanSms <= kAlign && kPlanSms < 256, "a byte per CTA");
@@ -42,7 +43,7 @@ mkv_status check_sizes(const mkv_page_pool &p, const mkv_page_lists &l)
 {
     if (p.n_pages < 0 || p.page_size <= 0 || p.head_dim <= 0) return MKV_ERR_INVALID_ARG;
     if (l.batch < 0 || l.heads < 0 || l.max_pages < 0) return MKV_ERR_INVALID_ARG;
-    if (!supported_head_dim(p.head_dim) || elem_bytes(p.dtype) == 0) return MKV_ERR_UNSUPPORTED;
+    if (!supported_head_dim(p.head_dim) || !pool_dtype(p.dtype)) return MKV_ERR_UNSUPPORTED;
     if (page_shift(p.page_size) < 0) return MKV_ERR_UNSUPPORTED;
     if ((int64_t)p.n_pages * p.page_size > (1 << 30) || (int64_t)l.max_pages * p.page_size > (1 << 30))
         return MKV_ERR_UNSUPPORTED;
@@ -130,7 +131,9 @@ mkv_status page_call(const mkv_page_pool &p, const mkv_page_lists &in, const int
     a->batch = in.batch;
     a->heads = in.heads;
     a->max_pages = in.max_pages;
-    a->row_bytes = (int64_t)p.head_dim * elem_bytes(p.dtype);
+    a->row_bytes = code_row_bytes(p.dtype, p.head_dim);
+    a->scale_bytes = scale_row_bytes(p.dtype, p.head_dim);
+    a->page_bytes = (a->row_bytes + a->scale_bytes) * p.page_size;
     a->k = static_cast<uint8_t *>(p.k_pages);
     a->v = static_cast<uint8_t *>(p.v_pages);
     a->table = in.table;
@@ -151,6 +154,107 @@ mkv_status page_call(const mkv_page_pool &p, const mkv_page_lists &in, const int
     a->row_chunks = (in.batch + kPlanRows - 1) / kPlanRows;
     a->page_chunks = (p.n_pages + kPlanPages - 1) / kPlanPages;
     return MKV_OK;
+}
+
+// A scale whose reciprocal codes are made with; next to a group's scale, down to 2^-9, too.
+bool scale_ok(float scale, int32_t dtype)
+{
+    return isfinite(scale) && scale > 0.f && isfinite((dtype == MKV_DTYPE_E2M1 ? 512.f : 1.f) / scale);
+}
+
+// What mkv_page_compact and mkv_page_quantize share; a: how rows become the pages'.
+mkv_status compact_call(const mkv_page_pool &pool, const mkv_page_lists &in, const int32_t *refs, const int32_t *idx,
+                        int32_t idx_stride, const int32_t *kept, const void *K, const void *V, int32_t t_max,
+                        const int32_t *seq_lens, const mkv_page_lists &out, int32_t *refs_out, void *workspace,
+                        size_t workspace_bytes, mkv_stream_t stream, PageArgs a)
+{
+    const mkv_status rc = page_call(pool, in, refs, out, refs_out, false, workspace, workspace_bytes, &a);
+    if (rc != MKV_OK) return rc;
+    if ((K == nullptr) != (V == nullptr) || !aligned(K, 16) || !aligned(V, 16)) return MKV_ERR_INVALID_ARG;
+    if (K && t_max < 0) return MKV_ERR_INVALID_ARG;
+    if (K && t_max > (1 << 30)) return MKV_ERR_UNSUPPORTED;
+    if (idx && idx_stride < 0) return MKV_ERR_INVALID_ARG;
+    if (!aligned(idx, 4) || !aligned(kept, 4) || !aligned(seq_lens, 4)) return MKV_ERR_INVALID_ARG;
+    if (no_lists(in)) {
+        if (refs_out != refs && pool.n_pages > 0)
+            return cuda_status(cudaMemcpyAsync(refs_out, refs, (size_t)pool.n_pages * sizeof(int32_t),
+                                               cudaMemcpyDeviceToDevice, reinterpret_cast<cudaStream_t>(stream)));
+        return MKV_OK;
+    }
+    if (!kept) return MKV_ERR_INVALID_ARG;
+    a.idx = idx;
+    a.idx_stride = idx_stride;
+    a.kept = kept;
+    a.K = static_cast<const uint8_t *>(K);
+    a.V = static_cast<const uint8_t *>(V);
+    a.t_max = t_max;
+    a.seq_lens = seq_lens;
+    return cuda_status(launch_page_call(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// What mkv_rope_append (axes NULL, n_axes 0) and mkv_rope_append_axes share.
+mkv_status rope_call(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V, int64_t v_stride,
+                     const mkv_new_tokens &tokens, const int32_t *positions, int32_t n_axes, const int32_t *axes,
+                     const float *inv_freq, int32_t rot_dim, mkv_rope_layout layout, float factor, void *Q_out,
+                     const mkv_page_pool &pool, const mkv_page_lists &lists, float k_scale, float v_scale,
+                     void *workspace, size_t workspace_bytes, mkv_stream_t stream)
+{
+    mkv_status rc = check_sizes(pool, lists);
+    if (rc != MKV_OK || (rc = check_tokens(tokens, lists)) != MKV_OK) return rc;
+    if ((rc = check_pointers(pool, lists)) != MKV_OK) return rc;
+    const int d = pool.head_dim, es = elem_bytes(pool.dtype);  // (4-bit pools: 0)
+    if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return MKV_ERR_INVALID_ARG;
+    if (layout != MKV_ROPE_HALF && layout != MKV_ROPE_INTERLEAVED) return MKV_ERR_INVALID_ARG;
+    if (!isfinite(factor) || !scale_ok(k_scale, pool.dtype) || !scale_ok(v_scale, pool.dtype)) return MKV_ERR_INVALID_ARG;
+    if (es == 2 && (k_scale != 1.f || v_scale != 1.f)) return MKV_ERR_INVALID_ARG;
+    const bool none = tokens.n_tokens == 0 || no_lists(lists);
+    if (!none) {
+        if (!rows_ok(Q, q_stride, tokens.q_heads, d) || !rows_ok(K, k_stride, lists.heads, d) ||
+            !rows_ok(V, v_stride, lists.heads, d) || !rows_ok(Q_out, (int64_t)tokens.q_heads * d, tokens.q_heads, d))
+            return MKV_ERR_INVALID_ARG;
+        if (Q_out == Q && q_stride != (int64_t)tokens.q_heads * d) return MKV_ERR_INVALID_ARG;
+        if (!tokens.q_start || !positions || !inv_freq) return MKV_ERR_INVALID_ARG;
+        if (!aligned(tokens.q_start, 4) || !aligned(positions, 4) || !aligned(inv_freq, 4)) return MKV_ERR_INVALID_ARG;
+        if (n_axes > 0 && (!axes || !aligned(axes, 4))) return MKV_ERR_INVALID_ARG;
+    }
+    if ((rc = check_ws(make_page_layout(pool, lists).total, workspace, workspace_bytes)) != MKV_OK) return rc;
+    if (none) return MKV_OK;
+    RopeArgs a = {};
+    a.Q = static_cast<const uint8_t *>(Q);
+    a.K = static_cast<const uint8_t *>(K);
+    a.V = static_cast<const uint8_t *>(V);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.Q_out = static_cast<uint8_t *>(Q_out);
+    a.positions = positions;
+    a.q_start = tokens.q_start;
+    a.table = lists.table;
+    a.lens = lists.lens;
+    a.inv_freq = inv_freq;
+    a.k = static_cast<uint8_t *>(pool.k_pages);
+    a.v = static_cast<uint8_t *>(pool.v_pages);
+    a.n_tokens = tokens.n_tokens;
+    a.q_heads = tokens.q_heads;
+    a.batch = lists.batch;
+    a.heads = lists.heads;
+    a.max_pages = lists.max_pages;
+    a.n_pages = pool.n_pages;
+    a.page_size = pool.page_size;
+    a.page_shift = page_shift(pool.page_size);
+    a.head_dim = d;
+    a.es = es;
+    a.rot_dim = rot_dim;
+    a.layout = layout;
+    a.factor = factor;
+    a.k_inv = 1.f / k_scale;
+    a.v_inv = 1.f / v_scale;
+    a.k_inv6 = Rounding(k_scale).inv6;
+    a.v_inv6 = Rounding(v_scale).inv6;
+    a.n_axes = n_axes;
+    a.axes = axes;
+    a.status = region<uint32_t>(workspace, 0);
+    return cuda_status(launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -191,28 +295,24 @@ mkv_status mkv_page_compact(mkv_page_pool pool, mkv_page_lists in, const int32_t
                             size_t workspace_bytes, mkv_stream_t stream)
 {
     PageArgs a = {};
-    const mkv_status rc = page_call(pool, in, refs, out, refs_out, false, workspace, workspace_bytes, &a);
-    if (rc != MKV_OK) return rc;
-    if ((K == nullptr) != (V == nullptr) || !aligned(K, 16) || !aligned(V, 16)) return MKV_ERR_INVALID_ARG;
-    if (K && t_max < 0) return MKV_ERR_INVALID_ARG;
-    if (K && t_max > (1 << 30)) return MKV_ERR_UNSUPPORTED;
-    if (idx && idx_stride < 0) return MKV_ERR_INVALID_ARG;
-    if (!aligned(idx, 4) || !aligned(kept, 4) || !aligned(seq_lens, 4)) return MKV_ERR_INVALID_ARG;
-    if (no_lists(in)) {
-        if (refs_out != refs && pool.n_pages > 0)
-            return cuda_status(cudaMemcpyAsync(refs_out, refs, (size_t)pool.n_pages * sizeof(int32_t),
-                                               cudaMemcpyDeviceToDevice, reinterpret_cast<cudaStream_t>(stream)));
-        return MKV_OK;
-    }
-    if (!kept) return MKV_ERR_INVALID_ARG;
-    a.idx = idx;
-    a.idx_stride = idx_stride;
-    a.kept = kept;
-    a.K = static_cast<const uint8_t *>(K);
-    a.V = static_cast<const uint8_t *>(V);
-    a.t_max = t_max;
-    a.seq_lens = seq_lens;
-    return cuda_status(launch_page_call(a, reinterpret_cast<cudaStream_t>(stream)));
+    if (pool.dtype == MKV_DTYPE_E2M1 && (K || V)) return MKV_ERR_UNSUPPORTED;
+    return compact_call(pool, in, refs, idx, idx_stride, kept, K, V, t_max, seq_lens, out, refs_out, workspace,
+                        workspace_bytes, stream, a);
+}
+
+mkv_status mkv_page_quantize(mkv_page_pool pool, mkv_page_lists in, const int32_t *refs, const int32_t *idx,
+                             int32_t idx_stride, const int32_t *kept, const void *K, const void *V, int32_t t_max,
+                             const int32_t *seq_lens, float k_scale, float v_scale, mkv_page_lists out,
+                             int32_t *refs_out, void *workspace, size_t workspace_bytes, mkv_stream_t stream)
+{
+    PageArgs a = {};
+    if (pool.dtype == MKV_DTYPE_BF16) return MKV_ERR_UNSUPPORTED;
+    if (!K || !V || !scale_ok(k_scale, pool.dtype) || !scale_ok(v_scale, pool.dtype)) return MKV_ERR_INVALID_ARG;
+    a.quantize = pool.dtype == MKV_DTYPE_E2M1 ? 2 : 1;
+    a.k_round = Rounding(k_scale);
+    a.v_round = Rounding(v_scale);
+    return compact_call(pool, in, refs, idx, idx_stride, kept, K, V, t_max, seq_lens, out, refs_out, workspace,
+                        workspace_bytes, stream, a);
 }
 
 mkv_status mkv_rope_append(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V,
@@ -221,59 +321,38 @@ mkv_status mkv_rope_append(const void *Q, int64_t q_stride, const void *K, int64
                            mkv_page_lists lists, float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
                            mkv_stream_t stream)
 {
-    mkv_status rc = check_sizes(pool, lists);
-    if (rc != MKV_OK || (rc = check_tokens(tokens, lists)) != MKV_OK) return rc;
-    if ((rc = check_pointers(pool, lists)) != MKV_OK) return rc;
-    const int d = pool.head_dim, es = elem_bytes(pool.dtype);
-    if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return MKV_ERR_INVALID_ARG;
-    if (layout != MKV_ROPE_HALF && layout != MKV_ROPE_INTERLEAVED) return MKV_ERR_INVALID_ARG;
-    if (!isfinite(factor) || !isfinite(k_scale) || !isfinite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f) ||
-        !isfinite(1.f / k_scale) || !isfinite(1.f / v_scale))
-        return MKV_ERR_INVALID_ARG;
-    if (es == 2 && (k_scale != 1.f || v_scale != 1.f)) return MKV_ERR_INVALID_ARG;
-    const bool none = tokens.n_tokens == 0 || no_lists(lists);
-    if (!none) {
-        if (!rows_ok(Q, q_stride, tokens.q_heads, d) || !rows_ok(K, k_stride, lists.heads, d) ||
-            !rows_ok(V, v_stride, lists.heads, d) || !rows_ok(Q_out, (int64_t)tokens.q_heads * d, tokens.q_heads, d))
-            return MKV_ERR_INVALID_ARG;
-        if (Q_out == Q && q_stride != (int64_t)tokens.q_heads * d) return MKV_ERR_INVALID_ARG;
-        if (!tokens.q_start || !positions || !inv_freq) return MKV_ERR_INVALID_ARG;
-        if (!aligned(tokens.q_start, 4) || !aligned(positions, 4) || !aligned(inv_freq, 4)) return MKV_ERR_INVALID_ARG;
+    return rope_call(Q, q_stride, K, k_stride, V, v_stride, tokens, positions, 0, nullptr, inv_freq, rot_dim, layout,
+                     factor, Q_out, pool, lists, k_scale, v_scale, workspace, workspace_bytes, stream);
+}
+
+mkv_status mkv_rope_append_axes(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V,
+                                int64_t v_stride, mkv_new_tokens tokens, const int32_t *positions, int32_t n_axes,
+                                const int32_t *axes, const float *inv_freq, int32_t rot_dim, mkv_rope_layout layout,
+                                float factor, void *Q_out, mkv_page_pool pool, mkv_page_lists lists, float k_scale,
+                                float v_scale, void *workspace, size_t workspace_bytes, mkv_stream_t stream)
+{
+    if (n_axes < 1 || n_axes > kMaxAxes) return MKV_ERR_INVALID_ARG;
+    return rope_call(Q, q_stride, K, k_stride, V, v_stride, tokens, positions, n_axes, axes, inv_freq, rot_dim, layout,
+                     factor, Q_out, pool, lists, k_scale, v_scale, workspace, workspace_bytes, stream);
+}
+
+int32_t mkv_rope_axes(int32_t rot_dim, int32_t n_axes, const int32_t *sections, int32_t dealt, int32_t *axes)
+{
+    if (rot_dim <= 0 || rot_dim % 16 != 0 || n_axes < 1 || n_axes > kMaxAxes || !sections || !axes) return -1;
+    int64_t sum = 0;
+    for (int32_t a = 0; a < n_axes; ++a) {
+        if (sections[a] < 0) return -1;
+        sum += sections[a];
     }
-    if ((rc = check_ws(make_page_layout(pool, lists).total, workspace, workspace_bytes)) != MKV_OK) return rc;
-    if (none) return MKV_OK;
-    RopeArgs a = {};
-    a.Q = static_cast<const uint8_t *>(Q);
-    a.K = static_cast<const uint8_t *>(K);
-    a.V = static_cast<const uint8_t *>(V);
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.Q_out = static_cast<uint8_t *>(Q_out);
-    a.positions = positions;
-    a.q_start = tokens.q_start;
-    a.table = lists.table;
-    a.lens = lists.lens;
-    a.inv_freq = inv_freq;
-    a.k = static_cast<uint8_t *>(pool.k_pages);
-    a.v = static_cast<uint8_t *>(pool.v_pages);
-    a.n_tokens = tokens.n_tokens;
-    a.q_heads = tokens.q_heads;
-    a.batch = lists.batch;
-    a.heads = lists.heads;
-    a.max_pages = lists.max_pages;
-    a.n_pages = pool.n_pages;
-    a.page_size = pool.page_size;
-    a.page_shift = page_shift(pool.page_size);
-    a.head_dim = d;
-    a.es = es;
-    a.rot_dim = rot_dim;
-    a.layout = layout;
-    a.factor = factor;
-    a.k_inv = 1.f / k_scale;
-    a.v_inv = 1.f / v_scale;
-    a.status = region<uint32_t>(workspace, 0);
-    return cuda_status(launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)));
+    if (sum != rot_dim / 2) return -1;
+    int32_t given[kMaxAxes] = {};
+    for (int32_t i = 0, a = 0; i < rot_dim / 2; ++i) {
+        while (given[a] == sections[a]) a = (a + 1) % n_axes;
+        axes[i] = a;
+        ++given[a];
+        if (dealt) a = (a + 1) % n_axes;
+    }
+    return 0;
 }
 
 int32_t mkv_rope_frequencies(int32_t rot_dim, double theta, mkv_rope_scaling scaling, double scale,
@@ -378,6 +457,7 @@ mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens t
     a.sinks = sinks;
     a.scale_log2 = scale_log2;
     a.v_scale = v_scale;
+    a.tile_rows = plan.tile_rows;
     a.tiles = plan.tiles;
     a.ctas = plan.ctas;
     a.by_tiles = FastDiv(plan.tiles);

@@ -25,6 +25,7 @@
 #include <stdint.h>
 
 #include "mkv_device.cuh"
+#include "mkv_e2m1.cuh"
 #include "mkv_pages.h"
 
 namespace mkv {
@@ -78,13 +79,91 @@ __device__ __forceinline__ int row_of_token(const int32_t *q_start, int batch, i
     return lo < batch && q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
 }
 
+// The rotated values of this lane's 16 dims (x, y as loaded) as 64-bit
+// arithmetic gives them, rounded once to fp32: pair e of the lane's 8 turns by
+// the position of its axis. Not inlined: 4-bit keys next to a border take it,
+// one in a few hundred groups of heads.
+template <bool AXES>
+__device__ __noinline__ void rotate_exactly(const RopeArgs &a, int t, int u, uint4 xr, uint4 yr, float (&x)[8], float (&y)[8])
+{
+    float p[8], q[8];
+    bf16x8_to_f32(xr, p);
+    bf16x8_to_f32(yr, q);
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+        const int pair = 8 * u + e;
+        int axis = AXES ? a.axes[pair] : 0;
+        if (AXES && (uint32_t)axis >= (uint32_t)a.n_axes) axis = 0;
+        double sn, cn;
+        sincos((double)a.positions[(int64_t)axis * a.n_tokens + t] * (double)a.inv_freq[pair], &sn, &cn);
+        sn *= a.factor;
+        cn *= a.factor;
+        // pairs (x[e], y[e]); neighbouring ones: x holds the lane's first four, y the others
+        const bool half = a.layout == MKV_ROPE_HALF;
+        const float c0 = half ? p[e] : e < 4 ? p[2 * e & 7] : q[2 * e & 7];
+        const float c1 = half ? q[e] : e < 4 ? p[(2 * e + 1) & 7] : q[(2 * e + 1) & 7];
+        const float r0 = (float)(c0 * cn - c1 * sn), r1 = (float)(c0 * sn + c1 * cn);
+        if (half) {
+            x[e] = r0;
+            y[e] = r1;
+        } else if (e < 4) {
+            x[2 * e & 7] = r0;
+            x[(2 * e + 1) & 7] = r1;
+        } else {
+            y[2 * e & 7] = r0;
+            y[(2 * e + 1) & 7] = r1;
+        }
+    }
+}
+
+// Where the other eight dims of a group of 16 are, when the row is one of pairs
+// (i, i + rot / 2) and its rotated part is `halves` times 8 pairs: eights are
+// numbered along the row, a lane u < halves has numbers u (its x) and halves + u
+// (its y). Lane in the lower bits, 32 for its y.
+__device__ __forceinline__ int other_eight(int eight, int halves)
+{
+    const int o = eight ^ 1;
+    return o < halves ? o : 32 + o - halves;
+}
+
+// Codes of a lane's eight values t = x r where x is known to +-err only: flags
+// what another x within that could change.
+__device__ __forceinline__ uint32_t codes8_within(const float (&x)[8], float r, float err, bool &unsure)
+{
+    // (2^-19: the roundings of x r and of the sums below, values up to 8)
+    const float e = fmaf(err * 1.0001f, r, 1.9073486e-6f);
+    float lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = __fmul_rn(x[i], r);
+        lo[i] = t - e;
+        hi[i] = t + e;
+    }
+    const uint32_t l = f32x8_to_e2m1(lo), h = f32x8_to_e2m1(hi);
+    // (the ends of a small enough stretch have different signs only where both are zero; a large one is of groups whose
+    // scale is saturated, or of infinities and NaN)
+    unsure |= ((l ^ h) & 0x77777777u) != 0 || !(e < 0.125f);
+    return plain_zeros(l);
+}
+
 // A row of D dims is D / 16 units, one lane each (two groups of 8 dims that
 // belong together); the warp covers a group of 512 / D heads at a time: first
 // the groups of query heads, then of key heads, then of value heads. `parts`
 // warps share a token, group by group.
-template <int D>
-__global__ void __launch_bounds__(kRopeThreads, 3)
-k_rope_append(const RopeArgs a, int parts)
+//
+// FOUR: keys and values become 4-bit codes. A lane's two eights are one group of
+// 16 dims or, where pairs lie half a row apart, one each of two groups, whose
+// largest elements meet over shuffles. Codes of rotated keys have to be those of
+// the exact rotation, whose fp32 form here is off by up to kOff times its
+// operands (and 2^-50 of the angle, whose fraction of a turn comes from 64-bit
+// floating point): where that could change a code or a scale (its lower and upper ends
+// round differently) the warp works the rotation out in 64 bits.
+// AXES: pairs turn by the position of their own axis.
+constexpr float kOff = 1e-6f;
+
+template <int D, bool FOUR, bool AXES>
+__global__ void __launch_bounds__(kRopeThreads, FOUR ? 2 : 3)
+k_rope_append(const __grid_constant__ RopeArgs a, int parts)
 {
     constexpr int UNITS = D / 16, HS = 32 / UNITS, OWN = 8 / HS;
     const int lane = threadIdx.x & 31, u = lane % UNITS, sub = lane / UNITS;
@@ -101,9 +180,18 @@ k_rope_append(const RopeArgs a, int parts)
     }
     // the fractions of a turn per position of the pairs whose angles this lane works out
     unsigned long long frac[OWN];
+    const int32_t *place[AXES ? OWN : 1];  // and where those pairs' positions are
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
         frac[o] = 0;
+        if constexpr (AXES) {
+            place[o] = a.positions;
+            if (turned) {
+                const int axis = a.axes[8 * u + sub * OWN + o];
+                if ((uint32_t)axis < (uint32_t)a.n_axes) place[o] += (int64_t)axis * a.n_tokens;
+                else atomicOr(a.status, MKV_DEV_BAD_AXIS);
+            }
+        }
         if (turned) {
             double turns = (double)a.inv_freq[8 * u + sub * OWN + o] * 0.15915494309189533577;  // 1 / (2 pi)
             turns -= floor(turns);
@@ -114,6 +202,7 @@ k_rope_append(const RopeArgs a, int parts)
     for (int64_t item = (int64_t)blockIdx.x * kRopeWarps + (threadIdx.x >> 5); item < items; item += warps) {
         const int t = (int)(item / parts), part = (int)(item - (int64_t)t * parts);
         float2 cs[8];
+        float off = kOff;
         int b = -1, left = 0;
         for (int g0 = part; g0 < groups; g0 += parts * kRopeBatch) {
             uint4 xr[kRopeBatch], yr[kRopeBatch];
@@ -143,7 +232,9 @@ k_rope_append(const RopeArgs a, int parts)
                 }
             }
             if (g0 == part) {  // the token's row and angles, while its data is on the way
-                const int position = a.positions[t];
+                int position[AXES ? OWN : 1];
+#pragma unroll
+                for (int o = 0; o < (AXES ? OWN : 1); ++o) position[o] = AXES ? place[o][t] : a.positions[t];
                 b = row_of_token(a.q_start, a.batch, t);
                 if (b < 0) break;  // a token of no row
                 const int lo = a.q_start[b], hi = a.q_start[b + 1];
@@ -152,10 +243,19 @@ k_rope_append(const RopeArgs a, int parts)
                 float2 mine[OWN];
 #pragma unroll
                 for (int o = 0; o < OWN; ++o) {
-                    const long long phase = (long long)(frac[o] * (unsigned long long)(long long)position);
+                    const long long phase = (long long)(frac[o] * (unsigned long long)(long long)position[AXES ? o : 0]);
                     float sn, cn;
                     sincospif((float)phase * 1.0842021724855044e-19f, &sn, &cn);  // 2 x phase / 2^64 half turns
                     mine[o] = make_float2(cn * a.factor, sn * a.factor);
+                }
+                if constexpr (FOUR) {  // the largest angle of the lane's pairs
+                    float angle = 0.f;
+#pragma unroll
+                    for (int o = 0; o < OWN; ++o)
+                        if (turned) angle = fmaxf(angle, fabsf(a.inv_freq[8 * u + sub * OWN + o] * (float)position[AXES ? o : 0]));
+#pragma unroll
+                    for (int y = UNITS; y < 32; y <<= 1) angle = fmaxf(angle, __shfl_xor_sync(kFull, angle, y));
+                    off = kOff + angle * 8.9e-16f;
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -194,10 +294,24 @@ k_rope_append(const RopeArgs a, int parts)
                 int kind, head, d0, d1;
                 head_of(g0 + c * parts, kind, head);
                 dims(kind, d0, d1);
-                if (head < 0 || (kind > 0 && id[c] < 0)) continue;
+                // (rows that become codes: all lanes of the warp, which may have to work together)
+                if constexpr (FOUR) {
+                    if (!__any_sync(kFull, head >= 0 && (kind == 0 || id[c] >= 0))) continue;
+                    if (head < 0 || (kind > 0 && id[c] < 0)) xr[c] = yr[c] = make_uint4(0u, 0u, 0u, 0u);
+                } else if (head < 0 || (kind > 0 && id[c] < 0)) {
+                    continue;
+                }
                 float x[8], y[8];
                 bf16x8_to_f32(xr[c], x);
                 bf16x8_to_f32(yr[c], y);
+                float size = 0.f;  // of the lane's operands: pairs' |x| + |y| at most
+                if constexpr (FOUR) {
+                    if (turned && kind == 1) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) size = fmaxf(size, fabsf(x[e]) + fabsf(y[e]));
+                        if (a.layout == MKV_ROPE_INTERLEAVED) size *= 2.f;  // (pairs lie within x and within y)
+                    }
+                }
                 if (turned && kind < 2) {
                     if (a.layout == MKV_ROPE_HALF) {
 #pragma unroll
@@ -221,9 +335,73 @@ k_rope_append(const RopeArgs a, int parts)
                     }
                 }
                 if (kind == 0) {
+                    if (FOUR && head < 0) continue;
                     uint8_t *dst = a.Q_out + 2 * ((int64_t)t * a.q_heads + head) * D;
                     st_v4(dst + 2 * d0, pack8(x));
                     st_v4(dst + 2 * d1, pack8(y));
+                    continue;
+                }
+                if constexpr (FOUR) {
+                    const float inv = kind == 1 ? a.k_inv : a.v_inv, inv6 = kind == 1 ? a.k_inv6 : a.v_inv6;
+                    const int halves = a.rot_dim / 16;
+                    const bool split = kind == 1 && turned && a.layout == MKV_ROPE_HALF;  // two eights, two groups
+                    uint32_t sx, sy, wx, wy;
+                    for (int exact = 0;; ++exact) {
+                        const float mx = largest8(x), my = largest8(y);
+                        float gx = max_nan(mx, my), gy = gx, ex = exact ? 0.f : size * fabsf(a.factor) * off, ey = ex;
+                        if (kind == 1 && a.layout == MKV_ROPE_HALF) {
+                            const int ox = other_eight(u, halves), oy = other_eight(halves + u, halves), at = lane - u;
+                            const int lx = at + (ox & 31) % UNITS, ly = at + (oy & 31) % UNITS;
+                            const float xx = __shfl_sync(kFull, mx, lx), xy = __shfl_sync(kFull, my, lx);
+                            const float yx = __shfl_sync(kFull, mx, ly), yy = __shfl_sync(kFull, my, ly);
+                            const float fx = __shfl_sync(kFull, ex, lx), fy = __shfl_sync(kFull, ex, ly);
+                            if (split) {
+                                gx = max_nan(mx, ox < 32 ? xx : xy);
+                                gy = max_nan(my, oy < 32 ? yx : yy);
+                                ey = fmaxf(ex, fy);
+                                ex = fmaxf(ex, fx);
+                            }
+                        }
+                        // (2^-21: the roundings of the product)
+                        const uint32_t ends_x = f32x2_to_e4m3(max_nan(gx - ex, 0.f) * inv6, (gx + ex) * inv6);
+                        const uint32_t ends_y = f32x2_to_e4m3(max_nan(gy - ey, 0.f) * inv6, (gy + ey) * inv6);
+                        sx = ends_x & 0xFFu;
+                        sy = ends_y & 0xFFu;
+                        const float rx = code_factor(sx, inv), ry = code_factor(sy, inv);
+                        if (kind == 2 || exact) {
+                            wx = codes8(x, rx);
+                            wy = codes8(y, ry);
+                            break;
+                        }
+                        bool unsure = sx != ends_x >> 8 || sy != ends_y >> 8;
+                        wx = codes8_within(x, rx, ex, unsure);
+                        wy = codes8_within(y, ry, ey, unsure);
+                        if (!__any_sync(kFull, turned && unsure)) {
+                            if (!turned) {
+                                wx = codes8(x, rx);
+                                wy = codes8(y, ry);
+                            }
+                            break;
+                        }
+                        if (turned) {
+                            float p[8], q[8];
+                            rotate_exactly<AXES>(a, t, u, xr[c], yr[c], p, q);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                x[e] = p[e];
+                                y[e] = q[e];
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (head < 0 || id[c] < 0) continue;
+                    uint8_t *page = (kind == 1 ? a.k : a.v) + (int64_t)id[c] * (D * 9 / 16 << a.page_shift);
+                    const int row = slot[c] & (a.page_size - 1);
+                    *reinterpret_cast<uint32_t *>(page + row * (D / 2) + d0 / 2) = wx;
+                    *reinterpret_cast<uint32_t *>(page + row * (D / 2) + d1 / 2) = wy;
+                    uint8_t *scales = page + (D / 2 << a.page_shift) + row * (D / 16);
+                    if (d0 % 16 == 0) scales[d0 / 16] = (uint8_t)sx;
+                    if (d1 % 16 == 0) scales[d1 / 16] = (uint8_t)sy;
                     continue;
                 }
                 const int64_t row = ((int64_t)id[c] << a.page_shift) + (slot[c] & (a.page_size - 1));
@@ -241,14 +419,22 @@ k_rope_append(const RopeArgs a, int parts)
     }
 }
 
+template <bool FOUR, bool AXES>
+const void *rope_fn(int head_dim)
+{
+    return head_dim == 64    ? (const void *)k_rope_append<64, FOUR, AXES>
+           : head_dim == 128 ? (const void *)k_rope_append<128, FOUR, AXES>
+           : head_dim == 256 ? (const void *)k_rope_append<256, FOUR, AXES>
+                             : nullptr;
+}
+
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t st)
 {
-    const void *fn = a.head_dim == 64    ? (const void *)k_rope_append<64>
-                     : a.head_dim == 128 ? (const void *)k_rope_append<128>
-                     : a.head_dim == 256 ? (const void *)k_rope_append<256>
-                                         : nullptr;
+    const bool axes = a.n_axes > 0;
+    const void *fn = a.es ? (axes ? rope_fn<false, true>(a.head_dim) : rope_fn<false, false>(a.head_dim))
+                          : (axes ? rope_fn<true, true>(a.head_dim) : rope_fn<true, false>(a.head_dim));
     if (!fn) return cudaErrorInvalidValue;
     // a warp per token; with few tokens their heads are shared out
     int parts = 1;

@@ -97,17 +97,20 @@ typedef enum {
 #define MKV_DEV_BAD_PARENT 0x40u  /* a parent outside [-1, batch), or an n_new below 0 or beyond the list's capacity */
 #define MKV_DEV_BAD_TOKENS 0x80u  /* q_start decreases, leaves [0, n_tokens], or gives a row more than max_q tokens */
 #define MKV_DEV_BAD_INDEX 0x100u  /* a kept index outside its list (or contiguous head) */
+#define MKV_DEV_BAD_AXIS 0x200u   /* an axis outside [0, n_axes) (mkv_rope_append_axes) */
 
 typedef enum {
     MKV_MODE_L2 = 0,     /* s_t = |k_t - c| (ManifoldKV, abstract) */
     MKV_MODE_COSINE = 1  /* s_t = 1 - cos(k_t, c); 1 when |k_t||c| = 0 (the cosine baseline, abstract) */
 } mkv_mode;
 
-/* Element type of a cache. */
+/* Element type of a cache (2 and 3 are no types). */
 typedef enum {
     MKV_DTYPE_BF16 = 0,     /* bfloat16 */
-    MKV_DTYPE_FP8_E4M3 = 1  /* OCP 8-bit floating point E4M3 (torch.float8_e4m3fn): the method runs on the
+    MKV_DTYPE_FP8_E4M3 = 1, /* OCP 8-bit floating point E4M3 (torch.float8_e4m3fn): the method runs on the
                                decoded values, which fp32 holds exactly; the NaN codes are outside the contract */
+    MKV_DTYPE_E2M1 = 4      /* paged caches only: E2M1 codes of 4 bits with an E4M3 scale per 16 dims (see Paged
+                               caches); every other call refuses it (MKV_ERR_UNSUPPORTED) */
 } mkv_dtype;
 
 /* Shape of a cache. dtype: an mkv_dtype (0 = bf16). seq_lens: device int32
@@ -540,6 +543,22 @@ mkv_status mkv_inject_stalled_windows(const void *K, const void *V, mkv_shape sh
  * parent NULL may also run in place (table and lens both those of the input).
  * Table entries past a list's pages are not written.
  *
+ * 4-bit pages (MKV_DTYPE_E2M1). A page is page_size * head_dim / 2 bytes of
+ * codes, token after token, two dims to a byte (the even one in the lower
+ * half), then page_size * head_dim / 16 bytes of scales, token after token, an
+ * E4M3 number per 16 dims: page_size * head_dim * 9 / 16 bytes, and the pool's
+ * pages lie one after another. A code is a sign bit over the values 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6; an element is code * scale (exact in 16 bits) times k_scale
+ * or v_scale. A group x of 16 dims is written as
+ *     s = e4m3(max|x| * (1 / (6 k_scale))),  codes e2m1(x * ((1 / k_scale) / s)),
+ * every step one fp32 operation, (1 / (6 k_scale)) and (1 / k_scale) rounded
+ * once from 64 bits, both roundings to nearest with ties to the even code,
+ * saturated at 448 and 6; all codes are 0 where s is 0, and zero has no sign.
+ * Rotated keys are the exact ones (angles as products of 64-bit numbers) rounded
+ * once to fp32 before that: the same input gives the same bytes, next to any
+ * border. NaN among the 16 makes the group's scale NaN. Scales are positive,
+ * 512 times their reciprocals finite in fp32.
+ *
  * Contents. Tokens in [0, len) of a list are finite; anything may stand in
  * the rows behind them. The workspace of all calls on a paged cache is
  * mkv_page_workspace_size() bytes (attention: mkv_attention_workspace_size()),
@@ -552,7 +571,7 @@ typedef struct {
     int32_t page_size;
     int32_t head_dim; /* 64, 128 or 256 */
     int32_t dtype;    /* an mkv_dtype */
-    void *k_pages;    /* [n_pages, page_size, head_dim], 16-byte aligned */
+    void *k_pages;    /* [n_pages, page_size, head_dim] (4-bit pages: head_dim * 9 / 16 bytes a token), 16-byte aligned */
     void *v_pages;
 } mkv_page_pool;
 
@@ -574,8 +593,9 @@ typedef struct {
     const int32_t *q_start;
 } mkv_new_tokens;
 
-/* Bytes of workspace for mkv_page_update, mkv_page_compact and
- * mkv_rope_append (0 on a bad shape; pointers are not looked at). */
+/* Bytes of workspace for mkv_page_update, mkv_page_compact, mkv_page_quantize,
+ * mkv_rope_append and mkv_rope_append_axes (0 on a bad shape; pointers are not
+ * looked at). */
 size_t mkv_page_workspace_size(mkv_page_pool pool, mkv_page_lists lists);
 
 /* Page lists after a step (no counterpart on the pages this library follows;
@@ -597,7 +617,8 @@ mkv_status mkv_page_update(mkv_page_pool pool, mkv_page_lists in, const int32_t 
  * cache): list h of `out` has kept[h] tokens in new pages, token i a bit copy
  * of token idx[h * idx_stride + i] of list h of `in` -- or, with K and V
  * given, of the contiguous cache [batch, heads, t_max, head_dim] of the
- * pool's type (seq_lens: device int32 [batch] or NULL for t_max). idx NULL
+ * pool's type (seq_lens: device int32 [batch] or NULL for t_max; for 4-bit
+ * pools, which have no such cache, MKV_ERR_UNSUPPORTED). idx NULL
  * copies tokens 0 .. kept[h]-1 (idx_stride is then not looked at). idx and
  * kept are as mkv_compact and mkv_compress write them; any order of indices
  * is allowed, also the same one twice. Every page that the lists of `in` held
@@ -608,6 +629,16 @@ mkv_status mkv_page_compact(mkv_page_pool pool, mkv_page_lists in, const int32_t
                             int32_t idx_stride, const int32_t *kept, const void *K, const void *V, int32_t t_max,
                             const int32_t *seq_lens, mkv_page_lists out, int32_t *refs_out, void *workspace,
                             size_t workspace_bytes, mkv_stream_t stream);
+
+/* mkv_page_compact from a contiguous bf16 cache into pages of 8 or 4 bits: K
+ * and V [batch, heads, t_max, head_dim] of bf16 (neither may be NULL), the kept
+ * rows rounded as mkv_rope_append writes them (E4M3: value * (1 / scale),
+ * saturated at 448, the reciprocals finite; 4-bit pages: see there). Everything else is as for mkv_page_compact; a
+ * bf16 pool is MKV_ERR_UNSUPPORTED (mkv_page_compact copies into it). */
+mkv_status mkv_page_quantize(mkv_page_pool pool, mkv_page_lists in, const int32_t *refs, const int32_t *idx,
+                             int32_t idx_stride, const int32_t *kept, const void *K, const void *V, int32_t t_max,
+                             const int32_t *seq_lens, float k_scale, float v_scale, mkv_page_lists out,
+                             int32_t *refs_out, void *workspace, size_t workspace_bytes, mkv_stream_t stream);
 
 typedef enum {
     MKV_ROPE_HALF = 0,       /* pairs (i, i + rot_dim / 2) */
@@ -627,7 +658,8 @@ typedef enum {
  * head_dim], contiguous; may be Q itself when Q is contiguous. E4M3 pools
  * store round(value * (1 / k_scale)) (keys) and round(value * (1 / v_scale))
  * (values), saturated at 448, the reciprocals in fp32 (they must be finite);
- * for bf16 pools the scales must be 1. A token whose list or page is invalid
+ * 4-bit pages are written by their own rule (above); for bf16 pools the scales
+ * must be 1. A token whose list or page is invalid
  * is not written into it (MKV_DEV_BAD_SEQ_LEN when the list is shorter than the
  * row's new tokens or longer than its capacity, MKV_DEV_BAD_PAGE), nor is a
  * token of a row whose range leaves [0, n_tokens]; its query is written all
@@ -640,6 +672,26 @@ mkv_status mkv_rope_append(const void *Q, int64_t q_stride, const void *K, int64
                            int32_t rot_dim, mkv_rope_layout layout, float factor, void *Q_out, mkv_page_pool pool,
                            mkv_page_lists lists, float k_scale, float v_scale, void *workspace, size_t workspace_bytes,
                            mkv_stream_t stream);
+
+/* mkv_rope_append with positions on several axes (time, row, column, ... of
+ * image and video patches; text has the same place on all): pair i turns by
+ * positions[axes[i]][t] * inv_freq[i]. positions: device int32 [n_axes,
+ * n_tokens], 0 and up; axes: device int32 [rot_dim / 2] (mkv_rope_axes);
+ * n_axes in [1, 8], else MKV_ERR_INVALID_ARG. An axis outside [0, n_axes) sets
+ * MKV_DEV_BAD_AXIS and counts as 0. Everything else is as for mkv_rope_append,
+ * whose results are those of one axis. */
+mkv_status mkv_rope_append_axes(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V,
+                                int64_t v_stride, mkv_new_tokens tokens, const int32_t *positions, int32_t n_axes,
+                                const int32_t *axes, const float *inv_freq, int32_t rot_dim, mkv_rope_layout layout,
+                                float factor, void *Q_out, mkv_page_pool pool, mkv_page_lists lists, float k_scale,
+                                float v_scale, void *workspace, size_t workspace_bytes, mkv_stream_t stream);
+
+/* The axis of each pair (host helper): axis a turns sections[a] pairs, which
+ * add up to rot_dim / 2. dealt 0: in runs, axis 0's pairs first; dealt 1: pairs
+ * go to the axes in turn, past those that have all of theirs. Writes
+ * axes[rot_dim / 2]; returns 0, or -1 on a bad argument (rot_dim not a positive
+ * multiple of 16, n_axes outside [1, 8], a negative section, another sum, NULL). */
+int32_t mkv_rope_axes(int32_t rot_dim, int32_t n_axes, const int32_t *sections, int32_t dealt, int32_t *axes);
 
 typedef enum {
     MKV_ROPE_PLAIN = 0,   /* f_i = theta^(-2i / rot_dim) */
@@ -688,9 +740,9 @@ size_t mkv_attention_workspace_size(mkv_page_pool pool, mkv_page_lists lists, mk
  * keys are counted in 32 bits: batch * heads * ceil(max_q * (q_heads / heads) /
  * 16) * (max_len / 64 + 2) beyond 2^31 may be MKV_ERR_UNSUPPORTED.
  * Scores, sums and accumulators are fp32; the softmax weights are rounded to
- * 16 bits for the product with the values (bf16; fp16 next to E4M3 values, where
- * a weight below 2^-32 of its row's largest counts as 0). Next to E4M3 keys a
- * query row is fp16 times a power of two: elements below 2^-14 of its largest are
+ * 16 bits for the product with the values (bf16; fp16 next to E4M3 and 4-bit
+ * values, where a weight below 2^-32 of its row's largest counts as 0). Next to
+ * E4M3 and 4-bit keys a query row is fp16 times a power of two: elements below 2^-14 of its largest are
  * off by at most 2^-25 of that. Scores are to stay below 2^28 in magnitude: fp32
  * steps are of 16 and more there. */
 mkv_status mkv_paged_attention(const void *Q, int64_t q_stride, mkv_new_tokens tokens, int32_t max_q,
