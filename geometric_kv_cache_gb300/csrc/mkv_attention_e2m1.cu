@@ -33,7 +33,8 @@ namespace {
 
 using namespace dev;
 
-constexpr int kKeys = 16;  // keys of a warp's step: they lie in one page
+constexpr int kKeys = 16;  // keys of an MMA's rows: they lie in one page
+constexpr float kNothing = -3e38f;  // the reference point of a row that has seen nothing (finite: no case of its own)
 constexpr LineRule kLine = {1, 3, 3};  // see mkv_line.h
 
 // Shape of one instantiation: head dims, rows of a tile.
@@ -41,10 +42,12 @@ template <int D, int R>
 struct Attend4 {
     static constexpr int WARPS = D == 256 ? (R == 8 ? 12 : 8) : D == 128 && R == 16 ? 12 : 16;
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int KEYS = WARPS * kKeys;     // keys per block of the CTA
+    static constexpr int NK = D == 256 ? 1 : 2;    // groups of 16 keys of a warp's step
+    static constexpr int KT = NK * kKeys;          // its keys
+    static constexpr int KEYS = WARPS * KT;        // keys per block of the CTA
     static constexpr int CB = D / 2, SB = D / 16;  // bytes of a row's codes and scales
-    static constexpr int CODES = kKeys * CB, SCALES = kKeys * SB;
-    static constexpr int HALF = CODES + SCALES, STAGE = 2 * HALF;
+    static constexpr int CODES = kKeys * CB, SCALES = kKeys * SB;  // ... of 16 keys
+    static constexpr int HALF = CODES + SCALES, GROUP = 2 * HALF, STAGE = NK * GROUP;
     static constexpr int STAGES = 220 * 1024 / (WARPS * STAGE) < 6 ? 220 * 1024 / (WARPS * STAGE) : 6;
     static constexpr int RING = STAGES * STAGE;    // per warp
     static constexpr int OS = D + 4;               // floats between a result's rows
@@ -143,8 +146,15 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
     auto k_dim = [&](int x) -> int {
         return D == 64 ? 16 * tq + 8 * x : D == 128 ? 32 * tq + 8 * x : 128 * (x / 4) + 32 * tq + 8 * (x % 4);
     };
-    const int page_mask = a.page_size - 1;
-    const int64_t page_bytes = (int64_t)(A::CB + A::SB) << a.page_shift;
+    // What this lane copies of every step: chunks of one group's codes, and one chunk of its keys' or values' scales.
+    // Groups of 16 rows of the pool are numbered: number x has its codes at x CODES + (its page) PS SB, its scales at
+    // x SCALES + (its page + 1) PS CB, with PS rows in a page.
+    constexpr int LG = 32 / A::NK, PER_LANE = A::CODES / 16 / LG, SC = A::SCALES / 16;
+    const int own = lane / LG, chunk0 = lane % LG, sc_own = lane / (2 * SC), sc_kv = lane / SC % 2, sc_chunk = lane % SC;
+    const uint8_t *k_lane = a.k + chunk0 * 16, *v_lane = a.v + chunk0 * 16;
+    const uint8_t *sc_lane = (sc_kv ? a.v : a.k) + (A::CB << a.page_shift) + sc_chunk * 16;
+    const uint32_t sc_dst = sc_own * A::GROUP + sc_kv * A::HALF + A::CODES + sc_chunk * 16;
+    const int group_shift = a.page_shift - 4;  // groups of a page
     while (w.next<A::KEYS>(a, R)) {
         const Tile &t = w.t;
         const int first = w.from(), last = w.to();
@@ -190,44 +200,43 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
         const int p_lo = t.L - t.n + a.by_group(t.row0), p_hi = t.L - t.n + a.by_group(t.row0 + t.rows - 1);
 
         const uint32_t ring = saddr(smem) + warp * A::RING;
-        auto key0 = [&](int blk) -> int { return block_key<A::KEYS>(t, blk) + warp * kKeys; };
-        // the page entry of a block's keys, -1 where no row sees any of them
-        auto lookup = [&](int blk) -> int {
-            if (blk >= last) return -1;
-            const int s = key0(blk);
-            if (s >= t.end || (a.window > 0 && s + kKeys - 1 <= p_lo - a.window && s >= a.sinks)) return -1;
+        auto key0 = [&](int blk) -> int { return block_key<A::KEYS>(t, blk) + warp * A::KT; };
+        // Lane y: the group that it numbers, y groups on from block blk0 -- its number in the pool and, above bit 26, how
+        // many of its keys there are: none where no row sees any of them, or where the page is outside the pool.
+        auto lookup = [&](int blk0) -> uint32_t {
+            const int blk = blk0 + lane / A::NK;
+            if (blk >= last) return 0u;
+            const int s = key0(blk) + lane % A::NK * kKeys;
+            if (s >= t.end || (a.window > 0 && s + kKeys - 1 <= p_lo - a.window && s >= a.sinks)) return 0u;
             const int id = table[s >> a.page_shift];
-            if ((uint32_t)id < (uint32_t)a.n_pages) return id;
-            if (lane == 0) atomicOr(a.status, MKV_DEV_BAD_PAGE);
-            return -1;
+            if ((uint32_t)id >= (uint32_t)a.n_pages) {
+                atomicOr(a.status, MKV_DEV_BAD_PAGE);
+                return 0u;
+            }
+            return (uint32_t)((id << group_shift) + ((s & (a.page_size - 1)) >> 4)) | (uint32_t)min(kKeys, t.end - s) << 26;
         };
-        // Scales that are not there (keys behind the list's end, a bad page, keys
-        // that no row sees) arrive as zeros, which makes their elements zeros:
-        // nothing else has to be told apart, codes are finite whatever they are.
-        auto issue = [&](int stage, int blk, int id) {
-            if (blk < last) {
-                const int s = key0(blk);
-                const uint32_t dst = ring + stage * A::STAGE;
-                const int64_t page = max(id, 0) * page_bytes;
-                const int64_t codes = page + (s & page_mask) * A::CB;
-                if (id >= 0) {
+        // The copies of a step whose groups are `at` lanes on. Scales of keys that
+        // are not there arrive as zeros, which makes their elements zeros: nothing
+        // else has to be told apart, codes are finite whatever they are.
+        auto issue = [&](int stage, uint32_t groups, int at) {
+            const uint32_t dst = ring + stage * A::STAGE;
+            const uint32_t mine = __shfl_sync(kFull, groups, at + own), sc = __shfl_sync(kFull, groups, (at + sc_own) & 31);
+            const uint32_t x = mine & 0x3FFFFFFu, y = sc & 0x3FFFFFFu;
+            if (mine >> 26) {
+                const uint64_t off = (uint64_t)x * A::CODES + (uint64_t)(x >> group_shift) * (uint32_t)(A::SB << a.page_shift);
+                const uint8_t *ks = k_lane + off, *vs = v_lane + off;
+                const uint32_t to = dst + own * A::GROUP;
 #pragma unroll
-                    for (int o = lane; o < A::CODES / 16; o += 32) {
-                        const int r = o / (D / 32), c = o % (D / 32);
-                        cp16(dst + k_at<D>(r, c), a.k + codes + o * 16, 16);
-                        cp16(dst + A::HALF + v_at<D>(r, c), a.v + codes + o * 16, 16);
-                    }
-                }
-                const int64_t scales = page + (A::CB << a.page_shift) + (s & page_mask) * A::SB;
-                const int there = id < 0 ? 0 : min(kKeys, t.end - s) * A::SB;
-                // chunks of K's scales, then of V's
-                if (lane < 2 * (A::SCALES / 16)) {
-                    const int kv = lane >= A::SCALES / 16, c = lane - kv * (A::SCALES / 16);
-                    cp16(dst + kv * A::HALF + A::CODES + c * 16, (kv ? a.v : a.k) + scales + c * 16,
-                         min(max(there - 16 * c, 0), 16));
+                for (int i = 0; i < PER_LANE; ++i) {
+                    const int o = chunk0 + LG * i, r = o / (D / 32), c = o % (D / 32);
+                    cp16(to + k_at<D>(r, c), ks + LG * 16 * i, 16);
+                    cp16(to + A::HALF + v_at<D>(r, c), vs + LG * 16 * i, 16);
                 }
             }
-            cp_commit();
+            if (sc_own < A::NK)
+                cp16(dst + sc_dst,
+                     sc_lane + ((uint64_t)y * A::SCALES + (uint64_t)(y >> group_shift) * (uint32_t)(A::CB << a.page_shift)),
+                     min(max((int)(sc >> 26) * A::SB - 16 * sc_chunk, 0), 16));
         };
 
         float o[D / 16][NR][4];
@@ -238,99 +247,121 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
         float m[NR][2], l[NR][2];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            m[n][0] = m[n][1] = -CUDART_INF_F;
+            m[n][0] = m[n][1] = kNothing;
             l[n][0] = l[n][1] = 0.f;
         }
 
-        int id = lookup(first);
+        // groups are looked up for STEPS steps at once, the next ones while these are copied
+        constexpr int STEPS = 32 / A::NK;
+        uint32_t groups = lookup(first), next = lookup(first + STEPS);
+        int at = 0;  // the next step to copy: its place among `groups`
+        auto copy_step = [&](int stage) {
+            issue(stage, groups, at);
+            cp_commit();
+            at += A::NK;
+        };
 #pragma unroll
-        for (int s = 0; s < A::STAGES - 1; ++s) {
-            const int next = lookup(first + s + 1);
-            issue(s, first + s, id);
-            id = next;
-        }
+        for (int s = 0; s < A::STAGES - 1; ++s) copy_step(s);  // (past the last block nothing is copied but zeros)
         for (int blk = first, it = 0; blk < last; ++blk, it = it + 1 == A::STAGES ? 0 : it + 1) {
-            {
-                const int ahead = blk + A::STAGES - 1, next = lookup(ahead + 1);
-                issue(it == 0 ? A::STAGES - 1 : it - 1, ahead, id);
-                id = next;
+            copy_step(it == 0 ? A::STAGES - 1 : it - 1);
+            if (at == 32) {
+                at = 0;
+                groups = next;
+                next = lookup(blk + A::STAGES + STEPS);
             }
             cp_wait<A::STAGES - 1>();
             __syncwarp();
-            const uint32_t kb = ring + it * A::STAGE, vb = kb + A::HALF, ks = kb + A::CODES, vs = vb + A::CODES;
+            const uint32_t stage = ring + it * A::STAGE;
 
-            // scores: rows of the MMA are the keys gr and gr + 8
-            float s[NR][4];
-#pragma unroll
-            for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            // scores: rows of an MMA are the keys gr and gr + 8 of a group
+            float s[A::NK][NR][4];
             constexpr int WB = KW < 4 ? KW : 4;  // words of a load
 #pragma unroll
-            for (int x0 = 0; x0 < KW; x0 += WB) {
-                uint32_t kw[2][WB], sk[2][2];
+            for (int g = 0; g < A::NK; ++g) {
+                const uint32_t kb = stage + g * A::GROUP, ks = kb + A::CODES;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int key = gr + 8 * h;
-                    if constexpr (D == 64) {
-                        lds_words<WB>(kb + k_at<D>(key, tq >> 1) + 8 * (tq & 1), kw[h]);
-                        const uint32_t f = e4m3x2_to_f16x2(lds_u8(ks + key * A::SB + tq));
-                        sk[h][0] = sk[h][1] = __byte_perm(f, 0, 0x1010);
-                    } else {
-                        lds_words<WB>(kb + k_at<D>(key, tq + x0), kw[h]);
-                        const uint32_t f = e4m3x2_to_f16x2(lds_u16(ks + key * A::SB + 2 * (tq + x0)));
-                        sk[h][0] = __byte_perm(f, 0, 0x1010);
-                        sk[h][1] = __byte_perm(f, 0, 0x3232);
+                for (int n = 0; n < NR; ++n) s[g][n][0] = s[g][n][1] = s[g][n][2] = s[g][n][3] = 0.f;
+#pragma unroll
+                for (int x0 = 0; x0 < KW; x0 += WB) {
+                    uint32_t kw[2][WB], sk[2][2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = gr + 8 * h;
+                        if constexpr (D == 64) {
+                            lds_words<WB>(kb + k_at<D>(key, tq >> 1) + 8 * (tq & 1), kw[h]);
+                            const uint32_t f = e4m3x2_to_f16x2(lds_u8(ks + key * A::SB + tq));
+                            sk[h][0] = sk[h][1] = __byte_perm(f, 0, 0x1010);
+                        } else {
+                            lds_words<WB>(kb + k_at<D>(key, tq + x0), kw[h]);
+                            const uint32_t f = e4m3x2_to_f16x2(lds_u16(ks + key * A::SB + 2 * (tq + x0)));
+                            sk[h][0] = __byte_perm(f, 0, 0x1010);
+                            sk[h][1] = __byte_perm(f, 0, 0x3232);
+                        }
                     }
-                }
 #pragma unroll
-                for (int x = 0; x < WB; ++x) {
-                    uint32_t f[2][4];
-                    e2m1x8_to_f16(kw[0][x], f[0]);
-                    e2m1x8_to_f16(kw[1][x], f[1]);
+                    for (int x = 0; x < WB; ++x) {
+                        uint32_t f[2][4];
+                        e2m1x8_to_f16(kw[0][x], f[0]);
+                        e2m1x8_to_f16(kw[1][x], f[1]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t k[4] = {mul_f16x2(f[0][2 * e], sk[0][x >> 1]), mul_f16x2(f[1][2 * e], sk[1][x >> 1]),
-                                               mul_f16x2(f[0][2 * e + 1], sk[0][x >> 1]),
-                                               mul_f16x2(f[1][2 * e + 1], sk[1][x >> 1])};
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t k[4] = {mul_f16x2(f[0][2 * e], sk[0][x >> 1]), mul_f16x2(f[1][2 * e], sk[1][x >> 1]),
+                                                   mul_f16x2(f[0][2 * e + 1], sk[0][x >> 1]),
+                                                   mul_f16x2(f[1][2 * e + 1], sk[1][x >> 1])};
 #pragma unroll
-                        for (int n = 0; n < NR; ++n) {
-                            const uint32_t(&b)[2] = q[n][2 * (x0 + x) + e];
-                            mma_f16(s[n], k, b[0], b[1]);
+                            for (int n = 0; n < NR; ++n) {
+                                const uint32_t(&b)[2] = q[n][2 * (x0 + x) + e];
+                                mma_f16(s[g][n], k, b[0], b[1]);
+                            }
                         }
                     }
                 }
             }
 
-            // mask, reference point, weights
-            const int k0 = key0(blk), k1 = k0 + kKeys - 1;
+            // the scores above the rows' reference points (s c - m), masked; weights
+            const int k0 = key0(blk), k1 = k0 + A::KT - 1;
             const bool whole = k1 <= p_lo && (a.window <= 0 || k0 > p_hi - a.window || k1 < a.sinks);
-            bool grow = false;
+            float d[A::NK][NR][4], top = -CUDART_INF_F;
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+            for (int g = 0; g < A::NK; ++g)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = s[n][e] * sc[n][e & 1];
-                    if (!whole) {
-                        const int key = k0 + gr + 8 * (e >> 1), at = p[n][e & 1];
-                        const bool seen = (key <= at) & ((a.window <= 0) | (key > at - a.window) | (key < a.sinks));
-                        x = seen ? x : -CUDART_INF_F;
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(s[g][n][e], sc[n][e & 1], -m[n][e & 1]);
+                        if (!whole) {
+                            const int key = k0 + g * kKeys + gr + 8 * (e >> 1), at = p[n][e & 1];
+                            const bool seen = (key <= at) & ((a.window <= 0) | (key > at - a.window) | (key < a.sinks));
+                            x = seen ? x : -CUDART_INF_F;
+                        }
+                        d[g][n][e] = x;
+                        top = fmaxf(top, x);
                     }
-                    s[n][e] = x;
-                    grow |= x - m[n][e & 1] > kLag<1>;
-                }
-            if (__any_sync(kFull, grow)) {
+            if (__any_sync(kFull, top > kLag<1>)) {
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float x = fmaxf(s[n][c], s[n][2 + c]);
+                        float x = -CUDART_INF_F;
+#pragma unroll
+                        for (int g = 0; g < A::NK; ++g)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (d[g][n][2 * h + c] > -CUDART_INF_F) x = fmaxf(x, s[g][n][2 * h + c] * sc[n][c]);
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
                         const float to = fmaxf(m[n][c], x - kBase<1>);
-                        // (a row that has seen nothing yet has l = 0 and O = 0: any finite factor)
-                        const float f = m[n][c] == -CUDART_INF_F ? 0.f : exp2_approx(m[n][c] - to);
+                        const float f = exp2_approx(m[n][c] - to);  // (0 for a row that had seen nothing)
                         m[n][c] = to;
                         l[n][c] *= f;
+#pragma unroll
+                        for (int g = 0; g < A::NK; ++g)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float &y = d[g][n][2 * h + c];
+                                if (y != -CUDART_INF_F) y = fmaf(s[g][n][2 * h + c], sc[n][c], -to);
+                            }
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             o[i][n][c] *= f;
@@ -338,57 +369,62 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
                         }
                     }
             }
-            uint32_t pw[NR][2];
+            uint32_t pw[A::NK][NR][2];
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                const float b0 = m[n][0] == -CUDART_INF_F ? 0.f : m[n][0], b1 = m[n][1] == -CUDART_INF_F ? 0.f : m[n][1];
-                const float e0 = exp2_approx(s[n][0] - b0), e1 = exp2_approx(s[n][1] - b1);
-                const float e2 = exp2_approx(s[n][2] - b0), e3 = exp2_approx(s[n][3] - b1);
-                l[n][0] += e0 + e2;
-                l[n][1] += e1 + e3;
-                pw[n][0] = transpose8(pack_weights<1>(e0, e1));
-                pw[n][1] = transpose8(pack_weights<1>(e2, e3));
-            }
-
-            // O^T: rows of the MMA are two of this lane's D / 8 consecutive dims, its contraction the 16 keys
-            uint32_t vw[4][VW], sv[2][2];  // keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
-            uint32_t sb[4];
+            for (int g = 0; g < A::NK; ++g)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const int key = 2 * tq + (y & 1) + 8 * (y >> 1);
-                if constexpr (D == 64) {
-                    lds_words<1>(vb + v_at<D>(key, gr >> 2) + 4 * (gr & 3), vw[y]);
-                    sb[y] = lds_u8(vs + key * A::SB + (gr >> 1));
-                } else if constexpr (D == 128) {
-                    lds_words<2>(vb + v_at<D>(key, gr >> 1) + 8 * (gr & 1), vw[y]);
-                    sb[y] = lds_u8(vs + key * A::SB + gr);
-                } else {
-                    lds_words<4>(vb + v_at<D>(key, gr), vw[y]);
-                    sb[y] = lds_u16(vs + key * A::SB + 2 * gr);
+                for (int n = 0; n < NR; ++n) {
+                    float e[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) e[x] = exp2_approx(d[g][n][x]);
+                    l[n][0] += e[0] + e[2];
+                    l[n][1] += e[1] + e[3];
+                    pw[g][n][0] = transpose8(pack_weights<1>(e[0], e[1]));
+                    pw[g][n][1] = transpose8(pack_weights<1>(e[2], e[3]));
                 }
-            }
+
+            // O^T: rows of an MMA are two of this lane's D / 8 consecutive dims, its contraction 16 keys
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sv[h][0] = e4m3x2_to_f16x2(__byte_perm(sb[2 * h], sb[2 * h + 1], 0x40));
-                sv[h][1] = D == 256 ? e4m3x2_to_f16x2(__byte_perm(sb[2 * h], sb[2 * h + 1], 0x51)) : sv[h][0];
-            }
+            for (int g = 0; g < A::NK; ++g) {
+                const uint32_t vb = stage + g * A::GROUP + A::HALF, vs = vb + A::CODES;
+                uint32_t vw[4][VW], sv[2][2], sb[4];  // keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
 #pragma unroll
-            for (int x = 0; x < VW; ++x) {
-                uint32_t ev[2][4], od[2][4];
+                for (int y = 0; y < 4; ++y) {
+                    const int key = 2 * tq + (y & 1) + 8 * (y >> 1);
+                    if constexpr (D == 64) {
+                        lds_words<1>(vb + v_at<D>(key, gr >> 2) + 4 * (gr & 3), vw[y]);
+                        sb[y] = lds_u8(vs + key * A::SB + (gr >> 1));
+                    } else if constexpr (D == 128) {
+                        lds_words<2>(vb + v_at<D>(key, gr >> 1) + 8 * (gr & 1), vw[y]);
+                        sb[y] = lds_u8(vs + key * A::SB + gr);
+                    } else {
+                        lds_words<4>(vb + v_at<D>(key, gr), vw[y]);
+                        sb[y] = lds_u16(vs + key * A::SB + 2 * gr);
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    // two keys' codes of the same dim side by side: even dims, odd dims
-                    const uint32_t u = vw[2 * h][x], v = vw[2 * h + 1][x];
-                    e2m1x8_to_f16((u & 0x0F0F0F0Fu) | (v << 4 & 0xF0F0F0F0u), ev[h]);
-                    e2m1x8_to_f16((u >> 4 & 0x0F0F0F0Fu) | (v & 0xF0F0F0F0u), od[h]);
+                    sv[h][0] = e4m3x2_to_f16x2(__byte_perm(sb[2 * h], sb[2 * h + 1], 0x40));
+                    sv[h][1] = D == 256 ? e4m3x2_to_f16x2(__byte_perm(sb[2 * h], sb[2 * h + 1], 0x51)) : sv[h][0];
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int hf = x * 8 + 2 * e >= 16 ? 1 : 0;  // the second scale of a lane's 32 dims
-                    const uint32_t f[4] = {mul_f16x2(ev[0][e], sv[0][hf]), mul_f16x2(od[0][e], sv[0][hf]),
-                                           mul_f16x2(ev[1][e], sv[1][hf]), mul_f16x2(od[1][e], sv[1][hf])};
+                for (int x = 0; x < VW; ++x) {
+                    uint32_t ev[2][4], od[2][4];
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) mma_f16(o[4 * x + e][n], f, pw[n][0], pw[n][1]);
+                    for (int h = 0; h < 2; ++h) {
+                        // two keys' codes of the same dim side by side: even dims, odd dims
+                        const uint32_t u = vw[2 * h][x], v = vw[2 * h + 1][x];
+                        e2m1x8_to_f16((u & 0x0F0F0F0Fu) | (v << 4 & 0xF0F0F0F0u), ev[h]);
+                        e2m1x8_to_f16((u >> 4 & 0x0F0F0F0Fu) | (v & 0xF0F0F0F0u), od[h]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int hf = x * 8 + 2 * e >= 16 ? 1 : 0;  // the second scale of a lane's 32 dims
+                        const uint32_t f[4] = {mul_f16x2(ev[0][e], sv[0][hf]), mul_f16x2(od[0][e], sv[0][hf]),
+                                               mul_f16x2(ev[1][e], sv[1][hf]), mul_f16x2(od[1][e], sv[1][hf])};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma_f16(o[4 * x + e][n], f, pw[g][n][0], pw[g][n][1]);
+                    }
                 }
             }
             __syncwarp();  // the stage is free for the next copies
