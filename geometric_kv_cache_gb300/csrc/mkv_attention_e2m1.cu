@@ -20,6 +20,7 @@
 // cut tiles joined by the CTA that comes last (mkv_attention.cuh).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -34,6 +35,7 @@ namespace {
 using namespace dev;
 
 constexpr int kKeys = 16;  // keys of an MMA's rows: they lie in one page
+constexpr float kTop = 32768.f;        // 2^kLag<1>
 constexpr float kNothing = -3e38f;  // the reference point of a row that has seen nothing (finite: no case of its own)
 constexpr LineRule kLine = {1, 3, 3};  // see mkv_line.h
 
@@ -58,7 +60,14 @@ struct Attend4 {
     static constexpr int VW = D / 64 ? D / 64 : 1; // ... V: 8 dims to a word
 };
 
-// 16 bytes to shared memory, of which the first n come from src, the others are zeros.
+// 16 bytes to shared memory, if `real`.
+__device__ __forceinline__ void cp16_if(bool real, uint32_t dst, const void *src)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p cp.async.cg.shared.global [%0], [%1], 16; }" ::"r"(dst), "l"(src),
+                 "r"((uint32_t)real)
+                 : "memory");
+}
+// 16 bytes, of which the first n come from src, the others are zeros.
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int n)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -153,15 +162,34 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
     const int own = lane / LG, chunk0 = lane % LG, sc_own = lane / (2 * SC), sc_kv = lane / SC % 2, sc_chunk = lane % SC;
     const uint8_t *k_lane = a.k + chunk0 * 16, *v_lane = a.v + chunk0 * 16;
     const uint8_t *sc_lane = (sc_kv ? a.v : a.k) + (A::CB << a.page_shift) + sc_chunk * 16;
-    const uint32_t sc_dst = sc_own * A::GROUP + sc_kv * A::HALF + A::CODES + sc_chunk * 16;
     const int group_shift = a.page_shift - 4;  // groups of a page
+    const uint32_t page_scales = A::SB << a.page_shift, page_codes = A::CB << a.page_shift;
+    // Offsets in a stage of what it copies, and of what it loads (a key's or value's words, its scales). A copy's
+    // further chunks follow at fixed distances, those of V from one of two places in turn; so do the keys of a load.
+    constexpr int STEP_ROWS = LG / (D / 32);
+    const uint32_t k_to = own * A::GROUP + k_at<D>(chunk0 / (D / 32), chunk0 % (D / 32));
+    const uint32_t sc_to = sc_own * A::GROUP + sc_kv * A::HALF + A::CODES + sc_chunk * 16;
+    uint32_t v_to[2], v_from[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v_to[i] = own * A::GROUP + A::HALF + v_at<D>(chunk0 / (D / 32) + STEP_ROWS * i, chunk0 % (D / 32)) - i * LG * 16;
+        v_from[i] = A::HALF + (D == 64    ? v_at<D>(2 * tq + i, gr >> 2) + 4 * (gr & 3)
+                               : D == 128 ? v_at<D>(2 * tq + i, gr >> 1) + 8 * (gr & 1)
+                                          : v_at<D>(2 * tq + i, gr));
+    }
+    const uint32_t k_from = D == 64 ? k_at<D>(gr, tq >> 1) + 8 * (tq & 1) : k_at<D>(gr, tq);
+    const uint32_t k_from2 = D == 256 ? k_at<D>(gr, tq + 4) : 0u;
+    const uint32_t ks_from = A::CODES + gr * A::SB + (D == 64 ? tq : 2 * tq);
+    const uint32_t vs_from = A::HALF + A::CODES + 2 * tq * A::SB + (D == 64 ? gr >> 1 : D == 128 ? gr : 2 * gr);
     while (w.next<A::KEYS>(a, R)) {
         const Tile &t = w.t;
         const int first = w.from(), last = w.to();
         const int32_t *table = a.table + ((int64_t)t.b * a.heads + t.j) * a.max_pages;
         const int qrow0 = a.q_start[t.b];
 
-        // queries: column gr of each column tile, this lane's dims, as fp16 with a power of two taken out
+        // queries: column gr of each column tile, this lane's dims, as fp16 with a power of two taken out. (They take
+        // the scale's sign, and a factor of zero becomes the smallest normal number: zero times a masked score's
+        // -inf would be NaN.)
         uint32_t q[NR][2 * KW][2];
         float sc[NR][2];  // of this lane's columns of scores, 2 tq and 2 tq + 1
         int p[NR][2];     // their places in the list
@@ -182,7 +210,7 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
             const int E = row_exponent(m);
-            const float down = down_by(E);
+            const float down = a.scale_log2 < 0.f ? -down_by(E) : down_by(E);
 #pragma unroll
             for (int x = 0; x < KW; ++x) {
                 float f[8];
@@ -192,7 +220,7 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                sc[n][c] = a.scale_log2 * up_by(__shfl_sync(kFull, E, (2 * tq + c) * 4));
+                sc[n][c] = fmaxf(fabsf(a.scale_log2) * up_by(__shfl_sync(kFull, E, (2 * tq + c) * 4)), FLT_MIN);
                 p[n][c] = t.L - t.n + a.by_group(t.row0 + min(8 * n + 2 * tq + c, t.rows - 1));
             }
         }
@@ -218,24 +246,19 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
         // The copies of a step whose groups are `at` lanes on. Scales of keys that
         // are not there arrive as zeros, which makes their elements zeros: nothing
         // else has to be told apart, codes are finite whatever they are.
-        auto issue = [&](int stage, uint32_t groups, int at) {
-            const uint32_t dst = ring + stage * A::STAGE;
+        auto issue = [&](uint32_t dst, uint32_t groups, int at) {
             const uint32_t mine = __shfl_sync(kFull, groups, at + own), sc = __shfl_sync(kFull, groups, (at + sc_own) & 31);
             const uint32_t x = mine & 0x3FFFFFFu, y = sc & 0x3FFFFFFu;
-            if (mine >> 26) {
-                const uint64_t off = (uint64_t)x * A::CODES + (uint64_t)(x >> group_shift) * (uint32_t)(A::SB << a.page_shift);
-                const uint8_t *ks = k_lane + off, *vs = v_lane + off;
-                const uint32_t to = dst + own * A::GROUP;
+            const uint64_t off = (uint64_t)x * A::CODES + (uint64_t)(x >> group_shift) * page_scales;
+            const uint8_t *ks = k_lane + off, *vs = v_lane + off;
+            const bool real = mine >> 26 != 0;
 #pragma unroll
-                for (int i = 0; i < PER_LANE; ++i) {
-                    const int o = chunk0 + LG * i, r = o / (D / 32), c = o % (D / 32);
-                    cp16(to + k_at<D>(r, c), ks + LG * 16 * i, 16);
-                    cp16(to + A::HALF + v_at<D>(r, c), vs + LG * 16 * i, 16);
-                }
+            for (int i = 0; i < PER_LANE; ++i) {
+                cp16_if(real, dst + k_to + i * LG * 16, ks + i * LG * 16);
+                cp16_if(real, dst + v_to[i & 1] + i * LG * 16, vs + i * LG * 16);
             }
-            if (sc_own < A::NK)
-                cp16(dst + sc_dst,
-                     sc_lane + ((uint64_t)y * A::SCALES + (uint64_t)(y >> group_shift) * (uint32_t)(A::CB << a.page_shift)),
+            if (SC * 2 * A::NK == 32 || sc_own < A::NK)
+                cp16(dst + sc_to, sc_lane + ((uint64_t)y * A::SCALES + (uint64_t)(y >> group_shift) * page_codes),
                      min(max((int)(sc >> 26) * A::SB - 16 * sc_chunk, 0), 16));
         };
 
@@ -255,15 +278,17 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
         constexpr int STEPS = 32 / A::NK;
         uint32_t groups = lookup(first), next = lookup(first + STEPS);
         int at = 0;  // the next step to copy: its place among `groups`
-        auto copy_step = [&](int stage) {
-            issue(stage, groups, at);
+        auto copy_step = [&](uint32_t dst) {
+            issue(dst, groups, at);
             cp_commit();
             at += A::NK;
         };
+        const uint32_t ring_end = ring + A::RING;
 #pragma unroll
-        for (int s = 0; s < A::STAGES - 1; ++s) copy_step(s);  // (past the last block nothing is copied but zeros)
-        for (int blk = first, it = 0; blk < last; ++blk, it = it + 1 == A::STAGES ? 0 : it + 1) {
-            copy_step(it == 0 ? A::STAGES - 1 : it - 1);
+        for (int s = 0; s < A::STAGES - 1; ++s) copy_step(ring + s * A::STAGE);  // (past the last block: zeros alone)
+        uint32_t stage = ring, fill = ring_end - A::STAGE;
+        for (int blk = first; blk < last; ++blk, fill = stage, stage = stage + A::STAGE == ring_end ? ring : stage + A::STAGE) {
+            copy_step(fill);
             if (at == 32) {
                 at = 0;
                 groups = next;
@@ -271,14 +296,13 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
             }
             cp_wait<A::STAGES - 1>();
             __syncwarp();
-            const uint32_t stage = ring + it * A::STAGE;
 
             // scores: rows of an MMA are the keys gr and gr + 8 of a group
             float s[A::NK][NR][4];
             constexpr int WB = KW < 4 ? KW : 4;  // words of a load
 #pragma unroll
             for (int g = 0; g < A::NK; ++g) {
-                const uint32_t kb = stage + g * A::GROUP, ks = kb + A::CODES;
+                const uint32_t group = stage + g * A::GROUP;
 #pragma unroll
                 for (int n = 0; n < NR; ++n) s[g][n][0] = s[g][n][1] = s[g][n][2] = s[g][n][3] = 0.f;
 #pragma unroll
@@ -286,14 +310,13 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
                     uint32_t kw[2][WB], sk[2][2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int key = gr + 8 * h;
+                        lds_words<WB>(group + (x0 ? k_from2 : k_from) + 8 * h * A::CB, kw[h]);
+                        const uint32_t sc_at = group + ks_from + 8 * h * A::SB + 2 * x0;
                         if constexpr (D == 64) {
-                            lds_words<WB>(kb + k_at<D>(key, tq >> 1) + 8 * (tq & 1), kw[h]);
-                            const uint32_t f = e4m3x2_to_f16x2(lds_u8(ks + key * A::SB + tq));
+                            const uint32_t f = e4m3x2_to_f16x2(lds_u8(sc_at));
                             sk[h][0] = sk[h][1] = __byte_perm(f, 0, 0x1010);
                         } else {
-                            lds_words<WB>(kb + k_at<D>(key, tq + x0), kw[h]);
-                            const uint32_t f = e4m3x2_to_f16x2(lds_u16(ks + key * A::SB + 2 * (tq + x0)));
+                            const uint32_t f = e4m3x2_to_f16x2(lds_u16(sc_at));
                             sk[h][0] = __byte_perm(f, 0, 0x1010);
                             sk[h][1] = __byte_perm(f, 0, 0x3232);
                         }
@@ -318,36 +341,48 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
                 }
             }
 
-            // the scores above the rows' reference points (s c - m), masked; weights
+            // Weights 2^(s c - m) of the visible keys. Where a lane's sum of a row's is
+            // above 2^kLag, a score may be that far above the row's reference point.
             const int k0 = key0(blk), k1 = k0 + A::KT - 1;
             const bool whole = k1 <= p_lo && (a.window <= 0 || k0 > p_hi - a.window || k1 < a.sinks);
-            float d[A::NK][NR][4], top = -CUDART_INF_F;
+            float d[A::NK][NR][4], sum[NR][2];
+            auto weights = [&]() {
+                float top = 0.f;
 #pragma unroll
-            for (int g = 0; g < A::NK; ++g)
+                for (int n = 0; n < NR; ++n) {
 #pragma unroll
-                for (int n = 0; n < NR; ++n)
+                    for (int c = 0; c < 2; ++c) {
+                        sum[n][c] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(s[g][n][e], sc[n][e & 1], -m[n][e & 1]);
-                        if (!whole) {
-                            const int key = k0 + g * kKeys + gr + 8 * (e >> 1), at = p[n][e & 1];
-                            const bool seen = (key <= at) & ((a.window <= 0) | (key > at - a.window) | (key < a.sinks));
-                            x = seen ? x : -CUDART_INF_F;
+                        for (int x = 0; x < 2 * A::NK; ++x) {
+                            const int g = x >> 1, e = 2 * (x & 1) + c;
+                            d[g][n][e] = exp2_approx(fmaf(s[g][n][e], sc[n][c], -m[n][c]));
+                            sum[n][c] += d[g][n][e];
                         }
-                        d[g][n][e] = x;
-                        top = fmaxf(top, x);
+                        top = fmaxf(top, sum[n][c]);
                     }
-            if (__any_sync(kFull, top > kLag<1>)) {
+                }
+                return top;
+            };
+            if (!whole)
+#pragma unroll
+                for (int g = 0; g < A::NK; ++g)
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = k0 + g * kKeys + gr + 8 * (e >> 1), at_key = p[n][e & 1];
+                            const bool seen = (key <= at_key) & ((a.window <= 0) | (key > at_key - a.window) | (key < a.sinks));
+                            s[g][n][e] = seen ? s[g][n][e] : -CUDART_INF_F;
+                        }
+            if (__any_sync(kFull, weights() > kTop)) {
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         float x = -CUDART_INF_F;
 #pragma unroll
-                        for (int g = 0; g < A::NK; ++g)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (d[g][n][2 * h + c] > -CUDART_INF_F) x = fmaxf(x, s[g][n][2 * h + c] * sc[n][c]);
+                        for (int g = 0; g < A::NK; ++g) x = fmaxf(x, fmaxf(s[g][n][c] * sc[n][c], s[g][n][2 + c] * sc[n][c]));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
@@ -356,51 +391,35 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
                         m[n][c] = to;
                         l[n][c] *= f;
 #pragma unroll
-                        for (int g = 0; g < A::NK; ++g)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float &y = d[g][n][2 * h + c];
-                                if (y != -CUDART_INF_F) y = fmaf(s[g][n][2 * h + c], sc[n][c], -to);
-                            }
-#pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             o[i][n][c] *= f;
                             o[i][n][2 + c] *= f;
                         }
                     }
+                weights();
             }
             uint32_t pw[A::NK][NR][2];
 #pragma unroll
-            for (int g = 0; g < A::NK; ++g)
+            for (int n = 0; n < NR; ++n) {
+                l[n][0] += sum[n][0];
+                l[n][1] += sum[n][1];
 #pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    float e[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) e[x] = exp2_approx(d[g][n][x]);
-                    l[n][0] += e[0] + e[2];
-                    l[n][1] += e[1] + e[3];
-                    pw[g][n][0] = transpose8(pack_weights<1>(e[0], e[1]));
-                    pw[g][n][1] = transpose8(pack_weights<1>(e[2], e[3]));
+                for (int g = 0; g < A::NK; ++g) {
+                    pw[g][n][0] = transpose8(pack_weights<1>(d[g][n][0], d[g][n][1]));
+                    pw[g][n][1] = transpose8(pack_weights<1>(d[g][n][2], d[g][n][3]));
                 }
+            }
 
             // O^T: rows of an MMA are two of this lane's D / 8 consecutive dims, its contraction 16 keys
 #pragma unroll
             for (int g = 0; g < A::NK; ++g) {
-                const uint32_t vb = stage + g * A::GROUP + A::HALF, vs = vb + A::CODES;
+                const uint32_t group = stage + g * A::GROUP;
                 uint32_t vw[4][VW], sv[2][2], sb[4];  // keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const int key = 2 * tq + (y & 1) + 8 * (y >> 1);
-                    if constexpr (D == 64) {
-                        lds_words<1>(vb + v_at<D>(key, gr >> 2) + 4 * (gr & 3), vw[y]);
-                        sb[y] = lds_u8(vs + key * A::SB + (gr >> 1));
-                    } else if constexpr (D == 128) {
-                        lds_words<2>(vb + v_at<D>(key, gr >> 1) + 8 * (gr & 1), vw[y]);
-                        sb[y] = lds_u8(vs + key * A::SB + gr);
-                    } else {
-                        lds_words<4>(vb + v_at<D>(key, gr), vw[y]);
-                        sb[y] = lds_u16(vs + key * A::SB + 2 * gr);
-                    }
+                    lds_words<VW>(group + v_from[y & 1] + 8 * (y >> 1) * A::CB, vw[y]);
+                    const uint32_t sc_at = group + vs_from + ((y & 1) + 8 * (y >> 1)) * A::SB;
+                    sb[y] = D == 256 ? lds_u16(sc_at) : lds_u8(sc_at);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
