@@ -42,7 +42,7 @@ constexpr LineRule kLine = {1, 3, 3};  // see mkv_line.h
 // Shape of one instantiation: head dims, rows of a tile.
 template <int D, int R>
 struct Attend4 {
-    static constexpr int WARPS = D == 256 ? (R == 8 ? 12 : 8) : D == 128 && R == 16 ? 12 : 16;
+    static constexpr int WARPS = D == 256 ? (R == 8 ? 12 : 8) : D == 128 ? 12 : 16;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int NK = D == 256 ? 1 : 2;    // groups of 16 keys of a warp's step
     static constexpr int KT = NK * kKeys;          // its keys
@@ -50,7 +50,7 @@ struct Attend4 {
     static constexpr int CB = D / 2, SB = D / 16;  // bytes of a row's codes and scales
     static constexpr int CODES = kKeys * CB, SCALES = kKeys * SB;  // ... of 16 keys
     static constexpr int HALF = CODES + SCALES, GROUP = 2 * HALF, STAGE = NK * GROUP;
-    static constexpr int STAGES = 220 * 1024 / (WARPS * STAGE) < 6 ? 220 * 1024 / (WARPS * STAGE) : 6;
+    static constexpr int STAGES = D == 256 ? 220 * 1024 / (WARPS * STAGE) : 3;
     static constexpr int RING = STAGES * STAGE;    // per warp
     static constexpr int OS = D + 4;               // floats between a result's rows
     static constexpr int MERGE = WARPS * R * OS * 4;

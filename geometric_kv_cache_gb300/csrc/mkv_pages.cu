@@ -458,8 +458,8 @@ k_page_update(const PageArgs a)
 // An item's owner is read three items ahead, its indices two and its page
 // entries one, so that every row copy (groups of LPR lanes, 16 bytes each, 4
 // rows of K and of V in flight per lane) finds its addresses in registers.
-// ROWS: what a row is. Of 4-bit pages a lane also copies the scales of its own
-// token, with one load of each. Rows that become codes are 32 bytes of bf16 per
+// ROWS: what a row is. Rows of 4-bit pages are short: a warp takes two items at
+// once, and a lane also copies the scales of its own token, with one load of each. Rows that become codes are 32 bytes of bf16 per
 // lane, one group of 16 dims: its largest element never leaves the lane.
 template <int BYTES>
 struct ScaleWord {
@@ -505,8 +505,9 @@ k_page_compact(const PageArgs a, int list_ctas)
 {
     constexpr bool ROUND = ROWS == kToE4m3 || ROWS == kToE2m1;
     constexpr int RB = LPR * (ROUND ? 32 : 16), RPS = 32 / LPR;  // bytes of a row (read), rows per step
+    constexpr int ITEMS = ROWS == kCopyCodes ? 2 : 1;  // at once: half a warp each
     constexpr int MOST = ROUND ? 2 : 4;
-    constexpr int STEPS = kItem / RPS, B = STEPS < MOST ? STEPS : MOST;  // steps, and of a batch
+    constexpr int STEPS = ITEMS * kItem / RPS, B = STEPS < MOST ? STEPS : MOST;  // steps, and of a batch
     constexpr int SB = ROWS == kCopyCodes ? LPR * 2 : ROWS == kToE2m1 ? LPR : 0;  // bytes of a row's scales
     constexpr int WB = ROWS == kToE2m1 ? LPR * 8 : LPR * 16;                      // bytes of a row written, without them
     pdl_wait();
@@ -537,18 +538,21 @@ k_page_compact(const PageArgs a, int list_ctas)
     const int64_t warps = (int64_t)(gridDim.x - list_ctas) * (kPageThreads / 32);
     const int64_t warp = (int64_t)(blockIdx.x - list_ctas) * (kPageThreads / 32) + (threadIdx.x >> 5);
     const int64_t items = (int64_t)a.verdict[1] << per_shift;  // pages taken
-    auto owner = [&](int64_t item) -> int2 {
+    // (of item x of the warps' count this lane has item x ITEMS + lane / kItem, which lanes of no item do not look up)
+    auto owner = [&](int64_t x) -> int2 {
+        const int64_t item = ITEMS == 1 ? x : x * ITEMS + lane / kItem;
         return item < items ? a.owners[item >> per_shift] : make_int2(-1, 0);
     };
     // an item: its list, its new page's rank, and this lane's token of it with its source (-1: none)
     struct Item {
         int h, rank, i, s;
     };
-    auto source = [&](int64_t item, int2 own) -> Item {
+    auto source = [&](int64_t x, int2 own) -> Item {
+        const int64_t item = ITEMS == 1 ? x : x * ITEMS + lane / kItem;
         Item it = {own.x, (int)(item >> per_shift), -1, -1};
-        if (own.x < 0 || lane >= kItem) return it;
+        if (own.x < 0 || lane >= ITEMS * kItem) return it;
         const int64_t h = own.x;
-        const int i = (own.y << a.page_shift) + (int)(item & ((1 << per_shift) - 1)) * kItem + lane;
+        const int i = (own.y << a.page_shift) + (int)(item & ((1 << per_shift) - 1)) * kItem + lane % kItem;
         // (read together: an index behind the kept ones is not looked at)
         const int kept = a.kept[h], s = !a.idx ? i : i < a.idx_stride ? a.idx[h * a.idx_stride + i] : -1;
         if (i >= kept) return it;
@@ -590,7 +594,7 @@ k_page_compact(const PageArgs a, int list_ctas)
     places(ahead, from, to);
     ahead = source(warp + warps, own);
     own = owner(warp + 2 * warps);
-    for (int64_t item = warp; item < items; item += warps) {
+    for (int64_t item = warp; item * ITEMS < items; item += warps) {
         int64_t next_from;
         int next_to;
         places(ahead, next_from, next_to);

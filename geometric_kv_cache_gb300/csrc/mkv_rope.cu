@@ -79,39 +79,61 @@ __device__ __forceinline__ int row_of_token(const int32_t *q_start, int batch, i
     return lo < batch && q_start[lo] <= t && t < q_start[lo + 1] ? lo : -1;
 }
 
-// The rotated values of this lane's 16 dims (x, y as loaded) as 64-bit
-// arithmetic gives them, rounded once to fp32: pair e of the lane's 8 turns by
-// the position of its axis. Not inlined: 4-bit keys next to a border take it,
-// one in a few hundred groups of heads.
-template <bool AXES>
-__device__ __noinline__ void rotate_exactly(const RopeArgs &a, int t, int u, uint4 xr, uint4 yr, float (&x)[8], float (&y)[8])
+// Sine and cosine, times `factor`, of the 64-bit product position * freq. The
+// angle in turns is a product with 1 / (2 pi) of 106 bits, whose whole turns drop
+// out exactly.
+__device__ __forceinline__ double2 turn_exactly(int position, float freq, float factor)
 {
+    const double angle = (double)position * (double)freq;
+    const double hi = angle * 0.15915494309189535, lo = fma(angle, 0.15915494309189535, -hi) + angle * -9.839338337591243e-18;
+    const double turns = (hi - rint(hi)) + lo;
+    double sn, cn;
+    sincospi(2.0 * turns, &sn, &cn);
+    return make_double2(cn * factor, sn * factor);
+}
+
+// The rotated values of this lane's 16 dims (x, y as loaded) as 64-bit
+// arithmetic gives them, rounded once to fp32, for a whole warp: a lane works out
+// the angles that it works out in 32 bits, and the others come from their lanes.
+// Not inlined: 4-bit keys next to a border take it, one in a few hundred groups
+// of heads. (64-bit operations are 1 / 64 of the 32-bit rate.)
+template <int D>
+__device__ __noinline__ void rotate_exactly(const RopeArgs &a, int t, uint4 xr, uint4 yr, float (&x)[8], float (&y)[8])
+{
+    constexpr int UNITS = D / 16, OWN = 8 * UNITS / 32;
+    const int lane = threadIdx.x & 31, u = lane % UNITS, sub = lane / UNITS;
+    double2 mine[OWN];
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        const int pair = 8 * u + sub * OWN + o;
+        mine[o] = make_double2(0.0, 0.0);
+        if (u < a.rot_dim / 16) {
+            int axis = a.n_axes > 0 ? a.axes[pair] : 0;
+            if ((uint32_t)axis >= (uint32_t)a.n_axes) axis = 0;
+            mine[o] = turn_exactly(a.positions[(int64_t)axis * a.n_tokens + t], a.inv_freq[pair], a.factor);
+        }
+    }
     float p[8], q[8];
     bf16x8_to_f32(xr, p);
     bf16x8_to_f32(yr, q);
-#pragma unroll 1
+    const bool half = a.layout == MKV_ROPE_HALF;
+#pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const int pair = 8 * u + e;
-        int axis = AXES ? a.axes[pair] : 0;
-        if (AXES && (uint32_t)axis >= (uint32_t)a.n_axes) axis = 0;
-        double sn, cn;
-        sincos((double)a.positions[(int64_t)axis * a.n_tokens + t] * (double)a.inv_freq[pair], &sn, &cn);
-        sn *= a.factor;
-        cn *= a.factor;
+        const double cn = __shfl_sync(kFull, mine[e % OWN].x, u + (e / OWN) * UNITS);
+        const double sn = __shfl_sync(kFull, mine[e % OWN].y, u + (e / OWN) * UNITS);
         // pairs (x[e], y[e]); neighbouring ones: x holds the lane's first four, y the others
-        const bool half = a.layout == MKV_ROPE_HALF;
-        const float c0 = half ? p[e] : e < 4 ? p[2 * e & 7] : q[2 * e & 7];
-        const float c1 = half ? q[e] : e < 4 ? p[(2 * e + 1) & 7] : q[(2 * e + 1) & 7];
+        const int i = 2 * e & 7;
+        const float c0 = half ? p[e] : e < 4 ? p[i] : q[i], c1 = half ? q[e] : e < 4 ? p[i + 1] : q[i + 1];
         const float r0 = (float)(c0 * cn - c1 * sn), r1 = (float)(c0 * sn + c1 * cn);
         if (half) {
             x[e] = r0;
             y[e] = r1;
         } else if (e < 4) {
-            x[2 * e & 7] = r0;
-            x[(2 * e + 1) & 7] = r1;
+            x[i] = r0;
+            x[i + 1] = r1;
         } else {
-            y[2 * e & 7] = r0;
-            y[(2 * e + 1) & 7] = r1;
+            y[i] = r0;
+            y[i + 1] = r1;
         }
     }
 }
@@ -383,16 +405,13 @@ k_rope_append(const __grid_constant__ RopeArgs a, int parts)
                             }
                             break;
                         }
-                        if (turned) {
-                            float p[8], q[8];
-                            rotate_exactly<AXES>(a, t, u, xr[c], yr[c], p, q);
+                        float p[8], q[8];
+                        rotate_exactly<D>(a, t, xr[c], yr[c], p, q);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                x[e] = p[e];
-                                y[e] = q[e];
-                            }
+                        for (int e = 0; e < 8; ++e) {
+                            x[e] = turned ? p[e] : x[e];
+                            y[e] = turned ? q[e] : y[e];
                         }
-                        __syncwarp();
                     }
                     if (head < 0 || id[c] < 0) continue;
                     uint8_t *page = (kind == 1 ? a.k : a.v) + (int64_t)id[c] * (D * 9 / 16 << a.page_shift);
