@@ -595,25 +595,10 @@ k_page_compact(const PageArgs a, int list_ctas)
     ahead = source(warp + warps, own);
     own = owner(warp + 2 * warps);
     for (int64_t item = warp; item * ITEMS < items; item += warps) {
-        int64_t next_from;
-        int next_to;
-        places(ahead, next_from, next_to);
-        ahead = source(item + 2 * warps, own);
-        own = owner(item + 3 * warps);
-        if constexpr (ROWS == kCopyCodes) {  // this lane's token
-            using S = typename ScaleWord<SB>::type;
-            if (to >= 0) {
-                const int64_t s = scales_at(from), d = scales_at(to);
-                const S x = *reinterpret_cast<const S *>(a.k + s), y = *reinterpret_cast<const S *>(a.v + s);
-                *reinterpret_cast<S *>(a.k + d) = x;
-                *reinterpret_cast<S *>(a.v + d) = y;
-            }
-        }
-#pragma unroll
-        for (int b0 = 0; b0 < STEPS; b0 += B) {
-            constexpr int N = ROUND ? 2 : 1;
-            uint4 kr[B][N], vr[B][N];
-            int dst[B];
+        constexpr int N = ROUND ? 2 : 1;
+        uint4 kr[B][N], vr[B][N];
+        int dst[B];
+        auto load = [&](int b0) {
 #pragma unroll
             for (int u = 0; u < B; ++u) {
                 const int row = (b0 + u) * RPS + g;
@@ -628,6 +613,26 @@ k_page_compact(const PageArgs a, int list_ctas)
                     }
                 }
             }
+        };
+        // short rows: the first ones are on their way while the next items' places are waited for (bf16 and E4M3 rows
+        // are not faster for it)
+        using S = typename ScaleWord<SB>::type;
+        S k_scales, v_scales;  // of this lane's token
+        if constexpr (ROWS == kCopyCodes)
+            if (to >= 0) {
+                const int64_t s = scales_at(from);
+                k_scales = *reinterpret_cast<const S *>(a.k + s);
+                v_scales = *reinterpret_cast<const S *>(a.v + s);
+            }
+        if constexpr (ROWS != kCopy) load(0);
+        int64_t next_from;
+        int next_to;
+        places(ahead, next_from, next_to);
+        ahead = source(item + 2 * warps, own);
+        own = owner(item + 3 * warps);
+#pragma unroll
+        for (int b0 = 0; b0 < STEPS; b0 += B) {
+            if (ROWS == kCopy || b0 > 0) load(b0);
 #pragma unroll
             for (int u = 0; u < B; ++u)
                 if (dst[u] >= 0) {
@@ -648,6 +653,12 @@ k_page_compact(const PageArgs a, int list_ctas)
                     }
                 }
         }
+        if constexpr (ROWS == kCopyCodes)
+            if (to >= 0) {
+                const int64_t d = scales_at(to);
+                *reinterpret_cast<S *>(a.k + d) = k_scales;
+                *reinterpret_cast<S *>(a.v + d) = v_scales;
+            }
         from = next_from;
         to = next_to;
     }
