@@ -551,33 +551,47 @@ k_attend_chunk(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
                         if (!ok) break;
                         const uint32_t from = saddr(raws + q * C::RAW), to = saddr(ring + s * C::SLOT);
                         constexpr int CPR = D / 16;  // groups of 16 codes per row
-#pragma unroll 4
-                        for (int o = quarter * 32 + lane; o < kKeys * CPR; o += 128) {
-                            const int key = o / CPR, c = o % CPR;
-                            if constexpr (ES == 0) {
-                                const uint32_t row = to + (c >> 2) * kBoxBytes + key * 128, x = (uint32_t)(c & 3) * 2;
-                                uint2 v = lds8(from + o * 8);
-                                uint32_t sc = lds1(from + C::CODES_BYTES + o);
-                                if (key >= live) sc = 0u;
-                                sc = e4m3x2_to_f16x2(sc | sc << 8);
-                                uint32_t h[8];
-                                e2m1x8_to_f16(v.x, *reinterpret_cast<uint32_t(*)[4]>(h));
-                                e2m1x8_to_f16(v.y, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) h[e] = mul_f16x2(h[e], sc);
-                                sts16(row + ((x ^ (key & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
-                                sts16(row + (((x + 1) ^ (key & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
-                                continue;
-                            }
-                            uint4 v = lds16(from + o * 16);
-                            if (key >= live) v = make_uint4(0u, 0u, 0u, 0u);
+                        if constexpr (ES == 0) {
+                            // A thread's groups are the same one of rows STEP apart, so its places are one of each kind and
+                            // fixed distances. (Eight lanes store into two rows of one box, whose swizzle gives them all chunks.)
+                            constexpr int STEP = 128 / CPR, ROUNDS = kKeys / STEP;
+                            const int o = quarter * 32 + lane, c = (o & 3) | (o >> 3 & (CPR / 4 - 1)) << 2;
+                            const int key = (o >> 2 & 1) | o / (2 * CPR) << 1;
+                            const uint32_t codes = from + (key * CPR + c) * 8, scales = from + C::CODES_BYTES + key * CPR + c;
                             const uint32_t row = to + (c >> 2) * kBoxBytes + key * 128, x = (uint32_t)(c & 3) * 2;
-                            sts16(row + ((x ^ (key & 7)) << 4),
-                                  make_uint4(e4m3x2_to_f16x2(v.x & 0xFFFFu), e4m3x2_to_f16x2(v.x >> 16),
-                                             e4m3x2_to_f16x2(v.y & 0xFFFFu), e4m3x2_to_f16x2(v.y >> 16)));
-                            sts16(row + (((x + 1) ^ (key & 7)) << 4),
-                                  make_uint4(e4m3x2_to_f16x2(v.z & 0xFFFFu), e4m3x2_to_f16x2(v.z >> 16),
-                                             e4m3x2_to_f16x2(v.w & 0xFFFFu), e4m3x2_to_f16x2(v.w >> 16)));
+                            const uint32_t lo = row + ((x ^ (key & 7)) << 4), hi = row + (((x + 1) ^ (key & 7)) << 4);
+                            static_assert(STEP % 8 == 0, "rows a step apart have one swizzle");
+#pragma unroll 4
+                            for (int i = 0; i < ROUNDS; ++i) {
+                                const uint2 v = lds8(codes + i * 1024);
+                                uint32_t sc = lds1(scales + i * 128);
+                                if (live < kKeys && key + STEP * i >= live) sc = 0u;
+                                sc = e4m3x2_to_f16x2(sc | sc << 8);
+                                uint32_t h[2][4];
+                                e2m1x8_to_f16(v.x, h[0]);
+                                e2m1x8_to_f16(v.y, h[1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    h[0][e] = mul_f16x2(h[0][e], sc);
+                                    h[1][e] = mul_f16x2(h[1][e], sc);
+                                }
+                                sts16(lo + i * STEP * 128, make_uint4(h[0][0], h[0][1], h[0][2], h[0][3]));
+                                sts16(hi + i * STEP * 128, make_uint4(h[1][0], h[1][1], h[1][2], h[1][3]));
+                            }
+                        } else {
+#pragma unroll 4
+                            for (int o = quarter * 32 + lane; o < kKeys * CPR; o += 128) {
+                                const int key = o / CPR, c = o % CPR;
+                                uint4 v = lds16(from + o * 16);
+                                if (key >= live) v = make_uint4(0u, 0u, 0u, 0u);
+                                const uint32_t row = to + (c >> 2) * kBoxBytes + key * 128, x = (uint32_t)(c & 3) * 2;
+                                sts16(row + ((x ^ (key & 7)) << 4),
+                                      make_uint4(e4m3x2_to_f16x2(v.x & 0xFFFFu), e4m3x2_to_f16x2(v.x >> 16),
+                                                 e4m3x2_to_f16x2(v.y & 0xFFFFu), e4m3x2_to_f16x2(v.y >> 16)));
+                                sts16(row + (((x + 1) ^ (key & 7)) << 4),
+                                      make_uint4(e4m3x2_to_f16x2(v.z & 0xFFFFu), e4m3x2_to_f16x2(v.z >> 16),
+                                                 e4m3x2_to_f16x2(v.w & 0xFFFFu), e4m3x2_to_f16x2(v.w >> 16)));
+                            }
                         }
                         fence_async();
                         __syncwarp();
