@@ -77,7 +77,7 @@ struct Chunk {
     static constexpr int SLOT = BOXES * BOX;        // one block of K or of V as the MMA reads it
     static constexpr int CODES_BYTES = ES == 0 ? KEYS * D / 2 : KEYS * D;   // ... as E4M3 or 4-bit codes
     static constexpr int RAW = CODES_BYTES + (ES == 0 ? KEYS * D / 16 : 0);  // (and their scales)
-    static constexpr int RAWS = ES == 2 ? 0 : ES == 0 || D == 64 ? 3 : 2;
+    static constexpr int RAWS = ES == 2 ? 0 : D == 64 ? 3 : 2;
     static constexpr int SLOTS = ES == 2 ? (D == 64 ? 8 : D == 128 ? 4 : 5) : (D == 64 ? 9 : 4);
     // The next tile's queries go to the MMAs before this one's output is written
     // (384 lists of 64 keys, 256 rows: E4M3 at 128 dims 43.5 us, else 44.7; bf16 at 256
@@ -92,9 +92,10 @@ struct Chunk {
     static constexpr int THREADS = (4 + SOFT + CODES) * 32;   // 256, 384 or 512
     // Registers per thread of warps 0-3, the softmax warps and the expanding
     // ones: at most what the launch has (256 x 224, 384 x 168 or 512 x 128).
-    static constexpr int REGS_FEED = THREADS == 256 ? 168 : THREADS == 384 ? 88 : 80;
-    static constexpr int REGS_SOFT = THREADS == 256 ? 240 : THREADS == 384 ? 208 : 176;
-    static constexpr int REGS_CODES = 80;
+    // (4-bit, 128 dims, 2048 tokens over 32768: 64 / 192 / 64 819 us, the 80 / 176 / 80 of E4M3, whose loop spills, 856.)
+    static constexpr int REGS_FEED = THREADS == 256 ? 168 : THREADS == 384 ? 88 : ES == 0 ? 64 : 80;
+    static constexpr int REGS_SOFT = THREADS == 256 || SOFT == 4 ? 240 : THREADS == 384 ? 208 : ES == 0 ? 192 : 176;
+    static constexpr int REGS_CODES = THREADS == 512 && ES == 0 ? 64 : 80;
     static constexpr int REGS_LAUNCH = THREADS == 256 ? 224 : THREADS == 384 ? 168 : 128;
     static_assert(4 * REGS_FEED + SOFT * REGS_SOFT + CODES * REGS_CODES <= THREADS / 32 * REGS_LAUNCH, "register split");
     static constexpr int TMEM = 512;
