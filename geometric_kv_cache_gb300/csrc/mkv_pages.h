@@ -82,6 +82,7 @@ struct RopeArgs {
     uint32_t *status;
 };
 cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t st);
+cudaError_t launch_rope_axes(const RopeArgs &a, cudaStream_t st);  // several axes, or 4-bit pages
 
 // Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiplication (Granlund and
 // Montgomery, "Division by Invariant Integers using Multiplication", PLDI 1994,
