@@ -17,8 +17,8 @@
 // own 2^-24 -- and 2^-50 of the angle, whose fraction of a turn comes from 64-bit
 // floating point. (|x| + |y| is at most sqrt(2) times that of the rotated pair over
 // |factor|, so rotated pairs tell it.) Where that could change a code or a scale,
-// because the ends of the stretch round differently, the warp works the rotation
-// out in 64 bits, at 1 / 64 of the 32-bit rate: a few groups of heads in a thousand.
+// because the ends of the stretch round differently, the element (for a scale, those
+// that can be the largest) is worked out in 64 bits, at 1 / 64 of the 32-bit rate.
 //
 // @@MEASURED@@
 #include <cuda_runtime.h>
@@ -97,23 +97,87 @@ __device__ __forceinline__ void rotate(float (&x)[8], float (&y)[8], const float
     }
 }
 
-// Sine and cosine, times `factor`, of the 64-bit product position * freq. The
-// angle in turns is a product with 1 / (2 pi) of 106 bits, whose whole turns drop
-// out exactly.
+// Cosine and sine, times `factor`, of the 64-bit product position * freq. The
+// angle in turns is a product with 1 / (2 pi) of 106 bits, of which whole quarters
+// drop out exactly; for what is left, at most pi / 4, the Taylor sums up to the 16th
+// power (the next terms are below 2^-54), by pairs of terms: a 64-bit operation waits
+// 62 cycles for the one before it, so the depth counts. 45 operations in a row
+// (sincospi) take 2800 cycles for one element.
 __device__ __forceinline__ double2 turn_exactly(int position, float freq, float factor)
 {
     const double angle = (double)position * (double)freq;
     const double hi = angle * 0.15915494309189535, lo = fma(angle, 0.15915494309189535, -hi) + angle * -9.839338337591243e-18;
-    const double turns = (hi - rint(hi)) + lo;
-    double sn, cn;
-    sincospi(2.0 * turns, &sn, &cn);
-    return make_double2(cn * factor, sn * factor);
+    const double quarters = rint(4.0 * hi);
+    const double x = (fma(quarters, -0.25, hi) + lo) * 6.283185307179586477, z = x * x, z2 = z * z, z4 = z2 * z2;
+    const double s = fma(z4, fma(z2, fma(z, 1.0 / 355687428096000.0, -1.0 / 1307674368000.0), fma(z, 1.0 / 6227020800.0, -1.0 / 39916800.0)),
+                         fma(z2, fma(z, 1.0 / 362880.0, -1.0 / 5040.0), fma(z, 1.0 / 120.0, -1.0 / 6.0)));
+    const double c = fma(z4, fma(z2, fma(z, 1.0 / 20922789888000.0, -1.0 / 87178291200.0), fma(z, 1.0 / 479001600.0, -1.0 / 3628800.0)),
+                         fma(z2, fma(z, 1.0 / 40320.0, -1.0 / 720.0), fma(z, 1.0 / 24.0, -1.0 / 2.0)));
+    const double sn = fma(x * z, s, x), cn = fma(z, c, 1.0);
+    const int q = (int)(long long)quarters & 3;
+    const double cq = q & 1 ? sn : cn, sq = q & 1 ? cn : sn;
+    return make_double2((q == 1 || q == 2 ? -cq : cq) * factor, (q >= 2 ? -sq : sq) * factor);
+}
+
+// One rotated element as 64-bit arithmetic gives it, rounded once to fp32: of pair
+// (c0, c1), the first or second. Not inlined: it is rare.
+__device__ __noinline__ float exact_element(const RopeArgs &a, int t, int pair, float c0, float c1, bool second)
+{
+    int axis = a.n_axes > 0 ? a.axes[pair] : 0;
+    if ((uint32_t)axis >= (uint32_t)a.n_axes) axis = 0;
+    const double2 turn = turn_exactly(a.positions[(int64_t)axis * a.n_tokens + t], a.inv_freq[pair], a.factor);
+    return (float)(second ? c0 * turn.y + c1 * turn.x : c0 * turn.x - c1 * turn.y);
+}
+
+// Element i of eight bf16.
+__device__ __forceinline__ float element(uint4 v, int i)
+{
+    const uint32_t w = i < 4 ? (i < 2 ? v.x : v.y) : (i < 6 ? v.z : v.w);
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+}
+
+// Element i of a lane's rotated x or y, worked out exactly.
+template <bool HALF>
+__device__ __forceinline__ float exact_of(const RopeArgs &a, int t, int u, uint4 xr, uint4 yr, bool is_y, int i)
+{
+    const uint4 row = is_y ? yr : xr;
+    const int pair = HALF ? 8 * u + i : 8 * u + (is_y ? 4 : 0) + (i >> 1);
+    const float c0 = HALF ? element(xr, i) : element(row, i & 6), c1 = HALF ? element(yr, i) : element(row, i | 1);
+    return exact_element(a, t, pair, c0, c1, HALF ? is_y : (i & 1) != 0);
+}
+
+// The codes w of a lane's x or y with those of the elements that `unsure` marks, in
+// the lowest bits of their codes, settled.
+template <bool HALF>
+__device__ __forceinline__ uint32_t settle(const RopeArgs &a, int t, int u, uint4 xr, uint4 yr, bool is_y, float r,
+                                           uint32_t w, uint32_t unsure)
+{
+    for (; unsure; unsure &= unsure - 1) {
+        const int bit = __ffs(unsure) - 1;
+        const float f[8] = {__fmul_rn(exact_of<HALF>(a, t, u, xr, yr, is_y, bit >> 2), r)};
+        w = (w & ~(15u << bit)) | (plain_zeros(f32x8_to_e2m1(f)) & 15u) << bit;
+    }
+    return w;
+}
+
+// The largest magnitude of a lane's x or y (v, as rotated in fp32), worked out
+// exactly; only elements from `least` on can be it.
+template <bool HALF>
+__device__ __forceinline__ float exact_largest(const RopeArgs &a, int t, int u, uint4 xr, uint4 yr, bool is_y,
+                                               const float (&v)[8], float least)
+{
+    uint32_t can = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) can |= fabsf(v[i]) >= least ? 1u << i : 0u;
+    float m = 0.f;
+    for (; can; can &= can - 1) m = fmaxf(m, fabsf(exact_of<HALF>(a, t, u, xr, yr, is_y, __ffs(can) - 1)));
+    return m;
 }
 
 // The rotated values of this lane's 16 dims (x, y as loaded) as 64-bit
 // arithmetic gives them, rounded once to fp32, for a whole warp: a lane works out
-// the angles that it works out in 32 bits, the others come from their lanes. Not
-// inlined: it is rare.
+// the angles that it works out in 32 bits, the others come from their lanes. For
+// groups far beyond the largest scale, infinities and NaN; not inlined.
 template <int D, bool HALF>
 __device__ __noinline__ void rotate_exactly(const RopeArgs &a, int t, uint4 xr, uint4 yr, float (&x)[8], float (&y)[8])
 {
@@ -173,8 +237,9 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float r)
 }
 
 // Codes of a lane's eight rotated values t = x r, each known to within `off` times
-// its pair's |x| + |other|: flags what another x within that could change.
-__device__ __forceinline__ uint32_t codes_within(const float (&x)[8], const float (&other)[8], float r, float off, bool &unsure)
+// its pair's |x| + |other|. unsure: the lowest bits of the codes that another x
+// within that could change.
+__device__ __forceinline__ uint32_t codes_within(const float (&x)[8], const float (&other)[8], float r, float off, uint32_t &unsure)
 {
     float lo[8], hi[8];
     const float o = off * r;
@@ -188,7 +253,8 @@ __device__ __forceinline__ uint32_t codes_within(const float (&x)[8], const floa
         put(hi, i, add2(t, e));
     }
     const uint32_t l = f32x8_to_e2m1(lo), h = f32x8_to_e2m1(hi);
-    unsure |= ((l ^ h) & 0x77777777u) != 0;  // (ends with different signs are both zero: see small enough, below)
+    const uint32_t d = l ^ h;  // (ends with different signs are both zero: see small enough, below)
+    unsure = (d | d >> 1 | d >> 2) & 0x11111111u;
     return plain_zeros(l);
 }
 
@@ -382,13 +448,20 @@ k_rope_axes(const __grid_constant__ RopeArgs a, int parts)
                     // largest elements of the two groups, and by how much they may be off
                     const float mx = largest8(x), my = largest8(y);
                     float gx = max_nan(mx, my), gy = gx, ex = turned && !exact ? 2.f * gx * off : 0.f, ey = ex;
+                    // (x and y: two eights of one group, or of two whose other eights lie in other lanes)
+                    auto others = [&](float p, float q, float &of_x, float &of_y) {
+                        const float xx = __shfl_sync(kFull, p, lx), xy = __shfl_sync(kFull, q, lx);
+                        const float yx = __shfl_sync(kFull, p, ly), yy = __shfl_sync(kFull, q, ly);
+                        of_x = ox < 32 ? xx : xy;
+                        of_y = oy < 32 ? yx : yy;
+                    };
                     if constexpr (HALF) {
-                        const float xx = __shfl_sync(kFull, mx, lx), xy = __shfl_sync(kFull, my, lx);
-                        const float yx = __shfl_sync(kFull, mx, ly), yy = __shfl_sync(kFull, my, ly);
+                        float of_x, of_y;
+                        others(mx, my, of_x, of_y);
                         const float fx = __shfl_sync(kFull, ex, lx), fy = __shfl_sync(kFull, ex, ly);
                         if (apart) {
-                            gx = max_nan(mx, ox < 32 ? xx : xy);
-                            gy = max_nan(my, oy < 32 ? yx : yy);
+                            gx = max_nan(mx, of_x);
+                            gy = max_nan(my, of_y);
                             ey = fmaxf(ex, fy);
                             ex = fmaxf(ex, fx);
                         }
@@ -397,34 +470,55 @@ k_rope_axes(const __grid_constant__ RopeArgs a, int parts)
                     const uint32_t ends_y = f32x2_to_e4m3(max_nan(gy - ey, 0.f) * a.k_inv6, (gy + ey) * a.k_inv6);
                     sx = ends_x & 0xFFu;
                     sy = ends_y & 0xFFu;
-                    const float rx = code_factor(sx, a.k_inv), ry = apart ? code_factor(sy, a.k_inv) : rx;
+                    const bool doubt_x = sx != ends_x >> 8, doubt_y = sy != ends_y >> 8;
+                    float rx = code_factor(sx, a.k_inv), ry = apart ? code_factor(sy, a.k_inv) : rx;
                     if (exact || !__any_sync(kFull, turned)) {
                         wx = codes_of(x, rx);
                         wy = codes_of(y, ry);
                         break;
                     }
-                    // Small enough: stretches of less than a quarter of a code's least border. (Larger ones are of groups whose
-                    // scale is saturated, or of infinities and NaN.)
-                    bool unsure = sx != ends_x >> 8 || sy != ends_y >> 8 || !(ex * rx < 0.06f) || !(ey * ry < 0.06f);
-                    const float mine = turned ? off : 0.f;
-                    if constexpr (HALF) {
-                        wx = codes_within(x, y, rx, mine, unsure);
-                        wy = codes_within(y, x, ry, mine, unsure);
-                    } else {
-                        float x1[8], y1[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            x1[e] = x[e ^ 1];
-                            y1[e] = y[e ^ 1];
+                    // Stretches of less than a quarter of a code's least border are told apart below. (Larger ones are of groups
+                    // far beyond the largest scale, or of infinities and NaN.)
+                    if (!__any_sync(kFull, turned && (!(ex * rx < 0.06f) || !(ey * ry < 0.06f)))) {
+                        if (__any_sync(kFull, doubt_x || doubt_y)) {  // scales first
+                            float px = doubt_x ? exact_largest<HALF>(a, t, u, r.x, r.y, false, x, gx - 2.f * ex) : 0.f;
+                            float py = doubt_y ? exact_largest<HALF>(a, t, u, r.x, r.y, true, y, gy - 2.f * ey) : 0.f;
+                            if constexpr (HALF) {
+                                float of_x, of_y;
+                                others(px, py, of_x, of_y);
+                                px = fmaxf(px, apart ? of_x : py);
+                                py = fmaxf(py, apart ? of_y : px);
+                            } else {
+                                px = py = fmaxf(px, py);
+                            }
+                            if (doubt_x) sx = f32x2_to_e4m3(px * a.k_inv6, 0.f) & 0xFFu;
+                            if (doubt_y) sy = f32x2_to_e4m3(py * a.k_inv6, 0.f) & 0xFFu;
+                            rx = code_factor(sx, a.k_inv);
+                            ry = code_factor(sy, a.k_inv);
                         }
-                        wx = codes_within(x, x1, rx, mine, unsure);
-                        wy = codes_within(y, y1, ry, mine, unsure);
+                        uint32_t x_unsure, y_unsure;
+                        if constexpr (HALF) {
+                            wx = codes_within(x, y, rx, off, x_unsure);
+                            wy = codes_within(y, x, ry, off, y_unsure);
+                        } else {
+                            float x1[8], y1[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                x1[e] = x[e ^ 1];
+                                y1[e] = y[e ^ 1];
+                            }
+                            wx = codes_within(x, x1, rx, off, x_unsure);
+                            wy = codes_within(y, y1, ry, off, y_unsure);
+                        }
+                        if (!turned) {  // (nothing is off)
+                            wx = codes_of(x, rx);
+                            wy = codes_of(y, ry);
+                        } else if (x_unsure | y_unsure) {
+                            wx = settle<HALF>(a, t, u, r.x, r.y, false, rx, wx, x_unsure);
+                            wy = settle<HALF>(a, t, u, r.x, r.y, true, ry, wy, y_unsure);
+                        }
+                        break;
                     }
-                    if (!turned) {  // (nothing is off)
-                        wx = codes_of(x, rx);
-                        wy = codes_of(y, ry);
-                    }
-                    if (!__any_sync(kFull, turned && unsure)) break;
                     float p[8], q[8];
                     rotate_exactly<D, HALF>(a, t, r.x, r.y, p, q);
 #pragma unroll
