@@ -44,13 +44,13 @@ template <int D, int R>
 struct Attend4 {
     static constexpr int WARPS = D == 256 ? (R == 8 ? 12 : 8) : D == 128 ? 12 : 16;
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int NK = D == 256 ? 1 : 2;    // groups of 16 keys of a warp's step
+    static constexpr int NK = 2;                   // groups of 16 keys of a warp's step
     static constexpr int KT = NK * kKeys;          // its keys
     static constexpr int KEYS = WARPS * KT;        // keys per block of the CTA
     static constexpr int CB = D / 2, SB = D / 16;  // bytes of a row's codes and scales
     static constexpr int CODES = kKeys * CB, SCALES = kKeys * SB;  // ... of 16 keys
     static constexpr int HALF = CODES + SCALES, GROUP = 2 * HALF, STAGE = NK * GROUP;
-    static constexpr int STAGES = D == 256 ? 220 * 1024 / (WARPS * STAGE) : 3;
+    static constexpr int STAGES = D == 256 && R == 8 ? 2 : 3;
     static constexpr int RING = STAGES * STAGE;    // per warp
     static constexpr int OS = D + 4;               // floats between a result's rows
     static constexpr int MERGE = WARPS * R * OS * 4;
@@ -159,24 +159,26 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
     // Groups of 16 rows of the pool are numbered: number x has its codes at x CODES + (its page) PS SB, its scales at
     // x SCALES + (its page + 1) PS CB, with PS rows in a page.
     constexpr int LG = 32 / A::NK, PER_LANE = A::CODES / 16 / LG, SC = A::SCALES / 16;
+    constexpr int SC_ROUNDS = (2 * SC * A::NK + 31) / 32, SC_STEP = 32 / (2 * SC);  // copies of scales, and groups of one
     const int own = lane / LG, chunk0 = lane % LG, sc_own = lane / (2 * SC), sc_kv = lane / SC % 2, sc_chunk = lane % SC;
     const uint8_t *k_lane = a.k + chunk0 * 16, *v_lane = a.v + chunk0 * 16;
     const uint8_t *sc_lane = (sc_kv ? a.v : a.k) + (A::CB << a.page_shift) + sc_chunk * 16;
     const int group_shift = a.page_shift - 4;  // groups of a page
     const uint32_t page_scales = A::SB << a.page_shift, page_codes = A::CB << a.page_shift;
     // Offsets in a stage of what it copies, and of what it loads (a key's or value's words, its scales). A copy's
-    // further chunks follow at fixed distances, those of V from one of two places in turn; so do the keys of a load.
-    constexpr int STEP_ROWS = LG / (D / 32);
+    // further chunks follow at fixed distances, those of V from one of a few places in turn; so do the keys of a load.
+    constexpr int STEP_ROWS = LG / (D / 32), TURNS = D == 64 ? 1 : 8 / STEP_ROWS < PER_LANE ? 8 / STEP_ROWS : PER_LANE;
     const uint32_t k_to = own * A::GROUP + k_at<D>(chunk0 / (D / 32), chunk0 % (D / 32));
     const uint32_t sc_to = sc_own * A::GROUP + sc_kv * A::HALF + A::CODES + sc_chunk * 16;
-    uint32_t v_to[2], v_from[2];
+    uint32_t v_to[TURNS], v_from[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < TURNS; ++i)
         v_to[i] = own * A::GROUP + A::HALF + v_at<D>(chunk0 / (D / 32) + STEP_ROWS * i, chunk0 % (D / 32)) - i * LG * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
         v_from[i] = A::HALF + (D == 64    ? v_at<D>(2 * tq + i, gr >> 2) + 4 * (gr & 3)
                                : D == 128 ? v_at<D>(2 * tq + i, gr >> 1) + 8 * (gr & 1)
                                           : v_at<D>(2 * tq + i, gr));
-    }
     const uint32_t k_from = D == 64 ? k_at<D>(gr, tq >> 1) + 8 * (tq & 1) : k_at<D>(gr, tq);
     const uint32_t k_from2 = D == 256 ? k_at<D>(gr, tq + 4) : 0u;
     const uint32_t ks_from = A::CODES + gr * A::SB + (D == 64 ? tq : 2 * tq);
@@ -247,19 +249,23 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
         // are not there arrive as zeros, which makes their elements zeros: nothing
         // else has to be told apart, codes are finite whatever they are.
         auto issue = [&](uint32_t dst, uint32_t groups, int at) {
-            const uint32_t mine = __shfl_sync(kFull, groups, at + own), sc = __shfl_sync(kFull, groups, (at + sc_own) & 31);
-            const uint32_t x = mine & 0x3FFFFFFu, y = sc & 0x3FFFFFFu;
+            const uint32_t mine = __shfl_sync(kFull, groups, at + own), x = mine & 0x3FFFFFFu;
             const uint64_t off = (uint64_t)x * A::CODES + (uint64_t)(x >> group_shift) * page_scales;
             const uint8_t *ks = k_lane + off, *vs = v_lane + off;
             const bool real = mine >> 26 != 0;
 #pragma unroll
             for (int i = 0; i < PER_LANE; ++i) {
                 cp16_if(real, dst + k_to + i * LG * 16, ks + i * LG * 16);
-                cp16_if(real, dst + v_to[i & 1] + i * LG * 16, vs + i * LG * 16);
+                cp16_if(real, dst + v_to[i % TURNS] + i * LG * 16, vs + i * LG * 16);
             }
-            if (SC * 2 * A::NK == 32 || sc_own < A::NK)
-                cp16(dst + sc_to, sc_lane + ((uint64_t)y * A::SCALES + (uint64_t)(y >> group_shift) * page_codes),
-                     min(max((int)(sc >> 26) * A::SB - 16 * sc_chunk, 0), 16));
+#pragma unroll
+            for (int i = 0; i < SC_ROUNDS; ++i) {
+                const uint32_t sc = __shfl_sync(kFull, groups, (at + sc_own + i * SC_STEP) & 31), y = sc & 0x3FFFFFFu;
+                if (SC * 2 * A::NK >= 32 || sc_own < A::NK)
+                    cp16(dst + sc_to + i * SC_STEP * A::GROUP,
+                         sc_lane + ((uint64_t)y * A::SCALES + (uint64_t)(y >> group_shift) * page_codes),
+                         min(max((int)(sc >> 26) * A::SB - 16 * sc_chunk, 0), 16));
+            }
         };
 
         float o[D / 16][NR][4];
