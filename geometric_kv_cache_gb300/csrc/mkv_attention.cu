@@ -506,9 +506,13 @@ bool takes_chunks(int64_t batch, int64_t heads, int32_t group, int64_t n_tokens,
                   int32_t head_dim, int32_t es)
 {
     const int64_t per_list = (max_q * group + kRows - 1) / kRows - 1, in_all = n_tokens * group / kRows;
+    if (es == 0) {
+        const int64_t half = chunk_tile_rows(head_dim) / 2 / kRows, tiles = per_list + 1;  // (more rows, no fewer further tiles)
+        const int64_t more = heads * std::min(batch * (tiles - std::max<int64_t>(2, (tiles + half - 1) / half)), in_all - in_all / half);
+        return (double)more * (double)(max_len + 2048) * (head_dim * 9 / 16 + 128) > kAgainBytes;
+    }
     const int64_t again = heads * std::min(batch * per_list, in_all);
-    const double row_bytes = es ? head_dim * es : head_dim * 9 / 16;
-    return (double)again * (double)(max_len + 1024) * (row_bytes + 128) > kAgainBytes;
+    return (double)again * (double)(max_len + 1024) * (head_dim * es + 128) > kAgainBytes;
 }
 
 AttnPlan attention_plan(int32_t batch, int32_t heads, int32_t group, int32_t n_tokens, int32_t max_q, int32_t max_len,
