@@ -56,6 +56,7 @@ struct Attend4 {
     static constexpr int MERGE = WARPS * R * OS * 4;
     static constexpr int SMEM = WARPS * RING > MERGE ? WARPS * RING : MERGE;
     static constexpr int NR = R / 8;               // column tiles of rows
+    static constexpr bool EARLY = R == 8 && D <= 128;  // queries of the next tile loaded ahead: else registers spill
     static constexpr int KW = D / 32;              // 32-bit words of codes per lane and key, K
     static constexpr int VW = D / 64 ? D / 64 : 1; // ... V: 8 dims to a word
 };
@@ -146,6 +147,8 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
     __shared__ LineScratch s_line;
     __shared__ int s_shift[kLineShifts];
     __shared__ int4 s_join[2];  // tiles to join: tile, first and last CTA with a part
+    __shared__ Walk s_next;     // after the next step of the walk, and whether it found a tile
+    __shared__ bool s_more;
     __shared__ float2 s_ml[A::WARPS][R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
     Walk w = cut_line<A::KEYS, A::THREADS>(a, R, kLine, s_line, s_shift);
@@ -183,11 +186,79 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
     const uint32_t k_from2 = D == 256 ? k_at<D>(gr, tq + 4) : 0u;
     const uint32_t ks_from = A::CODES + gr * A::SB + (D == 64 ? tq : 2 * tq);
     const uint32_t vs_from = A::HALF + A::CODES + 2 * tq * A::SB + (D == 64 ? gr >> 1 : D == 128 ? gr : 2 * gr);
-    while (w.next<A::KEYS>(a, R)) {
+    // The tile at hand: its blocks, its first and last row's places in the list, its queries as loaded, the groups of
+    // keys to copy next. All of it is fetched before the last tile's results are put together.
+    int first = 0, last = 0, qrow0 = 0, p_lo = 0, p_hi = 0;
+    const int32_t *table = nullptr;
+    uint4 raw[NR][KW];
+    uint32_t groups = 0, next = 0;
+    constexpr int STEPS = 32 / A::NK;  // groups are looked up for so many steps at once
+    const uint32_t ring = saddr(smem) + warp * A::RING;
+    auto key0 = [&](int blk) -> int { return block_key<A::KEYS>(w.t, blk) + warp * A::KT; };
+    // Lane y: the group that it numbers, y groups on from block blk0 -- its number in the pool and, above bit 26, how
+    // many of its keys there are: none where no row sees any of them, or where the page is outside the pool.
+    auto lookup = [&](int blk0) -> uint32_t {
+        const int blk = blk0 + lane / A::NK;
+        if (blk >= last) return 0u;
+        const int s = key0(blk) + lane % A::NK * kKeys;
+        if (s >= w.t.end || (a.window > 0 && s + kKeys - 1 <= p_lo - a.window && s >= a.sinks)) return 0u;
+        const int id = table[s >> a.page_shift];
+        if ((uint32_t)id >= (uint32_t)a.n_pages) {
+            atomicOr(a.status, MKV_DEV_BAD_PAGE);
+            return 0u;
+        }
+        return (uint32_t)((id << group_shift) + ((s & (a.page_size - 1)) >> 4)) | (uint32_t)min(kKeys, w.t.end - s) << 26;
+    };
+    // The copies of a step whose groups are `at` lanes on. Scales of keys that
+    // are not there arrive as zeros, which makes their elements zeros: nothing
+    // else has to be told apart, codes are finite whatever they are.
+    auto issue = [&](uint32_t dst, uint32_t groups, int at) {
+        const uint32_t mine = __shfl_sync(kFull, groups, at + own), x = mine & 0x3FFFFFFu;
+        const uint64_t off = (uint64_t)x * A::CODES + (uint64_t)(x >> group_shift) * page_scales;
+        const uint8_t *ks = k_lane + off, *vs = v_lane + off;
+        const bool real = mine >> 26 != 0;
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i) {
+            cp16_if(real, dst + k_to + i * LG * 16, ks + i * LG * 16);
+            cp16_if(real, dst + v_to[i % TURNS] + i * LG * 16, vs + i * LG * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < SC_ROUNDS; ++i) {
+            const uint32_t sc = __shfl_sync(kFull, groups, (at + sc_own + i * SC_STEP) & 31), y = sc & 0x3FFFFFFu;
+            if (SC * 2 * A::NK >= 32 || sc_own < A::NK)
+                cp16(dst + sc_to + i * SC_STEP * A::GROUP,
+                     sc_lane + ((uint64_t)y * A::SCALES + (uint64_t)(y >> group_shift) * page_codes),
+                     min(max((int)(sc >> 26) * A::SB - 16 * sc_chunk, 0), 16));
+        }
+    };
+
+    auto load_queries = [&]() {  // column gr of each column tile, this lane's dims
         const Tile &t = w.t;
-        const int first = w.from(), last = w.to();
-        const int32_t *table = a.table + ((int64_t)t.b * a.heads + t.j) * a.max_pages;
-        const int qrow0 = a.q_start[t.b];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const int Rq = t.row0 + min(8 * n + gr, t.rows - 1), i = a.by_group(Rq), g = Rq - i * a.group;
+            const uint8_t *src = a.Q + 2 * ((int64_t)(qrow0 + i) * a.q_stride + (int64_t)(t.j * a.group + g) * D);
+#pragma unroll
+            for (int x = 0; x < KW; ++x) raw[n][x] = *reinterpret_cast<const uint4 *>(src + 2 * k_dim(x));
+        }
+    };
+    auto begin_tile = [&]() {
+        const Tile &t = w.t;
+        first = w.from();
+        last = w.to();
+        table = a.table + ((int64_t)t.b * a.heads + t.j) * a.max_pages;
+        qrow0 = a.q_start[t.b];
+        p_lo = t.L - t.n + a.by_group(t.row0);
+        p_hi = t.L - t.n + a.by_group(t.row0 + t.rows - 1);
+        if (A::EARLY) load_queries();
+        groups = lookup(first);
+        next = lookup(first + STEPS);
+    };
+    bool more = w.next<A::KEYS>(a, R);
+    if (more) begin_tile();
+    while (more) {
+        const Tile &t = w.t;
+        if (!A::EARLY) load_queries();
 
         // queries: column gr of each column tile, this lane's dims, as fp16 with a power of two taken out. (They take
         // the scale's sign, and a factor of zero becomes the smallest normal number: zero times a masked score's
@@ -197,15 +268,11 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
         int p[NR][2];     // their places in the list
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const int Rq = t.row0 + min(8 * n + gr, t.rows - 1), i = a.by_group(Rq), g = Rq - i * a.group;
-            const uint8_t *src = a.Q + 2 * ((int64_t)(qrow0 + i) * a.q_stride + (int64_t)(t.j * a.group + g) * D);
             float m = 0.f;
-            uint4 v[KW];
 #pragma unroll
             for (int x = 0; x < KW; ++x) {
-                v[x] = *reinterpret_cast<const uint4 *>(src + 2 * k_dim(x));
                 float f[8];
-                bf16x8_to_f32(v[x], f);
+                bf16x8_to_f32(raw[n][x], f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
             }
@@ -216,7 +283,7 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
 #pragma unroll
             for (int x = 0; x < KW; ++x) {
                 float f[8];
-                bf16x8_to_f32(v[x], f);
+                bf16x8_to_f32(raw[n][x], f);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) q[n][2 * x + (e >> 1)][e & 1] = pack_f16(f[2 * e] * down, f[2 * e + 1] * down);
             }
@@ -226,48 +293,6 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
                 p[n][c] = t.L - t.n + a.by_group(t.row0 + min(8 * n + 2 * tq + c, t.rows - 1));
             }
         }
-        // places of the tile's first and last row
-        const int p_lo = t.L - t.n + a.by_group(t.row0), p_hi = t.L - t.n + a.by_group(t.row0 + t.rows - 1);
-
-        const uint32_t ring = saddr(smem) + warp * A::RING;
-        auto key0 = [&](int blk) -> int { return block_key<A::KEYS>(t, blk) + warp * A::KT; };
-        // Lane y: the group that it numbers, y groups on from block blk0 -- its number in the pool and, above bit 26, how
-        // many of its keys there are: none where no row sees any of them, or where the page is outside the pool.
-        auto lookup = [&](int blk0) -> uint32_t {
-            const int blk = blk0 + lane / A::NK;
-            if (blk >= last) return 0u;
-            const int s = key0(blk) + lane % A::NK * kKeys;
-            if (s >= t.end || (a.window > 0 && s + kKeys - 1 <= p_lo - a.window && s >= a.sinks)) return 0u;
-            const int id = table[s >> a.page_shift];
-            if ((uint32_t)id >= (uint32_t)a.n_pages) {
-                atomicOr(a.status, MKV_DEV_BAD_PAGE);
-                return 0u;
-            }
-            return (uint32_t)((id << group_shift) + ((s & (a.page_size - 1)) >> 4)) | (uint32_t)min(kKeys, t.end - s) << 26;
-        };
-        // The copies of a step whose groups are `at` lanes on. Scales of keys that
-        // are not there arrive as zeros, which makes their elements zeros: nothing
-        // else has to be told apart, codes are finite whatever they are.
-        auto issue = [&](uint32_t dst, uint32_t groups, int at) {
-            const uint32_t mine = __shfl_sync(kFull, groups, at + own), x = mine & 0x3FFFFFFu;
-            const uint64_t off = (uint64_t)x * A::CODES + (uint64_t)(x >> group_shift) * page_scales;
-            const uint8_t *ks = k_lane + off, *vs = v_lane + off;
-            const bool real = mine >> 26 != 0;
-#pragma unroll
-            for (int i = 0; i < PER_LANE; ++i) {
-                cp16_if(real, dst + k_to + i * LG * 16, ks + i * LG * 16);
-                cp16_if(real, dst + v_to[i % TURNS] + i * LG * 16, vs + i * LG * 16);
-            }
-#pragma unroll
-            for (int i = 0; i < SC_ROUNDS; ++i) {
-                const uint32_t sc = __shfl_sync(kFull, groups, (at + sc_own + i * SC_STEP) & 31), y = sc & 0x3FFFFFFu;
-                if (SC * 2 * A::NK >= 32 || sc_own < A::NK)
-                    cp16(dst + sc_to + i * SC_STEP * A::GROUP,
-                         sc_lane + ((uint64_t)y * A::SCALES + (uint64_t)(y >> group_shift) * page_codes),
-                         min(max((int)(sc >> 26) * A::SB - 16 * sc_chunk, 0), 16));
-            }
-        };
-
         float o[D / 16][NR][4];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -280,9 +305,6 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
             l[n][0] = l[n][1] = 0.f;
         }
 
-        // groups are looked up for STEPS steps at once, the next ones while these are copied
-        constexpr int STEPS = 32 / A::NK;
-        uint32_t groups = lookup(first), next = lookup(first + STEPS);
         int at = 0;  // the next step to copy: its place among `groups`
         auto copy_step = [&](uint32_t dst) {
             issue(dst, groups, at);
@@ -292,6 +314,14 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
         const uint32_t ring_end = ring + A::RING;
 #pragma unroll
         for (int s = 0; s < A::STAGES - 1; ++s) copy_step(ring + s * A::STAGE);  // (past the last block: zeros alone)
+        if (warp == 0) {  // where the walk goes on, while the first keys are on their way
+            Walk x = w;
+            const bool found = x.next<A::KEYS>(a, R);
+            if (lane == 0) {
+                s_next = x;
+                s_more = found;
+            }
+        }
         uint32_t stage = ring, fill = ring_end - A::STAGE;
         for (int blk = first; blk < last; ++blk, fill = stage, stage = stage + A::STAGE == ring_end ? ring : stage + A::STAGE) {
             copy_step(fill);
@@ -476,8 +506,16 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
                     *reinterpret_cast<float4 *>(mine + r * A::OS + gr * (D / 8) + 2 * i) =
                         make_float4(o[i][n][c], o[i][n][2 + c], o[i + 1][n][c], o[i + 1][n][2 + c]);
             }
+        struct {
+            int rows, row0, j, qrow0, first, last, units, tile;
+            int64_t part;
+            bool whole;
+        } const done = {t.rows, t.row0, t.j, qrow0, w.first, w.last, w.units, w.tile - 1, part_row(w, R), w.whole()};
+        more = s_more;
+        w = s_next;
+        if (more) begin_tile();
         __syncthreads();
-        for (int x = threadIdx.x; x < t.rows * (D / 4); x += A::THREADS) {
+        for (int x = threadIdx.x; x < done.rows * (D / 4); x += A::THREADS) {
             const int r = x / (D / 4), c = x % (D / 4);
             float M = -CUDART_INF_F;
 #pragma unroll
@@ -495,32 +533,32 @@ k_attend_e2m1(const __grid_constant__ AttnArgs a)
                 sum.w += f * v.w;
                 total += f * ml.y;
             }
-            if (!w.whole()) {
-                const int64_t part = part_row(w, R) + r;
+            if (!done.whole) {
+                const int64_t part = done.part + r;
                 reinterpret_cast<float4 *>(a.part_o)[part * (D / 4) + c] = sum;
                 if (c == 0) a.part_ml[part] = make_float2(M, total);
                 continue;
             }
             const float inv = inverse_sum(total, a.v_scale);
-            const int Rq = t.row0 + r, i = a.by_group(Rq), head = t.j * a.group + Rq - i * a.group;
-            *reinterpret_cast<uint2 *>(a.O + 2 * ((int64_t)(qrow0 + i) * a.o_stride + (int64_t)head * D + 4 * c)) =
+            const int Rq = done.row0 + r, i = a.by_group(Rq), head = done.j * a.group + Rq - i * a.group;
+            *reinterpret_cast<uint2 *>(a.O + 2 * ((int64_t)(done.qrow0 + i) * a.o_stride + (int64_t)head * D + 4 * c)) =
                 make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
-            if (c == 0 && a.lse) a.lse[(int64_t)(qrow0 + i) * a.q_heads + head] = log_sum(M, total);
+            if (c == 0 && a.lse) a.lse[(int64_t)(done.qrow0 + i) * a.q_heads + head] = log_sum(M, total);
         }
         __syncthreads();  // the next segment's copies may overwrite the results
-        if (!w.whole() && threadIdx.x == 0) {
+        if (!done.whole && threadIdx.x == 0) {
             // Parts of a tile count themselves in a byte of the workspace's head,
             // which the last one takes back to zero; it joins the parts below.
-            const int unit0 = at_unit - w.first, c0 = cta_of(unit0, s_line), c1 = cta_of(unit0 + w.units - 1, s_line);
+            const int unit0 = at_unit - done.first, c0 = cta_of(unit0, s_line), c1 = cta_of(unit0 + done.units - 1, s_line);
             uint32_t *word = a.counts + c0 / 4;
             const int shift = c0 % 4 * 8;
             __threadfence();
             if ((int)(atomicAdd(word, 1u << shift) >> shift & 255u) == c1 - c0) {
                 atomicSub(word, (uint32_t)(c1 - c0 + 1) << shift);
-                s_join[w.first > 0 ? 0 : 1] = make_int4(w.tile - 1, c0, c1, 0);
+                s_join[done.first > 0 ? 0 : 1] = make_int4(done.tile, c0, c1, 0);
             }
         }
-        at_unit += w.last - w.first;
+        at_unit += done.last - done.first;
     }
     __syncthreads();
     for (int k = 0; k < 2; ++k) {  // (a CTA's first segment and its last one)
