@@ -18,6 +18,19 @@
 // The split of work is that of the other form: tiles of packed rows, the line of
 // key blocks cut over 152 CTAs, a ring of cp.async stages per warp, the parts of
 // cut tiles joined by the CTA that comes last (mkv_attention.cuh).
+//
+// Measured (128 dims, group 4): 64 rows x 8 heads of 4K-16K tokens 143 us (floor 111),
+// two rows of 120K-131K tokens x 10 heads 69 (53), one row of 2K tokens x 8 heads 9. The
+// copies alone take 117 us of the 143, the arithmetic alone 129. What bounds the
+// arithmetic: 16 keys are 225 instructions without their copies -- 64 conversions
+// and 64 products at two a cycle and SM, 16 MMAs -- and of their mix an SM executes 2.1
+// a cycle, with 12 warps or with 16 (4 conversions, 4 products and an MMA that depends on
+// them take 5 cycles by themselves); 108 cycles where the bytes of the 16 keys take
+// 102. Steps on the way (64 rows): 16 keys per step and lookups and
+// addresses for each, 199 us, of its 410 instructions 107 for the copies; 32 keys, pages looked
+// up for 16 steps at once, one address per lane 154; a lane's places computed once 146; 12
+// warps instead of 16 143. 64 keys per step 142 (and one row of 2K tokens 10 instead of 9);
+// 14 warps, which share the SM's four parts unevenly, 157; 8 warps 157.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <float.h>

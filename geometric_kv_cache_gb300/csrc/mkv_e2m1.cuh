@@ -63,7 +63,7 @@ __device__ __forceinline__ float largest8(const float (&f)[8])
     return m;
 }
 
-// E4M3 codes of two fp32 >= 0 (to nearest, saturated at 448; NaN stays NaN), a in the lower byte.
+// E4M3 codes of two fp32 (to nearest, saturated at 448; NaN stays NaN), a in the lower byte.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3(float a, float b)
 {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
