@@ -233,3 +233,53 @@ def test_two_calls_at_once_on_their_own_workspaces():
     for p, s, ws in zip(problems, sets, spaces):
         assert mkv.mkv_device_status(ws) == 0
         p.check(s[6].cpu(), s[7].cpu())
+
+
+@pytest.mark.parametrize("dtype", [BF, U8])
+@pytest.mark.parametrize("start", [[0, 5, 3, 9], [-2, 1, 3, 9], [0, 3, 6, 1000], [9, 6, 3, 0]])
+def test_bad_row_starts_write_inside_the_lists_only(dtype, start):
+    p = Step(9, [3, 3, 3], 1, 2, 64, 16, dtype, 2)
+    p.start = torch.tensor(start, dtype=torch.int32)
+    p.lens.clamp_(min=9)
+    axes, inv_freq = mkv.mkv_rope_axes([16, 16]), mkv.mkv_rope_frequencies(64, 10000.0)
+    _, k, v = p.run(inv_freq, axes, "half", 1.0, (1.0, 1.0) if dtype is BF else (0.013, 0.3))
+    assert p.status & mkv.MKV_DEV_BAD_TOKENS
+    assert p.status & ~(mkv.MKV_DEV_BAD_TOKENS | mkv.MKV_DEV_BAD_SEQ_LEN | mkv.MKV_DEV_BAD_PAGE) == 0
+    held = torch.zeros(k.shape[0], dtype=torch.bool)
+    for b in range(3):
+        for q in p.table[b, 0, :pu.pages_of(int(p.lens[b, 0]), 16)].tolist():
+            if 0 <= q < len(held):
+                held[q] = True
+    raw = lambda x: x.view(torch.int16) if x.dtype is BF else x  # noqa: E731
+    for got, old in ((k, p.k), (v, p.v)):
+        assert torch.equal(raw(got)[~held], raw(old)[~held])
+
+
+@pytest.mark.parametrize("rows", [33, 1100])
+def test_many_rows(rows):
+    rng = random.Random(rows)
+    counts = [rng.choice([0, 0, 1, 2]) for _ in range(rows)]
+    p = Step(10, counts, 1, 1, 64, 16, U8, 2, pad_front=2, pad_back=3)
+    axes, inv_freq = mkv.mkv_rope_axes([16, 16]), mkv.mkv_rope_frequencies(64, 10000.0)
+    res = p.run(inv_freq, axes, "half", 1.0, (0.013, 0.3))
+    assert p.status == 0
+    p.check(res, inv_freq, axes, "half", 1.0, (0.013, 0.3))
+
+
+def test_no_tokens_no_lists_and_empty_lists():
+    d, z = 128, lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)  # noqa: E731
+    k, v = mkv.e2m1_pages(4, 16, d), mkv.e2m1_pages(4, 16, d)
+    none = torch.empty((0, 8, d), dtype=BF, device=DEV)
+    ws = mkv.page_workspace_for(k, z(2, 2, 1))
+    freq, axes = mkv.mkv_rope_frequencies(d, 10000.0).to(DEV), mkv.mkv_rope_axes([32, 32]).to(DEV)
+    mkv.mkv_rope_append_axes(none, none[:, :2], none[:, :2], z(2, 0), axes, freq, k, v, z(2, 2, 1), z(2, 2), z(3), none, ws)
+    K = torch.empty((2, 2, 0, d), dtype=BF, device=DEV)
+    refs, out, lens_out = z(4), z(2, 2, 1) + 9, z(2, 2) + 9
+    mkv.mkv_page_quantize(k, v, z(2, 2, 1), z(2, 2), refs, None, z(2, 2), K, K, out, lens_out, refs, ws)
+    assert mkv.mkv_device_status(ws) == 0 and int(lens_out.sum()) == 0 and int(refs.sum()) == 0 and (out == 9).all()
+    # rows with one new token each in lists that are empty: they see nothing
+    Q = torch.randn((2, 8, d), device=DEV).to(BF)
+    O, lse = torch.full_like(Q, 7.0), torch.full((2, 8), 7.0, device=DEV)
+    wa = mkv.attention_workspace_for(Q, k, z(2, 2, 1), 1, 16)
+    mkv.mkv_paged_attention(Q, k, v, z(2, 2, 1), z(2, 2), torch.arange(3, dtype=torch.int32, device=DEV), 1, 16, O, wa, lse=lse)
+    assert mkv.mkv_device_status(wa) == 0 and int((O != 0).sum()) == 0 and bool((lse == -math.inf).all())

@@ -172,13 +172,14 @@ def test_axes(dtype, layout, dealt, d, sections, H, G, page):
 
 
 @pytest.mark.parametrize("dtype", [BF, F8, U8])
-def test_axes_that_agree_give_the_bits_of_one(dtype):
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_axes_that_agree_give_the_bits_of_one(dtype, layout):
     p = Step(2, [17, 1, 300], 4, 3, 128, 16, dtype, 3)
     p.positions[1:] = p.positions[0]
     inv_freq, scales = mkv.mkv_rope_frequencies(128, 10000.0), _scales(dtype)
-    one = p.run(inv_freq, None, "half", 1.1, scales)
+    one = p.run(inv_freq, None, layout, 1.1, scales)
     for axes in (mkv.mkv_rope_axes([22, 21, 21], True), torch.zeros(64, dtype=torch.int32)):
-        three = p.run(inv_freq, axes, "half", 1.1, scales)
+        three = p.run(inv_freq, axes, layout, 1.1, scales)
         assert p.status == 0
         for x, y in zip(one, three):
             assert torch.equal(x.view(U8), y.view(U8))
