@@ -93,9 +93,10 @@ __device__ __forceinline__ long long warp_sum(long long v)
 }
 
 // The holders of this thread's pages of a chunk, consecutive ones; -1 past the pool.
-__device__ __forceinline__ void load_refs(const PageArgs &a, int chunk, int (&r)[kPlanPages / kPageThreads])
+constexpr int kThreadPages = kPlanPages / kPageThreads;
+__device__ __forceinline__ void load_refs(const PageArgs &a, int chunk, int (&r)[kThreadPages])
 {
-    constexpr int N = kPlanPages / kPageThreads;
+    constexpr int N = kThreadPages;
     const int64_t p0 = (int64_t)chunk * kPlanPages + threadIdx.x * N;
     if (p0 + N <= a.n_pages && (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0) {
 #pragma unroll
@@ -113,8 +114,8 @@ __device__ __forceinline__ void load_refs(const PageArgs &a, int chunk, int (&r)
 }
 
 // Chunk c of the rows, or after them of the pool: what its lists need, what is
-// free.
-__device__ __forceinline__ void count_chunk(const PageArgs &a, int c)
+// free. r: the chunk's holders (of the pool's chunks).
+__device__ __forceinline__ void count_chunk(const PageArgs &a, int c, int (&r)[kThreadPages])
 {
     __shared__ long long s_need[kPlanRows];
     __shared__ uint32_t s_bits[kPlanRows];
@@ -198,10 +199,10 @@ __device__ __forceinline__ void count_chunk(const PageArgs &a, int c)
         }
     } else {
         const int chunk = c - a.row_chunks;
-        int r[kPlanPages / kPageThreads], n = 0;
+        int n = 0;
         load_refs(a, chunk, r);
 #pragma unroll
-        for (int i = 0; i < kPlanPages / kPageThreads; ++i) n += r[i] == 0;
+        for (int i = 0; i < kThreadPages; ++i) n += r[i] == 0;
         n = __reduce_add_sync(kFull, n);
         if (lane == 0) s_free[warp] = n;
         __syncthreads();
@@ -243,7 +244,7 @@ __device__ __forceinline__ void block_sums(long long &x, long long &y, long long
 
 // The same chunk, once all are counted: its lists' first ranks among the new
 // pages, or its free pages by rank. Chunk 0 writes the verdict.
-__device__ __forceinline__ void assign_chunk(const PageArgs &a, int c)
+__device__ __forceinline__ void assign_chunk(const PageArgs &a, int c, const int (&r)[kThreadPages])
 {
     __shared__ uint32_t scratch[kPageThreads / 32];
     __shared__ long long s_row[kPlanRows];
@@ -264,6 +265,17 @@ __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c)
         free_pages += n;
         if (!rows && i < chunk) before += n;
     }
+    // (a row's first lists are looked up while the sums are made)
+    const int64_t b = (int64_t)chunk * kPlanRows + warp;
+    int2 src = make_int2(-1, 0);
+    int pages = 0;
+    if (rows && b < a.batch) {
+        src = a.row_src[b];
+        if (lane < a.heads) {
+            const ListPlan p = plan_list(a, (int)b, lane, src.x, src.y != 0);
+            pages = p.total - p.shared;
+        }
+    }
     block_sums(need, free_pages, before, bits);
     if (need > free_pages) bits |= MKV_DEV_NO_PAGES;
     if (c == 0 && threadIdx.x == 0) {
@@ -273,11 +285,9 @@ __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c)
     }
     if (rows) {
         if (bits) return;  // no list gets a page
-        const int64_t b = (int64_t)chunk * kPlanRows + warp;
-        const int2 src = b < a.batch ? a.row_src[b] : make_int2(-1, 0);
-        long long row = 0;
+        long long row = pages;
         if (b < a.batch)
-            for (int j = lane; j < a.heads; j += 32) {
+            for (int j = 32 + lane; j < a.heads; j += 32) {
                 const ListPlan p = plan_list(a, (int)b, j, src.x, src.y != 0);
                 row += p.total - p.shared;
             }
@@ -289,8 +299,8 @@ __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c)
         if (b >= a.batch) return;
         for (int j0 = 0; j0 < a.heads; j0 += 32) {
             const int j = j0 + lane;
-            int n = 0;
-            if (j < a.heads) {
+            int n = j0 ? 0 : pages;
+            if (j0 && j < a.heads) {
                 const ListPlan p = plan_list(a, (int)b, j, src.x, src.y != 0);
                 n = p.total - p.shared;
             }
@@ -309,10 +319,9 @@ __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c)
             off += __shfl_sync(kFull, x, 31);
         }
     } else {
-        constexpr int N = kPlanPages / kPageThreads;
+        constexpr int N = kThreadPages;
         const int64_t p0 = (int64_t)chunk * kPlanPages + threadIdx.x * N;
-        int r[N], n = 0;
-        load_refs(a, chunk, r);
+        int n = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) n += r[i] == 0;
         if (a.refs_out != a.refs) {
@@ -341,28 +350,20 @@ __global__ void __launch_bounds__(kPageThreads)
 k_page_count(const PageArgs a)
 {
     pdl_trigger();
-    count_chunk(a, (int)blockIdx.x);
+    int r[kThreadPages];
+    count_chunk(a, (int)blockIdx.x, r);
 }
 
+// (The call's inputs are there before k_page_count starts, which is nobody's
+// programmatic dependent: the launches after it read them before they wait.)
 __global__ void __launch_bounds__(kPageThreads)
 k_page_assign(const PageArgs a)
 {
     pdl_trigger();
+    int r[kThreadPages];
+    if ((int)blockIdx.x >= a.row_chunks) load_refs(a, (int)blockIdx.x - a.row_chunks, r);
     pdl_wait();
-    assign_chunk(a, (int)blockIdx.x);
-}
-
-// Both in one launch of one cluster, for problems of few chunks.
-__global__ void __launch_bounds__(kPageThreads)
-k_page_plan(const PageArgs a)
-{
-    pdl_trigger();
-    const bool mine = (int)blockIdx.x < a.row_chunks + a.page_chunks;
-    if (mine) count_chunk(a, (int)blockIdx.x);
-    __syncthreads();
-    // every CTA's counts are there
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (mine) assign_chunk(a, (int)blockIdx.x);
+    assign_chunk(a, (int)blockIdx.x, r);
 }
 
 __device__ __forceinline__ void add_ref(const PageArgs &a, int page, int by)
@@ -373,51 +374,104 @@ __device__ __forceinline__ void add_ref(const PageArgs &a, int page, int by)
         atomicOr(a.status, MKV_DEV_BAD_PAGE);
 }
 
-// One warp per list.
-__global__ void __launch_bounds__(kPageThreads)
-k_page_update(const PageArgs a)
+// What an update reads of its list h before it has the plan: its length, the list
+// that it goes on with (src -1: none), that one's length and last page, the new tokens,
+// and this lane's first pages of that list and, where they are given up, of its own
+// (kAhead of each; a loop of single ones waits for memory at every step).
+constexpr int kAhead = 4;
+struct ListInputs {
+    int own_len, src, old_len, add, last;
+    int from[kAhead], own[kAhead];
+};
+__device__ __forceinline__ void load_ids(const int32_t *ids, int p0, int n, int (&id)[kAhead])
 {
-    pdl_wait();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) id[i] = p0 + 32 * i < n ? ids[p0 + 32 * i] : -1;
+}
+
+__device__ __forceinline__ ListInputs update_inputs(const PageArgs &a, int64_t h)
+{
+    const int b = (int)(h / a.heads), j = (int)(h - (int64_t)b * a.heads);
+    ListInputs in;
+    in.own_len = a.lens[h];
+    in.add = a.n_new ? a.n_new[b] : 0;
+    in.src = b;
+    if (a.parent) {
+        in.src = a.parent[b];
+        if (in.src < -1 || in.src >= a.batch) in.src = -1;
+    }
+    const int64_t s = (int64_t)max(in.src, 0) * a.heads + j;
+    in.old_len = in.src == b ? in.own_len : in.src >= 0 ? a.lens[s] : 0;
     const int lane = threadIdx.x & 31;
-    const int64_t h = ((int64_t)blockIdx.x * kPageThreads + threadIdx.x) >> 5;
-    if (h >= (int64_t)a.batch * a.heads) return;
+    const bool good = len_ok(in.old_len, a);
+    in.last = in.src != b && good && (in.old_len & (a.page_size - 1)) ? a.table[s * a.max_pages + (in.old_len >> a.page_shift)] : -1;
+    load_ids(a.table + s * a.max_pages, lane, good && a.lens_out != a.lens ? pages_of(in.old_len, a) : 0, in.from);
+    load_ids(a.table + h * a.max_pages, lane, in.src != b && len_ok(in.own_len, a) ? pages_of(in.own_len, a) : 0, in.own);
+    return in;
+}
+
+// List h by one warp, once all chunks are assigned.
+__device__ __forceinline__ void update_list(const PageArgs &a, int64_t h, const ListInputs &in)
+{
+    const int lane = threadIdx.x & 31;
     const int b = (int)(h / a.heads), j = (int)(h - (int64_t)b * a.heads);
     const bool in_place = a.lens_out == a.lens;  // (lists without capacity may have no tables at all)
     const int32_t *mine = a.table + h * a.max_pages;
     int32_t *out = a.table_out + h * a.max_pages;
     // (read together; the last two mean nothing after a bad verdict)
-    const int own_len = a.lens[h];
     const uint32_t verdict = a.verdict[0];
     const int2 src = a.row_src[b];
     const int first = a.list_off[h];
     if (verdict) {  // the lists stay as they were
         if (in_place) return;
-        if (lane == 0) a.lens_out[h] = own_len;
-        if (len_ok(own_len, a))
-            for (int p = lane; p < pages_of(own_len, a); p += 32) out[p] = mine[p];
+        if (lane == 0) a.lens_out[h] = in.own_len;
+        if (len_ok(in.own_len, a))
+            for (int p = lane; p < pages_of(in.own_len, a); p += 32) out[p] = mine[p];
         return;
     }
-    const bool keeps = src.y != 0, moved = src.x != b;
-    const ListPlan lp = plan_list(a, b, j, src.x, keeps);
-    const int32_t *from = a.table + ((int64_t)(src.x < 0 ? b : src.x) * a.heads + j) * a.max_pages;
+    const bool keeps = src.y != 0, moved = in.src != b;
+    const int len = in.src < 0 ? 0 : in.old_len + in.add;
+    const int shared = keeps ? pages_of(in.old_len, a) : in.old_len >> a.page_shift, total = pages_of(len, a);
+    const int32_t *from = a.table + ((int64_t)(in.src < 0 ? b : in.src) * a.heads + j) * a.max_pages;
     __syncwarp();
     if (!in_place)
-        for (int p = lane; p < lp.shared; p += 32) {
-            const int id = from[p];
-            out[p] = id;
-            if (moved) add_ref(a, id, 1);
+        for (int p0 = lane; p0 < shared; p0 += 32 * kAhead) {
+            int id[kAhead];
+            if (p0 == lane) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) id[i] = in.from[i];
+            } else {
+                load_ids(from, p0, shared, id);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (p0 + 32 * i < shared) {
+                    out[p0 + 32 * i] = id[i];
+                    if (moved) add_ref(a, id[i], 1);
+                }
         }
-    for (int p = lp.shared + lane; p < lp.total; p += 32) {
-        const int id = a.free_ids[first + p - lp.shared];
+    for (int p = shared + lane; p < total; p += 32) {
+        const int id = a.free_ids[first + p - shared];
         out[p] = id;
         atomicAdd(a.refs_out + id, 1);
     }
     if (moved)  // nobody continues this list under its own row: its holder goes
-        for (int p = lane; p < pages_of(own_len, a); p += 32) add_ref(a, mine[p], -1);
-    if (lane == 0) a.lens_out[h] = lp.len;
-    const int rest = lp.old_len & (a.page_size - 1);
+        for (int p0 = lane, n = pages_of(in.own_len, a); p0 < n; p0 += 32 * kAhead) {
+            int id[kAhead];
+            if (p0 == lane) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) id[i] = in.own[i];
+            } else {
+                load_ids(mine, p0, n, id);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (p0 + 32 * i < n) add_ref(a, id[i], -1);
+        }
+    if (lane == 0) a.lens_out[h] = len;
+    const int rest = in.old_len & (a.page_size - 1);
     if (!keeps && rest > 0) {  // a copy of the partly filled last page
-        const int s = from[lp.shared], d = a.free_ids[first];
+        const int s = in.last, d = a.free_ids[first];
         if ((uint32_t)s >= (uint32_t)a.n_pages) {
             if (lane == 0) atomicOr(a.status, MKV_DEV_BAD_PAGE);
             return;
@@ -450,6 +504,48 @@ k_page_update(const PageArgs a)
                     st_v4(vd + o + 512 * u, y[u]);
                 }
         }
+    }
+}
+
+// One warp per list.
+__global__ void __launch_bounds__(kPageThreads)
+k_page_update(const PageArgs a)
+{
+    const int64_t h = ((int64_t)blockIdx.x * kPageThreads + threadIdx.x) >> 5;
+    const bool some = h < (int64_t)a.batch * a.heads;
+    ListInputs in;
+    if (some) in = update_inputs(a, h);
+    pdl_wait();
+    if (some) update_list(a, h, in);
+}
+
+// What every CTA of the cluster wrote is there for all.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Counts and places in one launch of one cluster, for problems of few chunks. UPDATE:
+// the lists as well, one per warp.
+template <bool UPDATE>
+__global__ void __launch_bounds__(kPageThreads)
+k_page_plan(const PageArgs a)
+{
+    if (!UPDATE) pdl_trigger();
+    const bool mine = (int)blockIdx.x < a.row_chunks + a.page_chunks;
+    const int64_t h = ((int64_t)blockIdx.x * kPageThreads + threadIdx.x) >> 5;
+    const bool some = UPDATE && h < (int64_t)a.batch * a.heads;
+    ListInputs in;
+    if (some) in = update_inputs(a, h);
+    int r[kThreadPages];
+    if (mine) count_chunk(a, (int)blockIdx.x, r);
+    __syncthreads();
+    cluster_sync();
+    if (mine) assign_chunk(a, (int)blockIdx.x, r);
+    if (UPDATE) {
+        __syncthreads();
+        cluster_sync();
+        if (some) update_list(a, h, in);
     }
 }
 
@@ -529,7 +625,8 @@ k_page_compact(const PageArgs a, int list_ctas)
     const int64_t lists = (int64_t)a.batch * a.heads;
     if ((int)blockIdx.x < list_ctas) {
         for (int64_t h = blockIdx.x; h < lists; h += list_ctas) {
-            const int own_len = a.lens[h], n = bad ? 0 : a.kept[h], first = bad ? 0 : a.list_off[h];
+            // (read together; the last means nothing after a bad verdict)
+            const int own_len = a.lens[h], kept = a.kept[h], first = a.list_off[h], n = bad ? 0 : kept;
             const int32_t *mine = a.table + h * a.max_pages;
             int32_t *out = a.table_out + h * a.max_pages;
             if (threadIdx.x == 0) a.lens_out[h] = bad ? own_len : n;
@@ -546,31 +643,45 @@ k_page_compact(const PageArgs a, int list_ctas)
         }
         return;
     }
-    if (bad) return;
     const int lane = threadIdx.x & 31, g = lane / LPR, lr = lane % LPR;
     const int per_shift = a.page_shift - 4;  // items of a page
     const int64_t warps = (int64_t)(gridDim.x - list_ctas) * (kPageThreads / 32);
     const int64_t warp = (int64_t)(blockIdx.x - list_ctas) * (kPageThreads / 32) + (threadIdx.x >> 5);
-    const int64_t items = (int64_t)a.verdict[1] << per_shift;  // pages taken
+    // a page that is taken: its list, its place in it, its number (list -1: none)
+    struct Owner {
+        int h, at, page;
+    };
     // (of item x of the warps' count this lane has item x ITEMS + lane / kItem, which lanes of no item do not look up)
-    auto owner = [&](int64_t x) -> int2 {
-        const int64_t item = ITEMS == 1 ? x : x * ITEMS + lane / kItem;
-        return item < items ? a.owners[item >> per_shift] : make_int2(-1, 0);
+    auto owner = [&](int64_t x, int64_t pages) -> Owner {
+        const int64_t page = (ITEMS == 1 ? x : x * ITEMS + lane / kItem) >> per_shift;
+        if (page >= pages) return {-1, 0, 0};
+        const int2 o = a.owners[page];
+        return {o.x, o.y, a.free_ids[page]};
     };
-    // an item: its list, its new page's rank, and this lane's token of it with its source (-1: none)
+    // (the first ones come with the verdict; what lies behind the pages taken is dropped)
+    const int64_t room = min((int64_t)a.n_pages, lists * a.max_pages);
+    Owner first = owner(warp, room), second = owner(warp + warps, room);
+    const int64_t taken = a.verdict[1], items = taken << per_shift;
+    if (bad) return;
+    auto drop = [&](int64_t x, Owner &o) {
+        if ((ITEMS == 1 ? x : x * ITEMS + lane / kItem) >= items) o = {-1, 0, 0};
+    };
+    drop(warp, first);
+    drop(warp + warps, second);
+    // an item: its list, its new page, and this lane's token of it with its source (-1: none)
     struct Item {
-        int h, rank, i, s;
+        int h, page, i, s;
     };
-    auto source = [&](int64_t x, int2 own) -> Item {
+    auto source = [&](int64_t x, Owner own) -> Item {
         const int64_t item = ITEMS == 1 ? x : x * ITEMS + lane / kItem;
-        Item it = {own.x, (int)(item >> per_shift), -1, -1};
-        if (own.x < 0 || lane >= ITEMS * kItem) return it;
-        const int64_t h = own.x;
-        const int i = (own.y << a.page_shift) + (int)(item & ((1 << per_shift) - 1)) * kItem + lane % kItem;
+        Item it = {own.h, own.page, -1, -1};
+        if (own.h < 0 || lane >= ITEMS * kItem) return it;
+        const int64_t h = own.h;
+        const int i = (own.at << a.page_shift) + (int)(item & ((1 << per_shift) - 1)) * kItem + lane % kItem;
         // (read together: an index behind the kept ones is not looked at)
         const int kept = a.kept[h], s = !a.idx ? i : i < a.idx_stride ? a.idx[h * a.idx_stride + i] : -1;
         if (i >= kept) return it;
-        const int T = !a.K ? a.lens[h] : a.seq_lens ? a.seq_lens[own.x / a.heads] : a.t_max;
+        const int T = !a.K ? a.lens[h] : a.seq_lens ? a.seq_lens[own.h / a.heads] : a.t_max;
         it.i = i;
         if (s < 0 || s >= T) atomicOr(a.status, MKV_DEV_BAD_INDEX);
         else it.s = s;
@@ -590,7 +701,7 @@ k_page_compact(const PageArgs a, int list_ctas)
             }
             from = (id << a.page_shift) + (it.s & (a.page_size - 1));
         }
-        to = (a.free_ids[it.rank] << a.page_shift) + (it.i & (a.page_size - 1));
+        to = (it.page << a.page_shift) + (it.i & (a.page_size - 1));
     };
     const uint8_t *ks = (a.K ? a.K : a.k) + lr * (RB / LPR), *vs = (a.K ? a.V : a.v) + lr * (RB / LPR);
     uint8_t *kd = a.k + lr * (WB / LPR), *vd = a.v + lr * (WB / LPR);
@@ -603,11 +714,11 @@ k_page_compact(const PageArgs a, int list_ctas)
     };
     int64_t from;
     int to;
-    Item ahead = source(warp, owner(warp));
-    int2 own = owner(warp + warps);
+    Item ahead = source(warp, first);
+    const Item next = source(warp + warps, second);
+    Owner own = owner(warp + 2 * warps, taken);
     places(ahead, from, to);
-    ahead = source(warp + warps, own);
-    own = owner(warp + 2 * warps);
+    ahead = next;
     for (int64_t item = warp; item * ITEMS < items; item += warps) {
         constexpr int N = ROUND ? 2 : 1;
         uint4 kr[B][N], vr[B][N];
@@ -643,7 +754,7 @@ k_page_compact(const PageArgs a, int list_ctas)
         int next_to;
         places(ahead, next_from, next_to);
         ahead = source(item + 2 * warps, own);
-        own = owner(item + 3 * warps);
+        own = owner(item + 3 * warps, taken);
 #pragma unroll
         for (int b0 = 0; b0 < STEPS; b0 += B) {
             if (ROWS == kCopy || b0 > 0) load(b0);
@@ -731,7 +842,10 @@ cudaError_t launch_page_call(const PageArgs &pa, cudaStream_t st)
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if ((e = cudaLaunchKernelExC(&cfg, (const void *)k_page_plan, args)) != cudaSuccess) return e;
+        // (as many warps as there are lists: their update comes along)
+        const bool update = !a.kept && lists <= kPlanCluster * (kPageThreads / 32);
+        const void *fn = update ? (const void *)k_page_plan<true> : (const void *)k_page_plan<false>;
+        if ((e = cudaLaunchKernelExC(&cfg, fn, args)) != cudaSuccess || update) return e;
     } else {
         k_page_count<<<plan, kPageThreads, 0, st>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
