@@ -7,7 +7,7 @@
 // cache retains). A serving engine keeps it in pages, one list per head.
 //
 // A call is three launches, each a programmatic dependent of the one before
-// (small problems do the first two in one, k_page_plan):
+// (small problems do the first two in one, k_page_plan, and small updates all three):
 //  1. k_page_count: per chunk of rows the pages its lists need, per chunk of
 //     the pool the free pages (refs 0);
 //  2. k_page_assign: every CTA sums the chunk totals before its own (a few KB
@@ -18,7 +18,7 @@
 //  3. k_page_update / k_page_compact: tables, counts and rows. On a bad
 //     verdict they write the input's lists.
 // Measured: the update of 512 rows of 8 lists (4096 lists, 350K pages, a quarter of
-// the rows moved) 15 us, of 8 rows 11 us: three round trips of latency each; the
+// the rows moved) 12 us, of 8 rows 9 us: round trips of latency each; the
 // compaction of 64 lists of 8K-32K tokens to half 122 us, 107 of it the copy, 6.3
 // TB/s, 0.93 of the measured copy peak. 4-bit pages of as many tokens 49 us (floor 28):
 // planned in the same 12, and every second row of 64 bytes is copied at 0.6 of memory's
@@ -41,10 +41,12 @@ using namespace dev;
 
 constexpr int kPageThreads = 256;
 // Problems of up to 8 chunks (of 8 rows, of 4096 pages) are planned by one
-// cluster, a chunk per CTA, in one launch; larger ones in two. 16 rows x 8 heads of
-// 500-2048 tokens (5 chunks): one launch 13.1 us per call from Python and 11.4 us
-// in a graph, two 15.2 and 11.1; 32 rows (10 chunks, two per CTA): 16.4 and 14.7
-// against 15.2 and 11.6.
+// cluster, a chunk per CTA, in one launch; larger ones in two. The update of 16 rows x
+// 8 heads of 500-2048 tokens (5 chunks): planned in one launch 13.1 us per call from
+// Python and 8.8 us in a graph, in two 15 and 9.1; 32 rows (10 chunks, two per CTA) took
+// 16.4 and 14.7 against 15.2 and 11.6. Updates of no more lists than the cluster has
+// warps come along in the same launch: 8 rows x 8 heads 10.9 us from Python and 9.0 in
+// a graph, with a launch of their own 13.0 and 8.3 (the host is what bounds it).
 constexpr int kPlanCluster = 8;
 // Tokens per item of the compaction: a page holds a whole number of them, and
 // small items even out the warps' shares. With 4 rows of K and of V in flight
@@ -526,7 +528,7 @@ __device__ __forceinline__ void cluster_sync()
 }
 
 // Counts and places in one launch of one cluster, for problems of few chunks. UPDATE:
-// the lists as well, one per warp.
+// the lists as well, one per warp (they would be as many warps in a launch of their own).
 template <bool UPDATE>
 __global__ void __launch_bounds__(kPageThreads)
 k_page_plan(const PageArgs a)
