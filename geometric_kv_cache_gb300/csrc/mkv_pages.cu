@@ -40,14 +40,14 @@ namespace {
 using namespace dev;
 
 constexpr int kPageThreads = 256;
-// Problems of up to 8 chunks (of 8 rows, of 4096 pages) are planned by one
+// Problems of up to 8 chunks (of 8 rows or runs of lists, of 4096 pages) are planned by one
 // cluster, a chunk per CTA, in one launch; larger ones in two. The update of 16 rows x
 // 8 heads of 500-2048 tokens (5 chunks): planned in one launch 13.1 us per call from
 // Python and 8.8 us in a graph, in two 15 and 9.1; 32 rows (10 chunks, two per CTA) took
 // 16.4 and 14.7 against 15.2 and 11.6. Updates of no more lists than the cluster has
 // warps come along in the same launch: 8 rows x 8 heads 10.9 us from Python and 9.0 in
 // a graph, with a launch of their own 13.0 and 8.3 (the host is what bounds it).
-constexpr int kPlanCluster = 8;
+static_assert(kPlanCluster <= 8, "a portable cluster");
 // Tokens per item of the compaction: a page holds a whole number of them, and
 // small items even out the warps' shares. With 4 rows of K and of V in flight
 // per lane and 3 CTAs per SM, 8 rows of 8K-32K tokens halved take 123 us (107 us
@@ -74,11 +74,6 @@ struct ListPlan {
 __device__ __forceinline__ ListPlan plan_list(const PageArgs &a, int b, int j, int src, bool keeps)
 {
     ListPlan p = {0, 0, 0, 0};
-    if (a.kept) {
-        p.len = a.kept[(int64_t)b * a.heads + j];
-        p.total = pages_of(p.len, a);
-        return p;
-    }
     if (src < 0) return p;
     p.old_len = a.lens[(int64_t)src * a.heads + j];
     p.len = p.old_len + (a.n_new ? a.n_new[b] : 0);
@@ -115,20 +110,39 @@ __device__ __forceinline__ void load_refs(const PageArgs &a, int chunk, int (&r)
     }
 }
 
-// Chunk c of the rows, or after them of the pool: what its lists need, what is
-// free. r: the chunk's holders (of the pool's chunks).
-__device__ __forceinline__ void count_chunk(const PageArgs &a, int c, int (&r)[kThreadPages])
+// Chunk c of the lists, or after them of the pool: what the lists need, what is
+// free. A warp has `run` lists, those of a row in an update, whose parents count.
+// Each list's need goes into list_off, and into `pages` that of this lane's first
+// one; r: the chunk's holders (of the pool's chunks).
+__device__ __forceinline__ void count_chunk(const PageArgs &a, int c, int (&r)[kThreadPages], int &pages)
 {
     __shared__ long long s_need[kPlanRows];
     __shared__ uint32_t s_bits[kPlanRows];
     __shared__ int s_free[kPageThreads / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (c < a.row_chunks) {
-        const int64_t b = (int64_t)c * kPlanRows + warp;
+        const int w = c * kPlanRows + warp, b = w;
         long long need = 0;
         uint32_t bits = 0;
-        if (b < a.batch) {
-            int src = (int)b;
+        pages = 0;
+        if (a.kept) {
+            const int lists = a.batch * a.heads, h0 = w * a.run, n = min(a.run, lists - h0);
+            for (int j = lane; j < n; j += 32) {
+                const int h = h0 + j, own_len = a.lens[h], kept = a.kept[h];
+                const int T = !a.K ? own_len : a.seq_lens ? a.seq_lens[h / a.heads] : a.t_max;
+                if (!len_ok(own_len, a) || (a.K && (T < 0 || T > a.t_max))) bits |= MKV_DEV_BAD_SEQ_LEN;
+                // (without indices tokens 0 .. kept-1 must be there)
+                if (!len_ok(kept, a) || kept > (a.idx ? a.idx_stride : T)) {
+                    bits |= MKV_DEV_BAD_N_KEEP;
+                    continue;
+                }
+                const int p = pages_of(kept, a);
+                a.list_off[h] = p;
+                if (j == lane) pages = p;
+                need += p;
+            }
+        } else if (b < a.batch) {
+            int src = b;
             bool keeps = true;
             if (a.parent) {
                 src = a.parent[b];
@@ -152,23 +166,12 @@ __device__ __forceinline__ void count_chunk(const PageArgs &a, int c, int (&r)[k
                 }
             }
             if (lane == 0) a.row_src[b] = make_int2(src, keeps ? 1 : 0);
-            const int add = a.n_new && src >= 0 && !a.kept ? a.n_new[b] : 0;
+            const int add = a.n_new && src >= 0 ? a.n_new[b] : 0;
             if (add < 0) bits |= MKV_DEV_BAD_PARENT;
             for (int j = lane; j < a.heads; j += 32) {
-                const int64_t h = b * a.heads + j;
+                const int h = b * a.heads + j;
                 if (!len_ok(a.lens[h], a)) bits |= MKV_DEV_BAD_SEQ_LEN;
-                if (a.kept) {
-                    const int n = a.kept[h];
-                    bool ok = len_ok(n, a) && (!a.idx || n <= a.idx_stride);
-                    if (ok && !a.idx) {  // tokens 0 .. n-1 must be there
-                        const int T = !a.K ? a.lens[h] : a.seq_lens ? a.seq_lens[b] : a.t_max;
-                        ok = n <= T;
-                    }
-                    if (!ok) {
-                        bits |= MKV_DEV_BAD_N_KEEP;
-                        continue;
-                    }
-                } else if (src >= 0) {
+                if (src >= 0) {
                     const int L = a.lens[(int64_t)src * a.heads + j];
                     if (!len_ok(L, a)) continue;  // reported by its own row
                     if (add < 0 || (long long)L + add > ((long long)a.max_pages << a.page_shift)) {
@@ -176,14 +179,14 @@ __device__ __forceinline__ void count_chunk(const PageArgs &a, int c, int (&r)[k
                         continue;
                     }
                 }
-                const ListPlan p = plan_list(a, (int)b, j, src, keeps);
+                const ListPlan p = plan_list(a, b, j, src, keeps);
+                a.list_off[h] = p.total - p.shared;
+                if (j == lane) pages = p.total - p.shared;
                 need += p.total - p.shared;
             }
-            if (a.kept && a.K && a.seq_lens && (a.seq_lens[b] < 0 || a.seq_lens[b] > a.t_max))
-                bits |= MKV_DEV_BAD_SEQ_LEN;
-            need = warp_sum(need);
-            bits = __reduce_or_sync(kFull, bits);
         }
+        need = warp_sum(need);
+        bits = __reduce_or_sync(kFull, bits);
         if (lane == 0) {
             s_need[warp] = need;
             s_bits[warp] = bits;
@@ -245,8 +248,8 @@ __device__ __forceinline__ void block_sums(long long &x, long long &y, long long
 }
 
 // The same chunk, once all are counted: its lists' first ranks among the new
-// pages, or its free pages by rank. Chunk 0 writes the verdict.
-__device__ __forceinline__ void assign_chunk(const PageArgs &a, int c, const int (&r)[kThreadPages])
+// pages, or its free pages by rank. Chunk 0 writes the verdict. r, pages: as counted.
+__device__ __forceinline__ void assign_chunk(const PageArgs &a, int c, const int (&r)[kThreadPages], int pages)
 {
     __shared__ uint32_t scratch[kPageThreads / 32];
     __shared__ long long s_row[kPlanRows];
@@ -267,17 +270,6 @@ __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c, const int
         free_pages += n;
         if (!rows && i < chunk) before += n;
     }
-    // (a row's first lists are looked up while the sums are made)
-    const int64_t b = (int64_t)chunk * kPlanRows + warp;
-    int2 src = make_int2(-1, 0);
-    int pages = 0;
-    if (rows && b < a.batch) {
-        src = a.row_src[b];
-        if (lane < a.heads) {
-            const ListPlan p = plan_list(a, (int)b, lane, src.x, src.y != 0);
-            pages = p.total - p.shared;
-        }
-    }
     block_sums(need, free_pages, before, bits);
     if (need > free_pages) bits |= MKV_DEV_NO_PAGES;
     if (c == 0 && threadIdx.x == 0) {
@@ -287,36 +279,28 @@ __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c, const int
     }
     if (rows) {
         if (bits) return;  // no list gets a page
+        const int h0 = (chunk * kPlanRows + warp) * a.run, lists = min(a.run, a.batch * a.heads - h0);
+        int32_t *offs = a.list_off + h0;
         long long row = pages;
-        if (b < a.batch)
-            for (int j = 32 + lane; j < a.heads; j += 32) {
-                const ListPlan p = plan_list(a, (int)b, j, src.x, src.y != 0);
-                row += p.total - p.shared;
-            }
+        for (int j = 32 + lane; j < lists; j += 32) row += offs[j];
         row = warp_sum(row);
         if (lane == 0) s_row[warp] = row;
         __syncthreads();
         int off = (int)before;  // at most n_pages: the verdict was good
         for (int i = 0; i < warp; ++i) off += (int)s_row[i];
-        if (b >= a.batch) return;
-        for (int j0 = 0; j0 < a.heads; j0 += 32) {
-            const int j = j0 + lane;
-            int n = j0 ? 0 : pages;
-            if (j0 && j < a.heads) {
-                const ListPlan p = plan_list(a, (int)b, j, src.x, src.y != 0);
-                n = p.total - p.shared;
-            }
+        for (int j0 = 0; j0 < lists; j0 += 32) {
+            const int j = j0 + lane, n = j0 == 0 ? pages : j < lists ? offs[j] : 0;
             int x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(kFull, x, o);
                 if (lane >= o) x += y;
             }
-            if (j < a.heads) a.list_off[b * a.heads + j] = off + x - n;
+            if (j < lists) offs[j] = off + x - n;
             if (a.kept)  // whose each new page is
-                for (int k = 0; k < min(32, a.heads - j0); ++k) {
+                for (int k = 0; k < min(32, lists - j0); ++k) {
                     const int m = __shfl_sync(kFull, n, k), at = off + __shfl_sync(kFull, x, k) - m;
-                    for (int q = lane; q < m; q += 32) a.owners[at + q] = make_int2((int)(b * a.heads) + j0 + k, q);
+                    for (int q = lane; q < m; q += 32) a.owners[at + q] = make_int2(h0 + j0 + k, q);
                 }
             off += __shfl_sync(kFull, x, 31);
         }
@@ -352,8 +336,8 @@ __global__ void __launch_bounds__(kPageThreads)
 k_page_count(const PageArgs a)
 {
     pdl_trigger();
-    int r[kThreadPages];
-    count_chunk(a, (int)blockIdx.x, r);
+    int r[kThreadPages], pages;
+    count_chunk(a, (int)blockIdx.x, r, pages);
 }
 
 // (The call's inputs are there before k_page_count starts, which is nobody's
@@ -365,7 +349,10 @@ k_page_assign(const PageArgs a)
     int r[kThreadPages];
     if ((int)blockIdx.x >= a.row_chunks) load_refs(a, (int)blockIdx.x - a.row_chunks, r);
     pdl_wait();
-    assign_chunk(a, (int)blockIdx.x, r);
+    int pages = 0;
+    const int h0 = ((int)blockIdx.x * kPlanRows + ((int)threadIdx.x >> 5)) * a.run, j = threadIdx.x & 31;
+    if ((int)blockIdx.x < a.row_chunks && j < min(a.run, a.batch * a.heads - h0)) pages = a.list_off[h0 + j];
+    assign_chunk(a, (int)blockIdx.x, r, pages);
 }
 
 __device__ __forceinline__ void add_ref(const PageArgs &a, int page, int by)
@@ -539,11 +526,11 @@ k_page_plan(const PageArgs a)
     const bool some = UPDATE && h < (int64_t)a.batch * a.heads;
     ListInputs in;
     if (some) in = update_inputs(a, h);
-    int r[kThreadPages];
-    if (mine) count_chunk(a, (int)blockIdx.x, r);
+    int r[kThreadPages], pages = 0;
+    if (mine) count_chunk(a, (int)blockIdx.x, r, pages);
     __syncthreads();
     cluster_sync();
-    if (mine) assign_chunk(a, (int)blockIdx.x, r);
+    if (mine) assign_chunk(a, (int)blockIdx.x, r, pages);
     if (UPDATE) {
         __syncthreads();
         cluster_sync();

@@ -14,7 +14,9 @@ namespace mkv {
 // need no device and results do not depend on one.
 constexpr int kPlanSms = 152;
 constexpr int kPlanPages = 4096;  // pages of refs per CTA of the plan kernels (256 threads x 16)
-constexpr int kPlanRows = 8;      // batch rows per CTA of the plan kernels (one warp each)
+constexpr int kPlanRows = 8;      // rows, or runs of lists, per CTA of the plan kernels (one warp each)
+constexpr int kPlanCluster = 8;   // chunks that one launch of the plan takes
+constexpr int kPlanRuns = 4096;   // runs of a compaction's lists
 
 // What a pool's rows are made of. es: bytes per element, 0 for 4-bit codes with
 // an E4M3 scale per 16 dims (a page is its rows' codes, then its rows' scales).
@@ -63,6 +65,7 @@ struct PageArgs {
     int32_t *page_free, *list_off, *free_ids;
     int2 *owners;  // compact: list and place in it of each page taken
     int32_t row_chunks, page_chunks;
+    int32_t run;  // lists of a warp of the plan: those of a row, or in a compaction any
 };
 
 cudaError_t launch_page_call(const PageArgs &a, cudaStream_t st);

@@ -79,7 +79,7 @@ bool rows_ok(const void *p, int64_t stride, int32_t heads, int32_t head_dim)
 PageLayout make_page_layout(const mkv_page_pool &p, const mkv_page_lists &l)
 {
     const size_t lists = (size_t)l.batch * l.heads;
-    const size_t row_chunks = ((size_t)l.batch + kPlanRows - 1) / kPlanRows;
+    const size_t row_chunks = (std::max((size_t)l.batch, std::min(lists, (size_t)kPlanRuns)) + kPlanRows - 1) / kPlanRows;
     const size_t page_chunks = ((size_t)p.n_pages + kPlanPages - 1) / kPlanPages;
     // no call takes more pages than the pool has, nor more than its lists hold
     const size_t taken = std::min((size_t)p.n_pages, lists * (size_t)l.max_pages);
@@ -152,6 +152,7 @@ mkv_status page_call(const mkv_page_pool &p, const mkv_page_lists &in, const int
     a->free_ids = region<int32_t>(ws, L.free_ids);
     a->owners = region<int2>(ws, L.owners);
     a->row_chunks = (in.batch + kPlanRows - 1) / kPlanRows;
+    a->run = in.heads;
     a->page_chunks = (p.n_pages + kPlanPages - 1) / kPlanPages;
     return MKV_OK;
 }
@@ -185,6 +186,13 @@ mkv_status compact_call(const mkv_page_pool &pool, const mkv_page_lists &in, con
     a.idx = idx;
     a.idx_stride = idx_stride;
     a.kept = kept;
+    // The plan's warps have a list each, as far as there are kPlanRuns of them; a few more each (up to 8) where that
+    // leaves the plan in one launch. A warp writes down whose each new page is: with the 8 lists of a row per warp that
+    // took 5 us for 64 lists of 640 new pages.
+    const int lists = in.batch * in.heads, warps = (kPlanCluster - a.page_chunks) * kPlanRows;
+    a.run = (lists + kPlanRuns - 1) / kPlanRuns;
+    if (warps > 0 && lists <= 8 * warps) a.run = std::max(a.run, (lists + warps - 1) / warps);
+    a.row_chunks = ((lists + a.run - 1) / a.run + kPlanRows - 1) / kPlanRows;
     a.K = static_cast<const uint8_t *>(K);
     a.V = static_cast<const uint8_t *>(V);
     a.t_max = t_max;
