@@ -114,6 +114,7 @@ __device__ __forceinline__ void load_refs(const PageArgs &a, int chunk, int (&r)
 // free. A warp has `run` lists, those of a row in an update, whose parents count.
 // Each list's need goes into list_off, and into `pages` that of this lane's first
 // one; r: the chunk's holders (of the pool's chunks).
+template <bool COMPACT>
 __device__ __forceinline__ void count_chunk(const PageArgs &a, int c, int (&r)[kThreadPages], int &pages)
 {
     __shared__ long long s_need[kPlanRows];
@@ -125,7 +126,7 @@ __device__ __forceinline__ void count_chunk(const PageArgs &a, int c, int (&r)[k
         long long need = 0;
         uint32_t bits = 0;
         pages = 0;
-        if (a.kept) {
+        if constexpr (COMPACT) {
             const int lists = a.batch * a.heads, h0 = w * a.run, n = min(a.run, lists - h0);
             for (int j = lane; j < n; j += 32) {
                 const int h = h0 + j, own_len = a.lens[h], kept = a.kept[h];
@@ -249,6 +250,7 @@ __device__ __forceinline__ void block_sums(long long &x, long long &y, long long
 
 // The same chunk, once all are counted: its lists' first ranks among the new
 // pages, or its free pages by rank. Chunk 0 writes the verdict. r, pages: as counted.
+template <bool COMPACT>
 __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c, const int (&r)[kThreadPages], int pages)
 {
     __shared__ uint32_t scratch[kPageThreads / 32];
@@ -297,7 +299,7 @@ __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c, const int
                 if (lane >= o) x += y;
             }
             if (j < lists) offs[j] = off + x - n;
-            if (a.kept)  // whose each new page is
+            if constexpr (COMPACT)  // whose each new page is
                 for (int k = 0; k < min(32, lists - j0); ++k) {
                     const int m = __shfl_sync(kFull, n, k), at = off + __shfl_sync(kFull, x, k) - m;
                     for (int q = lane; q < m; q += 32) a.owners[at + q] = make_int2(h0 + j0 + k, q);
@@ -332,16 +334,18 @@ __device__ __forceinline__ void assign_chunk(const PageArgs &a, int c, const int
     }
 }
 
+template <bool COMPACT>
 __global__ void __launch_bounds__(kPageThreads)
 k_page_count(const PageArgs a)
 {
     pdl_trigger();
     int r[kThreadPages], pages;
-    count_chunk(a, (int)blockIdx.x, r, pages);
+    count_chunk<COMPACT>(a, (int)blockIdx.x, r, pages);
 }
 
 // (The call's inputs are there before k_page_count starts, which is nobody's
 // programmatic dependent: the launches after it read them before they wait.)
+template <bool COMPACT>
 __global__ void __launch_bounds__(kPageThreads)
 k_page_assign(const PageArgs a)
 {
@@ -352,7 +356,7 @@ k_page_assign(const PageArgs a)
     int pages = 0;
     const int h0 = ((int)blockIdx.x * kPlanRows + ((int)threadIdx.x >> 5)) * a.run, j = threadIdx.x & 31;
     if ((int)blockIdx.x < a.row_chunks && j < min(a.run, a.batch * a.heads - h0)) pages = a.list_off[h0 + j];
-    assign_chunk(a, (int)blockIdx.x, r, pages);
+    assign_chunk<COMPACT>(a, (int)blockIdx.x, r, pages);
 }
 
 __device__ __forceinline__ void add_ref(const PageArgs &a, int page, int by)
@@ -516,7 +520,7 @@ __device__ __forceinline__ void cluster_sync()
 
 // Counts and places in one launch of one cluster, for problems of few chunks. UPDATE:
 // the lists as well, one per warp (they would be as many warps in a launch of their own).
-template <bool UPDATE>
+template <bool COMPACT, bool UPDATE>
 __global__ void __launch_bounds__(kPageThreads)
 k_page_plan(const PageArgs a)
 {
@@ -527,10 +531,10 @@ k_page_plan(const PageArgs a)
     ListInputs in;
     if (some) in = update_inputs(a, h);
     int r[kThreadPages], pages = 0;
-    if (mine) count_chunk(a, (int)blockIdx.x, r, pages);
+    if (mine) count_chunk<COMPACT>(a, (int)blockIdx.x, r, pages);
     __syncthreads();
     cluster_sync();
-    if (mine) assign_chunk(a, (int)blockIdx.x, r, pages);
+    if (mine) assign_chunk<COMPACT>(a, (int)blockIdx.x, r, pages);
     if (UPDATE) {
         __syncthreads();
         cluster_sync();
@@ -833,12 +837,16 @@ cudaError_t launch_page_call(const PageArgs &pa, cudaStream_t st)
         cfg.numAttrs = 1;
         // (as many warps as there are lists: their update comes along)
         const bool update = !a.kept && lists <= kPlanCluster * (kPageThreads / 32);
-        const void *fn = update ? (const void *)k_page_plan<true> : (const void *)k_page_plan<false>;
+        const void *fn = a.kept   ? (const void *)k_page_plan<true, false>
+                         : update ? (const void *)k_page_plan<false, true>
+                                  : (const void *)k_page_plan<false, false>;
         if ((e = cudaLaunchKernelExC(&cfg, fn, args)) != cudaSuccess || update) return e;
     } else {
-        k_page_count<<<plan, kPageThreads, 0, st>>>(a);
+        if (a.kept) k_page_count<true><<<plan, kPageThreads, 0, st>>>(a);
+        else k_page_count<false><<<plan, kPageThreads, 0, st>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if ((e = launch_dependent((const void *)k_page_assign, plan, args, st)) != cudaSuccess) return e;
+        const void *assign = a.kept ? (const void *)k_page_assign<true> : (const void *)k_page_assign<false>;
+        if ((e = launch_dependent(assign, plan, args, st)) != cudaSuccess) return e;
     }
     if (!a.kept)
         return launch_dependent((const void *)k_page_update, (lists * 32 + kPageThreads - 1) / kPageThreads, args, st);
