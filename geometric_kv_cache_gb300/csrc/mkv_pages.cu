@@ -19,10 +19,10 @@
 //     verdict they write the input's lists.
 // Measured: the update of 512 rows of 8 lists (4096 lists, 350K pages, a quarter of
 // the rows moved) 12 us, of 8 rows 9 us: round trips of latency each; the
-// compaction of 64 lists of 8K-32K tokens to half 122 us, 107 of it the copy, 6.3
-// TB/s, 0.93 of the measured copy peak. 4-bit pages of as many tokens 49 us (floor 28):
-// planned in the same 12, and every second row of 64 bytes is copied at 0.6 of memory's
-// rate; a bf16 cache into 4-bit pages (mkv_page_quantize) 85 us (64).
+// compaction of 64 lists of 8K-32K tokens to half 119 us, 107 of it the copy, 6.3
+// TB/s, 0.93 of the measured copy peak. 4-bit pages of as many tokens 45 us (floor 28):
+// planned in the same 9, and every second row of 64 bytes is copied at 0.6 of memory's
+// rate; a bf16 cache into 4-bit pages (mkv_page_quantize) 83 us (64).
 // Integers only decide, and every rank is a prefix sum: nothing depends on
 // the order of the atomics (counts are sums).
 #include <cuda_runtime.h>
@@ -50,9 +50,9 @@ constexpr int kPageThreads = 256;
 static_assert(kPlanCluster <= 8, "a portable cluster");
 // Tokens per item of the compaction: a page holds a whole number of them, and
 // small items even out the warps' shares. With 4 rows of K and of V in flight
-// per lane and 3 CTAs per SM, 8 rows of 8K-32K tokens halved take 123 us (107 us
-// of it the copy, 0.93 of the copy peak); 8 in flight and 2 CTAs 127 us, with
-// items of 32 tokens 128 us.
+// per lane and 3 CTAs per SM, 8 rows of 8K-32K tokens halved take 119 us (107 us
+// of it the copy, 0.93 of the copy peak); 8 in flight and 2 CTAs take 4 us more, items
+// of 32 tokens 5.
 constexpr int kItem = 16;
 
 __device__ __forceinline__ int pages_of(int len, const PageArgs &a)
@@ -592,7 +592,7 @@ __device__ __forceinline__ uint2 group_to_e2m1(uint4 lo, uint4 hi, Rounding r, u
 
 // 16 bytes of a short row, of which memory is to bring no more than 64: by itself it
 // brings 128, and of every second row kept 151 MB instead of 108 (64 lists of
-// 8K-32K 4-bit tokens of 128 dims halved: 52.4 us, with the hint 48.5).
+// 8K-32K 4-bit tokens of 128 dims halved: 4 us more of 45).
 __device__ __forceinline__ uint4 ld_short(const void *p)
 {
     uint4 r;
