@@ -9,6 +9,7 @@ import torch
 import e2m1_util as eu
 import geometric_kv_cache_gb300 as mkv
 import paged_util as pu
+from test_gpu_paged_rope import _close
 from test_gpu_rope_axes import Step
 
 pytestmark = pytest.mark.gpu
@@ -283,3 +284,40 @@ def test_no_tokens_no_lists_and_empty_lists():
     wa = mkv.attention_workspace_for(Q, k, z(2, 2, 1), 1, 16)
     mkv.mkv_paged_attention(Q, k, v, z(2, 2, 1), z(2, 2), torch.arange(3, dtype=torch.int32, device=DEV), 1, 16, O, wa, lse=lse)
     assert mkv.mkv_device_status(wa) == 0 and int((O != 0).sum()) == 0 and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F8, U8])
+@pytest.mark.parametrize("layout,sections", [("half", [16, 16]), ("interleaved", [12, 4])])
+def test_every_row_of_more_than_32_heads_with_a_warp_per_token(dtype, layout, sections):
+    # 1300 tokens: a warp has all heads of a token, and looks places up for 32 lists at a time, keys' and then values'
+    H, G, d, page = 70, 2, 64, 16
+    p = Step(H + sum(sections), [900, 400], H, G, d, page, dtype, 2, pad_back=3)
+    n_pages = p.k.shape[0]
+    p.table[0, H - 1, :] = n_pages  # one list's pages are not there
+    inv_freq, axes = mkv.mkv_rope_frequencies(2 * sum(sections), 10000.0), mkv.mkv_rope_axes(sections, True)
+    scales = {BF: (1.0, 1.0), F8: (0.02, 0.3), U8: (0.013, 0.3)}[dtype]
+    Q, *pages = p.run(inv_freq, axes, layout, 1.25, scales)
+    assert p.status == mkv.MKV_DEV_BAD_PAGE
+    y, size = p.rotated(inv_freq, axes, layout, 1.25)
+    hq, n = H * G, int(p.start[-1])
+    _close(Q[:n], y[:n, :hq], size[:n, :hq], BF, "Q")
+    assert (Q[n:] == 7.0).all()
+    t = torch.arange(n)
+    b = (t >= p.start[1]).long()
+    s = p.lens[b] - (p.start[b + 1] - t)[:, None]                     # [n, H]
+    at = p.table[b[:, None], torch.arange(H), (s // page).long()].long()
+    there = at < n_pages
+    assert int((~there).sum()) == 900
+    at, row = at[there], (s % page).long()[there]
+    for got, old, x, sz, scale in ((pages[0], p.k, y[:n, hq:hq + H][there], size[:n, hq:hq + H][there], scales[0]),
+                                   (pages[1], p.v, p.qkv[:n, hq + H:].double()[there], 0 * size[:n, hq:hq + H][there], scales[1])):
+        if dtype is U8:
+            want = eu.rows_of(old).view(U8).clone()
+            want[at, row] = torch.cat(eu.encode(x.float(), scale), -1)
+            assert torch.equal(eu.rows_of(got).view(U8), want)
+            continue
+        ref = x / scale
+        _close(pu.raw(got)[at, row].view(dtype), ref.clamp(-448, 448) if dtype is F8 else ref, sz / scale, dtype, "pages")
+        got, want = pu.raw(got).clone(), pu.raw(old).clone()
+        got[at, row] = want[at, row] = 0
+        assert torch.equal(got, want)
