@@ -95,9 +95,12 @@ struct Chunk {
     static constexpr int THREADS = (4 + SOFT + CODES) * 32;   // 256, 384 or 512
     // Registers per thread of warps 0-3, the softmax warps and the expanding
     // ones: at most what the launch has (256 x 224, 384 x 168 or 512 x 128).
-    // (4-bit, 128 dims, 2048 tokens over 32768: 64 / 192 / 64 819 us, the 80 / 176 / 80 of E4M3, whose loop spills, 856.)
+    // 512 threads, 4-bit pages (128 dims, 2048 tokens over 32768): 64 / 192 / 64 819 us, the 80 / 176 / 80 of E4M3 pages
+    // 856. (E4M3's loop spills with its 176 too, 20 bytes at 128 dims and 16 at 64; it keeps them, no other split of it
+    // has been timed.) 384 threads with codes (256 dims): 88 / 208 / 80; 240 for the softmax is no faster (2048 tokens
+    // over 16384, 4-bit 1375 us, E4M3 1419 with both), and the 4-bit loop spills a little more.
     static constexpr int REGS_FEED = THREADS == 256 ? 168 : THREADS == 384 ? 88 : ES == 0 ? 64 : 80;
-    static constexpr int REGS_SOFT = THREADS == 256 || SOFT == 4 ? 240 : THREADS == 384 ? 208 : ES == 0 ? 192 : 176;
+    static constexpr int REGS_SOFT = THREADS == 256 ? 240 : THREADS == 384 ? 208 : ES == 0 ? 192 : 176;
     static constexpr int REGS_CODES = THREADS == 512 && ES == 0 ? 64 : 80;
     static constexpr int REGS_LAUNCH = THREADS == 256 ? 224 : THREADS == 384 ? 168 : 128;
     static_assert(4 * REGS_FEED + SOFT * REGS_SOFT + CODES * REGS_CODES <= THREADS / 32 * REGS_LAUNCH, "register split");
