@@ -501,7 +501,18 @@ cudaError_t launch_one(const AttnArgs &a, cudaStream_t st)
 // dims, bf16): 8 lists of 1024 keys, 32 rows 12 / 16, 128 rows 17.5 / 19; 32 lists
 // of 4096 keys, 32 rows 29 / 27, 64 rows 44 / 29; 128 lists of 1024 keys, 32 rows
 // 28 / 21, 128 rows 87 / 23; E4M3, 128 lists of 4096 keys, 32 rows 65 / 70, 48 rows
-// 89 / 70.
+// 89 / 70. All this is of 8- and 16-bit pages.
+//
+// 4-bit pages: tiles of both forms expand all their keys, each for itself. Half a
+// tile of the other form (128 rows, 64 at 256 dims) is counted as one tile of this
+// one, and no list as less than two; what this form has more than that is weighed
+// as above, with 2048 keys' worth of start and end. Over 342 mixes (8 to 384 lists of 64 to 16384 keys, 24 to 256 rows,
+// group 4, all dims) that takes 3.3% more time than the better form of each, the rule
+// above 6.1%; at worst 1.7 times (lists of 64 keys, 24 to 48 rows, which this form keeps:
+// 128 dims, 384 lists, 32 rows 43 / 27) and the other way round 1.65 (256 dims, 8 lists of
+// 1024 keys, 256 rows 20 / 33). Measured (us, this form / the other, 128 dims): 8 lists of 1024 keys,
+// 128 rows 15 / 23; 8 of 16384 keys, 64 rows 32 / 32, 256 rows 78 / 47; 32 of 4096 keys, 64
+// rows 28 / 36, 128 rows 53 / 40; 128 of 1024 keys, 32 rows 25 / 27, 128 rows 75 / 29.
 bool takes_chunks(int64_t batch, int64_t heads, int32_t group, int64_t n_tokens, int64_t max_q, int64_t max_len,
                   int32_t head_dim, int32_t es)
 {

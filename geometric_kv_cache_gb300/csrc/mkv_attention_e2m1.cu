@@ -20,7 +20,10 @@
 // cut tiles joined by the CTA that comes last (mkv_attention.cuh).
 //
 // Measured (128 dims, group 4): 64 rows x 8 heads of 4K-16K tokens 143 us (floor 111),
-// two rows of 120K-131K tokens x 10 heads 69 (53), one row of 2K tokens x 8 heads 9. The
+// two rows of 120K-131K tokens x 10 heads 69 (53), one row of 2K tokens x 8 heads 9. 64
+// dims: the 64 rows 92 (56), the two rows 47 (27); 256 dims, 32 rows 132 (111). Group 16: 64
+// rows 193 at 128 dims, 122 at 64, 32 rows 183 at 256. 128 rows x 8 heads of 200-300 tokens
+// 31, 35 and 51 at 64, 128 and 256 dims (floors 3, 6, 11). At 128 dims the
 // copies alone take 117 us of the 143, the arithmetic alone 129. What bounds the
 // arithmetic: 16 keys are 225 instructions without their copies -- 64 conversions
 // and 64 products at two a cycle and SM, 16 MMAs -- and of their mix an SM executes 2.1
@@ -50,7 +53,15 @@ using namespace dev;
 constexpr int kKeys = 16;  // keys of an MMA's rows: they lie in one page
 constexpr float kTop = 32768.f;        // 2^kLag<1>
 constexpr float kNothing = -3e38f;  // the reference point of a row that has seen nothing (finite: no case of its own)
-constexpr LineRule kLine = {1, 3, 3};  // see mkv_line.h
+// Cuts move to tiles' ends for a slack of 3 blocks (of 256 to 512 keys; see mkv_line.h).
+// Measured (us, cuts never move / slack 1 / 3 / 6), 128 dims: 384 lists of 1536 keys 32.1 /
+// 32.4 / 29.4 / 28.9, 228 of 1536 19.9 / 19.7 / 21.3 / 21.1, lists of 192-768 keys: 152 of them
+// 16.3 / 17.1 / 14.1 / 14.1, 456 28.1 / 29.2 / 25.9 / 25.8; 256 dims, 228 lists of 4 blocks 30.9 /
+// 30.4 / 33.6 / 33.6, 152 of 2 to 8 blocks 32.9 / 33.1 / 33.6 / 36.1. Where lists are even and fill the
+// CTAs as they are, looking for moves costs 0.5 to 1 us. Over 125 mixes of 152 to 608 lists the
+// four take 1.4, 3.8, 2.8 and 3.1% more than the best of them: 3 is for short lists of
+// uneven length, which compressed caches have.
+constexpr LineRule kLine = {1, 3, 3};
 
 // Shape of one instantiation: head dims, rows of a tile.
 template <int D, int R>

@@ -22,7 +22,8 @@
 // compaction of 64 lists of 8K-32K tokens to half 119 us, 107 of it the copy, 6.3
 // TB/s, 0.93 of the measured copy peak. 4-bit pages of as many tokens 45 us (floor 28):
 // planned in the same 9, and every second row of 64 bytes is copied at 0.6 of memory's
-// rate; a bf16 cache into 4-bit pages (mkv_page_quantize) 83 us (64).
+// rate; a bf16 cache into 4-bit pages (mkv_page_quantize) 83 us (64), into E4M3 pages 89
+// (75). Very many lists: 140000 of 20-40 tokens halved 1.16 ms in bf16, 0.97 in 4 bits.
 // Integers only decide, and every rank is a prefix sum: nothing depends on
 // the order of the atomics (counts are sums).
 #include <cuda_runtime.h>
@@ -45,8 +46,11 @@ constexpr int kPageThreads = 256;
 // 8 heads of 500-2048 tokens (5 chunks): planned in one launch 13.1 us per call from
 // Python and 8.8 us in a graph, in two 15 and 9.1; 32 rows (10 chunks, two per CTA) took
 // 16.4 and 14.7 against 15.2 and 11.6. Updates of no more lists than the cluster has
-// warps come along in the same launch: 8 rows x 8 heads 10.9 us from Python and 9.0 in
-// a graph, with a launch of their own 13.0 and 8.3 (the host is what bounds it).
+// warps come along in the same launch. That is for the host's sake: from Python, 8 to 64
+// lists of 500-2048 tokens take 12 us, with a launch of their own 14, but in a graph 7.3 to
+// 10.4 against 6.9 to 9.9 (8 rows x 8 heads, a quarter moved 10.3 / 9.9; 4 rows, nearly
+// all moved 10.4 / 9.5): the second barrier of the cluster costs 0.1 to 0.9 us more than
+// a dependent launch.
 static_assert(kPlanCluster <= 8, "a portable cluster");
 // Tokens per item of the compaction: a page holds a whole number of them, and
 // small items even out the warps' shares. With 4 rows of K and of V in flight

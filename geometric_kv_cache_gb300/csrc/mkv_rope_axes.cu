@@ -23,8 +23,8 @@
 // Measured (16384 tokens of 32 + 2 x 8 heads of 128 dims, three axes): bf16 68 us, 0.88 of
 // the floor, E4M3 65 (54), 4-bit 72 (52): 36M instructions, where the form that mkv_rope.cu
 // has, extended, took 107 us and 62M. Groups of query heads on their way together (bf16 /
-// 4-bit): four 68 / 77 us, two 72 / 84, eight, which spill, 79 / 88; two with three CTAs per SM
-// 84 / 85. Chunks of 7 rows, 2300 tokens, 4-bit: 20 us, of which 64-bit work costs 2; as one
+// 4-bit, whose 64-bit work then took it 5 us longer): four 68 / 77 us, two 72 / 84, eight, which
+// spill, 79 / 88; two with three CTAs per SM 84 / 85. Chunks of 7 rows, 2300 tokens, 4-bit: 20 us, of which 64-bit work costs 2; as one
 // 64-bit rotation of all the warp's heads it cost 6, in a chain of 62 cycles per operation.
 #include <cuda_runtime.h>
 #include <limits.h>
